@@ -246,7 +246,7 @@ def _prepare_fork(c, seed):
                  refs_out=torch.empty(c["blocks"], dtype=torch.int32, device="cuda"), workspace=None)
     if own:
         import sparse_mla_decode_combine_gb300 as pkg
-        state["workspace"] = pkg.workspace_for_cache_pages(len(lens), G * n, table.shape[1], c["blocks"])
+        state["workspace"] = pkg.workspace_for_cache_pages(len(lens), G * n, c["blocks"])
     return state
 
 
@@ -264,7 +264,7 @@ def _prepare_compact(c, seed):
                  live=torch.empty(1, dtype=torch.int32, device="cuda"), workspace=None)
     if own:
         import sparse_mla_decode_combine_gb300 as pkg
-        state["workspace"] = pkg.workspace_for_cache_pages(len(lens), len(lens), table.shape[1], c["blocks"])
+        state["workspace"] = pkg.workspace_for_cache_pages(0, 0, c["blocks"])
     return state
 
 
@@ -278,7 +278,7 @@ def _prepare_copy(c, seed):
                  src=torch.from_numpy(src).cuda(), dst=torch.from_numpy(dst).cuda(), workspace=None)
     if own:
         import sparse_mla_decode_combine_gb300 as pkg
-        state["workspace"] = pkg.workspace_for_cache_pages(0, 0, 0, c["blocks"])
+        state["workspace"] = pkg.workspace_for_cache_pages(0, 0, c["blocks"])
     return state
 
 
