@@ -404,6 +404,182 @@ DSV4_API size_t dsv4_sparse_mla_decode_mtp_union_workspace_size(int32_t num_toke
                                                                int32_t topk_width, int32_t window);
 
 /*
+ * ---- the 4-bit cache --------------------------------------------------------------------------
+ *
+ * Cache entry in 4 bits (400 bytes; entries are token-major inside a page, page stride
+ * page_block * 400 bytes):
+ *   [0, 256)    512 E2M1 latent codes, element 2i in the low half of byte i, 2i + 1 in the high half
+ *               (code s.ee.m: magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6)
+ *   [256, 384)  64 BF16 RoPE values, little-endian
+ *   [384, 400)  16 UE8M0 scale bytes; byte b scales latent dims [32 b, 32 b + 32) by 2^(byte - 127)
+ *               (255: NaN)
+ * The key is k = [latent * scale, rope] (576 dims); the value is v = latent * scale (512 dims).
+ */
+
+/*
+ * dsv4_sparse_mla_decode_fp4 -- dsv4_sparse_mla_decode over a cache of 4-bit entries.
+ *
+ * No page has a 4-bit cache: this is the decode of dsv4_sparse_mla_decode (same lists, same
+ * formulas, same outputs) with the entry above, which takes 61 % of the bytes.  The dequantised
+ * keys are exact in BF16 (a product past its range becomes an infinity, as rounding to BF16 does).
+ *
+ * Arguments: those of dsv4_sparse_mla_decode, with
+ *   kv_cache        uint8 [num_blocks, page_block, 400], 16-byte aligned (num_blocks may be 0);
+ *   workspace       at least dsv4_sparse_mla_decode_fp4_workspace_size(...) bytes, 256-byte aligned,
+ *                   not used by anything else until the work enqueued by this call has finished (two
+ *                   captured graphs that may run at the same time need a workspace each).
+ * A token whose list is empty gets out = 0 and lse = the sink (-inf without one).
+ * Returns DSV4_OK, DSV4_ERR_INVALID_ARG, DSV4_ERR_UNSUPPORTED (num_heads, topk_width) or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(const void *q, int64_t q_token_stride, const void *kv_cache,
+                                                int32_t num_blocks, int32_t page_block, const int32_t *block_table,
+                                                int64_t bt_stride, int32_t max_blocks, int32_t num_reqs,
+                                                const int32_t *req_idx, const int32_t *topk_idx, int64_t topk_stride,
+                                                int32_t topk_width, const int32_t *topk_lens, const int32_t *seq_lens,
+                                                int32_t num_tokens, int32_t num_heads, int32_t window,
+                                                const float *sink, float softmax_scale, void *out, float *lse,
+                                                void *workspace, size_t workspace_bytes, dsv4_stream_t stream);
+
+/* Bytes of device workspace dsv4_sparse_mla_decode_fp4 needs; 0 for arguments it rejects. */
+DSV4_API size_t dsv4_sparse_mla_decode_fp4_workspace_size(int32_t num_tokens, int32_t num_heads, int32_t topk_width,
+                                                          int32_t window);
+
+/*
+ * dsv4_qk_norm_rope_kv_insert_fp4 -- norms of the queries (per head) and of the key, the rotation of
+ * both, and the insert of the key as a 4-bit entry.
+ *
+ * Source of the step: vllm #42953, section 实现拆解 4, as dsv4_qnorm_rope_kv_insert; the key's norm is
+ * that of vllm #40860 "[Model] DeepSeek V4", section 实现拆解 2 (fused RMSNorm + Rope + Quant).
+ *   q_out[t][h] = RoPE(q[t][h] / sqrt(mean over 576 dims of q[t][h]^2 + eps) * w_q)
+ *   k[t]        = RoPE(kv[t]), its first n = kv_norm_dims dims divided by sqrt(mean of their squares
+ *                 + eps) and multiplied by w_kv before the rotation
+ *   kv_cache[slot_mapping[t]] = entry(k[t]): per 32 latent values the smallest e with 6 * 2^e >= amax
+ *                 (0 for amax 0, clamped to [-127, 125]), E2M1 codes of k * 2^-e (nearest, ties to
+ *                 even), scale byte e + 127; the rope part in BF16
+ *   k_out[t]    = the values of that entry in BF16 (what a later decode reads: the chunk's own
+ *                 attention can use them without the cache)
+ * The rotation is that of dsv4_qnorm_rope_kv_insert.  Queries are computed in fp32 and rounded once;
+ * the codes and scales are those of the exact k (fp64 where fp32 could decide otherwise).  A NaN is
+ * stored as the code of 6, an infinity as 6 * 2^125.
+ *
+ * Arguments:
+ *   q, q_out         BF16 [num_tokens, num_heads, 576], token strides in elements (even, >=
+ *                    num_heads * 576); q_out may be q.  Both 4-byte aligned.
+ *   num_heads        1..128; q_norm_weight fp32 [576] or NULL (all ones); eps >= 0.
+ *   kv_norm_dims     0 (the key is not normalised), 512 (its latent) or 576 (all of it);
+ *                    kv_norm_weight fp32 [kv_norm_dims] or NULL (all ones).
+ *   kv               BF16 [num_tokens, 576] (512 latent, then 64 rope), token stride even, >= 576.
+ *   positions, slot_mapping  int64 [num_tokens].
+ *   cos_sin_cache    fp32 [max_position, 64]: 32 cosines, then 32 sines per position.
+ *   kv_cache         uint8 [num_slots, 400], 16-byte aligned.
+ *   k_out            BF16 [num_tokens, 576], token stride even, >= 576; or NULL.  Not kv itself.
+ * A negative slot writes no entry (a padding token; its queries and k_out are computed).  A slot >=
+ * num_slots, or a position outside [0, max_position), writes no entry and sets DSV4_ERR_BAD_INDEX in
+ * the device status word; at such a position nothing is rotated.  Two tokens of a call must not name
+ * one slot.  Nothing is allocated.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_qk_norm_rope_kv_insert_fp4(
+    const void *q, int64_t q_token_stride, void *q_out, int64_t q_out_token_stride, int32_t num_tokens,
+    int32_t num_heads, const float *q_norm_weight, const float *kv_norm_weight, int32_t kv_norm_dims, double eps,
+    const void *kv, int64_t kv_token_stride, const int64_t *positions, const int64_t *slot_mapping,
+    const float *cos_sin_cache, int32_t max_position, void *kv_cache, int64_t num_slots, void *k_out,
+    int64_t k_out_token_stride, dsv4_stream_t stream);
+
+/*
+ * ---- pages of a cache -------------------------------------------------------------------------
+ *
+ * A pool is num_layers caches of num_blocks pages, layer l at cache + l * layer_stride bytes, page b of
+ * a layer at b * page_block * entry_bytes (entries of 656, 400 or any other multiple of 16 bytes; the
+ * base 16-byte aligned, layer_stride a multiple of 16).  All layers share one block table, the rows'
+ * lengths and one reference count per page:
+ *   block_table  int32 [num_rows, max_blocks]: row r's pages in order, ceil(seq_lens[r] / page_block) of
+ *                them; the cells after those are not read
+ *   seq_lens     int32 [num_rows] (0 or less: an empty row)
+ *   ref_counts   int32 [num_blocks]: the rows (and other holders) that name a page; 0: the page is free
+ * The operators below run on the device alone: they can be captured, and no length, count or page number
+ * passes through the host.  A page number outside [0, num_blocks), or a length past max_blocks *
+ * page_block, in a row that is read sets DSV4_ERR_BAD_INDEX in the device status word; the cell becomes
+ * -1, the length is cut.  ref_counts must count every row of the table that is given.
+ *
+ * workspace: at least dsv4_cache_pages_workspace_size(num_rows, num_rows_out, num_blocks) bytes (the
+ * compact and the copies need no rows: 0, 0), 256-byte aligned, not used by anything else until the
+ * call's work has finished.
+ */
+DSV4_API size_t dsv4_cache_pages_workspace_size(int32_t num_rows, int32_t num_rows_out, int32_t num_blocks);
+
+/*
+ * dsv4_cache_fork_rows -- replace the table's rows by copies of them: forking, beam search's choice of
+ * parents, and freeing, in one call.
+ *
+ * Row r of the result is a copy of row parent[r]; a negative parent gives an empty row, and a row that is
+ * nobody's parent is freed (parent = 0, 1, .. with -1 for the finished rows frees those and keeps the
+ * rest).  Page j of a row is
+ *   shared   the parent's page, with one more reference, when `share` is not 0 and the page is full;
+ *   kept     the parent's page, for the lowest row of that parent, when its count on entry is 1;
+ *   taken    else: a free page that the page's entries are copied into, in every layer, count 1.
+ * So a partly filled page always ends with one holder, and appending to a row never writes into
+ * another's.  With share = 0 no two rows of the result share a page.  Pages that are free on entry are
+ * taken lowest first, in the order of (row, page); pages that this call frees are not taken by it.  A row
+ * that would need pages past the last free one becomes an empty row and sets DSV4_ERR_BAD_INDEX in the
+ * device status word.
+ *
+ * Arguments: the pool; block_table, seq_lens [num_rows], ref_counts: the state before the call;
+ *   parent           int32 [num_rows_out], each < num_rows (others: an empty row, and the status bit)
+ *   block_table_out  int32 [num_rows_out, max_blocks], row stride bt_out_stride; every cell is written
+ *                    (-1 after a row's pages).  Must not overlap block_table.
+ *   seq_lens_out     int32 [num_rows_out].  Must not overlap seq_lens.
+ *   ref_counts_out   int32 [num_blocks]; may be ref_counts.
+ * max_blocks <= 2^20, num_blocks <= 2^30.  Of a taken page only the entries that the row holds are
+ * written.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_cache_fork_rows(void *cache, int32_t num_layers, int64_t layer_stride, int32_t num_blocks,
+                                          int32_t page_block, int32_t entry_bytes, const int32_t *block_table,
+                                          int64_t bt_stride, const int32_t *seq_lens, int32_t num_rows,
+                                          const int32_t *parent, int32_t num_rows_out, int32_t max_blocks,
+                                          int32_t *block_table_out, int64_t bt_out_stride, int32_t *seq_lens_out,
+                                          const int32_t *ref_counts, int32_t *ref_counts_out, int32_t share,
+                                          void *workspace, size_t workspace_bytes, dsv4_stream_t stream);
+
+/*
+ * dsv4_cache_compact -- move the live pages to the front of the pool.
+ *
+ * With L pages of a count > 0, the k-th of them at or past L (ascending) moves, in every layer, to the k-th
+ * free page below L; the other live pages stay.  Afterwards pages [0, L) are live and [L, num_blocks) free.
+ *   block_table_out  int32 [num_rows, max_blocks]: block_table with the pages' new numbers, -1 after a
+ *                    row's pages; may be block_table (with the same stride)
+ *   ref_counts_out   int32 [num_blocks]: the counts of the pages in their new places; may be ref_counts
+ *   page_map         int32 [num_blocks]: the new number of each page, -1 for a free one (for page numbers
+ *                    that are held elsewhere)
+ *   num_live         int32 [1]: L
+ * A cell that names a page whose count is 0 becomes -1 and sets DSV4_ERR_BAD_INDEX in the device status
+ * word.  The entries of the pages from L on are left as they were.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG
+ * or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_cache_compact(void *cache, int32_t num_layers, int64_t layer_stride, int32_t num_blocks,
+                                        int32_t page_block, int32_t entry_bytes, const int32_t *block_table,
+                                        int64_t bt_stride, const int32_t *seq_lens, int32_t num_rows,
+                                        int32_t max_blocks, int32_t *block_table_out, int64_t bt_out_stride,
+                                        const int32_t *ref_counts, int32_t *ref_counts_out, int32_t *page_map,
+                                        int32_t *num_live, void *workspace, size_t workspace_bytes,
+                                        dsv4_stream_t stream);
+
+/*
+ * dsv4_cache_copy_pages -- copy the listed pages, in every layer, within a pool or into another one.
+ *
+ * Page src_pages[i] of src_cache goes to page dst_pages[i] of dst_cache, i < num_pages.  A target that is
+ * listed more than once receives its last pair.  In one pool (the same base, layer stride and number of
+ * pages), a pair whose source is also a target of the call is left out and sets DSV4_ERR_BAD_INDEX in the
+ * device status word, as does a page number out of range; two different pools must not overlap.
+ * Workspace: dsv4_cache_pages_workspace_size(0, 0, dst_num_blocks).  Returns DSV4_OK,
+ * DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_stride, int32_t dst_num_blocks,
+                                           const void *src_cache, int64_t src_layer_stride, int32_t src_num_blocks,
+                                           int32_t num_layers, int32_t page_block, int32_t entry_bytes,
+                                           const int32_t *src_pages, const int32_t *dst_pages, int32_t num_pages,
+                                           void *workspace, size_t workspace_bytes, dsv4_stream_t stream);
+
+/*
  * dsv4_get_device_status -- synchronise `stream`, then read and clear the current
  * device's sticky status word.
  *

@@ -33,7 +33,10 @@ EXPORTED = ("dsv4_combine_topk_swa_indices", "dsv4_combine_topk_swa_indices_comp
             "dsv4_qnorm_rope_kv_insert", "dsv4_selftest_wait_timeout",
             "dsv4_sparse_mla_decode_workspace_size", "dsv4_sparse_mla_decode", "dsv4_sparse_mla_decode_trace",
             "dsv4_sparse_mla_decode_noalloc", "dsv4_sparse_mla_decode_mtp_union",
-            "dsv4_sparse_mla_decode_mtp_union_workspace_size", "dsv4_get_device_status")
+            "dsv4_sparse_mla_decode_mtp_union_workspace_size", "dsv4_sparse_mla_decode_fp4",
+            "dsv4_sparse_mla_decode_fp4_workspace_size", "dsv4_qk_norm_rope_kv_insert_fp4",
+            "dsv4_cache_pages_workspace_size", "dsv4_cache_fork_rows", "dsv4_cache_compact", "dsv4_cache_copy_pages",
+            "dsv4_get_device_status")
 
 
 class Dsv4Error(RuntimeError):
@@ -92,6 +95,23 @@ def load_library():
                                                      i32, i32, P, ctypes.c_float, P, P, P, ctypes.c_size_t, P]
     lib.dsv4_sparse_mla_decode_mtp_union_workspace_size.restype = ctypes.c_size_t
     lib.dsv4_sparse_mla_decode_mtp_union_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.dsv4_sparse_mla_decode_fp4.restype = ctypes.c_int
+    lib.dsv4_sparse_mla_decode_fp4.argtypes = lib.dsv4_sparse_mla_decode.argtypes
+    lib.dsv4_sparse_mla_decode_fp4_workspace_size.restype = ctypes.c_size_t
+    lib.dsv4_sparse_mla_decode_fp4_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.dsv4_qk_norm_rope_kv_insert_fp4.restype = ctypes.c_int
+    lib.dsv4_qk_norm_rope_kv_insert_fp4.argtypes = [P, i64, P, i64, i32, i32, P, P, i32, ctypes.c_double, P, i64, P, P,
+                                                    P, i32, P, i64, P, i64, P]
+    lib.dsv4_cache_pages_workspace_size.restype = ctypes.c_size_t
+    lib.dsv4_cache_pages_workspace_size.argtypes = [i32, i32, i32]
+    lib.dsv4_cache_fork_rows.restype = ctypes.c_int
+    lib.dsv4_cache_fork_rows.argtypes = [P, i32, i64, i32, i32, i32, P, i64, P, i32, P, i32, i32, P, i64, P, P, P, i32,
+                                         P, ctypes.c_size_t, P]
+    lib.dsv4_cache_compact.restype = ctypes.c_int
+    lib.dsv4_cache_compact.argtypes = [P, i32, i64, i32, i32, i32, P, i64, P, i32, i32, P, i64, P, P, P, P, P,
+                                       ctypes.c_size_t, P]
+    lib.dsv4_cache_copy_pages.restype = ctypes.c_int
+    lib.dsv4_cache_copy_pages.argtypes = [P, i64, i32, P, i64, i32, i32, i32, i32, P, P, i32, P, ctypes.c_size_t, P]
     lib.dsv4_get_device_status.restype = ctypes.c_int
     lib.dsv4_get_device_status.argtypes = [P]
     _lib = lib
@@ -348,6 +368,205 @@ def dsv4_sparse_mla_decode_mtp_union(q: torch.Tensor, kv_cache: torch.Tensor, bl
         _stream(stream))
 
 
+# ----------------------------------------------------------------------------
+# the 4-bit cache and the page operators
+# ----------------------------------------------------------------------------
+def _on(dev: int, t: torch.Tensor, dtype, name: str, ndim: int) -> int:
+    """The pointer of a tensor that has to be on device `dev`, of this type and number of dims, with unit stride
+    along the last one."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: must be on the current CUDA device")
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim} dims, got {t.dim()}")
+    if ndim and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: last dim must be contiguous")
+    return t.data_ptr()
+
+
+def _device_and_stream(stream):
+    """The current device's number, and the stream's handle (that device's current one for None)."""
+    if stream is None:
+        stream = torch.cuda.current_stream()
+        return stream.device_index, stream.cuda_stream
+    return torch.cuda.current_device(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _row_stride(t: torch.Tensor, name: str, width: int) -> int:
+    """The stride of dim 0 (of a single row: any that is wide enough); rows must not overlap."""
+    if t.shape[0] <= 1:
+        return max(t.stride(0), width)
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.stride(0)
+
+
+def dsv4_sparse_mla_decode_fp4_workspace_size(num_tokens: int, num_heads: int, topk_width: int, window: int) -> int:
+    return int(load_library().dsv4_sparse_mla_decode_fp4_workspace_size(num_tokens, num_heads, topk_width, window))
+
+
+def dsv4_sparse_mla_decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
+                               req_idx: Optional[torch.Tensor], topk_idx: torch.Tensor,
+                               topk_lens: Optional[torch.Tensor], seq_lens: torch.Tensor, window: int,
+                               sink: Optional[torch.Tensor], softmax_scale: float, out: torch.Tensor,
+                               lse: Optional[torch.Tensor], workspace: torch.Tensor, stream=None) -> int:
+    """dsv4_sparse_mla_decode over a cache of 4-bit entries (see include/dsv4.h): kv_cache uint8
+    [num_blocks, page, 400]; workspace uint8 [>= dsv4_sparse_mla_decode_fp4_workspace_size(...)]; the other
+    arguments as there.  Every tensor is on the current device."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    T, H, D = q.shape
+    K = topk_idx.shape[1]
+    if D != 576 or q.stride(1) != 576 and H > 1:
+        raise ValueError("q: heads must be contiguous rows of 576")
+    if kv_cache.shape[-1] != 400 or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache: must be contiguous, with entries of 400 bytes")
+    if out.shape != (T, H, 512) or not out.is_contiguous():
+        raise ValueError("out: must be contiguous [tokens, heads, 512]")
+    if lse is not None and (lse.shape != (T, H) or not lse.is_contiguous()):
+        raise ValueError("lse: must be contiguous [tokens, heads]")
+    if topk_idx.shape[0] != T or seq_lens.numel() != T or (topk_lens is not None and topk_lens.numel() != T) or \
+            (req_idx is not None and req_idx.numel() != T):
+        raise ValueError("topk_idx, topk_lens, seq_lens, req_idx: must have a row for each token")
+    if sink is not None and sink.numel() != H:
+        raise ValueError("sink: must have a value for each head")
+    i32 = torch.int32
+    return lib.dsv4_sparse_mla_decode_fp4(
+        _on(dev, q, torch.bfloat16, "q", 3), _row_stride(q, "q", H * 576), _on(dev, kv_cache, torch.uint8, "kv_cache", 3),
+        kv_cache.shape[0], kv_cache.shape[1], _on(dev, block_table, i32, "block_table", 2),
+        _row_stride(block_table, "block_table", block_table.shape[1]), block_table.shape[1], block_table.shape[0],
+        None if req_idx is None else _on(dev, req_idx, i32, "req_idx", 1), _on(dev, topk_idx, i32, "topk_idx", 2) or None,
+        _row_stride(topk_idx, "topk_idx", K), K, None if topk_lens is None else _on(dev, topk_lens, i32, "topk_lens", 1),
+        _on(dev, seq_lens, i32, "seq_lens", 1), T, H, window,
+        None if sink is None else _on(dev, sink, torch.float32, "sink", 1), softmax_scale,
+        _on(dev, out, torch.bfloat16, "out", 3), None if lse is None else _on(dev, lse, torch.float32, "lse", 2),
+        _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(), st)
+
+
+def dsv4_qk_norm_rope_kv_insert_fp4(q: torch.Tensor, q_out: torch.Tensor, kv: torch.Tensor, positions: torch.Tensor,
+                                    slot_mapping: torch.Tensor, cos_sin_cache: torch.Tensor, kv_cache: torch.Tensor,
+                                    k_out: Optional[torch.Tensor] = None, q_norm_weight: Optional[torch.Tensor] = None,
+                                    kv_norm_weight: Optional[torch.Tensor] = None, kv_norm_dims: int = 512,
+                                    eps: float = 1e-6, stream=None) -> int:
+    """q, q_out bf16 [T, H, 576] (heads contiguous); kv, k_out bf16 [T, 576] (k_out may be None); positions,
+    slot_mapping int64 [T]; cos_sin_cache float32 [max_position, 64]; kv_cache uint8 [..., 400] (slots in order);
+    q_norm_weight float32 [576] or None; kv_norm_weight float32 [kv_norm_dims] or None."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    T, H, D = q.shape
+    bf16, i64, f32 = torch.bfloat16, torch.int64, torch.float32
+    if D != 576 or q_out.shape != q.shape or (H > 1 and (q.stride(1) != 576 or q_out.stride(1) != 576)):
+        raise ValueError("q, q_out: heads must be contiguous rows of 576, and the shapes the same")
+    if kv.shape != (T, 576) or (k_out is not None and k_out.shape != (T, 576)):
+        raise ValueError("kv, k_out: must be [tokens, 576]")
+    if positions.numel() != T or slot_mapping.numel() != T:
+        raise ValueError("positions, slot_mapping: must have a value for each token")
+    if cos_sin_cache.shape[-1] != 64 or not cos_sin_cache.is_contiguous():
+        raise ValueError("cos_sin_cache: must be contiguous [max_position, 64]")
+    if kv_cache.shape[-1] != 400 or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache: must be contiguous, with entries of 400 bytes")
+    if (q_norm_weight is not None and q_norm_weight.numel() != 576) or \
+            (kv_norm_weight is not None and kv_norm_weight.numel() != kv_norm_dims):
+        raise ValueError("norm weights: must have a value for each normalised dim")
+    return lib.dsv4_qk_norm_rope_kv_insert_fp4(
+        _on(dev, q, bf16, "q", 3), _row_stride(q, "q", H * 576), _on(dev, q_out, bf16, "q_out", 3),
+        _row_stride(q_out, "q_out", H * 576), T, H,
+        None if q_norm_weight is None else _on(dev, q_norm_weight, f32, "q_norm_weight", 1),
+        None if kv_norm_weight is None else _on(dev, kv_norm_weight, f32, "kv_norm_weight", 1), kv_norm_dims, eps,
+        _on(dev, kv, bf16, "kv", 2), _row_stride(kv, "kv", 576), _on(dev, positions, i64, "positions", 1),
+        _on(dev, slot_mapping, i64, "slot_mapping", 1), _on(dev, cos_sin_cache, f32, "cos_sin_cache", 2),
+        cos_sin_cache.shape[0], _on(dev, kv_cache, torch.uint8, "kv_cache", kv_cache.dim()), kv_cache.numel() // 400,
+        None if k_out is None else _on(dev, k_out, bf16, "k_out", 2),
+        0 if k_out is None else _row_stride(k_out, "k_out", 576), st)
+
+
+def _pool(dev: int, cache: torch.Tensor, name: str):
+    """(pointer, layers, layer stride, pages, page, entry bytes) of a pool uint8 [layers, pages, page, entry]."""
+    ptr = _on(dev, cache, torch.uint8, name, 4)
+    L, B, page, entry = cache.shape
+    s = cache.stride()
+    if cache.numel() and (s[2] != entry and page > 1 or s[1] != page * entry and B > 1):
+        raise ValueError(f"{name}: the pages of a layer must be contiguous")
+    return ptr, L, s[0], B, page, entry
+
+
+def dsv4_cache_pages_workspace_size(num_rows: int, num_rows_out: int, num_blocks: int) -> int:
+    return int(load_library().dsv4_cache_pages_workspace_size(num_rows, num_rows_out, num_blocks))
+
+
+def dsv4_cache_fork_rows(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                         ref_counts: torch.Tensor, parent: torch.Tensor, block_table_out: torch.Tensor,
+                         seq_lens_out: torch.Tensor, ref_counts_out: torch.Tensor, workspace: torch.Tensor,
+                         share: bool = True, stream=None) -> int:
+    """Rows of the result are copies of rows parent[r] (-1: empty); rows nobody descends from are freed (see
+    include/dsv4.h).  cache uint8 [layers, pages, page, entry bytes]; block_table int32 [rows, max_blocks],
+    block_table_out [rows out, max_blocks]; seq_lens, seq_lens_out, parent int32; ref_counts, ref_counts_out int32
+    [pages] (may be the same tensor); workspace uint8 [>= dsv4_cache_pages_workspace_size(rows, rows out, pages)]."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    ptr, L, ls, B, page, entry = _pool(dev, cache, "cache")
+    i32 = torch.int32
+    R, M = block_table.shape
+    Ro = parent.numel()
+    if seq_lens.numel() != R or seq_lens_out.numel() != Ro or block_table_out.shape != (Ro, M):
+        raise ValueError("block_table_out, seq_lens, seq_lens_out: must have a row for each row, and max_blocks cells")
+    if ref_counts.numel() != B or ref_counts_out.numel() != B:
+        raise ValueError("ref_counts, ref_counts_out: must have a count for each page")
+    return lib.dsv4_cache_fork_rows(
+        ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table", 2), _row_stride(block_table, "block_table", M),
+        _on(dev, seq_lens, i32, "seq_lens", 1), R, _on(dev, parent, i32, "parent", 1), Ro, M,
+        _on(dev, block_table_out, i32, "block_table_out", 2), _row_stride(block_table_out, "block_table_out", M),
+        _on(dev, seq_lens_out, i32, "seq_lens_out", 1), _on(dev, ref_counts, i32, "ref_counts", 1),
+        _on(dev, ref_counts_out, i32, "ref_counts_out", 1), 1 if share else 0,
+        _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(), st)
+
+
+def dsv4_cache_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
+                       block_table_out: torch.Tensor, ref_counts_out: torch.Tensor, page_map: torch.Tensor,
+                       num_live: torch.Tensor, workspace: torch.Tensor, stream=None) -> int:
+    """Live pages move to the front of the pool (see include/dsv4.h).  cache uint8 [layers, pages, page, entry bytes];
+    block_table, block_table_out int32 [rows, max_blocks] and ref_counts, ref_counts_out int32 [pages] (each pair may
+    be one tensor); page_map int32 [pages]; num_live int32 [1]; workspace uint8 [>=
+    dsv4_cache_pages_workspace_size(0, 0, pages)]."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    ptr, L, ls, B, page, entry = _pool(dev, cache, "cache")
+    i32 = torch.int32
+    R, M = block_table.shape
+    if seq_lens.numel() != R or block_table_out.shape != (R, M):
+        raise ValueError("seq_lens, block_table_out: must have a row for each row of block_table")
+    if ref_counts.numel() != B or ref_counts_out.numel() != B or page_map.numel() != B or num_live.numel() != 1:
+        raise ValueError("ref_counts, ref_counts_out, page_map: must have a value for each page, num_live one value")
+    return lib.dsv4_cache_compact(
+        ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table", 2), _row_stride(block_table, "block_table", M),
+        _on(dev, seq_lens, i32, "seq_lens", 1), R, M, _on(dev, block_table_out, i32, "block_table_out", 2),
+        _row_stride(block_table_out, "block_table_out", M), _on(dev, ref_counts, i32, "ref_counts", 1),
+        _on(dev, ref_counts_out, i32, "ref_counts_out", 1), _on(dev, page_map, i32, "page_map", 1),
+        _on(dev, num_live, i32, "num_live", 1), _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(), st)
+
+
+def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_pages: torch.Tensor,
+                          dst_pages: torch.Tensor, workspace: torch.Tensor, stream=None) -> int:
+    """Page src_pages[i] of src_cache to page dst_pages[i] of dst_cache, in every layer (see include/dsv4.h).
+    dst_cache, src_cache uint8 [layers, pages, page, entry bytes] (may be one tensor); src_pages, dst_pages int32 [n];
+    workspace uint8 [>= dsv4_cache_pages_workspace_size(0, 0, pages of dst_cache)]."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    dp, L, dls, dB, page, entry = _pool(dev, dst_cache, "dst_cache")
+    sp, sL, sls, sB, spage, sentry = _pool(dev, src_cache, "src_cache")
+    if (sL, spage, sentry) != (L, page, entry):
+        raise ValueError("dst_cache, src_cache: must have the same layers, page and entry sizes")
+    n = src_pages.numel()
+    if dst_pages.numel() != n:
+        raise ValueError("src_pages, dst_pages: must have the same length")
+    i32 = torch.int32
+    return lib.dsv4_cache_copy_pages(
+        dp, dls, dB, sp, sls, sB, L, page, entry, _on(dev, src_pages, i32, "src_pages", 1),
+        _on(dev, dst_pages, i32, "dst_pages", 1), n, _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(),
+        st)
+
+
 def dsv4_get_device_status(stream=None) -> int:
     return int(load_library().dsv4_get_device_status(_stream(stream)))
 
@@ -369,6 +588,27 @@ def workspace_for_mtp_union(num_tokens: int, num_heads: int, topk_width: int, wi
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+def _allocating_on(stream):
+    """A context in which what is allocated belongs to the stream that the call runs on."""
+    if stream is None or isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+
+
+def workspace_for_fp4(num_tokens: int, num_heads: int, topk_width: int, window: int, device=None) -> torch.Tensor:
+    n = dsv4_sparse_mla_decode_fp4_workspace_size(num_tokens, num_heads, topk_width, window)
+    if n == 0:
+        raise Dsv4Error(DSV4_ERR_INVALID_ARG, "workspace size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def workspace_for_cache_pages(num_rows: int, num_rows_out: int, num_blocks: int, device=None) -> torch.Tensor:
+    n = dsv4_cache_pages_workspace_size(num_rows, num_rows_out, num_blocks)
+    if n == 0:
+        raise Dsv4Error(DSV4_ERR_INVALID_ARG, "workspace size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
 def sparse_mla_decode(q, kv_cache, block_table, req_idx, topk_idx, topk_lens, seq_lens, window, sink,
                       softmax_scale, out=None, lse=None, workspace=None, stream=None):
     """Allocating wrapper of dsv4_sparse_mla_decode; returns (out, lse)."""
@@ -382,6 +622,52 @@ def sparse_mla_decode(q, kv_cache, block_table, req_idx, topk_idx, topk_lens, se
     check(dsv4_sparse_mla_decode(q, kv_cache, block_table, req_idx, topk_idx, topk_lens, seq_lens, window, sink,
                                  softmax_scale, out, lse, workspace, stream), "dsv4_sparse_mla_decode")
     return out, lse
+
+
+def sparse_mla_decode_fp4(q, kv_cache, block_table, req_idx, topk_idx, topk_lens, seq_lens, window, sink,
+                          softmax_scale, out=None, lse=None, workspace=None, stream=None):
+    """Allocating wrapper of dsv4_sparse_mla_decode_fp4; returns (out, lse)."""
+    T, H, _ = q.shape
+    with _allocating_on(stream):
+        if out is None:
+            out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = workspace_for_fp4(T, H, topk_idx.shape[1], window, q.device)
+        check(dsv4_sparse_mla_decode_fp4(q, kv_cache, block_table, req_idx, topk_idx, topk_lens, seq_lens, window, sink,
+                                         softmax_scale, out, lse, workspace, stream), "dsv4_sparse_mla_decode_fp4")
+    return out, lse
+
+
+def cache_fork_rows(cache, block_table, seq_lens, ref_counts, parent, share=True, workspace=None, stream=None):
+    """Allocating wrapper of dsv4_cache_fork_rows; returns (block_table, seq_lens, ref_counts) after the call.  The
+    cache is written in place."""
+    Ro, dev = parent.numel(), cache.device
+    with _allocating_on(stream):
+        table = torch.empty((Ro, block_table.shape[1]), dtype=torch.int32, device=dev)
+        lens = torch.empty((Ro,), dtype=torch.int32, device=dev)
+        refs = torch.empty_like(ref_counts)
+        if workspace is None:
+            workspace = workspace_for_cache_pages(block_table.shape[0], Ro, ref_counts.numel(), dev)
+        check(dsv4_cache_fork_rows(cache, block_table, seq_lens, ref_counts, parent, table, lens, refs, workspace, share,
+                                   stream), "dsv4_cache_fork_rows")
+    return table, lens, refs
+
+
+def cache_compact(cache, block_table, seq_lens, ref_counts, workspace=None, stream=None):
+    """Allocating wrapper of dsv4_cache_compact; returns (block_table, ref_counts, page_map, num_live) after the call.
+    The cache is written in place."""
+    dev = cache.device
+    with _allocating_on(stream):
+        table, refs, page_map = (torch.empty(t.shape, dtype=torch.int32, device=dev)
+                                 for t in (block_table, ref_counts, ref_counts))
+        live = torch.empty((1,), dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = workspace_for_cache_pages(0, 0, ref_counts.numel(), dev)
+        check(dsv4_cache_compact(cache, block_table, seq_lens, ref_counts, table, refs, page_map, live, workspace, stream),
+              "dsv4_cache_compact")
+    return table, refs, page_map, live
 
 
 def combine_topk_swa_indices(topk_idx, topk_lens, seq_lens, window, combined_width=None, stream=None):

@@ -20,7 +20,8 @@ std::mutex g_mu;
 unsigned *g_status_ptr[kMaxDevices];
 int g_sm_count[kMaxDevices];
 
-// Device address of the status word and the SM count of the current device.
+}  // namespace
+
 cudaError_t device_info(unsigned **status, int *sms)
 {
     int dev = 0;
@@ -48,6 +49,8 @@ cudaError_t device_info(unsigned **status, int *sms)
         *sms = g_sm_count[dev];
     return cudaSuccess;
 }
+
+namespace {
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -92,8 +92,11 @@ struct DecodeParams {
 // (device, kernel slot); later calls with no larger size touch no CUDA state, so a
 // call made after the first one on a device is safe inside stream capture.
 enum AttrSlot { kAttrCombine = 0, kAttrTc, kAttrTcLong, kAttrTcUnion, kAttrTcUnionLong, kAttrUnion, kAttrTopk,
-                kAttrTopkCluster, kAttrSlots };
+                kAttrTopkCluster, kAttrFp4, kAttrFp4Long, kAttrSlots };
 cudaError_t set_smem_once(const void *kernel, int bytes, AttrSlot slot);
+
+// Device address of the status word and the SM count of the current device (either may be null).
+cudaError_t device_info(unsigned **status, int *sms);
 
 int combine_table_bits(int topk_width);
 size_t combine_smem_bytes(int table_bits, int topk_width);

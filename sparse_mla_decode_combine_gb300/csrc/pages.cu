@@ -1,0 +1,508 @@
+// pages.cu -- operators on the pages of a paged cache: forking rows (with copy-on-write of their
+// last page, or private copies), compacting the live pages to the front of the pool, and copying
+// listed pages.  They move whole entries and never look into them, so any entry format will do.
+//
+// The pool's state is three arrays: the block table, the rows' lengths, and a reference count per
+// page (0: the page is free).  New pages are the lowest-numbered free ones, so the result of a call
+// depends on its inputs alone; integer sums are the only atomics.
+//
+// Every operator is two launches.  A planning kernel, one cluster of eight CTAs, does the index work
+// (counts, ranks and sums over the reference counts and rows, with a cluster barrier between dependent
+// steps: no launch, no wait on global memory) and writes which pages are copied where; a second kernel
+// over the whole GPU moves the pages of every layer.  The second kernel is bound by HBM (each
+// byte read and written once), the first by the latency of its steps (a few microseconds).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fp4.h"
+
+namespace dsv4 {
+namespace {
+
+constexpr int kCluster = 8;
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kCluster * kPlanThreads / 32;
+constexpr int kCopyThreads = 256;
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ int cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+
+// the copy of `v` in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ int ld_rank(const int *v, int rank)
+{
+    uint32_t a;
+    int x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(v)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+    return x;
+}
+
+// exclusive sum of v over the CTA's threads; *total receives the sum.  Two barriers.
+__device__ __forceinline__ int cta_scan(int v, int *wsum, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d)
+            x += y;
+    }
+    __syncthreads();   // (the previous use of wsum is over)
+    if (lane == 31)
+        wsum[warp] = x;
+    __syncthreads();
+    const int ws = wsum[lane];   // kPlanThreads / 32 = 32 warps
+    int before = lane < warp ? ws : 0, all = ws;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, d);
+        all += __shfl_xor_sync(0xffffffffu, all, d);
+    }
+    *total = all;
+    return before + x - v;
+}
+
+__device__ __forceinline__ int pages_of(int len, int page, int max_blocks)
+{
+    const int n = len <= 0 ? 0 : (len - 1) / page + 1;
+    return n < max_blocks ? n : max_blocks;
+}
+
+// entries that page j of a row of `len` entries holds
+__device__ __forceinline__ int entries_of(int len, int page, int j)
+{
+    const int64_t left = (int64_t)len - (int64_t)j * page;
+    return left < page ? (int)left : page;
+}
+
+// ---- fork ----------------------------------------------------------------------------------------
+
+// Row r of the output is a copy of row parent[r] (an empty row for a negative parent).  Page j of it is
+//   shared   (the parent's page, one more reference)  when share is set and the page is full;
+//   kept     (the parent's page)  otherwise, for the lowest output row of that parent, when the page
+//            has that one reference on entry;
+//   taken    (a free page, the parent's entries copied into it)  else.
+// Free pages are those with a count of 0 on entry, lowest first, given out in order of (row, page); a
+// row that needs pages past the last free one becomes an empty row and is flagged.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams p)
+{
+    __shared__ int wsum[32];
+    __shared__ int count;
+    const int rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31;
+    const int gtid = rank * kPlanThreads + tid, gwarp = gtid >> 5;
+    const int B = p.pool.num_blocks, page = p.pool.page;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the copy kernel waits for this grid itself)
+
+    // ---- the free pages of this CTA's part of the pool, and the rows' empty counters
+    const int part = (B + kCluster - 1) / kCluster;
+    const int lo = min(B, rank * part), hi = min(B, lo + part);
+    int mine = 0;
+    for (int i = lo + tid; i < hi; i += kPlanThreads)
+        mine += p.refs[i] == 0;
+    int total;
+    cta_scan(mine, wsum, &total);
+    if (tid == 0)
+        count = total;
+    for (int i = gtid; i < p.rows; i += kCluster * kPlanThreads) {
+        p.first[i] = INT32_MAX;
+        p.kids[i] = 0;
+    }
+    cluster_sync();
+    int free_before = 0, num_free = 0;
+    for (int k = 0; k < kCluster; ++k) {
+        const int v = ld_rank(&count, k);
+        free_before += k < rank ? v : 0;
+        num_free += v;
+    }
+    for (int r = gtid; r < p.rows_out; r += kCluster * kPlanThreads) {
+        const int par = p.parent[r];
+        if (par >= 0 && par < p.rows)
+            atomicMin(&p.first[par], r);
+        else if (par >= p.rows)
+            atomicOr(p.status, kStatusBadIndex);
+    }
+    cluster_sync();
+
+    // ---- each row's pages: shared and kept ones as they are, -2 for the ones to take, -1 past its end
+    for (int r = gwarp; r < p.rows_out; r += kPlanWarps) {
+        const int par = p.parent[r];
+        const bool there = par >= 0 && par < p.rows;
+        const int len = there ? p.lens[par] : 0;
+        const int np = pages_of(len, page, p.max_blocks);
+        const int full = p.share ? min(np, max(len, 0) / page) : 0;
+        const bool is_first = there && p.first[par] == r;
+        const int32_t *src = p.table + (int64_t)(there ? par : 0) * p.table_stride;
+        int32_t *dst = p.table_out + (int64_t)r * p.table_out_stride;
+        int need = 0;
+        for (int j = lane; j < p.max_blocks; j += 32) {
+            int v = -1;
+            if (j < np) {
+                v = src[j];
+                if (v < 0 || v >= B) {
+                    atomicOr(p.status, kStatusBadIndex);
+                    v = -1;
+                } else if (j >= full && !(is_first && p.refs[v] == 1)) {
+                    v = -2;
+                    ++need;
+                }
+            }
+            dst[j] = v;
+        }
+        if (there && len > (int64_t)p.max_blocks * page && lane == 0)
+            atomicOr(p.status, kStatusBadIndex);
+        need = __reduce_add_sync(0xffffffffu, need);
+        if (lane == 0)
+            p.need[r] = need;
+    }
+    cluster_sync();
+
+    // ---- where each row's new pages start in the list of free pages (CTA 0), and that list
+    int need_sum = 0;
+    for (int r0 = 0; r0 < p.rows_out; r0 += kPlanThreads) {
+        const int r = r0 + tid;
+        const int n = r < p.rows_out ? p.need[r] : 0;
+        const int before = need_sum + cta_scan(n, wsum, &total);
+        if (rank == 0 && r < p.rows_out)
+            p.offset[r] = n > 0 && before + n > num_free ? -1 : before;   // -1: not enough pages
+        need_sum = min(need_sum + total, INT32_MAX / 2);
+    }
+    const int wanted = min(need_sum, num_free);
+    int running = free_before;
+    for (int i0 = lo; i0 < hi; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        const int v = i < hi ? p.refs[i] : 1;
+        const int at = running + cta_scan(v == 0, wsum, &total);
+        if (v == 0 && at < wanted)
+            p.free_list[at] = i;
+        if (i < hi && p.refs_out != p.refs)
+            p.refs_out[i] = v;
+        running += total;
+    }
+    if (rank == 0 && tid == 0)
+        *p.num_copies = wanted;
+    // a row that got no pages leaves its share of the copy list unused
+    for (int i = gtid; i < wanted; i += kCluster * kPlanThreads)
+        p.copies[i] = make_int4(0, 0, 0, 0);
+    cluster_sync();
+
+    // ---- the new pages into the rows, and the copies that fill them
+    for (int r = gwarp; r < p.rows_out; r += kPlanWarps) {
+        const int par = p.parent[r];
+        const bool there = par >= 0 && par < p.rows;
+        const int off = p.offset[r];
+        const bool ok = there && off >= 0;
+        const int len = there ? min(p.lens[par], (int)min((int64_t)p.max_blocks * page, (int64_t)INT32_MAX)) : 0;
+        if (lane == 0) {
+            p.lens_out[r] = ok ? max(len, 0) : 0;
+            if (there && !ok)
+                atomicOr(p.status, kStatusBadIndex);
+            if (ok)
+                atomicAdd(&p.kids[par], 1);
+        }
+        int32_t *dst = p.table_out + (int64_t)r * p.table_out_stride;
+        if (!ok) {
+            if (there)
+                for (int j = lane; j < p.max_blocks; j += 32)
+                    dst[j] = -1;
+            continue;
+        }
+        if (p.need[r] == 0)
+            continue;
+        const int32_t *src = p.table + (int64_t)par * p.table_stride;
+        const int np = pages_of(len, page, p.max_blocks);
+        int at = off;
+        for (int j0 = 0; j0 < np; j0 += 32) {
+            const int j = j0 + lane;
+            const bool take = j < np && dst[j] == -2;
+            const unsigned m = __ballot_sync(0xffffffffu, take);
+            if (take) {
+                const int k = at + __popc(m & ((1u << lane) - 1u));
+                const int q = p.free_list[k];
+                dst[j] = q;
+                p.refs_out[q] = 1;
+                p.copies[k] = make_int4(src[j], q, entries_of(len, page, j), 0);
+            }
+            at += __popc(m);
+        }
+    }
+    cluster_sync();
+
+    // ---- the old rows' references go, their children's come (a full page of a row with c children
+    // changes by c - 1; a page that was kept does not change)
+    for (int i = gwarp; i < p.rows; i += kPlanWarps) {
+        const int len = p.lens[i];
+        const int np = pages_of(len, page, p.max_blocks);
+        const int full = p.share ? min(np, max(len, 0) / page) : 0;
+        const int c = p.kids[i], f = p.first[i];
+        const bool has = f != INT32_MAX && p.offset[f] >= 0;
+        const int32_t *src = p.table + (int64_t)i * p.table_stride;
+        const int32_t *kept = p.table_out + (int64_t)(has ? f : 0) * p.table_out_stride;
+        for (int j = lane; j < np; j += 32) {
+            const int v = src[j];
+            if (v < 0 || v >= B)
+                continue;
+            const int d = j < full ? c - 1 : (has && kept[j] == v ? 0 : -1);
+            if (d != 0)
+                atomicAdd(&p.refs_out[v], d);
+        }
+    }
+}
+
+// ---- compact -------------------------------------------------------------------------------------
+
+// With L live pages (count > 0), the k-th live page at or past L moves to the k-th free page below L.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactParams p)
+{
+    __shared__ int wsum[32];
+    __shared__ int count[2];
+    const int rank = cluster_rank(), tid = threadIdx.x;
+    const int B = p.pool.num_blocks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const int part = (B + kCluster - 1) / kCluster;
+    const int lo = min(B, rank * part), hi = min(B, lo + part);
+    int mine = 0, total;
+    for (int i = lo + tid; i < hi; i += kPlanThreads)
+        mine += p.refs[i] > 0;
+    cta_scan(mine, wsum, &total);
+    if (tid == 0)
+        count[0] = total;
+    cluster_sync();
+    int before = 0, L = 0;
+    for (int k = 0; k < kCluster; ++k) {
+        const int v = ld_rank(&count[0], k);
+        before += k < rank ? v : 0;
+        L += v;
+    }
+    // the live pages below L
+    mine = 0;
+    for (int i = lo + tid; i < min(hi, L); i += kPlanThreads)
+        mine += p.refs[i] > 0;
+    cta_scan(mine, wsum, &total);
+    if (tid == 0)
+        count[1] = total;
+    cluster_sync();
+    int below = 0;
+    for (int k = 0; k < kCluster; ++k)
+        below += ld_rank(&count[1], k);
+    const int moves = L - below;
+
+    int running = before;
+    for (int i0 = lo; i0 < hi; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        const int v = i < hi ? p.refs[i] : 0;
+        const bool live = v > 0;
+        const int r = running + cta_scan(live, wsum, &total);   // live pages before page i
+        running += total;
+        if (i >= hi)
+            continue;
+        if (live && i >= L) {
+            p.copies[r - below].x = i;
+        } else if (!live && i < L) {
+            p.copies[i - r].y = i;
+        } else if (p.refs_out != p.refs || v < 0) {
+            p.refs_out[i] = live ? v : 0;
+        }
+        if (!(live && i >= L))
+            p.page_map[i] = live ? i : -1;
+    }
+    if (rank == 0 && tid == 0) {
+        *p.num_live = L;
+        *p.num_copies = moves;
+    }
+    cluster_sync();
+    for (int k = rank * kPlanThreads + tid; k < moves; k += kCluster * kPlanThreads) {
+        const int4 c = p.copies[k];
+        p.page_map[c.x] = c.y;
+        p.refs_out[c.y] = p.refs[c.x];
+        p.refs_out[c.x] = 0;
+        p.copies[k].z = p.pool.page;
+    }
+}
+
+// ---- copies of listed pages ----------------------------------------------------------------------
+
+// A target that is listed twice receives its last pair.  In one pool, a pair whose source is also a
+// target of the call is refused (the page might be read before or after it is written).
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) copy_plan_kernel(const CopyPagesParams p)
+{
+    const int gtid = cluster_rank() * kPlanThreads + threadIdx.x;
+    constexpr int kStep = kCluster * kPlanThreads;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    auto good = [&](int s, int d) { return s >= 0 && s < p.src.num_blocks && d >= 0 && d < p.dst.num_blocks; };
+    for (int i = gtid; i < p.num_pages; i += kStep) {
+        const int s = p.src_pages[i], d = p.dst_pages[i];
+        if (good(s, d)) {
+            p.claim[d] = -1;
+            if (p.one_pool)
+                p.claim[s] = -1;
+        }
+    }
+    cluster_sync();
+    for (int i = gtid; i < p.num_pages; i += kStep) {
+        const int s = p.src_pages[i], d = p.dst_pages[i];
+        if (good(s, d))
+            atomicMax(&p.claim[d], i);
+        else
+            atomicOr(p.status, kStatusBadIndex);
+    }
+}
+
+// ---- the moving kernel ---------------------------------------------------------------------------
+
+struct MoveParams {
+    PagePool dst, src;
+    const int4 *copies;        // fork, compact: the planned copies, null in copies of listed pages
+    const int32_t *num_copies;
+    // copies of listed pages
+    const int32_t *src_pages;
+    const int32_t *dst_pages;
+    int32_t num_pages;
+    const int32_t *claim;
+    bool one_pool;
+    // compact: the block table through the page map
+    const int32_t *page_map;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *lens;
+    int32_t rows;
+    int32_t max_blocks;
+    int32_t *table_out;
+    int64_t table_out_stride;
+    unsigned *status;
+};
+
+__global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MoveParams p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int tid = threadIdx.x;
+    if (p.table != nullptr) {
+        const int64_t cells = (int64_t)p.rows * p.max_blocks;
+        for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + tid; i < cells; i += (int64_t)gridDim.x * kCopyThreads) {
+            const int r = (int)(i / p.max_blocks), j = (int)(i % p.max_blocks);
+            const int np = pages_of(p.lens[r], p.dst.page, p.max_blocks);
+            int v = -1;
+            if (j < np) {
+                v = p.table[(int64_t)r * p.table_stride + j];
+                v = v >= 0 && v < p.dst.num_blocks ? p.page_map[v] : -1;
+                if (v < 0)
+                    atomicOr(p.status, kStatusBadIndex);
+            }
+            p.table_out[(int64_t)r * p.table_out_stride + j] = v;
+        }
+    }
+    const int n = p.copies != nullptr ? *p.num_copies : p.num_pages;
+    const int64_t units = (int64_t)n * p.dst.num_layers;
+    const int64_t page_bytes = (int64_t)p.dst.page * p.dst.entry_bytes;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int i = (int)(u / p.dst.num_layers), layer = (int)(u % p.dst.num_layers);
+        int4 c;
+        if (p.copies != nullptr) {
+            c = p.copies[i];
+        } else {
+            c = make_int4(p.src_pages[i], p.dst_pages[i], p.dst.page, 0);
+            if (c.x < 0 || c.x >= p.src.num_blocks || c.y < 0 || c.y >= p.dst.num_blocks || p.claim[c.y] != i)
+                continue;
+            if (p.one_pool && p.claim[c.x] != -1) {
+                if (tid == 0 && layer == 0)
+                    atomicOr(p.status, kStatusBadIndex);
+                continue;
+            }
+        }
+        const uint4 *s = reinterpret_cast<const uint4 *>(p.src.base + layer * p.src.layer_stride + c.x * page_bytes);
+        uint4 *d = reinterpret_cast<uint4 *>(p.dst.base + layer * p.dst.layer_stride + c.y * page_bytes);
+        const int64_t pieces = (int64_t)c.z * p.dst.entry_bytes / 16;
+        for (int64_t i0 = 0; i0 < pieces; i0 += 4 * kCopyThreads) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i0 + k * kCopyThreads + tid < pieces)
+                    v[k] = s[i0 + k * kCopyThreads + tid];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (i0 + k * kCopyThreads + tid < pieces)
+                    d[i0 + k * kCopyThreads + tid] = v[k];
+        }
+    }
+}
+
+cudaError_t launch_move(const MoveParams &m, int sms, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms * 4));
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, move_pages_kernel, m);
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t stream)
+{
+    fork_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    MoveParams m{};
+    m.dst = m.src = p.pool;
+    m.copies = p.copies;
+    m.num_copies = p.num_copies;
+    return launch_move(m, sms, stream);
+}
+
+cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t stream)
+{
+    compact_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    MoveParams m{};
+    m.dst = m.src = p.pool;
+    m.copies = p.copies;
+    m.num_copies = p.num_copies;
+    m.page_map = p.page_map;
+    m.table = p.rows > 0 ? p.table : nullptr;
+    m.table_stride = p.table_stride;
+    m.lens = p.lens;
+    m.rows = p.rows;
+    m.max_blocks = p.max_blocks;
+    m.table_out = p.table_out;
+    m.table_out_stride = p.table_out_stride;
+    m.status = p.status;
+    return launch_move(m, sms, stream);
+}
+
+cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t stream)
+{
+    copy_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess)
+        return e;
+    MoveParams m{};
+    m.dst = p.dst;
+    m.src = p.src;
+    m.src_pages = p.src_pages;
+    m.dst_pages = p.dst_pages;
+    m.num_pages = p.num_pages;
+    m.claim = p.claim;
+    m.one_pool = p.one_pool;
+    m.status = p.status;
+    return launch_move(m, sms, stream);
+}
+
+}  // namespace dsv4
