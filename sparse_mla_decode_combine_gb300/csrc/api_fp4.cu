@@ -23,7 +23,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
-// ---- the decode's workspace: the combined lists and their lengths
+// ---- the decode's workspace (the combined lists and their lengths) and work decomposition
 struct Plan4 {
     int list_w;
     size_t off_lens, total;
@@ -39,6 +39,35 @@ bool plan4(int num_tokens, int num_heads, int topk_width, int window, Plan4 *pl)
     pl->off_lens = align_up(sizeof(int32_t) * (size_t)num_tokens * (size_t)pl->list_w, 256);
     pl->total = std::max<size_t>(256, align_up(pl->off_lens + sizeof(int32_t) * (size_t)num_tokens, 256));
     return true;
+}
+
+// How many CTAs share a unit's list, and how many entries each takes (multiples of 16): the split count
+// that minimises waves x time per CTA.  A 128-key block costs its products and softmax whatever its fill;
+// a CTA costs its start, and the exchange when the list is split.
+bool decompose(int num_tokens, int num_heads, int list_w, int *groups, int *splits, int *chunk)
+{
+    const int tile = decode_fp4_block_keys();
+    *groups = (num_heads + 63) / 64;
+    *splits = 1;
+    *chunk = std::max(16, (int)align_up(list_w, 16));
+    const long long units = (long long)num_tokens * *groups;
+    double best = 1e300;
+    for (int s = 1; s <= decode_fp4_max_splits(); ++s) {
+        const int c = std::max(16, (int)align_up((list_w + s - 1) / s, 16));
+        const int used = std::max(1, (list_w + c - 1) / c);
+        const int resident = used == s ? decode_fp4_resident_ctas(s) : 0;
+        if (resident <= 0)
+            continue;
+        const long long waves = (units * s + resident - 1) / resident;
+        const int blocks = std::max(1, (c + tile - 1) / tile);
+        const double cost = (double)waves * (blocks + 0.25 * c / tile + 0.5 + (s > 1 ? 1.0 : 0.0));
+        if (cost < best - 1e-9) {
+            best = cost;
+            *splits = s;
+            *chunk = c;
+        }
+    }
+    return best < 1e300;
 }
 
 // ---- the page operators' workspace
@@ -165,6 +194,8 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
     p.status = status;
+    if (!decompose(num_tokens, num_heads, pl.list_w, &p.groups, &p.splits, &p.chunk))
+        return DSV4_ERR_CUDA;
     return launch_decode_fp4(p, cs) == cudaSuccess ? DSV4_OK : DSV4_ERR_CUDA;
 }
 

@@ -1,129 +1,683 @@
-// decode_fp4.cu -- sparse-MLA decode over the 4-bit cache, plain form: one CTA per (token, eight
-// heads), one warp per head, 32 keys at a time dequantised to fp32 in shared memory, an online softmax.
-//   s_p = scale * q . k_p (576 dims), lse = ln(sum_p e^{s_p} + e^{sink}), out = sum_p e^{s_p - lse} v_p
-// over the token's combined list (positions), each position through the block table to its entry.
+// decode_fp4.cu -- sparse-MLA decode over the 4-bit cache on the tensor cores (tcgen05 / TMEM).
+//
+// Operation (per token t, head h, over the token's combined list of positions):
+//   s_p = scale * q_h . k_p (576 dims),  lse_h = ln(sum_p e^{s_p} + e^{sink_h}),  out_h = sum_p e^{s_p - lse_h} v_p
+// The lists come from the combine kernel ahead of this one in the stream.
+//
+// Contraction.  All heads share one key set, so a (token, 64 heads) unit is a pair of dense products, run
+// transposed (keys and value dims on the 128-row side of the tensor tile) because 64 heads do not fill it:
+//   S^T[128 keys x 64 heads]  = K_tile[128 x 576] . Q^T         (A = K tile, K-major)
+//   O^T[128 dv x 64 heads]   += V^T[128 dv x 128 keys] . P^T    (A = the same bytes, MN-major), four tiles
+// The K tile is the dequantised block in BF16 (exact: an E2M1 code times a power of two), nine 64-dim
+// column chunks of 128-byte-swizzled rows, 147 KB of shared memory beside the 74 KB of Q.
+//
+// One K tile leaves no room for a second block, so the block's steps form a chain, and the kernel's time is
+// that chain's length.  What shortens it:
+//   - the dequant of block b + 1 follows P.V of block b: value tile m, when its product is done, frees the two
+//     column chunks that pass m of the dequant writes, and S^T of b + 1 follows the dequant chunk by chunk;
+//   - a thread holds its quarter of a row's next entry in registers (seven 16-byte loads, issued as the
+//     registers of the present block are used up), so the gather is off the chain;
+//   - the softmax keeps a reference maximum per head from the unit's first block and exchanges maxima between
+//     warps again only when a logit exceeds it by 2^40: P and the sums are floating-point numbers, whose
+//     relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.  The
+//     usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
+//
+// CTA = 18 warps for one (token, 64-head group, split): lane 0 of warp 0 issues S^T, lane 0 of warp 17 P.V,
+// warps 1-16 do the rest: dequant, softmax, epilogue.  16 or 32 heads run as a 64-head group whose missing
+// heads have zero queries (their columns are computed and dropped).  The splits of a unit form a cluster and
+// merge through distributed shared memory.  Every mbarrier wait is bounded.
+//
+// Order of the dims inside a tile.  The eight 4-bit codes of a 32-bit word become the pairs (e_k, e_{k+4}):
+// code k and code k + 4 lie 16 bits apart, so one shift puts both at their places in a BF16 pair (two masked
+// shifts: magnitude and sign).  Inside each group of eight latent dims the tile therefore holds e0 e4 e1 e5 e2
+// e6 e3 e7; Q is stored in the same order, and the epilogue writes each value dim to its own place.
+#include <climits>
 #include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <stdint.h>
+#include <math.h>
 
 #include "fp4.h"
+#include "tcgen05.cuh"
 
 namespace dsv4 {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 32;
-constexpr int kPitch = kDim + 1;
-constexpr int kSmemBytes = (kTile * kPitch + kWarps * kDim) * 4;
+using namespace tc;
 
-__device__ __forceinline__ float scale_of(unsigned b)   // UE8M0
+constexpr int kThreads = 576;            // warp 0: S^T issue; warps 1-16: workers; warp 17: P.V issue
+constexpr int kPvWarp = 17;
+constexpr int kWorkers = 512;
+constexpr int kBK = 128;                 // keys per block = MMA M
+constexpr int kNH = 64;                  // heads per CTA = MMA N
+constexpr int kChunks = 9;               // 576 dims / 64
+constexpr int kQBytes = kChunks * kNH * 128;     // 73728
+constexpr int kKBytes = kChunks * kBK * 128;     // 147456
+constexpr int kChunkBytes = kBK * 128;           // 16384 (one 64-dim column chunk of the K tile)
+constexpr int kQChunkBytes = kNH * 128;          // 8192
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;            // S^T: 64 columns
+constexpr uint32_t kColO = 64;           // O^T: 4 tiles x 64 columns
+constexpr float kExceedLog2 = 40.f;
+constexpr int kMaxSplits = 8;            // portable cluster size
+
+// small shared region (after Q and the K tile)
+constexpr int kOffRed = 0;               // float [4][64]: per-quadrant head maxima, or row sums at the end
+constexpr int kOffMax = 1024;            // float [64]: this split's reference maximum per head (natural log units)
+constexpr int kOffFin = 1280;            // float [64]: the output factor, or this split's row sum
+constexpr int kOffValid = 1536;          // uint8 [2][128]: rows of the block that hold a key, by block parity
+constexpr int kOffBars = 1792;           // u64: bar_s, bar_p, bar_pv[4], bar_grp[3]
+constexpr int kOffTmem = 1872;           // u32
+constexpr int kOffAbort = 1880;          // int
+constexpr int kSmallBytes = 1920;
+constexpr int kSmemBytes = kQBytes + kKBytes + kSmallBytes + 1024;   // + alignment slack
+constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                 // 9 16-byte Q pieces per worker
+constexpr int kGroups = 3;               // S^T is issued as column chunks 0-3, 4-5 and 6-8 are written
+static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
+static_assert(kKBytes >= (kNH + kMaxSplits) * kLatent * (int)sizeof(float), "the partials fit the K tile");
+
+// instruction descriptors (kind::f16): D f32, A/B bf16, M = 128, N = 64
+constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kNH >> 3) << 17) |
+                                ((uint32_t)(kBK >> 4) << 24);
+constexpr uint32_t kIdescQK = kIdescBase;                           // A, B K-major
+constexpr uint32_t kIdescPV = kIdescBase | (1u << 15) | (1u << 16);  // A, B MN-major
+
+// 32 E2M1 codes times 2^(se - 127) -> 32 BF16 in four 16-byte units of row address rb (units xored with x).
+// A code's exponent and mantissa bits at the low end of the BF16 exponent are its value times 2^-126 (both
+// formats put the binary point the same way, subnormals included); one multiply by 2^(se - 1) gives the value.
+// Scales past 2 (se > 128, whose factor has no BF16 form) take a second multiply, 255 (NaN) among them.
+__device__ __forceinline__ void dequant32_store(const uint4 &v, uint32_t se, uint32_t rb, uint32_t u, uint32_t x)
 {
-    if (b == 0xFFu)
-        return __int_as_float(0x7FC00000);
-    return b == 0u ? 0x1p-127f : __int_as_float((int)(b << 23));
-}
-
-__device__ __forceinline__ float e2m1(unsigned code)
-{
-    const unsigned m = code & 7u;
-    // (a code's bits at the top of an fp32 exponent and mantissa are its value times 2^-126)
-    const float v = __int_as_float((int)(m << 22)) * 0x1p126f;
-    return code & 8u ? -v : v;
-}
-
-__device__ __forceinline__ float bf16(unsigned bits) { return __int_as_float((int)(bits << 16)); }
-
-__global__ void __launch_bounds__(kThreads) decode_fp4_kernel(const Decode4Params p)
-{
-    extern __shared__ float sm[];
-    __shared__ int ok[kTile];
-    float *key = sm, *q = sm + kTile * kPitch;
-    const int groups = p.num_heads / kWarps;
-    const int t = blockIdx.x / groups, h = blockIdx.x % groups * kWarps + (threadIdx.x >> 5);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int d = lane; d < kDim; d += 32)
-        q[warp * kDim + d] = bf16(p.q[t * p.q_token_stride + (int64_t)h * kDim + d]);
-    const int row = p.req_idx ? p.req_idx[t] : t;
-    const bool row_ok = row >= 0 && row < p.num_reqs;
-    const int n = p.lens[t];
-    if (!row_ok && n > 0 && threadIdx.x == 0)
-        atomicOr(p.status, kStatusBadIndex);
-    float m = -INFINITY, l = 0.f, acc[16] = {};
-    for (int k0 = 0; k0 < n; k0 += kTile) {
-        __syncthreads();
-        for (int k = warp; k < kTile; k += kWarps) {
-            int64_t slot = -1;
-            if (row_ok && k0 + k < n) {
-                const int pos = p.lists[(int64_t)t * p.list_w + k0 + k], blk = pos / p.page;
-                const int phys = blk < p.max_blocks ? p.block_table[row * p.bt_stride + blk] : -1;
-                if (phys >= 0 && phys < p.num_blocks)
-                    slot = (int64_t)phys * p.page + pos % p.page;
-                else
-                    atomicOr(p.status, kStatusBadIndex);
-            }
-            if (lane == 0)
-                ok[k] = slot >= 0;
-            const uint8_t *e = p.kv + slot * kEntry4Bytes;
-            for (int d = lane; d < kDim; d += 32) {
-                float v = 0.f;
-                if (slot >= 0)
-                    v = d < kLatent ? e2m1(e[d >> 1] >> (4 * (d & 1))) * scale_of(e[kScale4Offset + d / kScale4Block])
-                                    : bf16(reinterpret_cast<const uint16_t *>(e + kRope4Offset)[d - kLatent]);
-                key[k * kPitch + d] = v;
-            }
-        }
-        __syncthreads();
-        float s = 0.f;
-        for (int d = 0; d < kDim; ++d)
-            s = fmaf(q[warp * kDim + d], key[lane * kPitch + d], s);
-        s = ok[lane] ? s * p.scale : -INFINITY;
-        float mb = s;
-        for (int o = 16; o > 0; o >>= 1)
-            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-        const float mn = fmaxf(m, mb);
-        if (mn == -INFINITY && !__any_sync(0xffffffffu, isnan(s)))
-            continue;
-        const float w = ok[lane] ? expf(s - mn) : 0.f;
-        const float a = expf(m - mn);
-        float ws = w;
-        for (int o = 16; o > 0; o >>= 1)
-            ws += __shfl_xor_sync(0xffffffffu, ws, o);
-        l = l * a + ws;
-        m = mn;
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t f = (min(se, 128u) + 126u) << 7;
+    f |= f << 16;
+    uint32_t o[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[4 * i + 0] = ((w[i] << 6) & 0x01C001C0u) | ((w[i] << 12) & 0x80008000u);
+        o[4 * i + 1] = ((w[i] << 2) & 0x01C001C0u) | ((w[i] << 8) & 0x80008000u);
+        o[4 * i + 2] = ((w[i] >> 2) & 0x01C001C0u) | ((w[i] << 4) & 0x80008000u);
+        o[4 * i + 3] = ((w[i] >> 6) & 0x01C001C0u) | (w[i] & 0x80008000u);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        o[i] = mul_bf16x2(o[i], f);
+    if (se > 128u) {
+        uint32_t g = se == 255u ? 0x7FC0u : (se - 1u) << 7;   // 2^(se - 128)
+        g |= g << 16;
+#pragma unroll
         for (int i = 0; i < 16; ++i)
-            acc[i] *= a;
-        for (int k = 0; k < kTile; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
-            if (wk != 0.f)
-                for (int i = 0; i < 16; ++i)
-                    acc[i] = fmaf(wk, key[k * kPitch + lane + 32 * i], acc[i]);
+            o[i] = mul_bf16x2(o[i], g);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        st_shared_v4(rb + (((u + i) ^ x) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+}
+
+// Split merge inside a cluster of S CTAs (one per split of a token's keys).  The CTA of rank r owns heads
+// [r*hp, (r+1)*hp), hp = ceil(64 / S).  Every split s has pushed, into each owner's shared memory, its reference
+// maximum m_s (natural-log units, -inf for a split without keys) and row sum l_s for the owner's heads
+// (stat[s][hl] = (m_s, l_s)) and its unnormalised fp32 O_s (recv[s][hl][512]).  The owner forms
+//   m = max(max_s m_s, sink), Z = sum_s l_s e^{m_s - m} + e^{sink - m},
+//   out = sum_s e^{m_s - m} O_s / Z  (BF16),  lse = m + ln Z.
+__device__ __noinline__ void merge_splits(uint16_t *out, float *lse, const float *sink, int num_heads, int S, int t,
+                                          int h0, int rank, const float *recv, const float *stat, float *wts)
+{
+    const int hp = (kNH + S - 1) / S;
+    const int hb = rank * hp;
+    const int nh = max(0, min(min(kNH, num_heads - h0), hb + hp) - hb);   // owned heads that exist
+    const int tid = threadIdx.x;
+    if (tid < nh) {
+        float mk = -INFINITY;
+        for (int s = 0; s < S; ++s)
+            mk = fmaxf(mk, stat[2 * (s * hp + tid)]);
+        const float sk = sink != nullptr ? sink[h0 + hb + tid] : -INFINITY;
+        const float m = fmaxf(mk, sk);
+        float z = sk == -INFINITY ? 0.f : expf(sk - m);
+        for (int s = 0; s < S; ++s) {
+            const float ms = stat[2 * (s * hp + tid)];
+            const float w = ms == -INFINITY ? 0.f : expf(ms - m);
+            wts[tid * 10 + s] = w;
+            z += ms == -INFINITY ? 0.f : stat[2 * (s * hp + tid) + 1] * w;
+        }
+        const float f = mk == -INFINITY ? 0.f : 1.f / z;
+        for (int s = 0; s < S; ++s)
+            wts[tid * 10 + s] *= f;
+        wts[tid * 10 + 8] = m == -INFINITY ? -INFINITY : m + logf(z);
+    }
+    __syncthreads();
+    const int items = nh * (kLatent / 4);   // 16-byte pieces of the slice
+    for (int i = tid; i < items; i += kThreads) {
+        const int hl = i / (kLatent / 4);
+        const int c = i % (kLatent / 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < S; ++s) {
+            const float ws = wts[hl * 10 + s];
+            if (ws != 0.f) {   // (a split without keys has sent nothing)
+                const float4 v = *reinterpret_cast<const float4 *>(recv + ((size_t)(s * hp + hl)) * kLatent + 4 * c);
+                acc.x = fmaf(ws, v.x, acc.x);
+                acc.y = fmaf(ws, v.y, acc.y);
+                acc.z = fmaf(ws, v.z, acc.z);
+                acc.w = fmaf(ws, v.w, acc.w);
+            }
+        }
+        const int64_t row = (int64_t)t * num_heads + h0 + hb + hl;
+        *reinterpret_cast<uint2 *>(out + row * kLatent + 4 * c) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+        if (c == 0 && lse != nullptr)
+            lse[row] = wts[hl * 10 + 8];
+    }
+}
+
+// Sends the (m, l) pair of head h (0..63) of split `split` to the head's owner in the cluster.
+__device__ __forceinline__ void push_stat(uint32_t stat_s, int S, int split, int h, float m, float l)
+{
+    const int hp = (kNH + S - 1) / S;
+    const int r = h / hp;
+    st_cluster_v2(map_to_rank(stat_s + (uint32_t)(2 * (split * hp + (h - r * hp))) * 4u, (uint32_t)r), m, l);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    const int split = blockIdx.x % p.splits;   // = rank in the cluster when splits > 1
+    const int unit = blockIdx.x / p.splits;
+    const int t = unit / p.groups;
+    const int h0 = unit % p.groups * kNH;
+    const int nhv = min(kNH, p.num_heads - h0);   // heads of the group that exist
+    const bool is_worker = warp >= 1 && warp <= 16;
+    const int wid = tid - 32;                     // worker index 0..511
+
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;   // the swizzled tiles start on 1024-byte boundaries
+    uint8_t *gbase = smem_raw + (base - raw);
+    const uint32_t sQ = base;
+    const uint32_t sK = base + kQBytes;
+    const uint32_t sP = sK + 8 * kChunkBytes;   // P^T takes the rope column chunk once S^T is done
+    uint8_t *small = gbase + kQBytes + kKBytes;
+    float *red = reinterpret_cast<float *>(small + kOffRed);
+    float *smax = reinterpret_cast<float *>(small + kOffMax);
+    float *fin = reinterpret_cast<float *>(small + kOffFin);
+    uint8_t *valid = small + kOffValid;
+    const uint32_t bar_s = smem_u32(small + kOffBars);   // S^T of the block complete
+    const uint32_t bar_p = bar_s + 8;                    // P^T of the block written (16 warps)
+    const uint32_t bar_pv = bar_s + 16;                  // [4] O^T tile m of the block complete
+    const uint32_t bar_grp = bar_s + 48;                 // [3] column chunks 0-3, 4-5, 6-8 of the K tile written
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + kOffTmem);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(small + kOffAbort);
+
+    // ---- set-up that reads no input
+    if (tid == 0) {
+        mbar_init(bar_s, 1);
+        mbar_init(bar_p, kWorkers / 32);
+        for (int m = 0; m < 4; ++m)
+            mbar_init(bar_pv + 8 * m, 1);
+        for (int g = 0; g < kGroups; ++g)
+            mbar_init(bar_grp + 8 * g, kWorkers / 32);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *abort_flag = 0;
+    }
+    if (warp == 0)
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists come from the previous kernel
+
+    const int row = p.req_idx != nullptr ? p.req_idx[t] : t;
+    const bool row_ok = row >= 0 && row < p.num_reqs;
+    const int32_t *list = p.lists + (int64_t)t * p.list_w;
+    const int32_t *bt_row = p.block_table + (int64_t)(row_ok ? row : 0) * p.bt_stride;
+    const int kbeg = split * p.chunk;
+    const int klim = min(kbeg + p.chunk, p.list_w);
+
+    // dequant: lanes 8 q .. 8 q + 7 of worker warp ww take quarter q of eight rows whose numbers differ mod 8
+    // (no bank conflicts in the swizzled stores) and spread over the tile, so that a short block keeps every
+    // warp at work
+    const int qtr = lane >> 3;
+    const int rrow = 8 * (((warp - 1) - (lane & 7)) & 15) + (lane & 7);
+    // the list's position, then the cache slot, of this thread's row in block b; -1 past the list's end
+    auto position_of = [&](int b) {
+        const int i = kbeg + b * kBK + rrow;
+        return is_worker && i < klim ? __ldg(list + i) : -1;
+    };
+    auto slot_of = [&](int pos) {
+        if (pos < 0)
+            return -1;
+        const int blk = pos / p.page;
+        const int phys = row_ok && blk < p.max_blocks ? __ldg(bt_row + blk) : -1;
+        if (phys < 0 || phys >= p.num_blocks) {
+            atomicOr(p.status, kStatusBadIndex);
+            return -1;
+        }
+        return phys * p.page + (pos - blk * p.page);
+    };
+    uint4 pre[4], prope[2], psc;   // the entry of the block ahead: four code pieces, rope, scale bytes
+    bool pre_ok = false;
+    auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld_stream(e + 64 * m + 16 * qtr); };
+    auto load_rope = [&](const uint8_t *e) {
+        prope[0] = ld_stream(e + kRope4Offset + 16 * qtr);
+        prope[1] = ld_stream(e + kRope4Offset + 64 + 16 * qtr);
+    };
+    auto load_scales = [&](const uint8_t *e) { psc = ld_stream(e + kScale4Offset); };
+
+    int pos1 = -1, pos2 = -1, next_slot = -1;
+    if (is_worker) {
+        const int pos0 = position_of(0);
+        pos1 = position_of(1);
+        pos2 = position_of(2);
+        const int slot0 = slot_of(pos0);
+        pre_ok = slot0 >= 0;
+        if (pre_ok) {
+            const uint8_t *e = p.kv + (int64_t)slot0 * kEntry4Bytes;
+            load_scales(e);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+                load_piece(e, m);
+            load_rope(e);
+        }
+        next_slot = slot_of(pos1);
+        // Q -> swizzled K-major B operand in the tile's order of dims (zeros for heads that do not exist)
+        uint4 v[kQLoads];
+#pragma unroll
+        for (int j = 0; j < kQLoads; ++j) {
+            const int i = wid + kWorkers * j;
+            const int h = i / (kDim / 8), c = i % (kDim / 8);
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (h < nhv)
+                v[j] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride + (int64_t)(h0 + h) * kDim + 8 * c));
+        }
+#pragma unroll
+        for (int j = 0; j < kQLoads; ++j) {
+            const int i = wid + kWorkers * j;
+            const int h = i / (kDim / 8), c = i % (kDim / 8);
+            const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
+            if (c < kLatent / 8)
+                st_shared_v4(a, __byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
+                             __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
+            else
+                st_shared_v4(a, v[j].x, v[j].y, v[j].z, v[j].w);
         }
     }
-    const float sk = p.sink ? p.sink[h] : -INFINITY;
-    const float M = fmaxf(m, sk);
-    const float z = M == -INFINITY ? 0.f : l * expf(m - M) + expf(sk - M);
-    const float f = z > 0.f && m != -INFINITY ? expf(m - M) / z : 0.f;
-    const int64_t o = (int64_t)t * p.num_heads + h;
-    for (int i = 0; i < 16; ++i) {
-        const __nv_bfloat16 b = __float2bfloat16_rn(acc[i] * f);
-        p.out[o * kLatent + lane + 32 * i] = *reinterpret_cast<const uint16_t *>(&b);
+    const int L = p.lens[t];
+    const int nkeys = max(0, min(L, klim) - kbeg);
+    const int nblocks = (nkeys + kBK - 1) / kBK;
+    fence_async_smem();
+    before_sync();
+    __syncthreads();   // Q, barriers, TMEM address
+    after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (nblocks == 0) {   // no key in this split
+        if (warp == 0)
+            tmem_free(tmem, kTmemCols);
+        if (p.splits == 1) {   // zero output, the lse from the sink alone
+            if (tid < nhv && p.lse != nullptr)
+                p.lse[(int64_t)t * p.num_heads + h0 + tid] = p.sink != nullptr ? p.sink[h0 + tid] : -INFINITY;
+            for (int i = tid; i < nhv * kLatent / 8; i += kThreads)
+                *reinterpret_cast<uint4 *>(p.out + ((int64_t)t * p.num_heads + h0) * kLatent + 8 * i) = make_uint4(0, 0, 0, 0);
+            return;
+        }
+        cluster_sync();   // every split is past its products: partials may land
+        if (tid < kNH)
+            push_stat(smem_u32(gbase), p.splits, split, tid, -INFINITY, 0.f);
+        cluster_sync();   // every partial has landed
+        merge_splits(p.out, p.lse, p.sink, p.num_heads, p.splits, t, h0, split,
+                     reinterpret_cast<const float *>(gbase + kQBytes), reinterpret_cast<const float *>(gbase),
+                     reinterpret_cast<float *>(gbase + 2048));
+        return;
     }
-    if (lane == 0 && p.lse)
-        p.lse[o] = z > 0.f ? M + logf(z) : -INFINITY;
+
+    const int quad = warp & 3;                            // TMEM lane quadrant of this warp
+    const int hs = 16 * ((warp - 1) >> 2);                // workers: first of this warp's 16 heads
+    const int key = quad * 32 + lane;                     // softmax: key of the block; epilogue: row of a value tile
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+    // value dim of tile row `key` (the tile's order of dims)
+    const int dv0 = (key & ~7) | ((key >> 1) & 3) | ((key & 1) << 2);
+
+    if (warp == 0) {
+        // descriptors: K-major operands advance 32 B per 16 dims and one column chunk per 64
+        if (lane == 0) {
+            const uint64_t qk_a = sdesc(sK, 16, 1024);
+            const uint64_t qk_b = sdesc(sQ, 16, 1024);
+            for (int b = 0; b < nblocks; ++b) {
+                const uint32_t ph = (uint32_t)(b & 1);
+#pragma unroll 1
+                for (int g = 0; g < kGroups; ++g) {
+                    mbar_wait(bar_grp + 8 * g, ph, abort_flag, p.status);
+                    after_sync();
+                    const int c_lo = g == 0 ? 0 : g == 1 ? 4 : 6, c_hi = g == 0 ? 4 : g == 1 ? 6 : 9;
+#pragma unroll 1
+                    for (int c = c_lo; c < c_hi; ++c) {
+                        const uint64_t a = qk_a + (uint64_t)((c * kChunkBytes) >> 4);
+                        const uint64_t bq = qk_b + (uint64_t)((c * kQChunkBytes) >> 4);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16(tmem + kColS, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdescQK,
+                                     (c != 0 || k != 0) ? 1u : 0u);
+                    }
+                }
+                commit(bar_s);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kPvWarp) {
+        // MN-major operands advance 2 KB per 16 keys
+        if (lane == 0) {
+            const uint64_t pv_a = sdesc(sK, kChunkBytes, 1024);
+            const uint64_t pv_b = sdesc(sP, 1024, 1024);
+            for (int b = 0; b < nblocks; ++b) {
+                mbar_wait(bar_p, (uint32_t)(b & 1), abort_flag, p.status);
+                after_sync();
+                const int ksteps = min(kBK / 16, (nkeys - b * kBK + 15) / 16);   // 16-key steps that hold keys
+#pragma unroll 1
+                for (int m = 0; m < 4; ++m) {
+                    const uint64_t a = pv_a + (uint64_t)((2 * m * kChunkBytes) >> 4);
+#pragma unroll 1
+                    for (int kk = 0; kk < ksteps; ++kk)
+                        mma_bf16(tmem + kColO + 64 * m, a + (uint64_t)(kk * 128), pv_b + (uint64_t)(kk * 128), kIdescPV,
+                                 (b > 0 || kk > 0) ? 1u : 0u);
+                    commit(bar_pv + 8 * m);   // releases K chunks 2m, 2m+1 (tile 3: also P^T)
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
+        float mref[16], l[16];                            // heads hs ..: reference maximum (log2 units), this lane's sums
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            mref[j] = 0.f, l[j] = 0.f;
+        bool fresh = true;                                // no key has been seen: the references are not set
+        const uint32_t rb = sK + (uint32_t)(rrow >> 3) * 1024u + (uint32_t)(rrow & 7) * 128u;
+        const uint32_t x7 = (uint32_t)(rrow & 7);
+
+        for (int b = 0; b < nblocks; ++b) {
+            const uint32_t ph = (uint32_t)(b & 1);
+            // ---- dequant of block b (zeros for rows without a key); the next block's entry into the registers
+            const bool ok_next = next_slot >= 0;
+            const uint8_t *en = p.kv + (int64_t)(ok_next ? next_slot : 0) * kEntry4Bytes;
+            if (qtr == 0)
+                valid[(b & 1) * kBK + rrow] = pre_ok;
+            const uint32_t sc[4] = {psc.x, psc.y, psc.z, psc.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {   // dims 128 m + 32 qtr ..
+                if (b > 0)
+                    mbar_wait(bar_pv + 8 * m, ph ^ 1u, abort_flag, p.status);   // P.V of block b-1 is done with them
+                const uint32_t cb = rb + (uint32_t)(2 * m + (qtr >> 1)) * kChunkBytes;
+                const uint32_t u = 4u * (uint32_t)(qtr & 1);
+                if (pre_ok) {
+                    dequant32_store(pre[m], (sc[m] >> (8 * qtr)) & 0xFFu, cb, u, x7);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        st_shared_v4(cb + (((u + i) ^ x7) << 4), 0u, 0u, 0u, 0u);
+                }
+                if (ok_next)
+                    load_piece(en, m);
+                if (m == 3) {
+                    const uint32_t cr = rb + 8u * kChunkBytes;
+                    if (!pre_ok)
+                        prope[0] = prope[1] = make_uint4(0u, 0u, 0u, 0u);
+                    st_shared_v4(cr + (((uint32_t)qtr ^ x7) << 4), prope[0].x, prope[0].y, prope[0].z, prope[0].w);
+                    st_shared_v4(cr + (((uint32_t)(qtr + 4) ^ x7) << 4), prope[1].x, prope[1].y, prope[1].z, prope[1].w);
+                }
+                if (m >= 1) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar_grp + 8 * (m - 1));
+                }
+            }
+            if (ok_next) {
+                load_rope(en);
+                load_scales(en);
+            }
+            pre_ok = ok_next;
+            next_slot = slot_of(pos2);
+            pos2 = position_of(b + 3);
+
+            // ---- softmax of block b: this warp's 32 keys (TMEM lanes) x 16 heads
+            mbar_wait(bar_s, ph, abort_flag, p.status);
+            after_sync();
+            uint32_t s[16];
+            tmem_ld16(lane_base + kColS + hs, s);
+            const bool kv = valid[(b & 1) * kBK + key] != 0;   // (rows past the list's end are not)
+            tmem_ld_wait();
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                top = fmaxf(top, fmaf(__uint_as_float(s[j]), c2, -mref[j]));
+            if (named_bar_or(2 + ((warp - 1) >> 2), 128, kv && (fresh || top > kExceedLog2))) {
+                // new references: the block's maxima where they are larger, by the four warps of these heads
+                float mine = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float m = warp_max(kv ? __uint_as_float(s[j]) * c2 : -INFINITY);
+                    mine = lane == j ? m : mine;
+                }
+                if (lane < 16)
+                    red[quad * kNH + hs + lane] = mine;
+                named_bar(2 + ((warp - 1) >> 2), 128);
+                float al[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int h = hs + j;
+                    float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
+                    m = m == -INFINITY ? mref[j] : fresh ? m : fmaxf(m, mref[j]);   // (-inf: every logit is NaN)
+                    al[j] = fresh ? 1.f : exp2_approx(mref[j] - m);
+                    mref[j] = m;
+                    l[j] *= al[j];
+                }
+                named_bar(2 + ((warp - 1) >> 2), 128);   // (red is free again)
+                if (!fresh) {
+#pragma unroll 1
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t x[16];
+                        tmem_ld16(lane_base + kColO + 64 * m + hs, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            x[j] = __float_as_uint(__uint_as_float(x[j]) * al[j]);
+                        tmem_st16(lane_base + kColO + 64 * m + hs, x);
+                    }
+                    tmem_st_wait();
+                }
+                fresh = false;
+            }
+            // P = 2^(s c - m) -> BF16 P^T row `key`
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    const int i = 8 * half + j;
+                    const float p0 = kv ? exp2_approx(fmaf(__uint_as_float(s[i]), c2, -mref[i])) : 0.f;
+                    const float p1 = kv ? exp2_approx(fmaf(__uint_as_float(s[i + 1]), c2, -mref[i + 1])) : 0.f;
+                    l[i] += p0;
+                    l[i + 1] += p1;
+                    pk[j >> 1] = pack_bf16x2(p0, p1);
+                }
+                st_shared_v4(sP + sw128(key, (hs >> 3) + half), pk[0], pk[1], pk[2], pk[3]);
+            }
+            fence_async_smem();
+            before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_p);
+        }
+
+        // ---- epilogue: row sums across the 128 lanes, then the output's factors or the split's statistics
+        {
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                v[j] = l[j];
+            // halving exchange: after the step with distance d the lane keeps half of its heads, summed with the
+            // partner's; at the end lane i holds head 8 b4 + 4 b3 + 2 b2 + b1 of its number's bits
+#pragma unroll
+            for (int d = 16, n = 8; n > 0; d >>= 1, n >>= 1) {
+#pragma unroll
+                for (int k = 0; k < n; ++k) {
+                    const bool up = lane & d;
+                    const float give = up ? v[k] : v[k + n];
+                    const float keep = up ? v[k + n] : v[k];
+                    v[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+                }
+            }
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+            if ((lane & 1) == 0)
+                red[quad * kNH + hs + (lane >> 1)] = v[0];
+            if (quad == 0) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (lane == j)
+                        smax[hs + j] = fresh ? -INFINITY : mref[j] * 0.6931471805599453f;
+            }
+        }
+        named_bar(1, kWorkers);
+        if (wid < kNH) {
+            const int h = wid;
+            const float lsum = (red[h] + red[kNH + h]) + (red[2 * kNH + h] + red[3 * kNH + h]);
+            const float ms = smax[h];
+            if (p.splits == 1) {
+                const float sk = p.sink != nullptr && h < nhv ? p.sink[h0 + h] : -INFINITY;
+                const float M = fmaxf(ms, sk);
+                const float e = ms == -INFINITY ? 0.f : expf(ms - M);
+                const float Z = (ms == -INFINITY ? 0.f : lsum * e) + (sk == -INFINITY ? 0.f : expf(sk - M));
+                fin[h] = ms == -INFINITY ? 0.f : e / Z;
+                if (p.lse != nullptr && h < nhv)
+                    p.lse[(int64_t)t * p.num_heads + h0 + h] = M == -INFINITY ? -INFINITY : M + logf(Z);
+            } else {
+                fin[h] = lsum;
+            }
+        }
+        named_bar(1, kWorkers);
+        mbar_wait(bar_pv + 24, (uint32_t)((nblocks - 1) & 1), abort_flag, p.status);   // the last tile's product
+        after_sync();
+        if (p.splits == 1) {
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+                uint32_t x[16];
+                tmem_ld16(lane_base + kColO + 64 * m + hs, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int h = hs + j;
+                    if (h < nhv) {
+                        const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(x[j]) * fin[h]);
+                        p.out[((int64_t)t * p.num_heads + h0 + h) * kLatent + 128 * m + dv0] =
+                            *reinterpret_cast<const uint16_t *>(&o);
+                    }
+                }
+            }
+        }
+    }
+    if (p.splits > 1) {
+        // the split's partial goes from TMEM into the shared memory of each head's owner:
+        // recv[split][head - owner's first head][512] in the owner's K tile region
+        cluster_sync();   // every split is past its products: partials may land
+        if (is_worker) {
+            const int S = p.splits;
+            const int hp = (kNH + S - 1) / S;
+            if (wid < nhv)
+                push_stat(smem_u32(gbase), S, split, wid, smax[wid], fin[wid]);
+            const int r0 = hs / hp;   // this warp's 16 heads belong to owners r0, r0 + 1, r0 + 2 at most
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+                if (hs >= nhv)   // nhv is a multiple of 16: whole warps skip
+                    break;
+                uint32_t x[16];
+                tmem_ld16(lane_base + kColO + 64 * m + hs, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int h = hs + j;
+                    const int r = r0 + (h >= (r0 + 1) * hp) + (h >= (r0 + 2) * hp);
+                    const uint32_t off = (uint32_t)(((split * hp + h - r * hp) * kLatent + 128 * m + dv0) * 4);
+                    st_cluster_f32(map_to_rank(sK + off, (uint32_t)r), __uint_as_float(x[j]));
+                }
+            }
+        }
+    }
+    before_sync();
+    __syncthreads();
+    after_sync();
+    if (warp == 0)
+        tmem_free(tmem, kTmemCols);
+    if (p.splits > 1) {
+        cluster_sync();   // every partial has landed
+        merge_splits(p.out, p.lse, p.sink, p.num_heads, p.splits, t, h0, split,
+                     reinterpret_cast<const float *>(gbase + kQBytes), reinterpret_cast<const float *>(gbase),
+                     reinterpret_cast<float *>(gbase + 2048));
+    }
 }
 
 }  // namespace
+
+int decode_fp4_block_keys() { return kBK; }
+int decode_fp4_max_splits() { return kMaxSplits; }
+
+// Concurrently resident CTAs when launched in clusters of `splits` (whole clusters must fit inside one
+// GPC); cached per device.
+int decode_fp4_resident_ctas(int splits)
+{
+    static int cache[64][kMaxSplits + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || splits < 1 || splits > kMaxSplits)
+        return 0;
+    if (cache[dev][splits] > 0)
+        return cache[dev][splits];
+    if (set_smem_once(reinterpret_cast<const void *>(decode_fp4_kernel), kSmemBytes, kAttrFp4) != cudaSuccess)
+        return 0;
+    int n = 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    if (splits > 1) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(splits * n);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = splits;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, reinterpret_cast<const void *>(decode_fp4_kernel), &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        n = clusters * splits;
+    }
+    cache[dev][splits] = n;
+    return n;
+}
 
 cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
 {
     if (p.num_tokens <= 0)
         return cudaSuccess;
-    cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp4_kernel), kSmemBytes, kAttrFp4);
+    if (p.groups != (p.num_heads + kNH - 1) / kNH || p.splits < 1 || p.splits > kMaxSplits || p.chunk < 1)
+        return cudaErrorInvalidValue;
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp4_kernel), kSmemBytes, kAttrFp4);
     if (e != cudaSuccess)
         return e;
-    decode_fp4_kernel<<<p.num_tokens * (p.num_heads / kWarps), kThreads, kSmemBytes, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.num_tokens * (unsigned)p.groups * (unsigned)p.splits);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, decode_fp4_kernel, p);
 }
 
 }  // namespace dsv4

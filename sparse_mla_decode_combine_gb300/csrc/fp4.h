@@ -61,9 +61,15 @@ struct Decode4Params {
     float scale;
     uint16_t *out;             // BF16 [T, H, 512]
     float *lse;                // [T, H] or null
+    int32_t groups;            // 64-head groups
+    int32_t splits;            // CTAs that share a unit's list: one thread-block cluster
+    int32_t chunk;             // list entries per split
     unsigned *status;
 };
 cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream);
+int decode_fp4_block_keys();
+int decode_fp4_max_splits();
+int decode_fp4_resident_ctas(int splits);
 
 // ---- page operators
 
