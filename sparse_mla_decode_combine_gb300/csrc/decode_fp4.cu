@@ -61,7 +61,7 @@ constexpr int kMaxSplits = 8;            // portable cluster size
 
 // small shared region (after Q and the K tile)
 constexpr int kOffRed = 0;               // float [4][64]: per-quadrant head maxima, or row sums at the end
-constexpr int kOffMax = 1024;            // float [64]: this split's reference maximum per head (natural log units)
+constexpr int kOffMax = 1024;            // float [64]: reference maximum per head (log2 units; natural ones at the end)
 constexpr int kOffFin = 1280;            // float [64]: the output factor, or this split's row sum
 constexpr int kOffValid = 1536;          // uint8 [2][128]: rows of the block that hold a key, by block parity
 constexpr int kOffBars = 1792;           // u64: bar_s, bar_p, bar_pv[4], bar_grp[3]
@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
+    if (tid < kNH)
+        smax[tid] = 0.f;
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
 
@@ -382,10 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         __syncwarp();
     } else {
         const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
-        float mref[16], l[16];                            // heads hs ..: reference maximum (log2 units), this lane's sums
+        float l[16];                                      // this lane's row sums of heads hs ..
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-            mref[j] = 0.f, l[j] = 0.f;
+            l[j] = 0.f;
         bool fresh = true;                                // no key has been seen: the references are not set
         const uint32_t rb = sK + (uint32_t)(rrow >> 3) * 1024u + (uint32_t)(rrow & 7) * 128u;
         const uint32_t x7 = (uint32_t)(rrow & 7);
@@ -442,32 +444,44 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             tmem_ld16(lane_base + kColS + hs, s);
             const bool kv = valid[(b & 1) * kBK + key] != 0;   // (rows past the list's end are not)
             tmem_ld_wait();
+            // logits in log2 units above the heads' references
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) {
+                const float4 m = *reinterpret_cast<const float4 *>(smax + hs + j);
+                s[j] = __float_as_uint(fmaf(__uint_as_float(s[j]), c2, -m.x));
+                s[j + 1] = __float_as_uint(fmaf(__uint_as_float(s[j + 1]), c2, -m.y));
+                s[j + 2] = __float_as_uint(fmaf(__uint_as_float(s[j + 2]), c2, -m.z));
+                s[j + 3] = __float_as_uint(fmaf(__uint_as_float(s[j + 3]), c2, -m.w));
+            }
             float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                top = fmaxf(top, fmaf(__uint_as_float(s[j]), c2, -mref[j]));
+                top = fmaxf(top, __uint_as_float(s[j]));
             if (named_bar_or(2 + ((warp - 1) >> 2), 128, kv && (fresh || top > kExceedLog2))) {
-                // new references: the block's maxima where they are larger, by the four warps of these heads
+                // the block's maxima, by the four warps of these heads, become the references where they are larger
                 float mine = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float m = warp_max(kv ? __uint_as_float(s[j]) * c2 : -INFINITY);
+                    const float m = warp_max(kv ? __uint_as_float(s[j]) : -INFINITY);
                     mine = lane == j ? m : mine;
                 }
                 if (lane < 16)
                     red[quad * kNH + hs + lane] = mine;
                 named_bar(2 + ((warp - 1) >> 2), 128);
-                float al[16];
+                float up = 0.f;   // lane j: by how much the reference of head hs + j rises
+                if (lane < 16) {
+                    const int h = hs + lane;
+                    const float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
+                    up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);   // (-inf: every logit is NaN)
+                }
+                if (quad == 0 && lane < 16)
+                    smax[hs + lane] += up;
+                const float fall = fresh ? 1.f : exp2_approx(-up);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int h = hs + j;
-                    float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
-                    m = m == -INFINITY ? mref[j] : fresh ? m : fmaxf(m, mref[j]);   // (-inf: every logit is NaN)
-                    al[j] = fresh ? 1.f : exp2_approx(mref[j] - m);
-                    mref[j] = m;
-                    l[j] *= al[j];
+                    s[j] = __float_as_uint(__uint_as_float(s[j]) - __shfl_sync(0xffffffffu, up, j));
+                    l[j] *= __shfl_sync(0xffffffffu, fall, j);
                 }
-                named_bar(2 + ((warp - 1) >> 2), 128);   // (red is free again)
                 if (!fresh) {
 #pragma unroll 1
                     for (int m = 0; m < 4; ++m) {
@@ -476,22 +490,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            x[j] = __float_as_uint(__uint_as_float(x[j]) * al[j]);
+                            x[j] = __float_as_uint(__uint_as_float(x[j]) * __shfl_sync(0xffffffffu, fall, j));
                         tmem_st16(lane_base + kColO + 64 * m + hs, x);
                     }
                     tmem_st_wait();
                 }
                 fresh = false;
+                named_bar(2 + ((warp - 1) >> 2), 128);   // the references are written, and red is free again
             }
-            // P = 2^(s c - m) -> BF16 P^T row `key`
+            // P = 2^s -> BF16 P^T row `key`
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t pk[4];
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
                     const int i = 8 * half + j;
-                    const float p0 = kv ? exp2_approx(fmaf(__uint_as_float(s[i]), c2, -mref[i])) : 0.f;
-                    const float p1 = kv ? exp2_approx(fmaf(__uint_as_float(s[i + 1]), c2, -mref[i + 1])) : 0.f;
+                    const float p0 = kv ? exp2_approx(__uint_as_float(s[i])) : 0.f;
+                    const float p1 = kv ? exp2_approx(__uint_as_float(s[i + 1])) : 0.f;
                     l[i] += p0;
                     l[i + 1] += p1;
                     pk[j >> 1] = pack_bf16x2(p0, p1);
@@ -526,12 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
             if ((lane & 1) == 0)
                 red[quad * kNH + hs + (lane >> 1)] = v[0];
-            if (quad == 0) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (lane == j)
-                        smax[hs + j] = fresh ? -INFINITY : mref[j] * 0.6931471805599453f;
-            }
+            if (quad == 0 && lane < 16)
+                smax[hs + lane] = fresh ? -INFINITY : smax[hs + lane] * 0.6931471805599453f;
         }
         named_bar(1, kWorkers);
         if (wid < kNH) {
