@@ -70,7 +70,7 @@ constexpr int kOffAbort = 1880;          // int
 constexpr int kSmallBytes = 1920;
 constexpr int kSmemBytes = kQBytes + kKBytes + kSmallBytes + 1024;   // + alignment slack
 constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                 // 9 16-byte Q pieces per worker
-constexpr int kGroups = 3;               // S^T is issued as column chunks 0-3, 4-5 and 6-8 are written
+constexpr int kGroups = 3;               // S^T is issued as column chunks 0-3, then 4, 5 and 8, then 6 and 7 are written
 static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
 static_assert(kKBytes >= (kNH + kMaxSplits) * kLatent * (int)sizeof(float), "the partials fit the K tile");
 
@@ -80,22 +80,22 @@ constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)
 constexpr uint32_t kIdescQK = kIdescBase;                           // A, B K-major
 constexpr uint32_t kIdescPV = kIdescBase | (1u << 15) | (1u << 16);  // A, B MN-major
 
-// 32 E2M1 codes times 2^(se - 127) -> 32 BF16 in four 16-byte units of row address rb (units xored with x).
+// 32 E2M1 codes times 2^(se - 127) -> 16 BF16 pairs, exactly.
 // A code's exponent and mantissa bits at the low end of the BF16 exponent are its value times 2^-126 (both
 // formats put the binary point the same way, subnormals included); one multiply by 2^(se - 1) gives the value.
 // Scales past 2 (se > 128, whose factor has no BF16 form) take a second multiply, 255 (NaN) among them.
-__device__ __forceinline__ void dequant32_store(const uint4 &v, uint32_t se, uint32_t rb, uint32_t u, uint32_t x)
+__device__ __forceinline__ void dequant32(const uint4 &v, uint32_t se, uint32_t (&o)[16])
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t f = (min(se, 128u) + 126u) << 7;
     f |= f << 16;
-    uint32_t o[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        const uint32_t u = w[i] >> 8;
         o[4 * i + 0] = ((w[i] << 6) & 0x01C001C0u) | ((w[i] << 12) & 0x80008000u);
         o[4 * i + 1] = ((w[i] << 2) & 0x01C001C0u) | ((w[i] << 8) & 0x80008000u);
-        o[4 * i + 2] = ((w[i] >> 2) & 0x01C001C0u) | ((w[i] << 4) & 0x80008000u);
-        o[4 * i + 3] = ((w[i] >> 6) & 0x01C001C0u) | (w[i] & 0x80008000u);
+        o[4 * i + 2] = ((u << 6) & 0x01C001C0u) | ((w[i] << 4) & 0x80008000u);
+        o[4 * i + 3] = ((u << 2) & 0x01C001C0u) | (w[i] & 0x80008000u);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -107,9 +107,6 @@ __device__ __forceinline__ void dequant32_store(const uint4 &v, uint32_t se, uin
         for (int i = 0; i < 16; ++i)
             o[i] = mul_bf16x2(o[i], g);
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        st_shared_v4(rb + (((u + i) ^ x) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
 }
 
 // Split merge inside a cluster of S CTAs (one per split of a token's keys).  The CTA of rank r owns heads
@@ -202,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     const uint32_t bar_s = smem_u32(small + kOffBars);   // S^T of the block complete
     const uint32_t bar_p = bar_s + 8;                    // P^T of the block written (16 warps)
     const uint32_t bar_pv = bar_s + 16;                  // [4] O^T tile m of the block complete
-    const uint32_t bar_grp = bar_s + 48;                 // [3] column chunks 0-3, 4-5, 6-8 of the K tile written
+    const uint32_t bar_grp = bar_s + 48;                 // [3] column chunks 0-3, 4-5 and 8, 6-7 of the K tile written
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(small + kOffAbort);
 
@@ -222,8 +219,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // the lists come from the previous kernel
-
+    // Q into registers.  Only the lists come from the previous kernel, which began after everything before it in the
+    // stream had ended: whatever else the call reads is there already.
+    uint4 qv[kQLoads];
+    if (is_worker) {
+#pragma unroll
+        for (int j = 0; j < kQLoads; ++j) {
+            const int i = wid + kWorkers * j;
+            const int h = i / (kDim / 8), c = i % (kDim / 8);
+            qv[j] = make_uint4(0u, 0u, 0u, 0u);   // (zeros for heads that do not exist)
+            if (h < nhv)
+                qv[j] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride + (int64_t)(h0 + h) * kDim + 8 * c));
+        }
+    }
     const int row = p.req_idx != nullptr ? p.req_idx[t] : t;
     const bool row_ok = row >= 0 && row < p.num_reqs;
     const int32_t *list = p.lists + (int64_t)t * p.list_w;
@@ -261,11 +269,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     };
     auto load_scales = [&](const uint8_t *e) { psc = ld_stream(e + kScale4Offset); };
 
-    int pos1 = -1, pos2 = -1, next_slot = -1;
+    // L2 prefetch of a whole entry, by the lanes of its first quarter
+    auto prefetch = [&](int slot) {
+        if (qtr == 0 && slot >= 0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.kv + (int64_t)slot * kEntry4Bytes),
+                         "r"((uint32_t)kEntry4Bytes)
+                         : "memory");
+    };
+
+    // cache slots of the next two blocks, and the position of the row in the block after those
+    int slot1 = -1, slot2 = -1, pos3 = -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (is_worker) {
-        const int pos0 = position_of(0);
-        pos1 = position_of(1);
-        pos2 = position_of(2);
+        const int pos0 = position_of(0), pos1 = position_of(1), pos2 = position_of(2);
+        pos3 = position_of(3);
         const int slot0 = slot_of(pos0);
         pre_ok = slot0 >= 0;
         if (pre_ok) {
@@ -276,27 +293,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 load_piece(e, m);
             load_rope(e);
         }
-        next_slot = slot_of(pos1);
-        // Q -> swizzled K-major B operand in the tile's order of dims (zeros for heads that do not exist)
-        uint4 v[kQLoads];
-#pragma unroll
-        for (int j = 0; j < kQLoads; ++j) {
-            const int i = wid + kWorkers * j;
-            const int h = i / (kDim / 8), c = i % (kDim / 8);
-            v[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (h < nhv)
-                v[j] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride + (int64_t)(h0 + h) * kDim + 8 * c));
-        }
+        slot1 = slot_of(pos1);
+        prefetch(slot1);
+        slot2 = slot_of(pos2);
+        // Q -> swizzled K-major B operand, in the tile's order of dims
 #pragma unroll
         for (int j = 0; j < kQLoads; ++j) {
             const int i = wid + kWorkers * j;
             const int h = i / (kDim / 8), c = i % (kDim / 8);
             const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
             if (c < kLatent / 8)
-                st_shared_v4(a, __byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
-                             __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
+                st_shared_v4(a, __byte_perm(qv[j].x, qv[j].z, 0x5410), __byte_perm(qv[j].x, qv[j].z, 0x7632),
+                             __byte_perm(qv[j].y, qv[j].w, 0x5410), __byte_perm(qv[j].y, qv[j].w, 0x7632));
             else
-                st_shared_v4(a, v[j].x, v[j].y, v[j].z, v[j].w);
+                st_shared_v4(a, qv[j].x, qv[j].y, qv[j].z, qv[j].w);
         }
     }
     const int L = p.lens[t];
@@ -337,51 +347,47 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 
     if (warp == 0) {
         // descriptors: K-major operands advance 32 B per 16 dims and one column chunk per 64
-        if (lane == 0) {
-            const uint64_t qk_a = sdesc(sK, 16, 1024);
-            const uint64_t qk_b = sdesc(sQ, 16, 1024);
-            for (int b = 0; b < nblocks; ++b) {
-                const uint32_t ph = (uint32_t)(b & 1);
-#pragma unroll 1
-                for (int g = 0; g < kGroups; ++g) {
-                    mbar_wait(bar_grp + 8 * g, ph, abort_flag, p.status);
-                    after_sync();
-                    const int c_lo = g == 0 ? 0 : g == 1 ? 4 : 6, c_hi = g == 0 ? 4 : g == 1 ? 6 : 9;
-#pragma unroll 1
-                    for (int c = c_lo; c < c_hi; ++c) {
-                        const uint64_t a = qk_a + (uint64_t)((c * kChunkBytes) >> 4);
-                        const uint64_t bq = qk_b + (uint64_t)((c * kQChunkBytes) >> 4);
+        const uint32_t leader = elect_one();
+        const uint64_t qk_a = sdesc(sK, 16, 1024);
+        const uint64_t qk_b = sdesc(sQ, 16, 1024);
+        for (int b = 0; b < nblocks; ++b) {
+            const uint32_t ph = (uint32_t)(b & 1);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16(tmem + kColS, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdescQK,
-                                     (c != 0 || k != 0) ? 1u : 0u);
-                    }
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = i < 6 ? i : i == 6 ? 8 : i - 1;   // in the order in which they are written
+                if (i == 0 || i == 4 || i == 7) {
+                    mbar_wait(bar_grp + (i == 0 ? 0 : i == 4 ? 8 : 16), ph, abort_flag, p.status);
+                    after_sync();
                 }
-                commit(bar_s);
+                const uint64_t a = qk_a + (uint64_t)((c * kChunkBytes) >> 4);
+                const uint64_t bq = qk_b + (uint64_t)((c * kQChunkBytes) >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16(leader, tmem + kColS, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdescQK,
+                             (i != 0 || k != 0) ? 1u : 0u);
             }
+            commit(leader, bar_s);
         }
-        __syncwarp();
     } else if (warp == kPvWarp) {
         // MN-major operands advance 2 KB per 16 keys
-        if (lane == 0) {
-            const uint64_t pv_a = sdesc(sK, kChunkBytes, 1024);
-            const uint64_t pv_b = sdesc(sP, 1024, 1024);
-            for (int b = 0; b < nblocks; ++b) {
-                mbar_wait(bar_p, (uint32_t)(b & 1), abort_flag, p.status);
-                after_sync();
-                const int ksteps = min(kBK / 16, (nkeys - b * kBK + 15) / 16);   // 16-key steps that hold keys
-#pragma unroll 1
-                for (int m = 0; m < 4; ++m) {
-                    const uint64_t a = pv_a + (uint64_t)((2 * m * kChunkBytes) >> 4);
-#pragma unroll 1
-                    for (int kk = 0; kk < ksteps; ++kk)
-                        mma_bf16(tmem + kColO + 64 * m, a + (uint64_t)(kk * 128), pv_b + (uint64_t)(kk * 128), kIdescPV,
+        const uint32_t leader = elect_one();
+        const uint64_t pv_a = sdesc(sK, kChunkBytes, 1024);
+        const uint64_t pv_b = sdesc(sP, 1024, 1024);
+        for (int b = 0; b < nblocks; ++b) {
+            mbar_wait(bar_p, (uint32_t)(b & 1), abort_flag, p.status);
+            after_sync();
+            const int left = nkeys - b * kBK;   // 16-key steps without a key are left out
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint64_t a = pv_a + (uint64_t)((2 * m * kChunkBytes) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kBK / 16; ++kk)
+                    if (16 * kk < left)
+                        mma_bf16(leader, tmem + kColO + 64 * m, a + (uint64_t)(kk * 128), pv_b + (uint64_t)(kk * 128), kIdescPV,
                                  (b > 0 || kk > 0) ? 1u : 0u);
-                    commit(bar_pv + 8 * m);   // releases K chunks 2m, 2m+1 (tile 3: also P^T)
-                }
+                commit(leader, bar_pv + 8 * m);   // releases K chunks 2m, 2m+1 (tile 3: also P^T)
             }
         }
-        __syncwarp();
     } else {
         const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
         float l[16];                                      // this lane's row sums of heads hs ..
@@ -395,33 +401,45 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         for (int b = 0; b < nblocks; ++b) {
             const uint32_t ph = (uint32_t)(b & 1);
             // ---- dequant of block b (zeros for rows without a key); the next block's entry into the registers
-            const bool ok_next = next_slot >= 0;
-            const uint8_t *en = p.kv + (int64_t)(ok_next ? next_slot : 0) * kEntry4Bytes;
+            const bool ok_next = slot1 >= 0;
+            const uint8_t *en = p.kv + (int64_t)(ok_next ? slot1 : 0) * kEntry4Bytes;
+            prefetch(slot2);
             if (qtr == 0)
                 valid[(b & 1) * kBK + rrow] = pre_ok;
             const uint32_t sc[4] = {psc.x, psc.y, psc.z, psc.w};
+            uint32_t o[16];
+            auto convert = [&](int m) {
+                if (pre_ok) {
+                    dequant32(pre[m], (sc[m] >> (8 * qtr)) & 0xFFu, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = 0u;
+                }
+            };
+            convert(0);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {   // dims 128 m + 32 qtr ..
                 if (b > 0)
                     mbar_wait(bar_pv + 8 * m, ph ^ 1u, abort_flag, p.status);   // P.V of block b-1 is done with them
                 const uint32_t cb = rb + (uint32_t)(2 * m + (qtr >> 1)) * kChunkBytes;
                 const uint32_t u = 4u * (uint32_t)(qtr & 1);
-                if (pre_ok) {
-                    dequant32_store(pre[m], (sc[m] >> (8 * qtr)) & 0xFFu, cb, u, x7);
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        st_shared_v4(cb + (((u + i) ^ x7) << 4), 0u, 0u, 0u, 0u);
-                }
-                if (ok_next)
-                    load_piece(en, m);
-                if (m == 3) {
+                for (int i = 0; i < 4; ++i)
+                    st_shared_v4(cb + (((u + i) ^ x7) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                if (m == 2) {   // the rope chunk, whose place P^T had
+                    if (b > 0)
+                        mbar_wait(bar_pv + 24, ph ^ 1u, abort_flag, p.status);
                     const uint32_t cr = rb + 8u * kChunkBytes;
                     if (!pre_ok)
                         prope[0] = prope[1] = make_uint4(0u, 0u, 0u, 0u);
                     st_shared_v4(cr + (((uint32_t)qtr ^ x7) << 4), prope[0].x, prope[0].y, prope[0].z, prope[0].w);
                     st_shared_v4(cr + (((uint32_t)(qtr + 4) ^ x7) << 4), prope[1].x, prope[1].y, prope[1].z, prope[1].w);
                 }
+                if (ok_next)
+                    load_piece(en, m);
+                if (m < 3)
+                    convert(m + 1);   // while the stores drain and the next value tile's product runs
                 if (m >= 1) {
                     fence_async_smem();
                     __syncwarp();
@@ -434,8 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 load_scales(en);
             }
             pre_ok = ok_next;
-            next_slot = slot_of(pos2);
-            pos2 = position_of(b + 3);
+            slot1 = slot2;
+            slot2 = slot_of(pos3);
+            pos3 = position_of(b + 4);
 
             // ---- softmax of block b: this warp's 32 keys (TMEM lanes) x 16 heads
             mbar_wait(bar_s, ph, abort_flag, p.status);
