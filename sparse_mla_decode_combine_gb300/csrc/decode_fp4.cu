@@ -80,6 +80,11 @@ constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)
 constexpr uint32_t kIdescQK = kIdescBase;                           // A, B K-major
 constexpr uint32_t kIdescPV = kIdescBase | (1u << 15) | (1u << 16);  // A, B MN-major
 
+// 16 bytes of an entry.  Entries start at odd multiples of 16 bytes as often as at even ones, so a row's 64-byte
+// pieces share 32-byte sectors with their neighbours: L1 keeps them for the next piece (8 % of the kernel's time
+// against loads that do not allocate there).
+__device__ __forceinline__ uint4 ld16(const void *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
+
 // 32 E2M1 codes times 2^(se - 127) -> 16 BF16 pairs, exactly.
 // A code's exponent and mantissa bits at the low end of the BF16 exponent are its value times 2^-126 (both
 // formats put the binary point the same way, subnormals included); one multiply by 2^(se - 1) gives the value.
@@ -262,12 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     };
     uint4 pre[4], prope[2], psc;   // the entry of the block ahead: four code pieces, rope, scale bytes
     bool pre_ok = false;
-    auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld_stream(e + 64 * m + 16 * qtr); };
+    auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld16(e + 64 * m + 16 * qtr); };
     auto load_rope = [&](const uint8_t *e) {
-        prope[0] = ld_stream(e + kRope4Offset + 16 * qtr);
-        prope[1] = ld_stream(e + kRope4Offset + 64 + 16 * qtr);
+        prope[0] = ld16(e + kRope4Offset + 16 * qtr);
+        prope[1] = ld16(e + kRope4Offset + 64 + 16 * qtr);
     };
-    auto load_scales = [&](const uint8_t *e) { psc = ld_stream(e + kScale4Offset); };
+    auto load_scales = [&](const uint8_t *e) { psc = ld16(e + kScale4Offset); };
 
     // L2 prefetch of a whole entry, by the lanes of its first quarter
     auto prefetch = [&](int slot) {
@@ -417,11 +422,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         o[i] = 0u;
                 }
             };
-            convert(0);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {   // dims 128 m + 32 qtr ..
                 if (b > 0)
                     mbar_wait(bar_pv + 8 * m, ph ^ 1u, abort_flag, p.status);   // P.V of block b-1 is done with them
+                convert(m);
                 const uint32_t cb = rb + (uint32_t)(2 * m + (qtr >> 1)) * kChunkBytes;
                 const uint32_t u = 4u * (uint32_t)(qtr & 1);
 #pragma unroll
@@ -438,8 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 }
                 if (ok_next)
                     load_piece(en, m);
-                if (m < 3)
-                    convert(m + 1);   // while the stores drain and the next value tile's product runs
                 if (m >= 1) {
                     fence_async_smem();
                     __syncwarp();
