@@ -23,7 +23,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
-// ---- the decode's workspace (the combined lists and their lengths) and work decomposition
+// ---- the decode's workspace (the tokens' slot lists and their lengths) and work decomposition
 struct Plan4 {
     int list_w;
     size_t off_lens, total;
@@ -168,24 +168,34 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
         return DSV4_ERR_CUDA;
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    int32_t *lists = reinterpret_cast<int32_t *>(ws), *lens = reinterpret_cast<int32_t *>(ws + pl.off_lens);
-    cudaError_t e = launch_combine(topk_idx, topk_stride, topk_width, topk_lens, seq_lens, num_tokens, window, lists,
-                                   pl.list_w, pl.list_w, lens, combine_table_bits(topk_width), cs);
-    if (e != cudaSuccess)
-        return DSV4_ERR_CUDA;
+    Lists4Params l{};
+    l.topk = topk_idx;
+    l.topk_stride = topk_stride;
+    l.topk_width = topk_width;
+    l.topk_lens = topk_lens;
+    l.seq_lens = seq_lens;
+    l.num_tokens = num_tokens;
+    l.window = window;
+    l.block_table = block_table;
+    l.bt_stride = bt_stride;
+    l.max_blocks = max_blocks;
+    l.num_reqs = num_reqs;
+    l.req_idx = req_idx;
+    l.num_blocks = num_blocks;
+    l.page = page_block;
+    l.slots = reinterpret_cast<int32_t *>(ws);
+    l.lens = reinterpret_cast<int32_t *>(ws + pl.off_lens);
+    l.list_w = pl.list_w;
+    l.status = status;
     Decode4Params p{};
+    if (!decompose(num_tokens, num_heads, pl.list_w, &p.groups, &p.splits, &p.chunk) ||
+        launch_lists_fp4(l, cs) != cudaSuccess)
+        return DSV4_ERR_CUDA;
     p.q = static_cast<const uint16_t *>(q);
     p.q_token_stride = q_token_stride;
     p.kv = static_cast<const uint8_t *>(kv_cache);
-    p.num_blocks = num_blocks;
-    p.page = page_block;
-    p.block_table = block_table;
-    p.bt_stride = bt_stride;
-    p.max_blocks = max_blocks;
-    p.num_reqs = num_reqs;
-    p.req_idx = req_idx;
-    p.lists = lists;
-    p.lens = lens;
+    p.slots = l.slots;
+    p.lens = l.lens;
     p.list_w = pl.list_w;
     p.num_tokens = num_tokens;
     p.num_heads = num_heads;
@@ -194,8 +204,6 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
     p.status = status;
-    if (!decompose(num_tokens, num_heads, pl.list_w, &p.groups, &p.splits, &p.chunk))
-        return DSV4_ERR_CUDA;
     return launch_decode_fp4(p, cs) == cudaSuccess ? DSV4_OK : DSV4_ERR_CUDA;
 }
 

@@ -2,21 +2,22 @@
 //
 // Operation (per token t, head h, over the token's combined list of positions):
 //   s_p = scale * q_h . k_p (576 dims),  lse_h = ln(sum_p e^{s_p} + e^{sink_h}),  out_h = sum_p e^{s_p - lse_h} v_p
-// The lists come from the combine kernel ahead of this one in the stream.
+// The lists of cache slots come from the list kernel (lists_fp4.cu) ahead of this one in the stream.
 //
 // Contraction.  All heads share one key set, so a (token, 64 heads) unit is a pair of dense products, run
-// transposed (keys and value dims on the 128-row side of the tensor tile) because 64 heads do not fill it:
-//   S^T[128 keys x 64 heads]  = K_tile[128 x 576] . Q^T         (A = K tile, K-major)
-//   O^T[128 dv x 64 heads]   += V^T[128 dv x 128 keys] . P^T    (A = the same bytes, MN-major), four tiles
-// The K tile is the dequantised block in BF16 (exact: an E2M1 code times a power of two), nine 64-dim
-// column chunks of 128-byte-swizzled rows, 147 KB of shared memory beside the 74 KB of Q.
+// transposed (keys and value dims on the M side of the tensor tile):
+//   S^T[64 keys x 64 heads]   = K_tile[64 x 576] . Q^T          (A = K tile, K-major)
+//   O^T[128 dv x 64 heads]   += V^T[128 dv x 64 keys] . P^T     (A = the same bytes, MN-major), four tiles
+// A K tile is a dequantised block in BF16 (exact: an E2M1 code times a power of two), nine 64-dim column
+// chunks of 128-byte-swizzled rows: 74 KB, twice, beside the 74 KB of Q.
 //
-// One K tile leaves no room for a second block, so the block's steps form a chain, and the kernel's time is
-// that chain's length.  What shortens it:
-//   - the dequant of block b + 1 follows P.V of block b: value tile m, when its product is done, frees the two
-//     column chunks that pass m of the dequant writes, and S^T of b + 1 follows the dequant chunk by chunk;
-//   - a thread holds its quarter of a row's next entry in registers (seven 16-byte loads, issued as the
-//     registers of the present block are used up), so the gather is off the chain;
+// Pipeline over two K tiles.  While the workers do the softmax of block b in one tile, S^T of block b + 1 runs
+// from the other; while they write block b + 2 over block b (behind P.V of b, half the value dims at a time),
+// P.V of b runs.  What the tensor cores read (a product of M 128 or 64 x N 64 x K 16 takes 6 or 4 KB of
+// operands) and what the workers write share 128 B a cycle of shared memory: about 5 k cycles for 128 keys,
+// which bounds a long list.  (One 128-key tile, whose steps form a chain, took 8.5 k.)
+//   - a thread holds its eighth of a row's next entry in registers, loaded as those of the present block are
+//     used up; whole entries are prefetched to L2 two blocks before that;
 //   - the softmax keeps a reference maximum per head from the unit's first block and exchanges maxima between
 //     warps again only when a logit exceeds it by 2^40: P and the sums are floating-point numbers, whose
 //     relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.  The
@@ -43,42 +44,43 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 576;            // warp 0: S^T issue; warps 1-16: workers; warp 17: P.V issue
+constexpr int kThreads = 576;            // warp 0: S^T issue; 1-8: softmax; 9-16: dequant; 17: P.V issue
 constexpr int kPvWarp = 17;
-constexpr int kWorkers = 512;
-constexpr int kBK = 128;                 // keys per block = MMA M
+constexpr int kWorkers = 512;            // softmax and dequant: Q's layout, the epilogue
+constexpr int kSoftmaxWarps = 8;
+constexpr int kDequantWarps = 8;
+constexpr int kBK = 64;                  // keys per block = MMA M of the logits
+constexpr int kDvTile = 128;             // value dims per tile = MMA M of P.V
 constexpr int kNH = 64;                  // heads per CTA = MMA N
 constexpr int kChunks = 9;               // 576 dims / 64
 constexpr int kQBytes = kChunks * kNH * 128;     // 73728
-constexpr int kKBytes = kChunks * kBK * 128;     // 147456
-constexpr int kChunkBytes = kBK * 128;           // 16384 (one 64-dim column chunk of the K tile)
+constexpr int kKBytes = kChunks * kBK * 128;     // 73728: one of two K tiles
+constexpr int kChunkBytes = kBK * 128;           // 8192 (one 64-dim column chunk of a K tile)
 constexpr int kQChunkBytes = kNH * 128;          // 8192
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0;            // S^T: 64 columns
-constexpr uint32_t kColO = 64;           // O^T: 4 tiles x 64 columns
+constexpr uint32_t kColS = 0;            // S^T: 64 columns for each of the two K tiles
+constexpr uint32_t kColO = 128;          // O^T: 4 tiles x 64 columns
 constexpr float kExceedLog2 = 40.f;
 constexpr int kMaxSplits = 8;            // portable cluster size
 
-// small shared region (after Q and the K tile)
+// small shared region (after Q and the two K tiles)
 constexpr int kOffRed = 0;               // float [4][64]: per-quadrant head maxima, or row sums at the end
 constexpr int kOffMax = 1024;            // float [64]: reference maximum per head (log2 units; natural ones at the end)
-constexpr int kOffFin = 1280;            // float [64]: the output factor, or this split's row sum
-constexpr int kOffValid = 1536;          // uint8 [2][128]: rows of the block that hold a key, by block parity
-constexpr int kOffBars = 1792;           // u64: bar_s, bar_p, bar_pv[4], bar_grp[3]
-constexpr int kOffTmem = 1872;           // u32
-constexpr int kOffAbort = 1880;          // int
-constexpr int kSmallBytes = 1920;
-constexpr int kSmemBytes = kQBytes + kKBytes + kSmallBytes + 1024;   // + alignment slack
-constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                 // 9 16-byte Q pieces per worker
-constexpr int kGroups = 3;               // S^T is issued as column chunks 0-3, then 4, 5 and 8, then 6 and 7 are written
+constexpr int kOffFin = 1280;            // float [64]: the factor of a rescale; at the end the output's, or a split's row sum
+constexpr int kOffValid = 1536;          // uint8 [2][64]: rows of a K tile that hold a key
+constexpr int kOffBars = 1664;           // u64: bar_s[2], bar_p[2], bar_grp[2][2], bar_pv[2][4]
+constexpr int kOffTmem = 1792;           // u32
+constexpr int kOffAbort = 1796;          // int
+constexpr int kSmallBytes = 1856;
+constexpr int kSmemBytes = kQBytes + 2 * kKBytes + kSmallBytes + 1024;   // + alignment slack
+constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                     // 9 16-byte Q pieces per worker
 static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
-static_assert(kKBytes >= (kNH + kMaxSplits) * kLatent * (int)sizeof(float), "the partials fit the K tile");
+static_assert(2 * kKBytes >= (kNH + kMaxSplits) * kLatent * (int)sizeof(float), "the partials fit the K tiles");
 
-// instruction descriptors (kind::f16): D f32, A/B bf16, M = 128, N = 64
-constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kNH >> 3) << 17) |
-                                ((uint32_t)(kBK >> 4) << 24);
-constexpr uint32_t kIdescQK = kIdescBase;                           // A, B K-major
-constexpr uint32_t kIdescPV = kIdescBase | (1u << 15) | (1u << 16);  // A, B MN-major
+// instruction descriptors (kind::f16): D f32, A/B bf16, N = 64
+constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kNH >> 3) << 17);
+constexpr uint32_t kIdescQK = kIdescBase | ((uint32_t)(kBK >> 4) << 24);                              // A, B K-major
+constexpr uint32_t kIdescPV = kIdescBase | ((uint32_t)(kDvTile >> 4) << 24) | (1u << 15) | (1u << 16);   // A, B MN-major
 
 // 16 bytes of an entry.  Entries start at odd multiples of 16 bytes as often as at even ones, so a row's 64-byte
 // pieces share 32-byte sectors with their neighbours: L1 keeps them for the next piece (8 % of the kernel's time
@@ -194,28 +196,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     const uint32_t base = (raw + 1023u) & ~1023u;   // the swizzled tiles start on 1024-byte boundaries
     uint8_t *gbase = smem_raw + (base - raw);
     const uint32_t sQ = base;
-    const uint32_t sK = base + kQBytes;
-    const uint32_t sP = sK + 8 * kChunkBytes;   // P^T takes the rope column chunk once S^T is done
-    uint8_t *small = gbase + kQBytes + kKBytes;
+    const uint32_t sK = base + kQBytes;           // two K tiles; P^T takes a tile's rope chunk once its S^T is done
+    uint8_t *small = gbase + kQBytes + 2 * kKBytes;
     float *red = reinterpret_cast<float *>(small + kOffRed);
     float *smax = reinterpret_cast<float *>(small + kOffMax);
     float *fin = reinterpret_cast<float *>(small + kOffFin);
     uint8_t *valid = small + kOffValid;
-    const uint32_t bar_s = smem_u32(small + kOffBars);   // S^T of the block complete
-    const uint32_t bar_p = bar_s + 8;                    // P^T of the block written (16 warps)
-    const uint32_t bar_pv = bar_s + 16;                  // [4] O^T tile m of the block complete
-    const uint32_t bar_grp = bar_s + 48;                 // [3] column chunks 0-3, 4-5 and 8, 6-7 of the K tile written
+    const uint32_t bar_s = smem_u32(small + kOffBars);   // [tile] S^T complete
+    const uint32_t bar_p = bar_s + 16;                   // [tile] P^T written (softmax warps)
+    const uint32_t bar_grp = bar_s + 32;                 // [tile][2] column chunks 0-3, then 4-8 written (dequant warps)
+    const uint32_t bar_pv = bar_s + 64;                  // [tile][4] P.V of value tile m complete
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(small + kOffAbort);
 
-    // ---- set-up that reads no input
+    // ---- set-up that does not read the lists
     if (tid == 0) {
-        mbar_init(bar_s, 1);
-        mbar_init(bar_p, kWorkers / 32);
-        for (int m = 0; m < 4; ++m)
-            mbar_init(bar_pv + 8 * m, 1);
-        for (int g = 0; g < kGroups; ++g)
-            mbar_init(bar_grp + 8 * g, kWorkers / 32);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_s + 8 * i, 1);
+            mbar_init(bar_p + 8 * i, kSoftmaxWarps);
+        }
+        for (int i = 0; i < 4; ++i)
+            mbar_init(bar_grp + 8 * i, kDequantWarps);
+        for (int i = 0; i < 8; ++i)
+            mbar_init(bar_pv + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
@@ -223,7 +226,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         smax[tid] = 0.f;
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-
     // Q into registers.  Only the lists come from the previous kernel, which began after everything before it in the
     // stream had ended: whatever else the call reads is there already.
     uint4 qv[kQLoads];
@@ -237,35 +239,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 qv[j] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride + (int64_t)(h0 + h) * kDim + 8 * c));
         }
     }
-    const int row = p.req_idx != nullptr ? p.req_idx[t] : t;
-    const bool row_ok = row >= 0 && row < p.num_reqs;
-    const int32_t *list = p.lists + (int64_t)t * p.list_w;
-    const int32_t *bt_row = p.block_table + (int64_t)(row_ok ? row : 0) * p.bt_stride;
-    const int kbeg = split * p.chunk;
-    const int klim = min(kbeg + p.chunk, p.list_w);
 
-    // dequant: lanes 8 q .. 8 q + 7 of worker warp ww take quarter q of eight rows whose numbers differ mod 8
-    // (no bank conflicts in the swizzled stores) and spread over the tile, so that a short block keeps every
-    // warp at work
+    // Dequant: four threads to a row, each with a 16-byte piece of codes (32 dims) in every value tile, two of rope, and
+    // the scale bytes.  Lanes 8 q .. 8 q + 7 of a warp take quarter q of eight rows whose numbers differ mod 8 (no bank
+    // conflicts in the swizzled stores) and spread over the tile, so that a short block keeps every warp at work.
+    const bool is_dequant = warp >= 9 && warp <= 16;
     const int qtr = lane >> 3;
-    const int rrow = 8 * (((warp - 1) - (lane & 7)) & 15) + (lane & 7);
-    // the list's position, then the cache slot, of this thread's row in block b; -1 past the list's end
-    auto position_of = [&](int b) {
-        const int i = kbeg + b * kBK + rrow;
-        return is_worker && i < klim ? __ldg(list + i) : -1;
-    };
-    auto slot_of = [&](int pos) {
-        if (pos < 0)
-            return -1;
-        const int blk = pos / p.page;
-        const int phys = row_ok && blk < p.max_blocks ? __ldg(bt_row + blk) : -1;
-        if (phys < 0 || phys >= p.num_blocks) {
-            atomicOr(p.status, kStatusBadIndex);
-            return -1;
-        }
-        return phys * p.page + (pos - blk * p.page);
-    };
-    uint4 pre[4], prope[2], psc;   // the entry of the block ahead: four code pieces, rope, scale bytes
+    const int rrow = 8 * (((warp - 9) - (lane & 7)) & 7) + (lane & 7);
+    const int32_t *list = p.slots + (int64_t)t * p.list_w;
+    const int kbeg = split * p.chunk;
+    uint4 pre[4], prope[2], psc;   // the entry of the block ahead
     bool pre_ok = false;
     auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld16(e + 64 * m + 16 * qtr); };
     auto load_rope = [&](const uint8_t *e) {
@@ -273,34 +256,40 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         prope[1] = ld16(e + kRope4Offset + 64 + 16 * qtr);
     };
     auto load_scales = [&](const uint8_t *e) { psc = ld16(e + kScale4Offset); };
-
+    auto entry = [&](int slot) { return p.kv + (int64_t)(slot >= 0 ? slot : 0) * kEntry4Bytes; };
     // L2 prefetch of a whole entry, by the lanes of its first quarter
     auto prefetch = [&](int slot) {
         if (qtr == 0 && slot >= 0)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.kv + (int64_t)slot * kEntry4Bytes),
-                         "r"((uint32_t)kEntry4Bytes)
-                         : "memory");
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(entry(slot)), "r"((uint32_t)kEntry4Bytes) : "memory");
     };
 
-    // cache slots of the next two blocks, and the position of the row in the block after those
-    int slot1 = -1, slot2 = -1, pos3 = -1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (is_worker) {
-        const int pos0 = position_of(0), pos1 = position_of(1), pos2 = position_of(2);
-        pos3 = position_of(3);
-        const int slot0 = slot_of(pos0);
+    const int kend = min(p.lens[t], kbeg + p.chunk);
+    const int nkeys = max(0, kend - kbeg);
+    const int nblocks = (nkeys + kBK - 1) / kBK;
+    // the cache slot of this thread's row in block b; -1 past the list's end
+    auto slot_of = [&](int b) {
+        const int i = kbeg + b * kBK + rrow;
+        return i < kend ? __ldg(list + i) : -1;
+    };
+    int slot1 = -1, slot2 = -1, slot3 = -1;   // of the blocks ahead
+    if (is_dequant) {
+        const int slot0 = slot_of(0);
+        slot1 = slot_of(1);
+        slot2 = slot_of(2);
+        slot3 = slot_of(3);
         pre_ok = slot0 >= 0;
         if (pre_ok) {
-            const uint8_t *e = p.kv + (int64_t)slot0 * kEntry4Bytes;
-            load_scales(e);
+            load_scales(entry(slot0));
 #pragma unroll
             for (int m = 0; m < 4; ++m)
-                load_piece(e, m);
-            load_rope(e);
+                load_piece(entry(slot0), m);
+            load_rope(entry(slot0));
         }
-        slot1 = slot_of(pos1);
         prefetch(slot1);
-        slot2 = slot_of(pos2);
+        prefetch(slot2);
+    }
+    if (is_worker) {
         // Q -> swizzled K-major B operand, in the tile's order of dims
 #pragma unroll
         for (int j = 0; j < kQLoads; ++j) {
@@ -314,9 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 st_shared_v4(a, qv[j].x, qv[j].y, qv[j].z, qv[j].w);
         }
     }
-    const int L = p.lens[t];
-    const int nkeys = max(0, min(L, klim) - kbeg);
-    const int nblocks = (nkeys + kBK - 1) / kBK;
     fence_async_smem();
     before_sync();
     __syncthreads();   // Q, barriers, TMEM address
@@ -344,11 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     }
 
     const int quad = warp & 3;                            // TMEM lane quadrant of this warp
-    const int hs = 16 * ((warp - 1) >> 2);                // workers: first of this warp's 16 heads
-    const int key = quad * 32 + lane;                     // softmax: key of the block; epilogue: row of a value tile
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    // value dim of tile row `key` (the tile's order of dims)
-    const int dv0 = (key & ~7) | ((key >> 1) & 3) | ((key & 1) << 2);
+    const int vrow = quad * 32 + lane;                    // this lane's row of a value tile,
+    const int dv0 = (vrow & ~7) | ((vrow >> 1) & 3) | ((vrow & 1) << 2);   // and its value dim (the tile's order of dims)
 
     if (warp == 0) {
         // descriptors: K-major operands advance 32 B per 16 dims and one column chunk per 64
@@ -356,64 +340,60 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         const uint64_t qk_a = sdesc(sK, 16, 1024);
         const uint64_t qk_b = sdesc(sQ, 16, 1024);
         for (int b = 0; b < nblocks; ++b) {
-            const uint32_t ph = (uint32_t)(b & 1);
+            const int x = b & 1;
+            const uint32_t ph = (uint32_t)(b >> 1) & 1u;
+            const uint64_t ax = qk_a + (uint64_t)((x * kKBytes) >> 4);
 #pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c = i < 6 ? i : i == 6 ? 8 : i - 1;   // in the order in which they are written
-                if (i == 0 || i == 4 || i == 7) {
-                    mbar_wait(bar_grp + (i == 0 ? 0 : i == 4 ? 8 : 16), ph, abort_flag, p.status);
+            for (int c = 0; c < kChunks; ++c) {
+                if (c == 0 || c == 4) {
+                    mbar_wait(bar_grp + 16 * x + 2 * c, ph, abort_flag, p.status);
                     after_sync();
                 }
-                const uint64_t a = qk_a + (uint64_t)((c * kChunkBytes) >> 4);
+                const uint64_t a = ax + (uint64_t)((c * kChunkBytes) >> 4);
                 const uint64_t bq = qk_b + (uint64_t)((c * kQChunkBytes) >> 4);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    mma_bf16(leader, tmem + kColS, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdescQK,
-                             (i != 0 || k != 0) ? 1u : 0u);
+                    mma_bf16(leader, tmem + kColS + 64 * x, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdescQK,
+                             (c != 0 || k != 0) ? 1u : 0u);
             }
-            commit(leader, bar_s);
+            commit(leader, bar_s + 8 * x);
         }
     } else if (warp == kPvWarp) {
         // MN-major operands advance 2 KB per 16 keys
         const uint32_t leader = elect_one();
         const uint64_t pv_a = sdesc(sK, kChunkBytes, 1024);
-        const uint64_t pv_b = sdesc(sP, 1024, 1024);
+        const uint64_t pv_b = sdesc(sK + 8 * kChunkBytes, 1024, 1024);
         for (int b = 0; b < nblocks; ++b) {
-            mbar_wait(bar_p, (uint32_t)(b & 1), abort_flag, p.status);
+            const int x = b & 1;
+            mbar_wait(bar_p + 8 * x, (uint32_t)(b >> 1) & 1u, abort_flag, p.status);
             after_sync();
+            const uint64_t off = (uint64_t)((x * kKBytes) >> 4);
             const int left = nkeys - b * kBK;   // 16-key steps without a key are left out
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const uint64_t a = pv_a + (uint64_t)((2 * m * kChunkBytes) >> 4);
+                const uint64_t a = pv_a + off + (uint64_t)((2 * m * kChunkBytes) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kBK / 16; ++kk)
                     if (16 * kk < left)
-                        mma_bf16(leader, tmem + kColO + 64 * m, a + (uint64_t)(kk * 128), pv_b + (uint64_t)(kk * 128), kIdescPV,
-                                 (b > 0 || kk > 0) ? 1u : 0u);
-                commit(leader, bar_pv + 8 * m);   // releases K chunks 2m, 2m+1 (tile 3: also P^T)
+                        mma_bf16(leader, tmem + kColO + 64 * m, a + (uint64_t)(kk * 128), pv_b + off + (uint64_t)(kk * 128),
+                                 kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
+                commit(leader, bar_pv + 32 * x + 8 * m);   // releases K chunks 2m, 2m+1 (m = 3: also P^T)
             }
         }
-    } else {
-        const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
-        float l[16];                                      // this lane's row sums of heads hs ..
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            l[j] = 0.f;
-        bool fresh = true;                                // no key has been seen: the references are not set
-        const uint32_t rb = sK + (uint32_t)(rrow >> 3) * 1024u + (uint32_t)(rrow & 7) * 128u;
+    } else if (is_dequant) {
+        const uint32_t rb = (uint32_t)(rrow >> 3) * 1024u + (uint32_t)(rrow & 7) * 128u;
         const uint32_t x7 = (uint32_t)(rrow & 7);
-
-        for (int b = 0; b < nblocks; ++b) {
-            const uint32_t ph = (uint32_t)(b & 1);
-            // ---- dequant of block b (zeros for rows without a key); the next block's entry into the registers
+        for (int b = 0; b < nblocks; ++b) {   // block b into its K tile (zeros for rows without a key)
+            const int x = b & 1;
+            const uint32_t ph = (uint32_t)((b >> 1) - 1) & 1u;
+            const uint32_t tile = sK + (uint32_t)x * kKBytes + rb;
             const bool ok_next = slot1 >= 0;
-            const uint8_t *en = p.kv + (int64_t)(ok_next ? slot1 : 0) * kEntry4Bytes;
-            prefetch(slot2);
-            if (qtr == 0)
-                valid[(b & 1) * kBK + rrow] = pre_ok;
+            const uint8_t *en = entry(slot1);   // the next block's entry goes into the registers as they are used up
+            prefetch(slot3);
             const uint32_t sc[4] = {psc.x, psc.y, psc.z, psc.w};
-            uint32_t o[16];
-            auto convert = [&](int m) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {   // dims 128 m + 32 qtr ..
+                uint32_t o[16];
                 if (pre_ok) {
                     dequant32(pre[m], (sc[m] >> (8 * qtr)) & 0xFFu, o);
                 } else {
@@ -421,33 +401,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     for (int i = 0; i < 16; ++i)
                         o[i] = 0u;
                 }
-            };
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {   // dims 128 m + 32 qtr ..
-                if (b > 0)
-                    mbar_wait(bar_pv + 8 * m, ph ^ 1u, abort_flag, p.status);   // P.V of block b-1 is done with them
-                convert(m);
-                const uint32_t cb = rb + (uint32_t)(2 * m + (qtr >> 1)) * kChunkBytes;
+                if (ok_next)
+                    load_piece(en, m);
+                if (b >= 2)
+                    mbar_wait(bar_pv + 32 * x + 8 * m, ph, abort_flag, p.status);   // P.V of block b - 2 is done with them
+                if (m == 0 && qtr == 0)
+                    valid[x * kBK + rrow] = pre_ok;
+                const uint32_t cb = tile + (uint32_t)(2 * m + (qtr >> 1)) * kChunkBytes;
                 const uint32_t u = 4u * (uint32_t)(qtr & 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     st_shared_v4(cb + (((u + i) ^ x7) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                if (m == 2) {   // the rope chunk, whose place P^T had
-                    if (b > 0)
-                        mbar_wait(bar_pv + 24, ph ^ 1u, abort_flag, p.status);
-                    const uint32_t cr = rb + 8u * kChunkBytes;
+                if (m == 3) {   // the rope chunk, whose place P^T had
+                    const uint32_t cr = tile + 8u * kChunkBytes;
                     if (!pre_ok)
                         prope[0] = prope[1] = make_uint4(0u, 0u, 0u, 0u);
                     st_shared_v4(cr + (((uint32_t)qtr ^ x7) << 4), prope[0].x, prope[0].y, prope[0].z, prope[0].w);
                     st_shared_v4(cr + (((uint32_t)(qtr + 4) ^ x7) << 4), prope[1].x, prope[1].y, prope[1].z, prope[1].w);
                 }
-                if (ok_next)
-                    load_piece(en, m);
-                if (m >= 1) {
+                if (m & 1) {
                     fence_async_smem();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(bar_grp + 8 * (m - 1));
+                        mbar_arrive(bar_grp + 16 * x + 4 * (m - 1));
                 }
             }
             if (ok_next) {
@@ -456,116 +432,132 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             }
             pre_ok = ok_next;
             slot1 = slot2;
-            slot2 = slot_of(pos3);
-            pos3 = position_of(b + 4);
-
-            // ---- softmax of block b: this warp's 32 keys (TMEM lanes) x 16 heads
-            mbar_wait(bar_s, ph, abort_flag, p.status);
-            after_sync();
-            uint32_t s[16];
-            tmem_ld16(lane_base + kColS + hs, s);
-            const bool kv = valid[(b & 1) * kBK + key] != 0;   // (rows past the list's end are not)
-            tmem_ld_wait();
-            // logits in log2 units above the heads' references
+            slot2 = slot3;
+            slot3 = slot_of(b + 4);
+        }
+    } else {
+        const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
+        const int hw = 32 * ((warp - 1) >> 2);            // first of this warp's 32 heads; its 16 keys are the quadrant's
+        const int slice_bar = 2 + ((warp - 1) >> 2);      // the four warps of these heads
+        // this lane's keys are srow and srow + 8; its heads, j = 0..7:
+        const int srow = 16 * quad + (lane >> 2);
+        const int sh = hw + 2 * (lane & 3);
+        auto head = [&](int j) { return sh + 16 * (j >> 2) + 8 * ((j >> 1) & 1) + (j & 1); };
+        float l[8];                                       // row sums of those heads over this lane's keys
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-                const float4 m = *reinterpret_cast<const float4 *>(smax + hs + j);
-                s[j] = __float_as_uint(fmaf(__uint_as_float(s[j]), c2, -m.x));
-                s[j + 1] = __float_as_uint(fmaf(__uint_as_float(s[j + 1]), c2, -m.y));
-                s[j + 2] = __float_as_uint(fmaf(__uint_as_float(s[j + 2]), c2, -m.z));
-                s[j + 3] = __float_as_uint(fmaf(__uint_as_float(s[j + 3]), c2, -m.w));
+        for (int j = 0; j < 8; ++j)
+            l[j] = 0.f;
+        bool fresh = true;                                // no key has been seen: the references are not set
+
+        for (int b = 0; b < nblocks; ++b) {
+            const int x = b & 1;
+            const uint32_t ph = (uint32_t)(b >> 1) & 1u;
+            mbar_wait(bar_grp + 16 * x, ph, abort_flag, p.status);   // (complete by then: the rows' flags are visible)
+            const bool kv[2] = {valid[x * kBK + srow] != 0, valid[x * kBK + srow + 8] != 0};   // (not past the list's end)
+            float ref[8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float2 m = *reinterpret_cast<const float2 *>(smax + head(j));
+                ref[j] = m.x;
+                ref[j + 1] = m.y;
             }
+            mbar_wait(bar_s + 8 * x, ph, abort_flag, p.status);
+            after_sync();
+            uint32_t s[2][8];
+            tmem_ld_16x16(lane_base + kColS + 64 * x + hw, s[0]);
+            tmem_ld_16x16(lane_base + kColS + 64 * x + hw + 16, s[1]);
+            tmem_ld_wait();
+            // logits in log2 units above the heads' references: v[r][j] of key row r, head j
+            float v[2][8];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[r][j] = kv[r] ? fmaf(__uint_as_float(s[j >> 2][4 * ((j >> 1) & 1) + 2 * r + (j & 1)]), c2, -ref[j]) : -INFINITY;
             float top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                top = fmaxf(top, __uint_as_float(s[j]));
-            if (named_bar_or(2 + ((warp - 1) >> 2), 128, kv && (fresh || top > kExceedLog2))) {
+            for (int j = 0; j < 8; ++j)
+                top = fmaxf(top, fmaxf(v[0][j], v[1][j]));
+            if (named_bar_or(slice_bar, 128, (fresh && (kv[0] || kv[1])) || top > kExceedLog2)) {
                 // the block's maxima, by the four warps of these heads, become the references where they are larger
-                float mine = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float m = warp_max(kv ? __uint_as_float(s[j]) : -INFINITY);
-                    mine = lane == j ? m : mine;
+                for (int j = 0; j < 8; ++j) {
+                    float mx = fmaxf(v[0][j], v[1][j]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    if (lane < 4)
+                        red[quad * kNH + head(j)] = mx;
                 }
-                if (lane < 16)
-                    red[quad * kNH + hs + lane] = mine;
-                named_bar(2 + ((warp - 1) >> 2), 128);
-                float up = 0.f;   // lane j: by how much the reference of head hs + j rises
-                if (lane < 16) {
-                    const int h = hs + lane;
+                named_bar(slice_bar, 128);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int h = head(j);
                     const float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
-                    up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);   // (-inf: every logit is NaN)
+                    const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);   // (-inf: every logit is NaN)
+                    const float fall = fresh ? 1.f : exp2_approx(-up);
+                    l[j] *= fall;
+                    v[0][j] -= up;
+                    v[1][j] -= up;
+                    if (quad == 0 && lane < 4) {
+                        smax[h] += up;
+                        fin[h] = fall;
+                    }
                 }
-                if (quad == 0 && lane < 16)
-                    smax[hs + lane] += up;
-                const float fall = fresh ? 1.f : exp2_approx(-up);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    s[j] = __float_as_uint(__uint_as_float(s[j]) - __shfl_sync(0xffffffffu, up, j));
-                    l[j] *= __shfl_sync(0xffffffffu, fall, j);
-                }
+                named_bar(slice_bar, 128);   // the references and factors are written, and red is free again
                 if (!fresh) {
+                    // (b > 0: no key was seen before otherwise) P.V of block b - 1 has to be complete
+                    mbar_wait(bar_pv + 32 * (x ^ 1) + 24, (uint32_t)((b - 1) >> 1) & 1u, abort_flag, p.status);
+                    after_sync();
 #pragma unroll 1
-                    for (int m = 0; m < 4; ++m) {
-                        uint32_t x[16];
-                        tmem_ld16(lane_base + kColO + 64 * m + hs, x);
+                    for (int m = 0; m < 8; ++m) {
+                        const int hc = hw + 16 * (m & 1);
+                        uint32_t y[16];
+                        tmem_ld16(lane_base + kColO + 64 * (m >> 1) + hc, y);
                         tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            x[j] = __float_as_uint(__uint_as_float(x[j]) * __shfl_sync(0xffffffffu, fall, j));
-                        tmem_st16(lane_base + kColO + 64 * m + hs, x);
+                            y[j] = __float_as_uint(__uint_as_float(y[j]) * fin[hc + j]);
+                        tmem_st16(lane_base + kColO + 64 * (m >> 1) + hc, y);
                     }
                     tmem_st_wait();
                 }
                 fresh = false;
-                named_bar(2 + ((warp - 1) >> 2), 128);   // the references are written, and red is free again
             }
-            // P = 2^s -> BF16 P^T row `key`
+            // P = 2^v -> BF16 P^T rows srow and srow + 8
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t pk[4];
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
-                    const int i = 8 * half + j;
-                    const float p0 = kv ? exp2_approx(__uint_as_float(s[i])) : 0.f;
-                    const float p1 = kv ? exp2_approx(__uint_as_float(s[i + 1])) : 0.f;
-                    l[i] += p0;
-                    l[i + 1] += p1;
-                    pk[j >> 1] = pack_bf16x2(p0, p1);
+                    const float p0 = exp2_approx(v[r][j]), p1 = exp2_approx(v[r][j + 1]);
+                    l[j] += p0;
+                    l[j + 1] += p1;
+                    st_shared_u32(sK + (uint32_t)x * kKBytes + 8u * kChunkBytes + sw128(srow + 8 * r, (hw >> 3) + (j >> 1)) +
+                                      4u * (lane & 3),
+                                  pack_bf16x2(p0, p1));
                 }
-                st_shared_v4(sP + sw128(key, (hs >> 3) + half), pk[0], pk[1], pk[2], pk[3]);
-            }
             fence_async_smem();
             before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(bar_p);
+                mbar_arrive(bar_p + 8 * x);
         }
+        // row sums over the keys
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+                l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+            if (lane < 4)
+                red[quad * kNH + head(j)] = l[j];
+        }
+        if (quad == 0)
+            smax[hw + lane] = fresh ? -INFINITY : smax[hw + lane] * 0.6931471805599453f;
+    }
 
-        // ---- epilogue: row sums across the 128 lanes, then the output's factors or the split's statistics
-        {
-            float v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                v[j] = l[j];
-            // halving exchange: after the step with distance d the lane keeps half of its heads, summed with the
-            // partner's; at the end lane i holds head 8 b4 + 4 b3 + 2 b2 + b1 of its number's bits
-#pragma unroll
-            for (int d = 16, n = 8; n > 0; d >>= 1, n >>= 1) {
-#pragma unroll
-                for (int k = 0; k < n; ++k) {
-                    const bool up = lane & d;
-                    const float give = up ? v[k] : v[k + n];
-                    const float keep = up ? v[k + n] : v[k];
-                    v[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
-                }
-            }
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-            if ((lane & 1) == 0)
-                red[quad * kNH + hs + (lane >> 1)] = v[0];
-            if (quad == 0 && lane < 16)
-                smax[hs + lane] = fresh ? -INFINITY : smax[hs + lane] * 0.6931471805599453f;
-        }
+    // ---- epilogue: the output's factors or the split's statistics, then the value tiles
+    const int hs = 16 * ((warp - 1) >> 2);   // workers: first of this warp's 16 heads
+    if (is_worker) {
         named_bar(1, kWorkers);
         if (wid < kNH) {
             const int h = wid;
@@ -584,20 +576,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             }
         }
         named_bar(1, kWorkers);
-        mbar_wait(bar_pv + 24, (uint32_t)((nblocks - 1) & 1), abort_flag, p.status);   // the last tile's product
+        mbar_wait(bar_pv + 32 * ((nblocks - 1) & 1) + 24, (uint32_t)((nblocks - 1) >> 1) & 1u, abort_flag, p.status);
         after_sync();
         if (p.splits == 1) {
 #pragma unroll 1
             for (int m = 0; m < 4; ++m) {
-                uint32_t x[16];
-                tmem_ld16(lane_base + kColO + 64 * m + hs, x);
+                uint32_t y[16];
+                tmem_ld16(lane_base + kColO + 64 * m + hs, y);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const int h = hs + j;
                     if (h < nhv) {
-                        const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(x[j]) * fin[h]);
-                        p.out[((int64_t)t * p.num_heads + h0 + h) * kLatent + 128 * m + dv0] =
+                        const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(y[j]) * fin[h]);
+                        p.out[((int64_t)t * p.num_heads + h0 + h) * kLatent + kDvTile * m + dv0] =
                             *reinterpret_cast<const uint16_t *>(&o);
                     }
                 }
@@ -618,15 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             for (int m = 0; m < 4; ++m) {
                 if (hs >= nhv)   // nhv is a multiple of 16: whole warps skip
                     break;
-                uint32_t x[16];
-                tmem_ld16(lane_base + kColO + 64 * m + hs, x);
+                uint32_t y[16];
+                tmem_ld16(lane_base + kColO + 64 * m + hs, y);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const int h = hs + j;
                     const int r = r0 + (h >= (r0 + 1) * hp) + (h >= (r0 + 2) * hp);
-                    const uint32_t off = (uint32_t)(((split * hp + h - r * hp) * kLatent + 128 * m + dv0) * 4);
-                    st_cluster_f32(map_to_rank(sK + off, (uint32_t)r), __uint_as_float(x[j]));
+                    const uint32_t off = (uint32_t)(((split * hp + h - r * hp) * kLatent + kDvTile * m + dv0) * 4);
+                    st_cluster_f32(map_to_rank(sK + off, (uint32_t)r), __uint_as_float(y[j]));
                 }
             }
         }

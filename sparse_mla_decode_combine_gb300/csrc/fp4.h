@@ -41,18 +41,33 @@ struct Insert4Params {
 };
 cudaError_t launch_qk_norm_rope_kv_insert_fp4(const Insert4Params &p, cudaStream_t stream);
 
-struct Decode4Params {
-    const uint16_t *q;
-    int64_t q_token_stride;
-    const uint8_t *kv;
-    int32_t num_blocks;
-    int32_t page;
+struct Lists4Params {
+    const int32_t *topk;
+    int64_t topk_stride;
+    int32_t topk_width;
+    const int32_t *topk_lens;
+    const int32_t *seq_lens;
+    int32_t num_tokens;
+    int32_t window;
     const int32_t *block_table;
     int64_t bt_stride;
     int32_t max_blocks;
     int32_t num_reqs;
     const int32_t *req_idx;
-    const int32_t *lists;      // combined lists [T, list_w] (positions) and their lengths
+    int32_t num_blocks;
+    int32_t page;
+    int32_t *slots;            // [T, list_w]
+    int32_t *lens;             // [T]
+    int32_t list_w;            // topk_width + window
+    unsigned *status;
+};
+cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream);
+
+struct Decode4Params {
+    const uint16_t *q;
+    int64_t q_token_stride;
+    const uint8_t *kv;
+    const int32_t *slots;      // [T, list_w] cache slots (-1: no key), and how many each token has
     const int32_t *lens;
     int32_t list_w;
     int32_t num_tokens;
