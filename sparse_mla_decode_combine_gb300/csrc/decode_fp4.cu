@@ -23,8 +23,8 @@
 //     relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.  The
 //     usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
 //
-// CTA = 18 warps for one (token, 64-head group, split): lane 0 of warp 0 issues S^T, lane 0 of warp 17 P.V,
-// warps 1-16 do the rest: dequant, softmax, epilogue.  16 or 32 heads run as a 64-head group whose missing
+// CTA = 26 warps for one (token, 64-head group, split): warp 0 issues S^T, warp 25 P.V, warps 1-8 do the softmax,
+// warps 9-24 the dequant and the epilogue.  16 or 32 heads run as a 64-head group whose missing
 // heads have zero queries (their columns are computed and dropped).  The splits of a unit form a cluster and
 // merge through distributed shared memory.  Every mbarrier wait is bounded.
 //
@@ -44,11 +44,12 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 576;            // warp 0: S^T issue; 1-8: softmax; 9-16: dequant; 17: P.V issue
-constexpr int kPvWarp = 17;
-constexpr int kWorkers = 512;            // softmax and dequant: Q's layout, the epilogue
-constexpr int kSoftmaxWarps = 8;
-constexpr int kDequantWarps = 8;
+constexpr int kSoftmaxWarps = 8;         // warps 1-8 (warp 0 issues S^T)
+constexpr int kDequantWarp0 = 9;
+constexpr int kDequantWarps = 16;        // warps 9-24: also Q's layout and the epilogue
+constexpr int kPvWarp = 25;              // issues P.V
+constexpr int kThreads = 832;
+constexpr int kWorkers = 32 * kDequantWarps;
 constexpr int kBK = 64;                  // keys per block = MMA M of the logits
 constexpr int kDvTile = 128;             // value dims per tile = MMA M of P.V
 constexpr int kNH = 64;                  // heads per CTA = MMA N
@@ -189,8 +190,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     const int t = unit / p.groups;
     const int h0 = unit % p.groups * kNH;
     const int nhv = min(kNH, p.num_heads - h0);   // heads of the group that exist
-    const bool is_worker = warp >= 1 && warp <= 16;
-    const int wid = tid - 32;                     // worker index 0..511
+    const bool is_worker = warp >= kDequantWarp0 && warp < kDequantWarp0 + kDequantWarps;
+    const int ww = warp - kDequantWarp0;
+    const int wid = tid - 32 * kDequantWarp0;     // worker index 0..511
 
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;   // the swizzled tiles start on 1024-byte boundaries
@@ -240,28 +242,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         }
     }
 
-    // Dequant: four threads to a row, each with a 16-byte piece of codes (32 dims) in every value tile, two of rope, and
-    // the scale bytes.  Lanes 8 q .. 8 q + 7 of a warp take quarter q of eight rows whose numbers differ mod 8 (no bank
-    // conflicts in the swizzled stores) and spread over the tile, so that a short block keeps every warp at work.
-    const bool is_dequant = warp >= 9 && warp <= 16;
-    const int qtr = lane >> 3;
-    const int rrow = 8 * (((warp - 9) - (lane & 7)) & 7) + (lane & 7);
+    // Dequant: eight threads to a row, each with two 16-byte pieces of codes (32 dims each), one of rope and two scale
+    // bytes.  Lanes 8 i .. 8 i + 7 of a warp take one eighth of eight rows whose numbers differ mod 8 (no bank conflicts
+    // in the swizzled stores) and spread over the tile, so that a short block keeps every warp at work.
+    const int eighth = 4 * (ww & 1) + (lane >> 3);
+    const int rrow = 8 * (((ww >> 1) - (lane & 7)) & 7) + (lane & 7);
     const int32_t *list = p.slots + (int64_t)t * p.list_w;
     const int kbeg = split * p.chunk;
-    uint4 pre[4], prope[2], psc;   // the entry of the block ahead
+    uint4 pre[2], prope;   // the entry of the block ahead
+    uint32_t psc[2];
     bool pre_ok = false;
-    auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld16(e + 64 * m + 16 * qtr); };
-    auto load_rope = [&](const uint8_t *e) {
-        prope[0] = ld16(e + kRope4Offset + 16 * qtr);
-        prope[1] = ld16(e + kRope4Offset + 64 + 16 * qtr);
+    auto load_piece = [&](const uint8_t *e, int m) {
+        pre[m] = ld16(e + 128 * m + 16 * eighth);
+        psc[m] = __ldg(e + kScale4Offset + 8 * m + eighth);
     };
-    auto load_scales = [&](const uint8_t *e) { psc = ld16(e + kScale4Offset); };
+    auto load_rope = [&](const uint8_t *e) { prope = ld16(e + kRope4Offset + 16 * eighth); };
     auto entry = [&](int slot) { return p.kv + (int64_t)(slot >= 0 ? slot : 0) * kEntry4Bytes; };
-    // L2 prefetch of a whole entry, by the lanes of its first quarter
-    auto prefetch = [&](int slot) {
-        if (qtr == 0 && slot >= 0)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(entry(slot)), "r"((uint32_t)kEntry4Bytes) : "memory");
-    };
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int kend = min(p.lens[t], kbeg + p.chunk);
@@ -272,24 +268,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         const int i = kbeg + b * kBK + rrow;
         return i < kend ? __ldg(list + i) : -1;
     };
-    int slot1 = -1, slot2 = -1, slot3 = -1;   // of the blocks ahead
-    if (is_dequant) {
+    int slot1 = -1, slot2 = -1;   // of the blocks ahead
+    if (is_worker) {
         const int slot0 = slot_of(0);
         slot1 = slot_of(1);
         slot2 = slot_of(2);
-        slot3 = slot_of(3);
         pre_ok = slot0 >= 0;
         if (pre_ok) {
-            load_scales(entry(slot0));
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                load_piece(entry(slot0), m);
+            load_piece(entry(slot0), 0);
+            load_piece(entry(slot0), 1);
             load_rope(entry(slot0));
         }
-        prefetch(slot1);
-        prefetch(slot2);
-    }
-    if (is_worker) {
         // Q -> swizzled K-major B operand, in the tile's order of dims
 #pragma unroll
         for (int j = 0; j < kQLoads; ++j) {
@@ -380,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 commit(leader, bar_pv + 32 * x + 8 * m);   // releases K chunks 2m, 2m+1 (m = 3: also P^T)
             }
         }
-    } else if (is_dequant) {
+    } else if (is_worker) {
         const uint32_t rb = (uint32_t)(rrow >> 3) * 1024u + (uint32_t)(rrow & 7) * 128u;
         const uint32_t x7 = (uint32_t)(rrow & 7);
         for (int b = 0; b < nblocks; ++b) {   // block b into its K tile (zeros for rows without a key)
@@ -389,13 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             const uint32_t tile = sK + (uint32_t)x * kKBytes + rb;
             const bool ok_next = slot1 >= 0;
             const uint8_t *en = entry(slot1);   // the next block's entry goes into the registers as they are used up
-            prefetch(slot3);
-            const uint32_t sc[4] = {psc.x, psc.y, psc.z, psc.w};
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {   // dims 128 m + 32 qtr ..
+            for (int m = 0; m < 2; ++m) {   // dims 256 m + 32 eighth ..
                 uint32_t o[16];
                 if (pre_ok) {
-                    dequant32(pre[m], (sc[m] >> (8 * qtr)) & 0xFFu, o);
+                    dequant32(pre[m], psc[m], o);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -404,36 +391,29 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 if (ok_next)
                     load_piece(en, m);
                 if (b >= 2)
-                    mbar_wait(bar_pv + 32 * x + 8 * m, ph, abort_flag, p.status);   // P.V of block b - 2 is done with them
-                if (m == 0 && qtr == 0)
+                    mbar_wait(bar_pv + 32 * x + 16 * m + 8, ph, abort_flag, p.status);   // P.V of block b - 2 is done with them
+                if (m == 0 && eighth == 0)
                     valid[x * kBK + rrow] = pre_ok;
-                const uint32_t cb = tile + (uint32_t)(2 * m + (qtr >> 1)) * kChunkBytes;
-                const uint32_t u = 4u * (uint32_t)(qtr & 1);
+                const uint32_t cb = tile + (uint32_t)(4 * m + (eighth >> 1)) * kChunkBytes;
+                const uint32_t u = 4u * (uint32_t)(eighth & 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     st_shared_v4(cb + (((u + i) ^ x7) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                if (m == 3) {   // the rope chunk, whose place P^T had
-                    const uint32_t cr = tile + 8u * kChunkBytes;
+                if (m == 1) {   // the rope chunk, whose place P^T had
                     if (!pre_ok)
-                        prope[0] = prope[1] = make_uint4(0u, 0u, 0u, 0u);
-                    st_shared_v4(cr + (((uint32_t)qtr ^ x7) << 4), prope[0].x, prope[0].y, prope[0].z, prope[0].w);
-                    st_shared_v4(cr + (((uint32_t)(qtr + 4) ^ x7) << 4), prope[1].x, prope[1].y, prope[1].z, prope[1].w);
+                        prope = make_uint4(0u, 0u, 0u, 0u);
+                    st_shared_v4(tile + 8u * kChunkBytes + (((uint32_t)eighth ^ x7) << 4), prope.x, prope.y, prope.z, prope.w);
                 }
-                if (m & 1) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar_grp + 16 * x + 4 * (m - 1));
-                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_grp + 16 * x + 8 * m);
             }
-            if (ok_next) {
+            if (ok_next)
                 load_rope(en);
-                load_scales(en);
-            }
             pre_ok = ok_next;
             slot1 = slot2;
-            slot2 = slot3;
-            slot3 = slot_of(b + 4);
+            slot2 = slot_of(b + 3);
         }
     } else {
         const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
@@ -556,11 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     }
 
     // ---- epilogue: the output's factors or the split's statistics, then the value tiles
-    const int hs = 16 * ((warp - 1) >> 2);   // workers: first of this warp's 16 heads
-    if (is_worker) {
-        named_bar(1, kWorkers);
-        if (wid < kNH) {
-            const int h = wid;
+    const int hs = 16 * (ww >> 2);   // workers: first of this warp's 16 heads
+    if (warp >= 1 && warp <= kSoftmaxWarps) {
+        named_bar(1, 32 * kSoftmaxWarps);
+        if (tid - 32 < kNH) {
+            const int h = tid - 32;
             const float lsum = (red[h] + red[kNH + h]) + (red[2 * kNH + h] + red[3 * kNH + h]);
             const float ms = smax[h];
             if (p.splits == 1) {
@@ -575,7 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 fin[h] = lsum;
             }
         }
-        named_bar(1, kWorkers);
+    }
+    if (warp >= 1 && warp < kPvWarp)
+        named_bar(4, 32 * (kSoftmaxWarps + kDequantWarps));
+    if (is_worker) {
         mbar_wait(bar_pv + 32 * ((nblocks - 1) & 1) + 24, (uint32_t)((nblocks - 1) >> 1) & 1u, abort_flag, p.status);
         after_sync();
         if (p.splits == 1) {
