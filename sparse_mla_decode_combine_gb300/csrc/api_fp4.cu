@@ -23,51 +23,38 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
     return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
-// ---- the decode's workspace (the tokens' slot lists and their lengths) and work decomposition
+// ---- the decode's workspace: the tokens' slot lists, their lengths, and the parts of split units
 struct Plan4 {
-    int list_w;
-    size_t off_lens, total;
+    int list_w, groups, grid, ctas_per_unit;
+    bool split;
+    size_t off_lens, off_joins, off_parts, total;
 };
 
-bool plan4(int num_tokens, int num_heads, int topk_width, int window, Plan4 *pl)
+bool plan4(int num_tokens, int num_heads, int topk_width, int window, int sms, Plan4 *pl)
 {
     if (num_tokens < 0 || topk_width < 0 || topk_width > kMaxTopkWidth || window < 0 || window > kMaxWindow)
         return false;
     if (num_heads != 16 && num_heads != 32 && num_heads != 64 && num_heads != 128)
         return false;
     pl->list_w = topk_width + window;
-    pl->off_lens = align_up(sizeof(int32_t) * (size_t)num_tokens * (size_t)pl->list_w, 256);
-    pl->total = std::max<size_t>(256, align_up(pl->off_lens + sizeof(int32_t) * (size_t)num_tokens, 256));
-    return true;
-}
-
-// How many CTAs share a unit's list, and how many entries each takes (multiples of 16): the split count
-// that minimises waves x time per CTA.  A 128-key block costs its products and softmax whatever its fill;
-// a CTA costs its start, and the exchange when the list is split.
-bool decompose(int num_tokens, int num_heads, int list_w, int *groups, int *splits, int *chunk)
-{
+    pl->groups = (num_heads + 63) / 64;
     const int tile = decode_fp4_block_keys();
-    *groups = (num_heads + 63) / 64;
-    *splits = 1;
-    *chunk = std::max(16, (int)align_up(list_w, 16));
-    const long long units = (long long)num_tokens * *groups;
-    double best = 1e300;
-    for (int s = 1; s <= decode_fp4_max_splits(); ++s) {
-        const int c = std::max(16, (int)align_up((list_w + s - 1) / s, 16));
-        const int used = std::max(1, (list_w + c - 1) / c);
-        const int resident = used == s ? decode_fp4_resident_ctas(s) : 0;
-        if (resident <= 0)
-            continue;
-        const long long waves = (units * s + resident - 1) / resident;
-        const int blocks = std::max(1, (c + tile - 1) / tile);
-        const double cost = (double)waves * (blocks + 0.25 * c / tile + 0.5 + (s > 1 ? 1.0 : 0.0));
-        if (cost < best - 1e-9) {
-            best = cost;
-            *splits = s;
-            *chunk = c;
-        }
-    }
-    return best < 1e300;
+    if ((long long)num_tokens * pl->groups * ((pl->list_w + tile - 1) / tile) > INT_MAX)
+        return false;
+    // Half as many units as multiprocessors or fewer: each unit is shared by as many CTAs as there are for it (two
+    // blocks or more to each).  Otherwise every multiprocessor's CTA takes an equal run of all blocks, which splits units
+    // at the runs' ends; with eight or more units to a CTA the runs end between units, which leaves at most an eighth of
+    // a CTA's work uneven and nothing to join.
+    const int units = num_tokens * pl->groups;
+    const int most = std::max(1, (pl->list_w + 2 * tile - 1) / (2 * tile));   // CTAs that a unit's list can use
+    pl->ctas_per_unit = units <= sms / 2 ? std::max(1, std::min(sms / std::max(1, units), most)) : 0;
+    pl->grid = pl->ctas_per_unit > 0 ? std::max(1, units * pl->ctas_per_unit) : sms;
+    pl->split = pl->ctas_per_unit > 0 ? pl->ctas_per_unit > 1 : most > 1 && units < 8ll * sms;
+    pl->off_lens = align_up(sizeof(int32_t) * (size_t)num_tokens * (size_t)pl->list_w, 256);
+    pl->off_joins = align_up(pl->off_lens + sizeof(int32_t) * (size_t)num_tokens, 256);
+    pl->off_parts = align_up(pl->off_joins + sizeof(int2) * (size_t)num_tokens * pl->groups, 256);
+    pl->total = std::max<size_t>(256, pl->off_parts + (pl->split ? 2 * decode_fp4_part_bytes() * (size_t)pl->grid : 0));
+    return true;
 }
 
 // ---- the page operators' workspace
@@ -124,8 +111,9 @@ size_t table_bytes(int rows, int64_t stride, int max_blocks)
 extern "C" DSV4_API size_t dsv4_sparse_mla_decode_fp4_workspace_size(int32_t num_tokens, int32_t num_heads,
                                                                      int32_t topk_width, int32_t window)
 {
+    int sms = 0;
     Plan4 pl;
-    return plan4(num_tokens, num_heads, topk_width, window, &pl) ? pl.total : 0;
+    return device_info(nullptr, &sms) == cudaSuccess && plan4(num_tokens, num_heads, topk_width, window, sms, &pl) ? pl.total : 0;
 }
 
 extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
@@ -160,12 +148,15 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
         return DSV4_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(workspace, 256))
         return DSV4_ERR_INVALID_ARG;
-    Plan4 pl;
-    if (!plan4(num_tokens, num_heads, topk_width, window, &pl) || workspace_bytes < pl.total)
-        return DSV4_ERR_INVALID_ARG;
     unsigned *status = nullptr;
-    if (device_info(&status, nullptr) != cudaSuccess)
+    int sms = 1;
+    Plan4 pl;
+    if (!plan4(num_tokens, num_heads, topk_width, window, sms, &pl) || workspace_bytes < pl.total)   // (on any device)
+        return DSV4_ERR_INVALID_ARG;
+    if (device_info(&status, &sms) != cudaSuccess)
         return DSV4_ERR_CUDA;
+    if (!plan4(num_tokens, num_heads, topk_width, window, sms, &pl) || workspace_bytes < pl.total)
+        return DSV4_ERR_INVALID_ARG;
     char *ws = static_cast<char *>(workspace);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     Lists4Params l{};
@@ -186,11 +177,18 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
     l.slots = reinterpret_cast<int32_t *>(ws);
     l.lens = reinterpret_cast<int32_t *>(ws + pl.off_lens);
     l.list_w = pl.list_w;
+    l.joins = reinterpret_cast<int2 *>(ws + pl.off_joins);
+    l.groups = pl.groups;
     l.status = status;
-    Decode4Params p{};
-    if (!decompose(num_tokens, num_heads, pl.list_w, &p.groups, &p.splits, &p.chunk) ||
-        launch_lists_fp4(l, cs) != cudaSuccess)
+    if (launch_lists_fp4(l, cs) != cudaSuccess)
         return DSV4_ERR_CUDA;
+    Decode4Params p{};
+    p.groups = pl.groups;
+    p.grid = pl.grid;
+    p.ctas_per_unit = pl.ctas_per_unit;
+    p.split = pl.split;
+    p.parts = reinterpret_cast<float *>(ws + pl.off_parts);
+    p.joins = l.joins;
     p.q = static_cast<const uint16_t *>(q);
     p.q_token_stride = q_token_stride;
     p.kv = static_cast<const uint8_t *>(kv_cache);

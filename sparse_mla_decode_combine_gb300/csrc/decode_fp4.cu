@@ -23,15 +23,19 @@
 //     relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.  The
 //     usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
 //
-// CTA = 26 warps for one (token, 64-head group, split): warp 0 issues S^T, warp 25 P.V, warps 1-8 do the softmax,
-// warps 9-24 the dequant and the epilogue.  16 or 32 heads run as a 64-head group whose missing
-// heads have zero queries (their columns are computed and dropped).  The splits of a unit form a cluster and
-// merge through distributed shared memory.  Every mbarrier wait is bounded.
+// Work.  A persistent CTA per multiprocessor takes an equal run of the blocks of all units (the end of one unit,
+// whole units, the start of another), so lists of any lengths fill the machine; with one unit per CTA, 256 equal
+// units on 152 multiprocessors take two full waves.  26 warps: warp 0 issues S^T, warp 25 P.V, warps 1-8 do the
+// softmax and the epilogue, warps 9-24 bring Q and the K tiles; the roles meet only at mbarriers, so the first blocks
+// of a unit are dequantised while the last one's output is still written.  The parts of a unit that several CTAs share
+// go to the workspace in fp32 and are joined by a kernel of their own.  16 or 32 heads run as a 64-head group
+// whose missing heads have zero queries (their columns are computed and dropped).  Every mbarrier wait is bounded.
 //
 // Order of the dims inside a tile.  The eight 4-bit codes of a 32-bit word become the pairs (e_k, e_{k+4}):
 // code k and code k + 4 lie 16 bits apart, so one shift puts both at their places in a BF16 pair (two masked
 // shifts: magnitude and sign).  Inside each group of eight latent dims the tile therefore holds e0 e4 e1 e5 e2
 // e6 e3 e7; Q is stored in the same order, and the epilogue writes each value dim to its own place.
+#include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -62,21 +66,25 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;            // S^T: 64 columns for each of the two K tiles
 constexpr uint32_t kColO = 128;          // O^T: 4 tiles x 64 columns
 constexpr float kExceedLog2 = 40.f;
-constexpr int kMaxSplits = 8;            // portable cluster size
+constexpr int kJoinHeads = 4;            // heads per CTA of the joining kernel, a warp each
+constexpr int kJoinThreads = 32 * kJoinHeads;
+constexpr int kMinBlocks = 2;            // per CTA: below that, joining costs more than the blocks
 
 // small shared region (after Q and the two K tiles)
 constexpr int kOffRed = 0;               // float [4][64]: per-quadrant head maxima, or row sums at the end
 constexpr int kOffMax = 1024;            // float [64]: reference maximum per head (log2 units; natural ones at the end)
 constexpr int kOffFin = 1280;            // float [64]: the factor of a rescale; at the end the output's, or a split's row sum
 constexpr int kOffValid = 1536;          // uint8 [2][64]: rows of a K tile that hold a key
-constexpr int kOffBars = 1664;           // u64: bar_s[2], bar_p[2], bar_grp[2][2], bar_pv[2][4]
-constexpr int kOffTmem = 1792;           // u32
-constexpr int kOffAbort = 1796;          // int
-constexpr int kSmallBytes = 1856;
+constexpr int kOffBars = 1664;           // u64: bar_s[2], bar_p[2], bar_grp[2][2], bar_pv[2][4], bar_q, bar_o
+constexpr int kOffTmem = 1808;           // u32
+constexpr int kOffAbort = 1812;          // int
+constexpr int kOffStart = 1816;          // int [8]: the unit at the run's start, its first block and the next unit's; at its end
+constexpr int kOffScan = 1848;           // int [26]
+constexpr int kSmallBytes = 1984;
 constexpr int kSmemBytes = kQBytes + 2 * kKBytes + kSmallBytes + 1024;   // + alignment slack
 constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                     // 9 16-byte Q pieces per worker
 static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
-static_assert(2 * kKBytes >= (kNH + kMaxSplits) * kLatent * (int)sizeof(float), "the partials fit the K tiles");
+constexpr int kPartFloats = kNH * kLatent + 2 * kNH;   // a part in the workspace: O [64][512], then (m, l) [64]
 
 // instruction descriptors (kind::f16): D f32, A/B bf16, N = 64
 constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kNH >> 3) << 17);
@@ -88,96 +96,81 @@ constexpr uint32_t kIdescPV = kIdescBase | ((uint32_t)(kDvTile >> 4) << 24) | (1
 // against loads that do not allocate there).
 __device__ __forceinline__ uint4 ld16(const void *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
 
-// 32 E2M1 codes times 2^(se - 127) -> 16 BF16 pairs, exactly.
+// 32 E2M1 codes times 2^(se - 127) -> 32 BF16 values, exactly, into the four 16-byte units u .. u + 3 (xored with x)
+// of the row at shared address rb.
 // A code's exponent and mantissa bits at the low end of the BF16 exponent are its value times 2^-126 (both
 // formats put the binary point the same way, subnormals included); one multiply by 2^(se - 1) gives the value.
 // Scales past 2 (se > 128, whose factor has no BF16 form) take a second multiply, 255 (NaN) among them.
-__device__ __forceinline__ void dequant32(const uint4 &v, uint32_t se, uint32_t (&o)[16])
+__device__ __forceinline__ void dequant32_store(const uint4 &v, uint32_t se, uint32_t rb, uint32_t u, uint32_t x)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t f = (min(se, 128u) + 126u) << 7;
     f |= f << 16;
+    uint32_t g = se == 255u ? 0x7FC0u : (se - 1u) << 7;   // 2^(se - 128), where se > 128
+    g |= g << 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t u = w[i] >> 8;
-        o[4 * i + 0] = ((w[i] << 6) & 0x01C001C0u) | ((w[i] << 12) & 0x80008000u);
-        o[4 * i + 1] = ((w[i] << 2) & 0x01C001C0u) | ((w[i] << 8) & 0x80008000u);
-        o[4 * i + 2] = ((u << 6) & 0x01C001C0u) | ((w[i] << 4) & 0x80008000u);
-        o[4 * i + 3] = ((u << 2) & 0x01C001C0u) | (w[i] & 0x80008000u);
-    }
+        const uint32_t h = w[i] >> 8;
+        uint32_t o[4] = {((w[i] << 6) & 0x01C001C0u) | ((w[i] << 12) & 0x80008000u),
+                         ((w[i] << 2) & 0x01C001C0u) | ((w[i] << 8) & 0x80008000u),
+                         ((h << 6) & 0x01C001C0u) | ((w[i] << 4) & 0x80008000u),
+                         ((h << 2) & 0x01C001C0u) | (w[i] & 0x80008000u)};
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        o[i] = mul_bf16x2(o[i], f);
-    if (se > 128u) {
-        uint32_t g = se == 255u ? 0x7FC0u : (se - 1u) << 7;   // 2^(se - 128)
-        g |= g << 16;
+        for (int k = 0; k < 4; ++k)
+            o[k] = mul_bf16x2(o[k], f);
+        if (se > 128u) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            o[i] = mul_bf16x2(o[i], g);
+            for (int k = 0; k < 4; ++k)
+                o[k] = mul_bf16x2(o[k], g);
+        }
+        st_shared_v4(rb + (((u + i) ^ x) << 4), o[0], o[1], o[2], o[3]);
     }
 }
 
-// Split merge inside a cluster of S CTAs (one per split of a token's keys).  The CTA of rank r owns heads
-// [r*hp, (r+1)*hp), hp = ceil(64 / S).  Every split s has pushed, into each owner's shared memory, its reference
-// maximum m_s (natural-log units, -inf for a split without keys) and row sum l_s for the owner's heads
-// (stat[s][hl] = (m_s, l_s)) and its unnormalised fp32 O_s (recv[s][hl][512]).  The owner forms
-//   m = max(max_s m_s, sink), Z = sum_s l_s e^{m_s - m} + e^{sink - m},
-//   out = sum_s e^{m_s - m} O_s / Z  (BF16),  lse = m + ln Z.
-__device__ __noinline__ void merge_splits(uint16_t *out, float *lse, const float *sink, int num_heads, int S, int t,
-                                          int h0, int rank, const float *recv, const float *stat, float *wts)
+// The work of this CTA.  A unit is a (token, 64-head group), in the order of groups and then tokens (CTAs that take the
+// groups of one token then run at about the same time and find its entries in L2); blocks are counted over all units.
+// Every role of the CTA walks the same blocks.
+struct Walk {
+    int w, w1;        // blocks [w, w1) are still to do
+    int t, h0;        // token and first head of the unit of block w
+    int start;        // that unit's first block
+};
+
+struct Segment {
+    int t, h0;
+    int kb, nb;       // blocks kb .. kb + nb - 1 of the unit
+    int len;          // the unit's keys
+};
+
+__device__ __forceinline__ int blocks_of(int len) { return (len + kBK - 1) / kBK; }
+
+__device__ __forceinline__ bool next_segment(Walk &k, const Decode4Params &p, Segment &s)
 {
-    const int hp = (kNH + S - 1) / S;
-    const int hb = rank * hp;
-    const int nh = max(0, min(min(kNH, num_heads - h0), hb + hp) - hb);   // owned heads that exist
-    const int tid = threadIdx.x;
-    if (tid < nh) {
-        float mk = -INFINITY;
-        for (int s = 0; s < S; ++s)
-            mk = fmaxf(mk, stat[2 * (s * hp + tid)]);
-        const float sk = sink != nullptr ? sink[h0 + hb + tid] : -INFINITY;
-        const float m = fmaxf(mk, sk);
-        float z = sk == -INFINITY ? 0.f : expf(sk - m);
-        for (int s = 0; s < S; ++s) {
-            const float ms = stat[2 * (s * hp + tid)];
-            const float w = ms == -INFINITY ? 0.f : expf(ms - m);
-            wts[tid * 10 + s] = w;
-            z += ms == -INFINITY ? 0.f : stat[2 * (s * hp + tid) + 1] * w;
+    if (k.w >= k.w1)
+        return false;
+    int blocks;
+    while (true) {   // (units without keys have no block)
+        s.len = __ldcg(p.lens + k.t);
+        blocks = blocks_of(s.len);
+        if (k.start + blocks > k.w)
+            break;
+        k.start += blocks;
+        if (++k.t == p.num_tokens) {
+            k.t = 0;
+            k.h0 += kNH;
         }
-        const float f = mk == -INFINITY ? 0.f : 1.f / z;
-        for (int s = 0; s < S; ++s)
-            wts[tid * 10 + s] *= f;
-        wts[tid * 10 + 8] = m == -INFINITY ? -INFINITY : m + logf(z);
     }
-    __syncthreads();
-    const int items = nh * (kLatent / 4);   // 16-byte pieces of the slice
-    for (int i = tid; i < items; i += kThreads) {
-        const int hl = i / (kLatent / 4);
-        const int c = i % (kLatent / 4);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < S; ++s) {
-            const float ws = wts[hl * 10 + s];
-            if (ws != 0.f) {   // (a split without keys has sent nothing)
-                const float4 v = *reinterpret_cast<const float4 *>(recv + ((size_t)(s * hp + hl)) * kLatent + 4 * c);
-                acc.x = fmaf(ws, v.x, acc.x);
-                acc.y = fmaf(ws, v.y, acc.y);
-                acc.z = fmaf(ws, v.z, acc.z);
-                acc.w = fmaf(ws, v.w, acc.w);
-            }
-        }
-        const int64_t row = (int64_t)t * num_heads + h0 + hb + hl;
-        *reinterpret_cast<uint2 *>(out + row * kLatent + 4 * c) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-        if (c == 0 && lse != nullptr)
-            lse[row] = wts[hl * 10 + 8];
-    }
+    s.t = k.t;
+    s.h0 = k.h0;
+    s.kb = k.w - k.start;
+    s.nb = min(blocks - s.kb, k.w1 - k.w);
+    k.w += s.nb;
+    return true;
 }
 
-// Sends the (m, l) pair of head h (0..63) of split `split` to the head's owner in the cluster.
-__device__ __forceinline__ void push_stat(uint32_t stat_s, int S, int split, int h, float m, float l)
-{
-    const int hp = (kNH + S - 1) / S;
-    const int r = h / hp;
-    st_cluster_v2(map_to_rank(stat_s + (uint32_t)(2 * (split * hp + (h - r * hp))) * 4u, (uint32_t)r), m, l);
-}
+// first block of CTA c's run, and the CTA whose run holds block w (G runs over all W blocks)
+__device__ __forceinline__ int run_start(int c, int W, int G) { return (int)((long long)c * W / G); }
+__device__ __forceinline__ int run_of(int w, int W, int G) { return (int)(((long long)(w + 1) * G - 1) / W); }
 
 __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Params p)
 {
@@ -185,14 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
     const int lane = tid & 31;
-    const int split = blockIdx.x % p.splits;   // = rank in the cluster when splits > 1
-    const int unit = blockIdx.x / p.splits;
-    const int t = unit / p.groups;
-    const int h0 = unit % p.groups * kNH;
-    const int nhv = min(kNH, p.num_heads - h0);   // heads of the group that exist
     const bool is_worker = warp >= kDequantWarp0 && warp < kDequantWarp0 + kDequantWarps;
-    const int ww = warp - kDequantWarp0;
-    const int wid = tid - 32 * kDequantWarp0;     // worker index 0..511
 
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;   // the swizzled tiles start on 1024-byte boundaries
@@ -208,10 +194,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     const uint32_t bar_p = bar_s + 16;                   // [tile] P^T written (softmax warps)
     const uint32_t bar_grp = bar_s + 32;                 // [tile][2] column chunks 0-3, then 4-8 written (dequant warps)
     const uint32_t bar_pv = bar_s + 64;                  // [tile][4] P.V of value tile m complete
+    const uint32_t bar_q = bar_s + 128;                  // Q of the segment written (dequant warps)
+    const uint32_t bar_o = bar_s + 136;                  // O^T of the segment read (softmax warps)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(small + kOffAbort);
+    int *first = reinterpret_cast<int *>(small + kOffStart);
+    int *scan = reinterpret_cast<int *>(small + kOffScan);
 
-    // ---- set-up that does not read the lists
+    // ---- set-up that reads no list
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar_s + 8 * i, 1);
@@ -221,389 +211,465 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             mbar_init(bar_grp + 8 * i, kDequantWarps);
         for (int i = 0; i < 8; ++i)
             mbar_init(bar_pv + 8 * i, 1);
+        mbar_init(bar_q, kDequantWarps);
+        mbar_init(bar_o, kSoftmaxWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
-    if (tid < kNH)
-        smax[tid] = 0.f;
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    // Q into registers.  Only the lists come from the previous kernel, which began after everything before it in the
-    // stream had ended: whatever else the call reads is there already.
-    uint4 qv[kQLoads];
-    if (is_worker) {
-#pragma unroll
-        for (int j = 0; j < kQLoads; ++j) {
-            const int i = wid + kWorkers * j;
-            const int h = i / (kDim / 8), c = i % (kDim / 8);
-            qv[j] = make_uint4(0u, 0u, 0u, 0u);   // (zeros for heads that do not exist)
-            if (h < nhv)
-                qv[j] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride + (int64_t)(h0 + h) * kDim + 8 * c));
-        }
+    // Only the lists come from the previous kernel, which began after everything before it in the stream had ended:
+    // the queries are there already, and start towards L2.
+    if (p.ctas_per_unit > 0 && tid == 0) {
+        const int unit = blockIdx.x / p.ctas_per_unit, h0 = unit / p.num_tokens * kNH;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + unit % p.num_tokens * p.q_token_stride + h0 * kDim),
+                     "r"((uint32_t)(min(kNH, p.num_heads - h0) * kDim * 2))
+                     : "memory");
     }
-
-    // Dequant: eight threads to a row, each with two 16-byte pieces of codes (32 dims each), one of rope and two scale
-    // bytes.  Lanes 8 i .. 8 i + 7 of a warp take one eighth of eight rows whose numbers differ mod 8 (no bank conflicts
-    // in the swizzled stores) and spread over the tile, so that a short block keeps every warp at work.
-    const int eighth = 4 * (ww & 1) + (lane >> 3);
-    const int rrow = 8 * (((ww >> 1) - (lane & 7)) & 7) + (lane & 7);
-    const int32_t *list = p.slots + (int64_t)t * p.list_w;
-    const int kbeg = split * p.chunk;
-    uint4 pre[2], prope;   // the entry of the block ahead
-    uint32_t psc[2];
-    bool pre_ok = false;
-    auto load_piece = [&](const uint8_t *e, int m) {
-        pre[m] = ld16(e + 128 * m + 16 * eighth);
-        psc[m] = __ldg(e + kScale4Offset + 8 * m + eighth);
-    };
-    auto load_rope = [&](const uint8_t *e) { prope = ld16(e + kRope4Offset + 16 * eighth); };
-    auto entry = [&](int slot) { return p.kv + (int64_t)(slot >= 0 ? slot : 0) * kEntry4Bytes; };
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int kend = min(p.lens[t], kbeg + p.chunk);
-    const int nkeys = max(0, kend - kbeg);
-    const int nblocks = (nkeys + kBK - 1) / kBK;
-    // the cache slot of this thread's row in block b; -1 past the list's end
-    auto slot_of = [&](int b) {
-        const int i = kbeg + b * kBK + rrow;
-        return i < kend ? __ldg(list + i) : -1;
-    };
-    int slot1 = -1, slot2 = -1;   // of the blocks ahead
-    if (is_worker) {
-        const int slot0 = slot_of(0);
-        slot1 = slot_of(1);
-        slot2 = slot_of(2);
-        pre_ok = slot0 >= 0;
-        if (pre_ok) {
-            load_piece(entry(slot0), 0);
-            load_piece(entry(slot0), 1);
-            load_rope(entry(slot0));
-        }
-        // Q -> swizzled K-major B operand, in the tile's order of dims
+
+    // ---- this CTA's blocks
+    Walk walk;
+    int W = 0, G = 1, w0 = 0;
+    if (p.ctas_per_unit > 0) {   // an equal share of one unit
+        const int unit = blockIdx.x / p.ctas_per_unit, s = blockIdx.x % p.ctas_per_unit;
+        walk.t = unit % p.num_tokens;
+        walk.h0 = unit / p.num_tokens * kNH;
+        walk.start = 0;
+        W = blocks_of(__ldcg(p.lens + walk.t));
+        G = max(1, min(p.ctas_per_unit, (W + kMinBlocks - 1) / kMinBlocks));
+        walk.w = s < G ? run_start(s, W, G) : W;
+        walk.w1 = s < G ? run_start(s + 1, W, G) : W;
+        before_sync();
+    } else {                     // an equal run of the blocks of all units
+        const int per = (p.num_tokens + kThreads - 1) / kThreads;
+        const int t0 = min(p.num_tokens, tid * per), t1 = min(p.num_tokens, t0 + per);
+        int mine = 0;
+        for (int t = t0; t < t1; ++t)
+            mine += blocks_of(__ldcg(p.lens + t));
+        int incl = mine;
 #pragma unroll
-        for (int j = 0; j < kQLoads; ++j) {
-            const int i = wid + kWorkers * j;
-            const int h = i / (kDim / 8), c = i % (kDim / 8);
-            const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
-            if (c < kLatent / 8)
-                st_shared_v4(a, __byte_perm(qv[j].x, qv[j].z, 0x5410), __byte_perm(qv[j].x, qv[j].z, 0x7632),
-                             __byte_perm(qv[j].y, qv[j].w, 0x5410), __byte_perm(qv[j].y, qv[j].w, 0x7632));
-            else
-                st_shared_v4(a, qv[j].x, qv[j].y, qv[j].z, qv[j].w);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d)
+                incl += y;
         }
+        if (lane == 31)
+            scan[warp] = incl;
+        __syncthreads();
+        int excl = incl - mine, all = 0;   // of one group
+        for (int i = 0; i < kThreads / 32; ++i) {
+            excl += i < warp ? scan[i] : 0;
+            all += scan[i];
+        }
+        W = all * p.groups;
+        G = max(1, min((int)gridDim.x, (W + kMinBlocks - 1) / kMinBlocks));
+        walk.w = blockIdx.x < G ? run_start(blockIdx.x, W, G) : W;
+        walk.w1 = blockIdx.x < G ? run_start(blockIdx.x + 1, W, G) : W;
+        // the unit that holds block w: token, group, first block, and the next unit's
+        auto find = [&](int w, int *out) {
+            const int r = all > 0 ? w % all : 0;
+            if (w < W && mine > 0 && excl <= r && r < excl + mine) {
+                int at = excl, t = t0, n;
+                while (at + (n = blocks_of(__ldcg(p.lens + t))) <= r) {
+                    at += n;
+                    ++t;
+                }
+                out[0] = t;
+                out[1] = w / all * kNH;
+                out[2] = w - r + at;
+                out[3] = out[2] + n;
+            }
+        };
+        find(walk.w, first);
+        if (!p.split)
+            find(walk.w1, first + 4);
+        before_sync();
+        __syncthreads();
+        walk.t = first[0];
+        walk.h0 = first[1];
+        walk.start = first[2];
+        if (!p.split) {   // a run begins and ends at the next start of a unit
+            if (walk.w < W && walk.w > first[2])
+                walk.w = first[3];
+            if (walk.w1 < W)
+                walk.w1 = walk.w1 > first[6] ? first[7] : first[6];
+        }
+        w0 = walk.w;
     }
-    fence_async_smem();
-    before_sync();
-    __syncthreads();   // Q, barriers, TMEM address
+    // tokens without a key: zero output, the lse from the sink alone
+    for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
+        if (__ldcg(p.lens + t) > 0)
+            continue;
+        for (int i = tid; i < p.num_heads * kLatent / 8; i += kThreads)
+            *reinterpret_cast<uint4 *>(p.out + (int64_t)t * p.num_heads * kLatent + 8 * i) = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr && tid < p.num_heads)
+            p.lse[(int64_t)t * p.num_heads + tid] = p.sink != nullptr ? p.sink[tid] : -INFINITY;
+    }
+    __syncthreads();   // barriers, TMEM address
     after_sync();
     const uint32_t tmem = *tmem_slot;
 
-    if (nblocks == 0) {   // no key in this split
-        if (warp == 0)
-            tmem_free(tmem, kTmemCols);
-        if (p.splits == 1) {   // zero output, the lse from the sink alone
-            if (tid < nhv && p.lse != nullptr)
-                p.lse[(int64_t)t * p.num_heads + h0 + tid] = p.sink != nullptr ? p.sink[h0 + tid] : -INFINITY;
-            for (int i = tid; i < nhv * kLatent / 8; i += kThreads)
-                *reinterpret_cast<uint4 *>(p.out + ((int64_t)t * p.num_heads + h0) * kLatent + 8 * i) = make_uint4(0, 0, 0, 0);
-            return;
-        }
-        cluster_sync();   // every split is past its products: partials may land
-        if (tid < kNH)
-            push_stat(smem_u32(gbase), p.splits, split, tid, -INFINITY, 0.f);
-        cluster_sync();   // every partial has landed
-        merge_splits(p.out, p.lse, p.sink, p.num_heads, p.splits, t, h0, split,
-                     reinterpret_cast<const float *>(gbase + kQBytes), reinterpret_cast<const float *>(gbase),
-                     reinterpret_cast<float *>(gbase + 2048));
-        return;
-    }
-
     const int quad = warp & 3;                            // TMEM lane quadrant of this warp
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-    const int vrow = quad * 32 + lane;                    // this lane's row of a value tile,
-    const int dv0 = (vrow & ~7) | ((vrow >> 1) & 3) | ((vrow & 1) << 2);   // and its value dim (the tile's order of dims)
+    Segment seg;
 
     if (warp == 0) {
         // descriptors: K-major operands advance 32 B per 16 dims and one column chunk per 64
         const uint32_t leader = elect_one();
         const uint64_t qk_a = sdesc(sK, 16, 1024);
         const uint64_t qk_b = sdesc(sQ, 16, 1024);
-        for (int b = 0; b < nblocks; ++b) {
-            const int x = b & 1;
-            const uint32_t ph = (uint32_t)(b >> 1) & 1u;
-            const uint64_t ax = qk_a + (uint64_t)((x * kKBytes) >> 4);
+        uint32_t g = 0;   // blocks since the kernel began: tile g & 1, phase g >> 1
+        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
+            mbar_wait(bar_q, n & 1u, abort_flag, p.status);
+            for (int b = 0; b < seg.nb; ++b, ++g) {
+                const uint32_t x = g & 1u, ph = (g >> 1) & 1u;
+                const uint64_t ax = qk_a + (uint64_t)((x * kKBytes) >> 4);
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                if (c == 0 || c == 4) {
-                    mbar_wait(bar_grp + 16 * x + 2 * c, ph, abort_flag, p.status);
-                    after_sync();
+                for (int c = 0; c < kChunks; ++c) {
+                    if (c == 0 || c == 4) {
+                        mbar_wait(bar_grp + 16 * x + 2 * c, ph, abort_flag, p.status);
+                        after_sync();
+                    }
+                    const uint64_t a = ax + (uint64_t)((c * kChunkBytes) >> 4);
+                    const uint64_t bq = qk_b + (uint64_t)((c * kQChunkBytes) >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16(leader, tmem + kColS + 64 * x, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdescQK,
+                                 (c != 0 || k != 0) ? 1u : 0u);
                 }
-                const uint64_t a = ax + (uint64_t)((c * kChunkBytes) >> 4);
-                const uint64_t bq = qk_b + (uint64_t)((c * kQChunkBytes) >> 4);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16(leader, tmem + kColS + 64 * x, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdescQK,
-                             (c != 0 || k != 0) ? 1u : 0u);
+                commit(leader, bar_s + 8 * x);
             }
-            commit(leader, bar_s + 8 * x);
         }
     } else if (warp == kPvWarp) {
         // MN-major operands advance 2 KB per 16 keys
         const uint32_t leader = elect_one();
         const uint64_t pv_a = sdesc(sK, kChunkBytes, 1024);
         const uint64_t pv_b = sdesc(sK + 8 * kChunkBytes, 1024, 1024);
-        for (int b = 0; b < nblocks; ++b) {
-            const int x = b & 1;
-            mbar_wait(bar_p + 8 * x, (uint32_t)(b >> 1) & 1u, abort_flag, p.status);
-            after_sync();
-            const uint64_t off = (uint64_t)((x * kKBytes) >> 4);
-            const int left = nkeys - b * kBK;   // 16-key steps without a key are left out
+        uint32_t g = 0;
+        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
+            if (n > 0) {
+                mbar_wait(bar_o, (n - 1) & 1u, abort_flag, p.status);   // the last segment's O^T has been read
+                after_sync();
+            }
+            for (int b = 0; b < seg.nb; ++b, ++g) {
+                const uint32_t x = g & 1u;
+                mbar_wait(bar_p + 8 * x, (g >> 1) & 1u, abort_flag, p.status);
+                after_sync();
+                const uint64_t off = (uint64_t)((x * kKBytes) >> 4);
+                const int left = seg.len - (seg.kb + b) * kBK;   // 16-key steps without a key are left out
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const uint64_t a = pv_a + off + (uint64_t)((2 * m * kChunkBytes) >> 4);
+                for (int m = 0; m < 4; ++m) {
+                    const uint64_t a = pv_a + off + (uint64_t)((2 * m * kChunkBytes) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kBK / 16; ++kk)
-                    if (16 * kk < left)
-                        mma_bf16(leader, tmem + kColO + 64 * m, a + (uint64_t)(kk * 128), pv_b + off + (uint64_t)(kk * 128),
-                                 kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
-                commit(leader, bar_pv + 32 * x + 8 * m);   // releases K chunks 2m, 2m+1 (m = 3: also P^T)
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        if (16 * kk < left)
+                            mma_bf16(leader, tmem + kColO + 64 * m, a + (uint64_t)(kk * 128), pv_b + off + (uint64_t)(kk * 128),
+                                     kIdescPV, (b > 0 || kk > 0) ? 1u : 0u);
+                    commit(leader, bar_pv + 32 * x + 8 * m);   // releases K chunks 2m, 2m+1 (m = 3: also P^T)
+                }
             }
         }
     } else if (is_worker) {
+        // ---- Q's layout, and the dequant: eight threads to a row, each with two 16-byte pieces of codes (32 dims each),
+        // one of rope and two scale bytes.  A warp takes four rows whose numbers differ mod 4: eight lanes that store
+        // together (four rows, an even and an odd piece) meet eight different bank groups, and a load covers 128
+        // contiguous bytes of a row (against eight rows of 64 bytes: 4 % of the kernel's time).  The rows spread over the
+        // tile, so that a short block keeps every warp at work.
+        const int ww = warp - kDequantWarp0;
+        const int wid = 32 * ww + lane;
+        const int piece = 2 * (lane >> 3) + ((lane >> 2) & 1), runit = 4 * ((lane >> 2) & 1) + (lane >> 3);
+        const int rrow = 8 * (((ww >> 1) - (lane & 3)) & 7) + 4 * (ww & 1) + (lane & 3);
         const uint32_t rb = (uint32_t)(rrow >> 3) * 1024u + (uint32_t)(rrow & 7) * 128u;
         const uint32_t x7 = (uint32_t)(rrow & 7);
-        for (int b = 0; b < nblocks; ++b) {   // block b into its K tile (zeros for rows without a key)
-            const int x = b & 1;
-            const uint32_t ph = (uint32_t)((b >> 1) - 1) & 1u;
-            const uint32_t tile = sK + (uint32_t)x * kKBytes + rb;
-            const bool ok_next = slot1 >= 0;
-            const uint8_t *en = entry(slot1);   // the next block's entry goes into the registers as they are used up
+        uint32_t g = 0;
+        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
+            const int t = seg.t, h0 = seg.h0;
+            const int nhv = min(kNH, p.num_heads - h0);   // heads of the group that exist
+            const int32_t *list = p.slots + (int64_t)t * p.list_w;
+            // Cache slots (-1 past the list's end): a lane holds that of its row (lane % 4) in block lane / 4 of eight, so
+            // that one load in eight blocks, and no wait for it among the entries' loads, feeds the warp.
+            auto load_slots = [&](int b8) {
+                const int b = b8 + (lane >> 2), i = (seg.kb + b) * kBK + rrow;
+                return b < seg.nb && i < seg.len ? __ldcg(list + i) : -1;
+            };
+            int slots = load_slots(0), slots_next = load_slots(8);
+            auto slot_of = [&](int b) { return __shfl_sync(0xffffffffu, slots, 4 * (b & 7) + (lane & 3)); };
+            auto entry = [&](int slot) { return p.kv + (int64_t)(slot >= 0 ? slot : 0) * kEntry4Bytes; };
+            uint4 pre[2], prope;   // the entry of the block ahead
+            uint32_t psc[2];
+            auto load_piece = [&](const uint8_t *e, int m) {
+                pre[m] = ld16(e + 128 * m + 16 * piece);
+                psc[m] = __ldg(e + kScale4Offset + 8 * m + piece);
+            };
+            auto load_rope = [&](const uint8_t *e) { prope = ld16(e + kRope4Offset + 16 * runit); };
+            const int slot0 = slot_of(0);
+            // Q -> swizzled K-major B operand, in the tile's order of dims (zeros for heads that do not exist)
+            if (n > 0)   // S^T of the last segment's last block is done with its Q
+                mbar_wait(bar_s + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
+            const uint16_t *qt = p.q + (int64_t)t * p.q_token_stride + h0 * kDim;
+#pragma unroll 1
+            for (int j0 = 0; j0 < kQLoads; j0 += 3) {
+                uint4 qv[3];
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {   // dims 256 m + 32 eighth ..
-                uint32_t o[16];
-                if (pre_ok) {
-                    dequant32(pre[m], psc[m], o);
-                } else {
+                for (int j = 0; j < 3; ++j) {
+                    const int i = wid + kWorkers * (j0 + j);   // 16-byte piece i of the rows of 72
+                    qv[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (i < nhv * (kDim / 8))
+                        qv[j] = __ldg(reinterpret_cast<const uint4 *>(qt) + i);
+                }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[i] = 0u;
+                for (int j = 0; j < 3; ++j) {
+                    const int i = wid + kWorkers * (j0 + j);
+                    const int h = i / (kDim / 8), c = i % (kDim / 8);
+                    const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
+                    if (c < kLatent / 8)
+                        st_shared_v4(a, __byte_perm(qv[j].x, qv[j].z, 0x5410), __byte_perm(qv[j].x, qv[j].z, 0x7632),
+                                     __byte_perm(qv[j].y, qv[j].w, 0x5410), __byte_perm(qv[j].y, qv[j].w, 0x7632));
+                    else
+                        st_shared_v4(a, qv[j].x, qv[j].y, qv[j].z, qv[j].w);
+                }
+            }
+            bool pre_ok = slot0 >= 0;
+            if (pre_ok) {
+                load_piece(entry(slot0), 0);
+                load_piece(entry(slot0), 1);
+                load_rope(entry(slot0));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_q);
+
+            for (int b = 0; b < seg.nb; ++b, ++g) {   // a block into its K tile (zeros for rows without a key)
+                const uint32_t x = g & 1u, ph = ((g >> 1) - 1) & 1u;
+                const uint32_t tile = sK + x * kKBytes + rb;
+                if ((b & 7) == 7) {
+                    slots = slots_next;
+                    slots_next = load_slots(b + 9);
+                }
+                const int slot1 = slot_of(b + 1);
+                const bool ok_next = slot1 >= 0;
+                const uint8_t *en = entry(slot1);   // the next block's entry goes into the registers as they are used up
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {   // dims 256 m + 32 piece ..
+                    if (g >= 2)   // P.V of the block before the last is done with these chunks
+                        mbar_wait(bar_pv + 32 * x + 16 * m + 8, ph, abort_flag, p.status);
+                    if (m == 0 && piece == 0)
+                        valid[x * kBK + rrow] = pre_ok;
+                    const uint32_t cb = tile + (uint32_t)(4 * m + (piece >> 1)) * kChunkBytes;
+                    const uint32_t u = 4u * (uint32_t)(piece & 1);
+                    if (pre_ok) {
+                        dequant32_store(pre[m], psc[m], cb, u, x7);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            st_shared_v4(cb + (((u + i) ^ x7) << 4), 0u, 0u, 0u, 0u);
+                    }
+                    if (ok_next)
+                        load_piece(en, m);
+                    if (m == 1) {   // the rope chunk, whose place P^T had
+                        if (!pre_ok)
+                            prope = make_uint4(0u, 0u, 0u, 0u);
+                        st_shared_v4(tile + 8u * kChunkBytes + (((uint32_t)runit ^ x7) << 4), prope.x, prope.y, prope.z, prope.w);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar_grp + 16 * x + 8 * m);
                 }
                 if (ok_next)
-                    load_piece(en, m);
-                if (b >= 2)
-                    mbar_wait(bar_pv + 32 * x + 16 * m + 8, ph, abort_flag, p.status);   // P.V of block b - 2 is done with them
-                if (m == 0 && eighth == 0)
-                    valid[x * kBK + rrow] = pre_ok;
-                const uint32_t cb = tile + (uint32_t)(4 * m + (eighth >> 1)) * kChunkBytes;
-                const uint32_t u = 4u * (uint32_t)(eighth & 1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    st_shared_v4(cb + (((u + i) ^ x7) << 4), o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                if (m == 1) {   // the rope chunk, whose place P^T had
-                    if (!pre_ok)
-                        prope = make_uint4(0u, 0u, 0u, 0u);
-                    st_shared_v4(tile + 8u * kChunkBytes + (((uint32_t)eighth ^ x7) << 4), prope.x, prope.y, prope.z, prope.w);
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_grp + 16 * x + 8 * m);
+                    load_rope(en);
+                pre_ok = ok_next;
             }
-            if (ok_next)
-                load_rope(en);
-            pre_ok = ok_next;
-            slot1 = slot2;
-            slot2 = slot_of(b + 3);
         }
     } else {
+        // ---- softmax and epilogue
+        constexpr int kAll = 32 * kSoftmaxWarps;
+        const int wid = tid - 32;
         const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
         const int hw = 32 * ((warp - 1) >> 2);            // first of this warp's 32 heads; its 16 keys are the quadrant's
         const int slice_bar = 2 + ((warp - 1) >> 2);      // the four warps of these heads
+        const int vrow = quad * 32 + lane;                // this lane's row of a value tile,
+        const int dv0 = (vrow & ~7) | ((vrow >> 1) & 3) | ((vrow & 1) << 2);   // and its value dim (the tile's order of dims)
         // this lane's keys are srow and srow + 8; its heads, j = 0..7:
         const int srow = 16 * quad + (lane >> 2);
         const int sh = hw + 2 * (lane & 3);
         auto head = [&](int j) { return sh + 16 * (j >> 2) + 8 * ((j >> 1) & 1) + (j & 1); };
-        float l[8];                                       // row sums of those heads over this lane's keys
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            l[j] = 0.f;
-        bool fresh = true;                                // no key has been seen: the references are not set
-
-        for (int b = 0; b < nblocks; ++b) {
-            const int x = b & 1;
-            const uint32_t ph = (uint32_t)(b >> 1) & 1u;
-            mbar_wait(bar_grp + 16 * x, ph, abort_flag, p.status);   // (complete by then: the rows' flags are visible)
-            const bool kv[2] = {valid[x * kBK + srow] != 0, valid[x * kBK + srow + 8] != 0};   // (not past the list's end)
-            float ref[8];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float2 m = *reinterpret_cast<const float2 *>(smax + head(j));
-                ref[j] = m.x;
-                ref[j + 1] = m.y;
-            }
-            mbar_wait(bar_s + 8 * x, ph, abort_flag, p.status);
-            after_sync();
-            uint32_t s[2][8];
-            tmem_ld_16x16(lane_base + kColS + 64 * x + hw, s[0]);
-            tmem_ld_16x16(lane_base + kColS + 64 * x + hw + 16, s[1]);
-            tmem_ld_wait();
-            // logits in log2 units above the heads' references: v[r][j] of key row r, head j
-            float v[2][8];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[r][j] = kv[r] ? fmaf(__uint_as_float(s[j >> 2][4 * ((j >> 1) & 1) + 2 * r + (j & 1)]), c2, -ref[j]) : -INFINITY;
-            float top = -INFINITY;
+        uint32_t g = 0;
+        while (next_segment(walk, p, seg)) {
+            const int t = seg.t, h0 = seg.h0;
+            const int nhv = min(kNH, p.num_heads - h0);
+            if (quad == 0)
+                smax[hw + lane] = 0.f;
+            named_bar(slice_bar, 128);
+            float l[8];                                       // row sums of those heads over this lane's keys
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                top = fmaxf(top, fmaxf(v[0][j], v[1][j]));
-            if (named_bar_or(slice_bar, 128, (fresh && (kv[0] || kv[1])) || top > kExceedLog2)) {
-                // the block's maxima, by the four warps of these heads, become the references where they are larger
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float mx = fmaxf(v[0][j], v[1][j]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1)
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    if (lane < 4)
-                        red[quad * kNH + head(j)] = mx;
-                }
-                named_bar(slice_bar, 128);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int h = head(j);
-                    const float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
-                    const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);   // (-inf: every logit is NaN)
-                    const float fall = fresh ? 1.f : exp2_approx(-up);
-                    l[j] *= fall;
-                    v[0][j] -= up;
-                    v[1][j] -= up;
-                    if (quad == 0 && lane < 4) {
-                        smax[h] += up;
-                        fin[h] = fall;
-                    }
-                }
-                named_bar(slice_bar, 128);   // the references and factors are written, and red is free again
-                if (!fresh) {
-                    // (b > 0: no key was seen before otherwise) P.V of block b - 1 has to be complete
-                    mbar_wait(bar_pv + 32 * (x ^ 1) + 24, (uint32_t)((b - 1) >> 1) & 1u, abort_flag, p.status);
-                    after_sync();
-#pragma unroll 1
-                    for (int m = 0; m < 8; ++m) {
-                        const int hc = hw + 16 * (m & 1);
-                        uint32_t y[16];
-                        tmem_ld16(lane_base + kColO + 64 * (m >> 1) + hc, y);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            y[j] = __float_as_uint(__uint_as_float(y[j]) * fin[hc + j]);
-                        tmem_st16(lane_base + kColO + 64 * (m >> 1) + hc, y);
-                    }
-                    tmem_st_wait();
-                }
-                fresh = false;
-            }
-            // P = 2^v -> BF16 P^T rows srow and srow + 8
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
+                l[j] = 0.f;
+            bool fresh = true;                                // no key has been seen: the references are not set
+
+            for (int b = 0; b < seg.nb; ++b, ++g) {
+                const uint32_t x = g & 1u, ph = (g >> 1) & 1u;
+                mbar_wait(bar_grp + 16 * x, ph, abort_flag, p.status);   // (complete by then: the rows' flags are visible)
+                const bool kv[2] = {valid[x * kBK + srow] != 0, valid[x * kBK + srow + 8] != 0};   // (not past the list's end)
+                float ref[8];
 #pragma unroll
                 for (int j = 0; j < 8; j += 2) {
-                    const float p0 = exp2_approx(v[r][j]), p1 = exp2_approx(v[r][j + 1]);
-                    l[j] += p0;
-                    l[j + 1] += p1;
-                    st_shared_u32(sK + (uint32_t)x * kKBytes + 8u * kChunkBytes + sw128(srow + 8 * r, (hw >> 3) + (j >> 1)) +
-                                      4u * (lane & 3),
-                                  pack_bf16x2(p0, p1));
+                    const float2 m = *reinterpret_cast<const float2 *>(smax + head(j));
+                    ref[j] = m.x;
+                    ref[j + 1] = m.y;
                 }
-            fence_async_smem();
+                mbar_wait(bar_s + 8 * x, ph, abort_flag, p.status);
+                after_sync();
+                uint32_t s[2][8];
+                tmem_ld_16x16(lane_base + kColS + 64 * x + hw, s[0]);
+                tmem_ld_16x16(lane_base + kColS + 64 * x + hw + 16, s[1]);
+                tmem_ld_wait();
+                // logits in log2 units above the heads' references: v[r][j] of key row r, head j
+                float v[2][8];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[r][j] = kv[r] ? fmaf(__uint_as_float(s[j >> 2][4 * ((j >> 1) & 1) + 2 * r + (j & 1)]), c2, -ref[j]) : -INFINITY;
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    top = fmaxf(top, fmaxf(v[0][j], v[1][j]));
+                if (named_bar_or(slice_bar, 128, (fresh && (kv[0] || kv[1])) || top > kExceedLog2)) {
+                    // the block's maxima, by the four warps of these heads, become the references where they are larger
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float mx = fmaxf(v[0][j], v[1][j]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        if (lane < 4)
+                            red[quad * kNH + head(j)] = mx;
+                    }
+                    named_bar(slice_bar, 128);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int h = head(j);
+                        const float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
+                        const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);   // (-inf: every logit is NaN)
+                        const float fall = fresh ? 1.f : exp2_approx(-up);
+                        l[j] *= fall;
+                        v[0][j] -= up;
+                        v[1][j] -= up;
+                        if (quad == 0 && lane < 4) {
+                            smax[h] += up;
+                            fin[h] = fall;
+                        }
+                    }
+                    named_bar(slice_bar, 128);   // the references and factors are written, and red is free again
+                    if (!fresh) {
+                        // (b > 0: no key was seen before otherwise) P.V of the block before has to be complete
+                        mbar_wait(bar_pv + 32 * (x ^ 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
+                        after_sync();
+#pragma unroll 1
+                        for (int m = 0; m < 8; ++m) {
+                            const int hc = hw + 16 * (m & 1);
+                            uint32_t y[16];
+                            tmem_ld16(lane_base + kColO + 64 * (m >> 1) + hc, y);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                y[j] = __float_as_uint(__uint_as_float(y[j]) * fin[hc + j]);
+                            tmem_st16(lane_base + kColO + 64 * (m >> 1) + hc, y);
+                        }
+                        tmem_st_wait();
+                    }
+                    fresh = false;
+                }
+                // P = 2^v -> BF16 P^T rows srow and srow + 8
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const float p0 = exp2_approx(v[r][j]), p1 = exp2_approx(v[r][j + 1]);
+                        l[j] += p0;
+                        l[j + 1] += p1;
+                        st_shared_u32(sK + x * kKBytes + 8u * kChunkBytes + sw128(srow + 8 * r, (hw >> 3) + (j >> 1)) + 4u * (lane & 3),
+                                      pack_bf16x2(p0, p1));
+                    }
+                fence_async_smem();
+                before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_p + 8 * x);
+            }
+
+            // ---- the segment's row sums and maxima (natural-log units, -inf for a segment without keys)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1)
+                    l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
+                if (lane < 4)
+                    red[quad * kNH + head(j)] = l[j];
+            }
+            if (quad == 0)
+                smax[hw + lane] = fresh ? -INFINITY : smax[hw + lane] * 0.6931471805599453f;
+            named_bar(1, kAll);
+            const bool whole = seg.nb == blocks_of(seg.len);
+            float *part = nullptr;   // this CTA's part of a split unit
+            if (!whole) {
+                const int slot = walk.start > w0 ? 1 : 0;   // (the unit begins in this run, or with it or before it)
+                part = p.parts + (size_t)(2 * blockIdx.x + slot) * kPartFloats;
+                if (seg.kb == 0 && wid == 0) {   // its first part says how many there are, and which
+                    const int n = p.ctas_per_unit > 0 ? G : run_of(walk.start + blocks_of(seg.len) - 1, W, G) - (int)blockIdx.x + 1;
+                    p.joins[h0 / kNH * p.num_tokens + t] = make_int2(2 * blockIdx.x + slot, n);
+                }
+            }
+            if (wid < kNH) {
+                const int h = wid;
+                const float lsum = (red[h] + red[kNH + h]) + (red[2 * kNH + h] + red[3 * kNH + h]);
+                const float ms = smax[h];
+                if (whole) {
+                    const float sk = p.sink != nullptr && h < nhv ? p.sink[h0 + h] : -INFINITY;
+                    const float M = fmaxf(ms, sk);
+                    const float e = ms == -INFINITY ? 0.f : expf(ms - M);
+                    const float Z = (ms == -INFINITY ? 0.f : lsum * e) + (sk == -INFINITY ? 0.f : expf(sk - M));
+                    fin[h] = ms == -INFINITY ? 0.f : e / Z;
+                    if (p.lse != nullptr && h < nhv)
+                        p.lse[(int64_t)t * p.num_heads + h0 + h] = M == -INFINITY ? -INFINITY : M + logf(Z);
+                } else {
+                    part[kNH * kLatent + 2 * h] = ms;
+                    part[kNH * kLatent + 2 * h + 1] = ms == -INFINITY ? 0.f : lsum;
+                }
+            }
+            named_bar(1, kAll);
+            mbar_wait(bar_pv + 32 * ((g - 1) & 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
+            after_sync();
+            // ---- O^T out of TMEM: the output, or the part (this warp: its quadrant of every value tile, 32 heads)
+#pragma unroll 1
+            for (int m = 0; m < 8; ++m) {
+                const int hc = hw + 16 * (m & 1), dv = kDvTile * (m >> 1) + dv0;
+                if (hc >= nhv)   // nhv is a multiple of 16
+                    continue;
+                uint32_t y[16];
+                tmem_ld16(lane_base + kColO + 64 * (m >> 1) + hc, y);
+                tmem_ld_wait();
+                if (whole) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(y[j]) * fin[hc + j]);
+                        p.out[((int64_t)t * p.num_heads + h0 + hc + j) * kLatent + dv] = *reinterpret_cast<const uint16_t *>(&o);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        __stcg(part + (hc + j) * kLatent + dv, __uint_as_float(y[j]));
+                }
+            }
             before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(bar_p + 8 * x);
-        }
-        // row sums over the keys
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1)
-                l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
-            if (lane < 4)
-                red[quad * kNH + head(j)] = l[j];
-        }
-        if (quad == 0)
-            smax[hw + lane] = fresh ? -INFINITY : smax[hw + lane] * 0.6931471805599453f;
-    }
-
-    // ---- epilogue: the output's factors or the split's statistics, then the value tiles
-    const int hs = 16 * (ww >> 2);   // workers: first of this warp's 16 heads
-    if (warp >= 1 && warp <= kSoftmaxWarps) {
-        named_bar(1, 32 * kSoftmaxWarps);
-        if (tid - 32 < kNH) {
-            const int h = tid - 32;
-            const float lsum = (red[h] + red[kNH + h]) + (red[2 * kNH + h] + red[3 * kNH + h]);
-            const float ms = smax[h];
-            if (p.splits == 1) {
-                const float sk = p.sink != nullptr && h < nhv ? p.sink[h0 + h] : -INFINITY;
-                const float M = fmaxf(ms, sk);
-                const float e = ms == -INFINITY ? 0.f : expf(ms - M);
-                const float Z = (ms == -INFINITY ? 0.f : lsum * e) + (sk == -INFINITY ? 0.f : expf(sk - M));
-                fin[h] = ms == -INFINITY ? 0.f : e / Z;
-                if (p.lse != nullptr && h < nhv)
-                    p.lse[(int64_t)t * p.num_heads + h0 + h] = M == -INFINITY ? -INFINITY : M + logf(Z);
-            } else {
-                fin[h] = lsum;
-            }
-        }
-    }
-    if (warp >= 1 && warp < kPvWarp)
-        named_bar(4, 32 * (kSoftmaxWarps + kDequantWarps));
-    if (is_worker) {
-        mbar_wait(bar_pv + 32 * ((nblocks - 1) & 1) + 24, (uint32_t)((nblocks - 1) >> 1) & 1u, abort_flag, p.status);
-        after_sync();
-        if (p.splits == 1) {
-#pragma unroll 1
-            for (int m = 0; m < 4; ++m) {
-                uint32_t y[16];
-                tmem_ld16(lane_base + kColO + 64 * m + hs, y);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int h = hs + j;
-                    if (h < nhv) {
-                        const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(y[j]) * fin[h]);
-                        p.out[((int64_t)t * p.num_heads + h0 + h) * kLatent + kDvTile * m + dv0] =
-                            *reinterpret_cast<const uint16_t *>(&o);
-                    }
-                }
-            }
-        }
-    }
-    if (p.splits > 1) {
-        // the split's partial goes from TMEM into the shared memory of each head's owner:
-        // recv[split][head - owner's first head][512] in the owner's K tile region
-        cluster_sync();   // every split is past its products: partials may land
-        if (is_worker) {
-            const int S = p.splits;
-            const int hp = (kNH + S - 1) / S;
-            if (wid < nhv)
-                push_stat(smem_u32(gbase), S, split, wid, smax[wid], fin[wid]);
-            const int r0 = hs / hp;   // this warp's 16 heads belong to owners r0, r0 + 1, r0 + 2 at most
-#pragma unroll 1
-            for (int m = 0; m < 4; ++m) {
-                if (hs >= nhv)   // nhv is a multiple of 16: whole warps skip
-                    break;
-                uint32_t y[16];
-                tmem_ld16(lane_base + kColO + 64 * m + hs, y);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int h = hs + j;
-                    const int r = r0 + (h >= (r0 + 1) * hp) + (h >= (r0 + 2) * hp);
-                    const uint32_t off = (uint32_t)(((split * hp + h - r * hp) * kLatent + kDvTile * m + dv0) * 4);
-                    st_cluster_f32(map_to_rank(sK + off, (uint32_t)r), __uint_as_float(y[j]));
-                }
-            }
+                mbar_arrive(bar_o);
+            named_bar(1, kAll);   // red, smax and fin are free again
         }
     }
     before_sync();
@@ -611,81 +677,96 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     after_sync();
     if (warp == 0)
         tmem_free(tmem, kTmemCols);
-    if (p.splits > 1) {
-        cluster_sync();   // every partial has landed
-        merge_splits(p.out, p.lse, p.sink, p.num_heads, p.splits, t, h0, split,
-                     reinterpret_cast<const float *>(gbase + kQBytes), reinterpret_cast<const float *>(gbase),
-                     reinterpret_cast<float *>(gbase + 2048));
+}
+
+// Joins the parts of the units that several CTAs shared, a warp to a head, in the order of the parts:
+//   m = max(max_c m_c, sink), Z = sum_c l_c e^{m_c - m} + e^{sink - m},
+//   out = sum_c e^{m_c - m} O_c / Z  (BF16),  lse = m + ln Z
+// The parts come from L2.  (Joined inside the decode, by the CTA of a unit that finished last, the 256 threads that are
+// free there hold too few bytes in flight: a unit took 25 us.)
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4Params p)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int unit = blockIdx.x;
+    const int2 join = __ldcg(p.joins + unit);   // (slot of the first part, parts); zeros for a unit of one part
+    if (join.y == 0)
+        return;
+    const int t = unit % p.num_tokens, h0 = unit / p.num_tokens * kNH;
+    const int h = kJoinHeads * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;   // head of the group
+    // the first part may be its CTA's second; the others are their CTAs' first
+    auto part_of = [&](int c) { return p.parts + (size_t)(c == 0 ? join.x : 2 * (join.x / 2 + c)) * kPartFloats; };
+    const float sk = p.sink != nullptr ? p.sink[h0 + h] : -INFINITY;
+    float mk = -INFINITY;
+    for (int c = lane; c < join.y; c += 32)
+        mk = fmaxf(mk, __ldcg(part_of(c) + kNH * kLatent + 2 * h));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, d));
+    const float M = fmaxf(mk, sk);
+    float Z = sk == -INFINITY ? 0.f : expf(sk - M);
+    float4 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int c = 0; c < join.y; ++c) {
+        const float *pc = part_of(c);
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pc + kNH * kLatent + 2 * h));
+        float4 o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = __ldcg(reinterpret_cast<const float4 *>(pc + h * kLatent + 128 * k + 4 * lane));
+        const float w = ml.x == -INFINITY ? 0.f : expf(ml.x - M);   // (-inf: a part without keys, whose O and l are zeros)
+        Z = fmaf(ml.y, w, Z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            acc[k].x = fmaf(w, o[k].x, acc[k].x);
+            acc[k].y = fmaf(w, o[k].y, acc[k].y);
+            acc[k].z = fmaf(w, o[k].z, acc[k].z);
+            acc[k].w = fmaf(w, o[k].w, acc[k].w);
+        }
     }
+    const float f = mk == -INFINITY ? 0.f : 1.f / Z;
+    const int64_t row = (int64_t)t * p.num_heads + h0 + h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint2 *>(p.out + row * kLatent + 128 * k + 4 * lane) =
+            make_uint2(pack_bf16x2(acc[k].x * f, acc[k].y * f), pack_bf16x2(acc[k].z * f, acc[k].w * f));
+    if (lane == 0 && p.lse != nullptr)
+        p.lse[row] = M == -INFINITY ? -INFINITY : M + logf(Z);
 }
 
 }  // namespace
 
 int decode_fp4_block_keys() { return kBK; }
-int decode_fp4_max_splits() { return kMaxSplits; }
-
-// Concurrently resident CTAs when launched in clusters of `splits` (whole clusters must fit inside one
-// GPC); cached per device.
-int decode_fp4_resident_ctas(int splits)
-{
-    static int cache[64][kMaxSplits + 1];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || splits < 1 || splits > kMaxSplits)
-        return 0;
-    if (cache[dev][splits] > 0)
-        return cache[dev][splits];
-    if (set_smem_once(reinterpret_cast<const void *>(decode_fp4_kernel), kSmemBytes, kAttrFp4) != cudaSuccess)
-        return 0;
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    if (splits > 1) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(splits * n);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmemBytes;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = splits;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, reinterpret_cast<const void *>(decode_fp4_kernel), &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        n = clusters * splits;
-    }
-    cache[dev][splits] = n;
-    return n;
-}
+size_t decode_fp4_part_bytes() { return sizeof(float) * (size_t)kPartFloats; }
 
 cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
 {
     if (p.num_tokens <= 0)
         return cudaSuccess;
-    if (p.groups != (p.num_heads + kNH - 1) / kNH || p.splits < 1 || p.splits > kMaxSplits || p.chunk < 1)
+    if (p.groups != (p.num_heads + kNH - 1) / kNH || p.grid < 1)
         return cudaErrorInvalidValue;
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp4_kernel), kSmemBytes, kAttrFp4);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.num_tokens * (unsigned)p.groups * (unsigned)p.splits);
+    cfg.gridDim = dim3((unsigned)p.grid);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.splits;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, decode_fp4_kernel, p);
+    cfg.numAttrs = 1;
+    cudaError_t r = cudaLaunchKernelEx(&cfg, decode_fp4_kernel, p);
+    if (r != cudaSuccess || !p.split)
+        return r;
+    cfg.gridDim = dim3((unsigned)p.num_tokens * (unsigned)p.groups, (unsigned)(std::min(p.num_heads, kNH) / kJoinHeads));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_parts_kernel, p);
 }
 
 }  // namespace dsv4

@@ -59,6 +59,8 @@ struct Lists4Params {
     int32_t *slots;            // [T, list_w]
     int32_t *lens;             // [T]
     int32_t list_w;            // topk_width + window
+    int2 *joins;               // [groups * T] set to zero
+    int32_t groups;
     unsigned *status;
 };
 cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream);
@@ -77,14 +79,16 @@ struct Decode4Params {
     uint16_t *out;             // BF16 [T, H, 512]
     float *lse;                // [T, H] or null
     int32_t groups;            // 64-head groups
-    int32_t splits;            // CTAs that share a unit's list: one thread-block cluster
-    int32_t chunk;             // list entries per split
+    int32_t grid;              // CTAs
+    int32_t ctas_per_unit;     // CTAs that share each unit; 0: every CTA takes an equal run of the blocks of all units
+    bool split;                // whether several CTAs may share a unit
+    float *parts;              // [2 * grid] partial results of units that several CTAs share
+    int2 *joins;               // [groups * T] such a unit's first part and their number, zeroed by the list kernel
     unsigned *status;
 };
 cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream);
 int decode_fp4_block_keys();
-int decode_fp4_max_splits();
-int decode_fp4_resident_ctas(int splits);
+size_t decode_fp4_part_bytes();
 
 // ---- page operators
 

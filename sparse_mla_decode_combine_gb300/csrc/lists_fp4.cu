@@ -47,6 +47,8 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
     extern __shared__ unsigned long long tab[];
     __shared__ int wsum[kPassLoads][kWarps];
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < p.groups)
+        p.joins[tid * gridDim.x + t] = make_int2(0, 0);
     const int seq_len = p.seq_lens[t];
     const int row = p.req_idx != nullptr ? p.req_idx[t] : t;
     int n = p.topk_width;

@@ -229,6 +229,8 @@ def test_same_call_twice_is_the_same():
 
 def test_refusals():
     need_gpu()
+    size = pkg.dsv4_sparse_mla_decode_fp4_workspace_size
+    assert size(0, 16, 0, 0) > 0 and size(4, 64, 512, 128) >= 4 * 4 * 640 and size(2, 64, 0, 8193) > 0
     w = to_fp4(small(1))
     d = synth.to_device(w, "cuda")
     ws = pkg.workspace_for_fp4(w.num_tokens, w.num_heads, w.topk_width, w.window)

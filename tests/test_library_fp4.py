@@ -33,7 +33,6 @@ def test_decode(lib):
                       (22, ctypes.c_void_p(16)), (4, 1 << 31 - 1)], BAD)
     each(call, good, [(15, 0)], OK)
     size = lib.dsv4_sparse_mla_decode_fp4_workspace_size
-    assert size(0, 16, 0, 0) > 0 and size(4, 64, 512, 128) >= 4 * 4 * 640
     assert size(1, 48, 4, 4) == 0 and size(1, 16, 8193, 4) == 0 and size(-1, 16, 4, 4) == 0 and size(1, 16, 4, -1) == 0
 
 
