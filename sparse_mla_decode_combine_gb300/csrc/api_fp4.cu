@@ -179,6 +179,10 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
     l.list_w = pl.list_w;
     l.joins = reinterpret_cast<int2 *>(ws + pl.off_joins);
     l.groups = pl.groups;
+    l.sink = sink;
+    l.num_heads = num_heads;
+    l.out = static_cast<uint16_t *>(out);
+    l.lse = lse;
     l.status = status;
     if (launch_lists_fp4(l, cs) != cudaSuccess)
         return DSV4_ERR_CUDA;

@@ -134,6 +134,7 @@ struct Walk {
     int w, w1;        // blocks [w, w1) are still to do
     int t, h0;        // token and first head of the unit of block w
     int start;        // that unit's first block
+    int len;          // its keys
 };
 
 struct Segment {
@@ -150,8 +151,7 @@ __device__ __forceinline__ bool next_segment(Walk &k, const Decode4Params &p, Se
         return false;
     int blocks;
     while (true) {   // (units without keys have no block)
-        s.len = __ldcg(p.lens + k.t);
-        blocks = blocks_of(s.len);
+        blocks = blocks_of(k.len);
         if (k.start + blocks > k.w)
             break;
         k.start += blocks;
@@ -159,7 +159,9 @@ __device__ __forceinline__ bool next_segment(Walk &k, const Decode4Params &p, Se
             k.t = 0;
             k.h0 += kNH;
         }
+        k.len = __ldcg(p.lens + k.t);
     }
+    s.len = k.len;
     s.t = k.t;
     s.h0 = k.h0;
     s.kb = k.w - k.start;
@@ -237,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         walk.t = unit % p.num_tokens;
         walk.h0 = unit / p.num_tokens * kNH;
         walk.start = 0;
-        W = blocks_of(__ldcg(p.lens + walk.t));
+        walk.len = __ldcg(p.lens + walk.t);
+        W = blocks_of(walk.len);
         G = max(1, min(p.ctas_per_unit, (W + kMinBlocks - 1) / kMinBlocks));
         walk.w = s < G ? run_start(s, W, G) : W;
         walk.w1 = s < G ? run_start(s + 1, W, G) : W;
@@ -290,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         walk.t = first[0];
         walk.h0 = first[1];
         walk.start = first[2];
+        walk.len = walk.w < walk.w1 ? __ldcg(p.lens + walk.t) : 0;
         if (!p.split) {   // a run begins and ends at the next start of a unit
             if (walk.w < W && walk.w > first[2])
                 walk.w = first[3];
@@ -298,19 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         }
         w0 = walk.w;
     }
-    // tokens without a key: zero output, the lse from the sink alone
-    for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-        if (__ldcg(p.lens + t) > 0)
-            continue;
-        for (int i = tid; i < p.num_heads * kLatent / 8; i += kThreads)
-            *reinterpret_cast<uint4 *>(p.out + (int64_t)t * p.num_heads * kLatent + 8 * i) = make_uint4(0, 0, 0, 0);
-        if (p.lse != nullptr && tid < p.num_heads)
-            p.lse[(int64_t)t * p.num_heads + tid] = p.sink != nullptr ? p.sink[tid] : -INFINITY;
-    }
     __syncthreads();   // barriers, TMEM address
     after_sync();
     const uint32_t tmem = *tmem_slot;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the joining kernel waits for this grid itself)
     const int quad = warp & 3;                            // TMEM lane quadrant of this warp
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     Segment seg;

@@ -61,6 +61,12 @@ struct Lists4Params {
     int32_t list_w;            // topk_width + window
     int2 *joins;               // [groups * T] set to zero
     int32_t groups;
+    // the outputs of tokens without a key
+    const float *sink;
+    int32_t num_heads;
+    uint16_t *out;
+    float *lse;
+    int32_t smem_bytes;        // (set by the launch)
     unsigned *status;
 };
 cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream);

@@ -6,12 +6,17 @@
 //   slots[t][0 .. L) = block_table[row][p / page] * page + p % page  (-1 for a page out of range, which is
 //   flagged),  lens[t] = L.   Entries from L on are not written.
 //
-// One CTA per token.  First occurrences come from a shared-memory hash set of 64-bit slots, (position << 32) |
-// smallest top-k index, at most half full: the first writer of a position claims its slot with one CAS, a
-// repeat lowers the index; each thread remembers the slots of its first entries.  Ballots over up to four
-// passes of the row give the output order.  The steps are dependent latencies (row, set, ballots, table, store);
-// a row's entries sit one per thread and pass, so every step is one round for rows of up to 2048 entries.
+// A token without a key gets its outputs here: zeros, and the sink (or -inf) as its lse.
+//
+// One CTA per token.  The steps are dependent latencies (row, set, block table, store), so each is one round for rows
+// of up to 2048 entries, four to a thread, and loads that do not depend on one another are issued together.
+// Repeats are looked for in a bitmap of the positions (one 32-bit shared-memory OR an entry).  Only a row that has one,
+// or positions past the bitmap, goes through a hash set of 64-bit slots, (position << 32) | smallest top-k index, at
+// most half full, which says which of the repeats comes first: its 64-bit compare-and-swaps alone took 7 us for 2048
+// entries.  Ballots over up to four passes of the row give the output order.
+#include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include "fp4.h"
 
@@ -47,8 +52,11 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
     extern __shared__ unsigned long long tab[];
     __shared__ int wsum[kPassLoads][kWarps];
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < p.groups)
-        p.joins[tid * gridDim.x + t] = make_int2(0, 0);
+    const int32_t *trow = p.topk + (int64_t)t * p.topk_stride;
+    int tv[kPassLoads];
+#pragma unroll
+    for (int u = 0; u < kPassLoads; ++u)
+        tv[u] = u * kThreads + tid < p.topk_width ? __ldg(trow + u * kThreads + tid) : -1;
     const int seq_len = p.seq_lens[t];
     const int row = p.req_idx != nullptr ? p.req_idx[t] : t;
     int n = p.topk_width;
@@ -56,19 +64,9 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
         n = p.topk_lens[t];
         n = n < 0 ? 0 : (n > p.topk_width ? p.topk_width : n);
     }
-    const int32_t *trow = p.topk + (int64_t)t * p.topk_stride;
+    if (tid < p.groups)
+        p.joins[tid * gridDim.x + t] = make_int2(0, 0);
     const int npass = (n + kThreads - 1) / kThreads;
-    int tv[kPassLoads];
-#pragma unroll
-    for (int u = 0; u < kPassLoads; ++u)
-        tv[u] = u * kThreads + tid < n ? __ldg(trow + u * kThreads + tid) : -1;
-    // the set of this row's size
-    int bits = 6;
-    while ((1 << bits) < 2 * n)
-        ++bits;
-    const int table = 1 << bits;
-    for (int i = tid; i < table; i += kThreads)
-        tab[i] = kEmpty;
     const bool row_ok = row >= 0 && row < p.num_reqs;
     const int32_t *bt_row = p.block_table + (int64_t)(row_ok ? row : 0) * p.bt_stride;
     // window [win_lo, pos]; the top-k survivors are the first occurrences of positions in [0, win_lo)
@@ -86,24 +84,54 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
         }
         return phys * p.page + (v - blk * p.page);
     };
-    __syncthreads();
-    unsigned hs[kPassLoads];
 #pragma unroll
-    for (int u = 0; u < kPassLoads; ++u)
-        hs[u] = tv[u] >= 0 && tv[u] < win_lo ? insert(tab, bits, tv[u], u * kThreads + tid) : 0u;
+    for (int u = 0; u < kPassLoads; ++u)   // entries that are not selectable: -1
+        tv[u] = u * kThreads + tid < n && tv[u] >= 0 && tv[u] < win_lo ? tv[u] : -1;
+
+    // ---- is any position listed twice?
+    unsigned *seen = reinterpret_cast<unsigned *>(tab);
+    bool hashed = win_lo > p.smem_bytes * 8;
+    if (!hashed) {
+        for (int i = tid; i < (win_lo + 31) / 32; i += kThreads)
+            seen[i] = 0u;
+        __syncthreads();
+        bool twice = false;
+#pragma unroll
+        for (int u = 0; u < kPassLoads; ++u)
+            if (tv[u] >= 0)
+                twice |= (atomicOr(&seen[tv[u] >> 5], 1u << (tv[u] & 31)) >> (tv[u] & 31)) & 1u;
 #pragma unroll 1
-    for (int ps = kPassLoads; ps < npass; ++ps) {
-        const int i = ps * kThreads + tid;
-        const int v = i < n ? __ldg(trow + i) : -1;
-        if (v >= 0 && v < win_lo)
-            insert(tab, bits, v, i);
+        for (int i = kPassLoads * kThreads + tid; i < n; i += kThreads) {
+            const int v = __ldg(trow + i);
+            if (v >= 0 && v < win_lo)
+                twice |= (atomicOr(&seen[v >> 5], 1u << (v & 31)) >> (v & 31)) & 1u;
+        }
+        hashed = __syncthreads_or(twice);
     }
     // the entries' slots do not depend on which of them are kept
     int sv[kPassLoads];
 #pragma unroll
     for (int u = 0; u < kPassLoads; ++u)
-        sv[u] = tv[u] >= 0 && tv[u] < win_lo ? slot_of(tv[u]) : -1;
-    __syncthreads();
+        sv[u] = tv[u] >= 0 ? slot_of(tv[u]) : -1;
+    int bits = 6;
+    while ((1 << bits) < 2 * n)
+        ++bits;
+    unsigned hs[kPassLoads];
+    if (hashed) {
+        for (int i = tid; i < 1 << bits; i += kThreads)
+            tab[i] = kEmpty;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kPassLoads; ++u)
+            hs[u] = tv[u] >= 0 ? insert(tab, bits, tv[u], u * kThreads + tid) : 0u;
+#pragma unroll 1
+        for (int i = kPassLoads * kThreads + tid; i < n; i += kThreads) {
+            const int v = __ldg(trow + i);
+            if (v >= 0 && v < win_lo)
+                insert(tab, bits, v, i);
+        }
+        __syncthreads();
+    }
     int total = 0;
 #pragma unroll 1
     for (int pg = 0; pg < npass; pg += kPassLoads) {
@@ -112,15 +140,16 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
 #pragma unroll
         for (int u = 0; u < kPassLoads; ++u) {
             const int i = (pg + u) * kThreads + tid;
-            const int v = pg == 0 ? tv[u] : (i < n ? __ldg(trow + i) : -1);
+            int v = pg == 0 ? tv[u] : (i < n ? __ldg(trow + i) : -1);
+            v = v < win_lo ? v : -1;
             vg[u] = v;
-            bool keep = false;
-            if (v >= 0 && v < win_lo) {
+            bool keep = v >= 0;
+            if (keep && hashed) {
                 unsigned h = hs[u];
                 if (pg != 0) {
                     h = hash_pos(v, bits);
                     while ((unsigned)(tab[h] >> 32) != (unsigned)v)
-                        h = (h + 1u) & (unsigned)(table - 1);
+                        h = (h + 1u) & ((1u << bits) - 1u);
                 }
                 keep = (unsigned)tab[h] == (unsigned)i;
             }
@@ -142,8 +171,15 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
     }
     for (int k = tid; k < swa; k += kThreads)
         out[total + k] = slot_of(win_lo + k);
+    const int len = total + swa;
     if (tid == 0)
-        p.lens[t] = total + swa;
+        p.lens[t] = len;
+    if (len == 0) {
+        for (int i = tid; i < p.num_heads * kLatent / 8; i += kThreads)
+            *reinterpret_cast<uint4 *>(p.out + (int64_t)t * p.num_heads * kLatent + 8 * i) = make_uint4(0, 0, 0, 0);
+        if (p.lse != nullptr && tid < p.num_heads)
+            p.lse[(int64_t)t * p.num_heads + tid] = p.sink != nullptr ? p.sink[tid] : -INFINITY;
+    }
 }
 
 }  // namespace
@@ -155,11 +191,12 @@ cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream)
     int bits = 6;
     while ((1 << bits) < 2 * p.topk_width)
         ++bits;
-    const int bytes = 8 << bits;
-    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(lists_fp4_kernel), bytes, kAttrFp4Lists);
+    Lists4Params q = p;
+    q.smem_bytes = std::max(8 << bits, 32768);   // the hash set; as a bitmap at least 262144 positions
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(lists_fp4_kernel), q.smem_bytes, kAttrFp4Lists);
     if (e != cudaSuccess)
         return e;
-    lists_fp4_kernel<<<p.num_tokens, kThreads, bytes, stream>>>(p);
+    lists_fp4_kernel<<<p.num_tokens, kThreads, q.smem_bytes, stream>>>(q);
     return cudaGetLastError();
 }
 
