@@ -371,35 +371,41 @@ def dsv4_sparse_mla_decode_mtp_union(q: torch.Tensor, kv_cache: torch.Tensor, bl
 # ----------------------------------------------------------------------------
 # the 4-bit cache and the page operators
 # ----------------------------------------------------------------------------
-def _on(dev: int, t: torch.Tensor, dtype, name: str, ndim: int) -> int:
-    """The pointer of a tensor that has to be on device `dev`, of this type and number of dims, with unit stride
-    along the last one."""
+def _on(dev: int, t: torch.Tensor, dtype, name: str) -> int:
+    """The pointer of a tensor that has to be on device `dev`, of this type, with unit stride along its last dim."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: must be on the current CUDA device")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim} dims, got {t.dim()}")
-    if ndim and t.stride(-1) != 1 and t.shape[-1] > 1:
+    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: last dim must be contiguous")
     return t.data_ptr()
 
 
+def _opt(dev: int, t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
+    return None if t is None else _on(dev, t, dtype, name)
+
+
+# the current stream's handle without a Stream object (most of a small call's host time, otherwise)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _device_and_stream(stream):
     """The current device's number, and the stream's handle (that device's current one for None)."""
+    dev = torch.cuda.current_device()
     if stream is None:
-        stream = torch.cuda.current_stream()
-        return stream.device_index, stream.cuda_stream
-    return torch.cuda.current_device(), stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
+    return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _row_stride(t: torch.Tensor, name: str, width: int) -> int:
+def _row_stride(t: torch.Tensor, name: str, rows: int, width: int) -> int:
     """The stride of dim 0 (of a single row: any that is wide enough); rows must not overlap."""
-    if t.shape[0] <= 1:
-        return max(t.stride(0), width)
-    if t.stride(0) < width:
-        raise ValueError(f"{name}: rows must not overlap")
-    return t.stride(0)
+    s = t.stride(0)
+    if s < width:
+        if rows > 1:
+            raise ValueError(f"{name}: rows must not overlap")
+        return width
+    return s
 
 
 def dsv4_sparse_mla_decode_fp4_workspace_size(num_tokens: int, num_heads: int, topk_width: int, window: int) -> int:
@@ -417,31 +423,30 @@ def dsv4_sparse_mla_decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, block_ta
     lib = _lib or load_library()
     dev, st = _device_and_stream(stream)
     T, H, D = q.shape
-    K = topk_idx.shape[1]
-    if D != 576 or q.stride(1) != 576 and H > 1:
+    blocks, page, entry = kv_cache.shape
+    R, M = block_table.shape
+    Tk, K = topk_idx.shape
+    if D != 576 or (H > 1 and q.stride(1) != 576):
         raise ValueError("q: heads must be contiguous rows of 576")
-    if kv_cache.shape[-1] != 400 or not kv_cache.is_contiguous():
+    if entry != 400 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache: must be contiguous, with entries of 400 bytes")
     if out.shape != (T, H, 512) or not out.is_contiguous():
         raise ValueError("out: must be contiguous [tokens, heads, 512]")
     if lse is not None and (lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse: must be contiguous [tokens, heads]")
-    if topk_idx.shape[0] != T or seq_lens.numel() != T or (topk_lens is not None and topk_lens.numel() != T) or \
-            (req_idx is not None and req_idx.numel() != T):
+    if Tk != T or seq_lens.shape != (T,) or (topk_lens is not None and topk_lens.shape != (T,)) or \
+            (req_idx is not None and req_idx.shape != (T,)):
         raise ValueError("topk_idx, topk_lens, seq_lens, req_idx: must have a row for each token")
-    if sink is not None and sink.numel() != H:
+    if sink is not None and sink.shape != (H,):
         raise ValueError("sink: must have a value for each head")
-    i32 = torch.int32
+    i32, bf16 = torch.int32, torch.bfloat16
     return lib.dsv4_sparse_mla_decode_fp4(
-        _on(dev, q, torch.bfloat16, "q", 3), _row_stride(q, "q", H * 576), _on(dev, kv_cache, torch.uint8, "kv_cache", 3),
-        kv_cache.shape[0], kv_cache.shape[1], _on(dev, block_table, i32, "block_table", 2),
-        _row_stride(block_table, "block_table", block_table.shape[1]), block_table.shape[1], block_table.shape[0],
-        None if req_idx is None else _on(dev, req_idx, i32, "req_idx", 1), _on(dev, topk_idx, i32, "topk_idx", 2) or None,
-        _row_stride(topk_idx, "topk_idx", K), K, None if topk_lens is None else _on(dev, topk_lens, i32, "topk_lens", 1),
-        _on(dev, seq_lens, i32, "seq_lens", 1), T, H, window,
-        None if sink is None else _on(dev, sink, torch.float32, "sink", 1), softmax_scale,
-        _on(dev, out, torch.bfloat16, "out", 3), None if lse is None else _on(dev, lse, torch.float32, "lse", 2),
-        _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(), st)
+        _on(dev, q, bf16, "q"), _row_stride(q, "q", T, H * 576), _on(dev, kv_cache, torch.uint8, "kv_cache"), blocks, page,
+        _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M), M, R,
+        _opt(dev, req_idx, i32, "req_idx"), _on(dev, topk_idx, i32, "topk_idx"), _row_stride(topk_idx, "topk_idx", T, K), K,
+        _opt(dev, topk_lens, i32, "topk_lens"), _on(dev, seq_lens, i32, "seq_lens"), T, H, int(window),
+        _opt(dev, sink, torch.float32, "sink"), float(softmax_scale), _on(dev, out, bf16, "out"),
+        _opt(dev, lse, torch.float32, "lse"), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), st)
 
 
 def dsv4_qk_norm_rope_kv_insert_fp4(q: torch.Tensor, q_out: torch.Tensor, kv: torch.Tensor, positions: torch.Tensor,
@@ -456,39 +461,37 @@ def dsv4_qk_norm_rope_kv_insert_fp4(q: torch.Tensor, q_out: torch.Tensor, kv: to
     dev, st = _device_and_stream(stream)
     T, H, D = q.shape
     bf16, i64, f32 = torch.bfloat16, torch.int64, torch.float32
-    if D != 576 or q_out.shape != q.shape or (H > 1 and (q.stride(1) != 576 or q_out.stride(1) != 576)):
+    if D != 576 or q_out.shape != (T, H, D) or (H > 1 and (q.stride(1) != 576 or q_out.stride(1) != 576)):
         raise ValueError("q, q_out: heads must be contiguous rows of 576, and the shapes the same")
     if kv.shape != (T, 576) or (k_out is not None and k_out.shape != (T, 576)):
         raise ValueError("kv, k_out: must be [tokens, 576]")
-    if positions.numel() != T or slot_mapping.numel() != T:
+    if positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("positions, slot_mapping: must have a value for each token")
-    if cos_sin_cache.shape[-1] != 64 or not cos_sin_cache.is_contiguous():
+    max_pos, width = cos_sin_cache.shape
+    if width != 64 or not cos_sin_cache.is_contiguous():
         raise ValueError("cos_sin_cache: must be contiguous [max_position, 64]")
     if kv_cache.shape[-1] != 400 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache: must be contiguous, with entries of 400 bytes")
-    if (q_norm_weight is not None and q_norm_weight.numel() != 576) or \
-            (kv_norm_weight is not None and kv_norm_weight.numel() != kv_norm_dims):
+    if (q_norm_weight is not None and q_norm_weight.shape != (576,)) or \
+            (kv_norm_weight is not None and kv_norm_weight.shape != (kv_norm_dims,)):
         raise ValueError("norm weights: must have a value for each normalised dim")
     return lib.dsv4_qk_norm_rope_kv_insert_fp4(
-        _on(dev, q, bf16, "q", 3), _row_stride(q, "q", H * 576), _on(dev, q_out, bf16, "q_out", 3),
-        _row_stride(q_out, "q_out", H * 576), T, H,
-        None if q_norm_weight is None else _on(dev, q_norm_weight, f32, "q_norm_weight", 1),
-        None if kv_norm_weight is None else _on(dev, kv_norm_weight, f32, "kv_norm_weight", 1), kv_norm_dims, eps,
-        _on(dev, kv, bf16, "kv", 2), _row_stride(kv, "kv", 576), _on(dev, positions, i64, "positions", 1),
-        _on(dev, slot_mapping, i64, "slot_mapping", 1), _on(dev, cos_sin_cache, f32, "cos_sin_cache", 2),
-        cos_sin_cache.shape[0], _on(dev, kv_cache, torch.uint8, "kv_cache", kv_cache.dim()), kv_cache.numel() // 400,
-        None if k_out is None else _on(dev, k_out, bf16, "k_out", 2),
-        0 if k_out is None else _row_stride(k_out, "k_out", 576), st)
+        _on(dev, q, bf16, "q"), _row_stride(q, "q", T, H * 576), _on(dev, q_out, bf16, "q_out"),
+        _row_stride(q_out, "q_out", T, H * 576), T, H, _opt(dev, q_norm_weight, f32, "q_norm_weight"),
+        _opt(dev, kv_norm_weight, f32, "kv_norm_weight"), int(kv_norm_dims), float(eps), _on(dev, kv, bf16, "kv"),
+        _row_stride(kv, "kv", T, 576), _on(dev, positions, i64, "positions"), _on(dev, slot_mapping, i64, "slot_mapping"),
+        _on(dev, cos_sin_cache, f32, "cos_sin_cache"), max_pos, _on(dev, kv_cache, torch.uint8, "kv_cache"),
+        kv_cache.numel() // 400, _opt(dev, k_out, bf16, "k_out"),
+        0 if k_out is None else _row_stride(k_out, "k_out", T, 576), st)
 
 
 def _pool(dev: int, cache: torch.Tensor, name: str):
     """(pointer, layers, layer stride, pages, page, entry bytes) of a pool uint8 [layers, pages, page, entry]."""
-    ptr = _on(dev, cache, torch.uint8, name, 4)
     L, B, page, entry = cache.shape
-    s = cache.stride()
-    if cache.numel() and (s[2] != entry and page > 1 or s[1] != page * entry and B > 1):
+    ls, bs, ps, _ = cache.stride()
+    if (ps != entry and page > 1 or bs != page * entry and B > 1) and cache.numel():
         raise ValueError(f"{name}: the pages of a layer must be contiguous")
-    return ptr, L, s[0], B, page, entry
+    return _on(dev, cache, torch.uint8, name), L, ls, B, page, entry
 
 
 def dsv4_cache_pages_workspace_size(num_rows: int, num_rows_out: int, num_blocks: int) -> int:
@@ -508,18 +511,18 @@ def dsv4_cache_fork_rows(cache: torch.Tensor, block_table: torch.Tensor, seq_len
     ptr, L, ls, B, page, entry = _pool(dev, cache, "cache")
     i32 = torch.int32
     R, M = block_table.shape
-    Ro = parent.numel()
-    if seq_lens.numel() != R or seq_lens_out.numel() != Ro or block_table_out.shape != (Ro, M):
+    (Ro,) = parent.shape
+    if seq_lens.shape != (R,) or seq_lens_out.shape != (Ro,) or block_table_out.shape != (Ro, M):
         raise ValueError("block_table_out, seq_lens, seq_lens_out: must have a row for each row, and max_blocks cells")
-    if ref_counts.numel() != B or ref_counts_out.numel() != B:
+    if ref_counts.shape != (B,) or ref_counts_out.shape != (B,):
         raise ValueError("ref_counts, ref_counts_out: must have a count for each page")
     return lib.dsv4_cache_fork_rows(
-        ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table", 2), _row_stride(block_table, "block_table", M),
-        _on(dev, seq_lens, i32, "seq_lens", 1), R, _on(dev, parent, i32, "parent", 1), Ro, M,
-        _on(dev, block_table_out, i32, "block_table_out", 2), _row_stride(block_table_out, "block_table_out", M),
-        _on(dev, seq_lens_out, i32, "seq_lens_out", 1), _on(dev, ref_counts, i32, "ref_counts", 1),
-        _on(dev, ref_counts_out, i32, "ref_counts_out", 1), 1 if share else 0,
-        _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(), st)
+        ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M),
+        _on(dev, seq_lens, i32, "seq_lens"), R, _on(dev, parent, i32, "parent"), Ro, M,
+        _on(dev, block_table_out, i32, "block_table_out"), _row_stride(block_table_out, "block_table_out", Ro, M),
+        _on(dev, seq_lens_out, i32, "seq_lens_out"), _on(dev, ref_counts, i32, "ref_counts"),
+        _on(dev, ref_counts_out, i32, "ref_counts_out"), 1 if share else 0,
+        _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), st)
 
 
 def dsv4_cache_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
@@ -534,16 +537,16 @@ def dsv4_cache_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens:
     ptr, L, ls, B, page, entry = _pool(dev, cache, "cache")
     i32 = torch.int32
     R, M = block_table.shape
-    if seq_lens.numel() != R or block_table_out.shape != (R, M):
+    if seq_lens.shape != (R,) or block_table_out.shape != (R, M):
         raise ValueError("seq_lens, block_table_out: must have a row for each row of block_table")
-    if ref_counts.numel() != B or ref_counts_out.numel() != B or page_map.numel() != B or num_live.numel() != 1:
+    if ref_counts.shape != (B,) or ref_counts_out.shape != (B,) or page_map.shape != (B,) or num_live.shape != (1,):
         raise ValueError("ref_counts, ref_counts_out, page_map: must have a value for each page, num_live one value")
     return lib.dsv4_cache_compact(
-        ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table", 2), _row_stride(block_table, "block_table", M),
-        _on(dev, seq_lens, i32, "seq_lens", 1), R, M, _on(dev, block_table_out, i32, "block_table_out", 2),
-        _row_stride(block_table_out, "block_table_out", M), _on(dev, ref_counts, i32, "ref_counts", 1),
-        _on(dev, ref_counts_out, i32, "ref_counts_out", 1), _on(dev, page_map, i32, "page_map", 1),
-        _on(dev, num_live, i32, "num_live", 1), _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(), st)
+        ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M),
+        _on(dev, seq_lens, i32, "seq_lens"), R, M, _on(dev, block_table_out, i32, "block_table_out"),
+        _row_stride(block_table_out, "block_table_out", R, M), _on(dev, ref_counts, i32, "ref_counts"),
+        _on(dev, ref_counts_out, i32, "ref_counts_out"), _on(dev, page_map, i32, "page_map"),
+        _on(dev, num_live, i32, "num_live"), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), st)
 
 
 def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_pages: torch.Tensor,
@@ -557,13 +560,13 @@ def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_
     sp, sL, sls, sB, spage, sentry = _pool(dev, src_cache, "src_cache")
     if (sL, spage, sentry) != (L, page, entry):
         raise ValueError("dst_cache, src_cache: must have the same layers, page and entry sizes")
-    n = src_pages.numel()
-    if dst_pages.numel() != n:
+    (n,) = src_pages.shape
+    if dst_pages.shape != (n,):
         raise ValueError("src_pages, dst_pages: must have the same length")
     i32 = torch.int32
     return lib.dsv4_cache_copy_pages(
-        dp, dls, dB, sp, sls, sB, L, page, entry, _on(dev, src_pages, i32, "src_pages", 1),
-        _on(dev, dst_pages, i32, "dst_pages", 1), n, _on(dev, workspace, torch.uint8, "workspace", 1), workspace.numel(),
+        dp, dls, dB, sp, sls, sB, L, page, entry, _on(dev, src_pages, i32, "src_pages"),
+        _on(dev, dst_pages, i32, "dst_pages"), n, _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(),
         st)
 
 

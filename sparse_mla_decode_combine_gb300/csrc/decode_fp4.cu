@@ -171,8 +171,41 @@ __device__ __forceinline__ bool next_segment(Walk &k, const Decode4Params &p, Se
 }
 
 // first block of CTA c's run, and the CTA whose run holds block w (G runs over all W blocks)
-__device__ __forceinline__ int run_start(int c, int W, int G) { return (int)((long long)c * W / G); }
+__device__ __forceinline__ int run_start(int c, int W, int G)   // floor(c W / G)
+{
+    const unsigned q = (unsigned)W / (unsigned)G, r = (unsigned)W % (unsigned)G;
+    return (int)(q * (unsigned)c + r * (unsigned)c / (unsigned)G);
+}
+
 __device__ __forceinline__ int run_of(int w, int W, int G) { return (int)(((long long)(w + 1) * G - 1) / W); }
+
+// The queries of 64 heads -> swizzled K-major B operand, in the tile's order of dims (zeros for heads that do not
+// exist), by worker wid of 512.
+__device__ __forceinline__ void store_q(const Decode4Params &p, int t, int h0, uint32_t sQ, int wid)
+{
+    const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride + h0 * kDim);
+    const int pieces = min(kNH, p.num_heads - h0) * (kDim / 8);
+#pragma unroll 1
+    for (int j0 = 0; j0 < kQLoads; j0 += 3) {
+        uint4 v[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const int i = wid + kWorkers * (j0 + j);
+            v[j] = i < pieces ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            const int i = wid + kWorkers * (j0 + j);
+            const int h = i / (kDim / 8), c = i % (kDim / 8);
+            const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
+            if (c < kLatent / 8)
+                st_shared_v4(a, __byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
+                             __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
+            else
+                st_shared_v4(a, v[j].x, v[j].y, v[j].z, v[j].w);
+        }
+    }
+}
 
 __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Params p)
 {
@@ -221,12 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     // Only the lists come from the previous kernel, which began after everything before it in the stream had ended:
-    // the queries are there already, and start towards L2.
-    if (p.ctas_per_unit > 0 && tid == 0) {
-        const int unit = blockIdx.x / p.ctas_per_unit, h0 = unit / p.num_tokens * kNH;
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + unit % p.num_tokens * p.q_token_stride + h0 * kDim),
-                     "r"((uint32_t)(min(kNH, p.num_heads - h0) * kDim * 2))
-                     : "memory");
+    // the queries are there already, and where the unit is known they are read while the lists are made.
+    if (p.ctas_per_unit > 0 && is_worker) {
+        const int unit = blockIdx.x / p.ctas_per_unit;
+        store_q(p, unit % p.num_tokens, unit / p.num_tokens * kNH, sQ, tid - 32 * kDequantWarp0);
     }
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -382,7 +413,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         uint32_t g = 0;
         for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
             const int t = seg.t, h0 = seg.h0;
-            const int nhv = min(kNH, p.num_heads - h0);   // heads of the group that exist
             const int32_t *list = p.slots + (int64_t)t * p.list_w;
             // Cache slots (-1 past the list's end): a lane holds that of its row (lane % 4) in block lane / 4 of eight, so
             // that one load in eight blocks, and no wait for it among the entries' loads, feeds the warp.
@@ -401,37 +431,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             };
             auto load_rope = [&](const uint8_t *e) { prope = ld16(e + kRope4Offset + 16 * runit); };
             const int slot0 = slot_of(0);
-            // Q -> swizzled K-major B operand, in the tile's order of dims (zeros for heads that do not exist)
-            if (n > 0)   // S^T of the last segment's last block is done with its Q
-                mbar_wait(bar_s + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
-            const uint16_t *qt = p.q + (int64_t)t * p.q_token_stride + h0 * kDim;
-#pragma unroll 1
-            for (int j0 = 0; j0 < kQLoads; j0 += 3) {
-                uint4 qv[3];
-#pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    const int i = wid + kWorkers * (j0 + j);   // 16-byte piece i of the rows of 72
-                    qv[j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (i < nhv * (kDim / 8))
-                        qv[j] = __ldg(reinterpret_cast<const uint4 *>(qt) + i);
-                }
-#pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    const int i = wid + kWorkers * (j0 + j);
-                    const int h = i / (kDim / 8), c = i % (kDim / 8);
-                    const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
-                    if (c < kLatent / 8)
-                        st_shared_v4(a, __byte_perm(qv[j].x, qv[j].z, 0x5410), __byte_perm(qv[j].x, qv[j].z, 0x7632),
-                                     __byte_perm(qv[j].y, qv[j].w, 0x5410), __byte_perm(qv[j].y, qv[j].w, 0x7632));
-                    else
-                        st_shared_v4(a, qv[j].x, qv[j].y, qv[j].z, qv[j].w);
-                }
-            }
             bool pre_ok = slot0 >= 0;
             if (pre_ok) {
                 load_piece(entry(slot0), 0);
                 load_piece(entry(slot0), 1);
                 load_rope(entry(slot0));
+            }
+            if (n > 0 || p.ctas_per_unit == 0) {
+                if (n > 0)   // S^T of the last segment's last block is done with its Q
+                    mbar_wait(bar_s + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
+                store_q(p, t, h0, sQ, wid);
             }
             fence_async_smem();
             __syncwarp();
@@ -642,23 +651,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             after_sync();
             // ---- O^T out of TMEM: the output, or the part (this warp: its quadrant of every value tile, 32 heads)
 #pragma unroll 1
-            for (int m = 0; m < 8; ++m) {
-                const int hc = hw + 16 * (m & 1), dv = kDvTile * (m >> 1) + dv0;
-                if (hc >= nhv)   // nhv is a multiple of 16
-                    continue;
-                uint32_t y[16];
-                tmem_ld16(lane_base + kColO + 64 * (m >> 1) + hc, y);
+            for (int m = 0; m < 4; ++m) {
+                const int dv = kDvTile * m + dv0;
+                if (hw >= nhv)   // nhv is a multiple of 16
+                    break;
+                uint32_t y[2][16];
+                tmem_ld16(lane_base + kColO + 64 * m + hw, y[0]);
+                tmem_ld16(lane_base + kColO + 64 * m + hw + 16, y[1]);
                 tmem_ld_wait();
-                if (whole) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(y[j]) * fin[hc + j]);
-                        p.out[((int64_t)t * p.num_heads + h0 + hc + j) * kLatent + dv] = *reinterpret_cast<const uint16_t *>(&o);
+                for (int i = 0; i < 2; ++i) {
+                    const int hc = hw + 16 * i;
+                    if (hc >= nhv)
+                        break;
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(y[i][j]) * fin[hc + j]);
+                            p.out[((int64_t)t * p.num_heads + h0 + hc + j) * kLatent + dv] = *reinterpret_cast<const uint16_t *>(&o);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            __stcg(part + (hc + j) * kLatent + dv, __uint_as_float(y[i][j]));
                     }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        __stcg(part + (hc + j) * kLatent + dv, __uint_as_float(y[j]));
                 }
             }
             before_sync();
@@ -678,51 +694,80 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 // Joins the parts of the units that several CTAs shared, a warp to a head, in the order of the parts:
 //   m = max(max_c m_c, sink), Z = sum_c l_c e^{m_c - m} + e^{sink - m},
 //   out = sum_c e^{m_c - m} O_c / Z  (BF16),  lse = m + ln Z
-// The parts come from L2.  (Joined inside the decode, by the CTA of a unit that finished last, the 256 threads that are
-// free there hold too few bytes in flight: a unit took 25 us.)
+// The parts come from L2, kJoinBatch at a time with every load in flight: four where few CTAs share each unit (latency
+// is all there is; they are read before it is known how many of them had work), two where runs of blocks end inside
+// units (two parts are usual, and more registers would leave fewer warps: 8 against 10.5 us for 151 split units).  (Joined inside the decode, by the CTA of a unit that finished last, the 256
+// threads that are free there hold too few bytes in flight: a unit took 25 us.)
+template <int kJoinBatch>
 __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4Params p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int unit = blockIdx.x;
-    const int2 join = __ldcg(p.joins + unit);   // (slot of the first part, parts); zeros for a unit of one part
-    if (join.y == 0)
-        return;
     const int t = unit % p.num_tokens, h0 = unit / p.num_tokens * kNH;
     const int h = kJoinHeads * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;   // head of the group
-    // the first part may be its CTA's second; the others are their CTAs' first
-    auto part_of = [&](int c) { return p.parts + (size_t)(c == 0 ? join.x : 2 * (join.x / 2 + c)) * kPartFloats; };
     const float sk = p.sink != nullptr ? p.sink[h0 + h] : -INFINITY;
-    float mk = -INFINITY;
-    for (int c = lane; c < join.y; c += 32)
-        mk = fmaxf(mk, __ldcg(part_of(c) + kNH * kLatent + 2 * h));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, d));
-    const float M = fmaxf(mk, sk);
-    float Z = sk == -INFINITY ? 0.f : expf(sk - M);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 join = __ldcg(p.joins + unit);   // (slot of the first part, parts); zeros for a unit of one part
+    int first = 2 * unit * p.ctas_per_unit, most = p.ctas_per_unit;
+    if (p.ctas_per_unit == 0) {
+        first = join.x;
+        most = join.y;
+    }
+    float M = sk, Z = sk == -INFINITY ? 0.f : 1.f;
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int c = 0; c < join.y; ++c) {
-        const float *pc = part_of(c);
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(pc + kNH * kLatent + 2 * h));
-        float4 o[4];
+    for (int c0 = 0; c0 < most; c0 += kJoinBatch) {
+        float2 ml[kJoinBatch];
+        float4 o[kJoinBatch][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = __ldcg(reinterpret_cast<const float4 *>(pc + h * kLatent + 128 * k + 4 * lane));
-        const float w = ml.x == -INFINITY ? 0.f : expf(ml.x - M);   // (-inf: a part without keys, whose O and l are zeros)
-        Z = fmaf(ml.y, w, Z);
+        for (int c = 0; c < kJoinBatch; ++c) {
+            // the first part may be its CTA's second; the others are their CTAs' first
+            const float *pc = p.parts + (size_t)(c0 + c == 0 ? first : 2 * (first / 2 + c0 + c)) * kPartFloats;
+            if (c0 + c < most) {
+                ml[c] = __ldcg(reinterpret_cast<const float2 *>(pc + kNH * kLatent + 2 * h));
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[c][k] = __ldcg(reinterpret_cast<const float4 *>(pc + h * kLatent + 128 * k + 4 * lane));
+            }
+        }
+        if (c0 >= join.y)
+            break;
+        float m = M;
+#pragma unroll
+        for (int c = 0; c < kJoinBatch; ++c) {
+            if (c0 + c >= join.y)
+                ml[c] = make_float2(-INFINITY, 0.f);
+            m = fmaxf(m, ml[c].x);
+        }
+        const float fall = M == -INFINITY ? 0.f : expf(M - m);
+        Z *= fall;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            acc[k].x = fmaf(w, o[k].x, acc[k].x);
-            acc[k].y = fmaf(w, o[k].y, acc[k].y);
-            acc[k].z = fmaf(w, o[k].z, acc[k].z);
-            acc[k].w = fmaf(w, o[k].w, acc[k].w);
+            acc[k].x *= fall;
+            acc[k].y *= fall;
+            acc[k].z *= fall;
+            acc[k].w *= fall;
         }
+#pragma unroll
+        for (int c = 0; c < kJoinBatch; ++c) {
+            if (ml[c].x == -INFINITY)   // no part, or one without keys
+                continue;
+            const float w = expf(ml[c].x - m);
+            Z = fmaf(ml[c].y, w, Z);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[k].x = fmaf(w, o[c][k].x, acc[k].x);
+                acc[k].y = fmaf(w, o[c][k].y, acc[k].y);
+                acc[k].z = fmaf(w, o[c][k].z, acc[k].z);
+                acc[k].w = fmaf(w, o[c][k].w, acc[k].w);
+            }
+        }
+        M = m;
     }
-    const float f = mk == -INFINITY ? 0.f : 1.f / Z;
+    if (join.y == 0)
+        return;
+    const float f = Z > 0.f || Z != Z ? 1.f / Z : 0.f;   // (no key and no sink: zeros)
     const int64_t row = (int64_t)t * p.num_heads + h0 + h;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -762,7 +807,7 @@ cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
     cfg.gridDim = dim3((unsigned)p.num_tokens * (unsigned)p.groups, (unsigned)(std::min(p.num_heads, kNH) / kJoinHeads));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, join_parts_kernel, p);
+    return p.ctas_per_unit > 0 ? cudaLaunchKernelEx(&cfg, join_parts_kernel<4>, p) : cudaLaunchKernelEx(&cfg, join_parts_kernel<2>, p);
 }
 
 }  // namespace dsv4

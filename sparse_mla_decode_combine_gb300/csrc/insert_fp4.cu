@@ -15,9 +15,13 @@
 // lies within 2^-21 of a border of its code or its block's exponent; the few tokens that have one
 // (about one in seven hundred) repeat the quantisation in fp64.
 //
-// One CTA per token: warps 0..15 take the query heads, four at a time (their loads all in flight
-// before any use), lane l holding the BF16 pairs l + 32 j (j < 9; j = 8 is the rope part, pair i = l)
-// so a pair never leaves its lane; warp 16 builds the entry, half a warp to a block of 32 values.
+// Work.  A warp per four heads of a token, a warp per key.  Eight lanes share a head, each with nine 16-byte pieces
+// (8 values) of its 1152 bytes, so a load or store covers 128 contiguous bytes of four heads, the sum of squares takes
+// three shuffles for all four, and no lane is idle; all loads of a warp are in flight before any use.  Bound by HBM:
+// every query is read and written once.  (Pairs of 4 bytes to a lane and a warp to a head took 2.4 times as long for
+// 8191 tokens x 64 heads; queries whose rows are not 16-byte aligned still go by fours of such loads.)  The keys' warps
+// come first: their fp64 chain is the longest.
+#include <climits>
 #include <cuda_bf16.h>
 #include <cuda_fp4.h>
 #include <cuda_runtime.h>
@@ -28,9 +32,8 @@
 namespace dsv4 {
 namespace {
 
-constexpr int kQWarps = 16;
-constexpr int kHeadsIter = 4;      // heads a warp has in flight at once
-constexpr int kThreads = 32 * (kQWarps + 1);
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kPairs = kDim / 2;   // 288 BF16 pairs per head; pairs 256.. are the rope part
 constexpr float kNear = 1.f / (1 << 21);
 
@@ -44,14 +47,6 @@ __device__ __forceinline__ uint32_t pack_rn_bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
 }
 
 __device__ __forceinline__ double warp_sum(double v)
@@ -126,70 +121,102 @@ __device__ __forceinline__ float value_of(uint32_t code)
     return code & 8u ? -m : m;
 }
 
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kv_insert_fp4_kernel(const Insert4Params p)
+// four pairs at a (16-byte aligned when kWide)
+template <bool kWide>
+__device__ __forceinline__ uint4 load4(const uint32_t *a)
 {
-    const int t = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (kWide)
+        return __ldg(reinterpret_cast<const uint4 *>(a));
+    return make_uint4(__ldg(a), __ldg(a + 1), __ldg(a + 2), __ldg(a + 3));
+}
+
+template <bool kWide>
+__device__ __forceinline__ void store4(uint32_t *a, const uint32_t (&v)[4])
+{
+    if (kWide) {
+        *reinterpret_cast<uint4 *>(a) = make_uint4(v[0], v[1], v[2], v[3]);
+    } else {
+        a[0] = v[0];
+        a[1] = v[1];
+        a[2] = v[2];
+        a[3] = v[3];
+    }
+}
+
+// Heads 4 quad .. 4 quad + 3 of token t.
+template <bool kWide>
+__device__ __forceinline__ void norm_rope_queries(const Insert4Params &p, int t, int quad, int lane)
+{
+    const int h = 4 * quad + (lane >> 3), l8 = lane & 7;
+    const bool there = h < p.num_heads;
+    const int64_t pos = p.positions[t];
+    const uint32_t *a = p.q + t * p.q_stride + (int64_t)(there ? h : 4 * quad) * kPairs + 4 * l8;
+    uint4 x[9];   // pieces l8 + 8 j of the head; j = 8: rope pairs 4 l8 .. 4 l8 + 3
+#pragma unroll
+    for (int j = 0; j < 9; ++j)
+        x[j] = load4<kWide>(a + 32 * j);
+    const bool rot = pos >= 0 && pos < p.max_pos;
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (rot) {
+        const float *cs = p.cos_sin + pos * 64 + 4 * l8;
+        c = make_float4(__ldg(cs), __ldg(cs + 1), __ldg(cs + 2), __ldg(cs + 3));
+        s = make_float4(__ldg(cs + 32), __ldg(cs + 33), __ldg(cs + 34), __ldg(cs + 35));
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < 9; ++j) {
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack_bf16x2(w[k]);
+            ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
+        }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = 1.f / sqrtf(ss / (float)kDim + (float)p.eps);
+    uint32_t *o = p.q_out + t * p.q_out_stride + (int64_t)h * kPairs + 4 * l8;
+#pragma unroll
+    for (int j = 0; j < 9; ++j) {
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 v = unpack_bf16x2(w[k]);
+            float y0 = v.x * r, y1 = v.y * r;
+            if (p.q_w != nullptr) {
+                const float2 g = make_float2(__ldg(p.q_w + 64 * j + 8 * l8 + 2 * k), __ldg(p.q_w + 64 * j + 8 * l8 + 2 * k + 1));
+                y0 *= g.x;
+                y1 *= g.y;
+            }
+            if (j == 8) {
+                const float ck = k == 0 ? c.x : k == 1 ? c.y : k == 2 ? c.z : c.w;
+                const float sk = k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w;
+                const float u = y0 * ck - y1 * sk;
+                y1 = y0 * sk + y1 * ck;
+                y0 = u;
+            }
+            y[k] = pack_rn_bf16x2(y0, y1);
+        }
+        if (there)
+            store4<kWide>(o + 32 * j, y);
+    }
+}
+
+// Token t's key.  Lane l holds the BF16 pairs l + 32 j (j < 9; j = 8 is the rope part, pair i = l), so half a warp holds
+// a block of 32 values.
+__device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int lane)
+{
     const int64_t pos = p.positions[t];
     const bool rot = pos >= 0 && pos < p.max_pos;
     float c = 1.f, s = 0.f;   // this lane's rope pair i = lane
     if (rot) {
         c = __ldg(p.cos_sin + pos * 64 + lane);
         s = __ldg(p.cos_sin + pos * 64 + 32 + lane);
-    } else if (threadIdx.x == 0) {
+    } else if (lane == 0) {
         atomicOr(p.status, kStatusBadIndex);
     }
-
-    if (warp < kQWarps) {
-        float w[18];   // the norm weight of this lane's 18 dims (pairs lane + 32 j)
-#pragma unroll
-        for (int j = 0; j < 9; ++j) {
-            const int d = 2 * (lane + 32 * j);
-            w[2 * j] = p.q_w ? __ldg(p.q_w + d) : 1.f;
-            w[2 * j + 1] = p.q_w ? __ldg(p.q_w + d + 1) : 1.f;
-        }
-        for (int h0 = warp; h0 < p.num_heads; h0 += kHeadsIter * kQWarps) {
-            uint32_t x[kHeadsIter][9];
-#pragma unroll
-            for (int k = 0; k < kHeadsIter; ++k) {   // every head's loads in flight before any use
-                const int h = h0 + k * kQWarps;
-                const uint32_t *a = p.q + t * p.q_stride + (int64_t)h * kPairs;
-#pragma unroll
-                for (int j = 0; j < 9; ++j)
-                    x[k][j] = h < p.num_heads ? __ldg(a + lane + 32 * j) : 0u;
-            }
-#pragma unroll
-            for (int k = 0; k < kHeadsIter; ++k) {
-                const int h = h0 + k * kQWarps;
-                if (h >= p.num_heads)
-                    break;
-                float ss = 0.f;
-#pragma unroll
-                for (int j = 0; j < 9; ++j) {
-                    const float2 v = unpack_bf16x2(x[k][j]);
-                    ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
-                }
-                ss = warp_sum(ss);
-                const float r = 1.f / sqrtf(ss / (float)kDim + (float)p.eps);
-                uint32_t *o = p.q_out + t * p.q_out_stride + (int64_t)h * kPairs;
-#pragma unroll
-                for (int j = 0; j < 9; ++j) {
-                    const float2 v = unpack_bf16x2(x[k][j]);
-                    float y0 = v.x * r * w[2 * j], y1 = v.y * r * w[2 * j + 1];
-                    if (j == 8) {
-                        const float u0 = y0 * c - y1 * s;
-                        const float u1 = y0 * s + y1 * c;
-                        y0 = u0;
-                        y1 = u1;
-                    }
-                    o[lane + 32 * j] = pack_rn_bf16x2(y0, y1);
-                }
-            }
-        }
-        return;
-    }
-
-    // ---- warp 16: the token's key
     const int64_t slot = p.slots[t];
     if (lane == 0 && slot >= p.num_slots)
         atomicOr(p.status, kStatusBadIndex);
@@ -275,13 +302,35 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kv_insert_fp4_kernel(co
     }
 }
 
+// kWide: the queries' rows are 16-byte aligned
+template <bool kWide>
+__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kv_insert_fp4_kernel(const Insert4Params p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int quads = (p.num_heads + 3) / 4;
+    if (item < p.num_tokens)
+        insert_key(p, (int)item, lane);
+    else if (item < (int64_t)p.num_tokens * (1 + quads))
+        norm_rope_queries<kWide>(p, (int)((item - p.num_tokens) / quads), (int)((item - p.num_tokens) % quads), lane);
+}
+
 }  // namespace
 
 cudaError_t launch_qk_norm_rope_kv_insert_fp4(const Insert4Params &p, cudaStream_t stream)
 {
     if (p.num_tokens <= 0)
         return cudaSuccess;
-    qk_norm_rope_kv_insert_fp4_kernel<<<p.num_tokens, kThreads, 0, stream>>>(p);
+    const long long items = (long long)p.num_tokens * (1 + (p.num_heads + 3) / 4);
+    const long long grid = (items + kWarps - 1) / kWarps;
+    if (grid > INT_MAX)
+        return cudaErrorInvalidValue;
+    const bool wide = (((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.q_out)) & 15u) == 0) &&
+                      ((p.q_stride | p.q_out_stride) & 3) == 0;
+    if (wide)
+        qk_norm_rope_kv_insert_fp4_kernel<true><<<(unsigned)grid, kThreads, 0, stream>>>(p);
+    else
+        qk_norm_rope_kv_insert_fp4_kernel<false><<<(unsigned)grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
