@@ -10,10 +10,10 @@
 //
 // Arithmetic.  Queries: fp32, one rounding to BF16.  The key's codes are those of the exactly computed
 // key: a 4-bit step is a quarter of the value or more, so a value that fp32 puts on the wrong side of a
-// rounding border would be off by all of it.  The sum of squares and the root are taken in fp64 (BF16
-// squares are exact there); the values themselves in fp32, with a check whether any value of the entry
-// lies within 2^-21 of a border of its code or its block's exponent; the few tokens that have one
-// (about one in seven hundred) repeat the quantisation in fp64.
+// rounding border would be off by all of it.  The key is computed in fp32 too, to within 15 roundings (2^-20: a
+// sum of squares of 16 terms a lane and five levels, halved by the root; root, reciprocal and two products),
+// with a check whether any value of a block, or its maximum, lies that near to a border; the blocks that have
+// one (about one in two hundred) are done again in fp64.
 //
 // Work.  A warp per four heads of a token, a warp per key.  Eight lanes share a head, each with nine 16-byte pieces
 // (8 values) of its 1152 bytes, so a load or store covers 128 contiguous bytes of four heads, the sum of squares takes
@@ -35,7 +35,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPairs = kDim / 2;   // 288 BF16 pairs per head; pairs 256.. are the rope part
-constexpr float kNear = 1.f / (1 << 21);
+constexpr float kNear = 0x1p-20f;
 
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v)
 {
@@ -49,7 +49,8 @@ __device__ __forceinline__ uint32_t pack_rn_bf16x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ double warp_sum(double v)
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
@@ -68,18 +69,15 @@ __device__ __forceinline__ T half_warp_max(T v)
     return v;
 }
 
-// Smallest integer e with 6 * 2^e >= amax (0 for amax 0), clamped to [-127, 125].  For amax in
-// [2^k, 2^(k+1)) the answer is k - 2 or k - 1; one exact comparison decides.
-__device__ __forceinline__ int exponent_of(float amax)
+// Smallest integer e with 6 * 2^e >= amax (0 for amax 0), clamped to [-127, 125]: k - 2 for amax in [2^k, 1.5 * 2^k],
+// k - 1 from there to 2^(k+1).  *near: amax is within about 2^-20 of the border 1.5 * 2^k, or too small to tell.
+__device__ __forceinline__ int exponent_of(float amax, bool *near)
 {
-    if (!(amax > 0.f))
+    const int bits = __float_as_int(amax), m = bits & 0x7FFFFF;
+    *near = (unsigned)(m - 0x400000 + 16) <= 32u || (amax < 0x1p-100f && amax > 0.f);
+    if (bits == 0)
         return 0;
-    if (amax > 1.5f * 0x1p127f)   // past 6 * 2^125
-        return 125;
-    int e = ilogbf(amax) - 2;
-    if (ldexpf(6.f, e) < amax)
-        ++e;
-    return e < -127 ? -127 : e;
+    return max(-127, min(125, (bits >> 23) - 129 + (m > 0x400000 ? 1 : 0)));
 }
 
 __device__ __forceinline__ int exponent_of(double amax)
@@ -114,27 +112,56 @@ __device__ __forceinline__ uint32_t code_of(double t)
     return c | (signbit(t) && !isnan(t) ? 8u : 0u);
 }
 
-__device__ __forceinline__ float value_of(uint32_t code)
+// the value of a code times 2^e (a code's bits at the low end of an fp32 exponent are its value times 2^-126)
+__device__ __forceinline__ float value_of(uint32_t code, int e)
 {
-    const float m = (code & 6u) == 0u ? 0.5f * (float)(code & 1u)
-                                      : (1.f + 0.5f * (float)(code & 1u)) * pow2f((int)((code >> 1) & 3u) - 1);
-    return code & 8u ? -m : m;
+    const float m = __uint_as_float(((code & 7u) << 22) | ((code & 8u) << 28)) * 0x1p126f;
+    return e < -126 ? m * 0x1p-126f * 0.5f : m * pow2f(e);
 }
 
-// four pairs at a (16-byte aligned when kWide)
+// Block pair j of token t's key (values of pairs lane + 32 j) in fp64: the lane's two codes, and its half warp's block
+// exponent + 127 from bit 8.
+__device__ __noinline__ uint32_t exact_codes(const Insert4Params &p, int t, int j, int lane)
+{
+    const uint32_t *a = p.kv + t * p.kv_stride + lane;
+    const int nj = p.kv_norm_dims / 64;
+    double ss = 0.0;
+    for (int i = 0; i < nj; ++i) {
+        const float2 v = unpack_bf16x2(__ldg(a + 32 * i));
+        ss = fma((double)v.x, (double)v.x, fma((double)v.y, (double)v.y, ss));
+    }
+    const double root = sqrt(warp_sum(ss) / (double)p.kv_norm_dims + p.eps);
+    const float2 v = unpack_bf16x2(__ldg(a + 32 * j));
+    const int d = 2 * (lane + 32 * j);
+    const double y0 = (double)v.x / root * (p.kv_w ? (double)__ldg(p.kv_w + d) : 1.0);
+    const double y1 = (double)v.y / root * (p.kv_w ? (double)__ldg(p.kv_w + d + 1) : 1.0);
+    const double a0 = isnan(y0) ? 0.0 : fabs(y0), a1 = isnan(y1) ? 0.0 : fabs(y1);
+    const int e = exponent_of(half_warp_max(a0 > a1 ? a0 : a1));
+    return code_of(ldexp(y0, -e)) | code_of(ldexp(y1, -e)) << 4 | (uint32_t)(e + 127) << 8;
+}
+
+// 16 bytes at a (16-byte aligned when kWide)
 template <bool kWide>
-__device__ __forceinline__ uint4 load4(const uint32_t *a)
+__device__ __forceinline__ uint4 load4(const void *a)
 {
     if (kWide)
         return __ldg(reinterpret_cast<const uint4 *>(a));
-    return make_uint4(__ldg(a), __ldg(a + 1), __ldg(a + 2), __ldg(a + 3));
+    const uint32_t *b = static_cast<const uint32_t *>(a);
+    return make_uint4(__ldg(b), __ldg(b + 1), __ldg(b + 2), __ldg(b + 3));
 }
 
+__device__ __forceinline__ float4 as_floats(const uint4 &v)
+{
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+// The queries stream through: written so that they leave L2 first, they do not push out what else the step keeps
+// there (128 tokens x 128 heads: 7.9 against 11.4 us with the inputs of other calls in L2; 8191 x 64: the same).
 template <bool kWide>
 __device__ __forceinline__ void store4(uint32_t *a, const uint32_t (&v)[4])
 {
     if (kWide) {
-        *reinterpret_cast<uint4 *>(a) = make_uint4(v[0], v[1], v[2], v[3]);
+        __stcs(reinterpret_cast<uint4 *>(a), make_uint4(v[0], v[1], v[2], v[3]));
     } else {
         a[0] = v[0];
         a[1] = v[1];
@@ -159,8 +186,8 @@ __device__ __forceinline__ void norm_rope_queries(const Insert4Params &p, int t,
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (rot) {
         const float *cs = p.cos_sin + pos * 64 + 4 * l8;
-        c = make_float4(__ldg(cs), __ldg(cs + 1), __ldg(cs + 2), __ldg(cs + 3));
-        s = make_float4(__ldg(cs + 32), __ldg(cs + 33), __ldg(cs + 34), __ldg(cs + 35));
+        c = as_floats(load4<kWide>(cs));
+        s = as_floats(load4<kWide>(cs + 32));
     }
     float ss = 0.f;
 #pragma unroll
@@ -179,17 +206,19 @@ __device__ __forceinline__ void norm_rope_queries(const Insert4Params &p, int t,
     uint32_t *o = p.q_out + t * p.q_out_stride + (int64_t)h * kPairs + 4 * l8;
 #pragma unroll
     for (int j = 0; j < 9; ++j) {
+        // (kept packed across the reduction: unpacked, the 72 values of a lane would spill)
+        asm volatile("" : "+r"(x[j].x), "+r"(x[j].y), "+r"(x[j].z), "+r"(x[j].w));
         const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        float4 g[2] = {make_float4(1.f, 1.f, 1.f, 1.f), make_float4(1.f, 1.f, 1.f, 1.f)};
+        if (p.q_w != nullptr) {
+            g[0] = as_floats(load4<kWide>(p.q_w + 64 * j + 8 * l8));
+            g[1] = as_floats(load4<kWide>(p.q_w + 64 * j + 8 * l8 + 4));
+        }
         uint32_t y[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float2 v = unpack_bf16x2(w[k]);
-            float y0 = v.x * r, y1 = v.y * r;
-            if (p.q_w != nullptr) {
-                const float2 g = make_float2(__ldg(p.q_w + 64 * j + 8 * l8 + 2 * k), __ldg(p.q_w + 64 * j + 8 * l8 + 2 * k + 1));
-                y0 *= g.x;
-                y1 *= g.y;
-            }
+            float y0 = v.x * r * (k & 1 ? g[k >> 1].z : g[k >> 1].x), y1 = v.y * r * (k & 1 ? g[k >> 1].w : g[k >> 1].y);
             if (j == 8) {
                 const float ck = k == 0 ? c.x : k == 1 ? c.y : k == 2 ? c.z : c.w;
                 const float sk = k == 0 ? s.x : k == 1 ? s.y : k == 2 ? s.z : s.w;
@@ -226,85 +255,82 @@ __device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int la
     for (int j = 0; j < 9; ++j)
         x[j] = __ldg(p.kv + t * p.kv_stride + lane + 32 * j);
     const int nj = p.kv_norm_dims / 64;   // pairs lane + 32 j with j < nj are normalised
-    double root = 1.0;
+    float r = 1.f;
     if (nj > 0) {
-        double ss = 0.0;
+        float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < 9; ++j) {
             const float2 v = unpack_bf16x2(x[j]);
             if (j < nj)
-                ss = fma((double)v.x, (double)v.x, fma((double)v.y, (double)v.y, ss));
+                ss = fmaf(v.x, v.x, fmaf(v.y, v.y, ss));
         }
-        root = sqrt(warp_sum(ss) / (double)p.kv_norm_dims + p.eps);
+        r = 1.f / sqrtf(warp_sum(ss) / (float)p.kv_norm_dims + (float)p.eps);
     }
-    const float r = (float)(1.0 / root);
-    float2 y[9];
-    float2 w[9];
-#pragma unroll
-    for (int j = 0; j < 9; ++j) {
-        const bool normed = j < nj;
-        const int d = 2 * (lane + 32 * j);
-        w[j] = make_float2(1.f, 1.f);
-        if (normed && p.kv_w)
-            w[j] = make_float2(__ldg(p.kv_w + d), __ldg(p.kv_w + d + 1));
-        const float2 v = unpack_bf16x2(x[j]);
-        y[j] = normed ? make_float2(v.x * r * w[j].x, v.y * r * w[j].y) : v;
-    }
-    int ex[8];
-    uint32_t code[8];
-    bool near = false;   // some value or block maximum lies next to a border
+    // the sum of squares of such keys may pass fp32's range (or the root lose its precision): all in fp64
+    const bool wild = nj > 0 && !(r > 0x1p-60f && r < 0x1p60f);
+    uint8_t *e = p.cache + (write ? slot : 0) * kEntry4Bytes;
+    uint32_t *o = p.k_out + t * p.k_out_stride;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {   // blocks 2 j (lanes 0..15) and 2 j + 1 (lanes 16..31)
-        const float a0 = fabsf(y[j].x), a1 = fabsf(y[j].y);
-        const float amax = half_warp_max(fmaxf(fmaxf(a0, a1), 0.f));   // (a NaN counts as 0)
-        ex[j] = exponent_of(amax);
-        const float f = pow2f(-ex[j]);
-        const float t0 = y[j].x * f, t1 = y[j].y * f;
-        code[j] = codes_of(t0, t1);
-        if (nj > 0) {
-            near |= exponent_of(amax * (1.f - kNear)) != exponent_of(amax * (1.f + kNear)) ||
-                    (amax < 0x1p-100f && amax > 0.f);
-            near |= codes_of(t0 * (1.f - kNear), t1 * (1.f - kNear)) != codes_of(t0 * (1.f + kNear), t1 * (1.f + kNear));
+        const float2 v = unpack_bf16x2(x[j]);
+        float y0 = v.x, y1 = v.y;
+        if (j < nj) {
+            y0 *= r;
+            y1 *= r;
+            if (p.kv_w != nullptr) {
+                y0 *= __ldg(p.kv_w + 2 * (lane + 32 * j));
+                y1 *= __ldg(p.kv_w + 2 * (lane + 32 * j) + 1);
+            }
         }
-    }
-    if (__any_sync(0xffffffffu, near)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 v = unpack_bf16x2(x[j]);
-            const double y0 = (double)v.x / root * (double)w[j].x, y1 = (double)v.y / root * (double)w[j].y;
-            const double a0 = fabs(y0), a1 = fabs(y1);
-            double a = a0 > a1 || isnan(a1) ? a0 : a1;
-            a = isnan(a) ? 0.0 : a;
-            ex[j] = exponent_of(half_warp_max(a));
-            code[j] = code_of(ldexp(y0, -ex[j])) | code_of(ldexp(y1, -ex[j])) << 4;
+        bool near;
+        int ex = exponent_of(half_warp_max(fmaxf(fmaxf(fabsf(y0), fabsf(y1)), 0.f)), &near);   // (a NaN counts as 0)
+        const float f = pow2f(-ex), t0 = y0 * f, t1 = y1 * f;
+        uint32_t code = codes_of(t0, t1);
+        if (nj > 0) {   // (without a norm the key is BF16 and everything above is exact)
+            near |= wild || codes_of(t0 * (1.f - kNear), t1 * (1.f - kNear)) != codes_of(t0 * (1.f + kNear), t1 * (1.f + kNear));
+            if (__any_sync(0xffffffffu, near)) {
+                const uint32_t c = exact_codes(p, t, j, lane);
+                code = c & 0xFFu;
+                ex = (int)(c >> 8) - 127;
+            }
         }
-    }
-    const uint32_t rope = [&] {
-        const float2 v = y[8];
-        return pack_rn_bf16x2(v.x * c - v.y * s, v.x * s + v.y * c);
-    }();
-    if (write) {
-        uint8_t *e = p.cache + slot * kEntry4Bytes;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            e[lane + 32 * j] = (uint8_t)code[j];
+        if (write) {
+            e[lane + 32 * j] = (uint8_t)code;
             if ((lane & 15) == 0)
-                e[kScale4Offset + 2 * j + (lane >> 4)] = (uint8_t)(ex[j] + 127);
+                e[kScale4Offset + 2 * j + (lane >> 4)] = (uint8_t)(ex + 127);
         }
+        if (p.k_out != nullptr)
+            o[lane + 32 * j] = pack_rn_bf16x2(value_of(code & 15u, ex), value_of(code >> 4, ex));
+    }
+    float2 v = unpack_bf16x2(x[8]);
+    if (nj > 8) {
+        v.x *= r;
+        v.y *= r;
+        if (wild) {   // (as the latent: from the fp64 root)
+            double ss = 0.0;
+            for (int i = 0; i < 9; ++i) {
+                const float2 u = unpack_bf16x2(__ldg(p.kv + t * p.kv_stride + lane + 32 * i));
+                ss = fma((double)u.x, (double)u.x, fma((double)u.y, (double)u.y, ss));
+            }
+            const double root = sqrt(warp_sum(ss) / (double)kDim + p.eps);
+            const float2 u = unpack_bf16x2(x[8]);
+            v = make_float2((float)((double)u.x / root), (float)((double)u.y / root));
+        }
+        if (p.kv_w != nullptr) {
+            v.x *= __ldg(p.kv_w + kLatent + 2 * lane);
+            v.y *= __ldg(p.kv_w + kLatent + 2 * lane + 1);
+        }
+    }
+    const uint32_t rope = pack_rn_bf16x2(v.x * c - v.y * s, v.x * s + v.y * c);
+    if (write)
         *reinterpret_cast<uint32_t *>(e + kRope4Offset + 4 * lane) = rope;
-    }
-    if (p.k_out) {
-        uint32_t *o = p.k_out + t * p.k_out_stride;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            o[lane + 32 * j] = pack_rn_bf16x2(ldexpf(value_of(code[j] & 15u), ex[j]), ldexpf(value_of(code[j] >> 4), ex[j]));
-        o[lane + 256] = rope;
-    }
+    if (p.k_out != nullptr)
+        o[256 + lane] = rope;
 }
 
-// kWide: the queries' rows are 16-byte aligned
+// kWide: the queries' rows, their weight and the rotation table are 16-byte aligned
 template <bool kWide>
-__global__ void __launch_bounds__(kThreads, 3) qk_norm_rope_kv_insert_fp4_kernel(const Insert4Params p)
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kv_insert_fp4_kernel(const Insert4Params p)
 {
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -325,7 +351,8 @@ cudaError_t launch_qk_norm_rope_kv_insert_fp4(const Insert4Params &p, cudaStream
     const long long grid = (items + kWarps - 1) / kWarps;
     if (grid > INT_MAX)
         return cudaErrorInvalidValue;
-    const bool wide = (((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.q_out)) & 15u) == 0) &&
+    const bool wide = (((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.q_out) |
+                         reinterpret_cast<uintptr_t>(p.q_w) | reinterpret_cast<uintptr_t>(p.cos_sin)) & 15u) == 0) &&
                       ((p.q_stride | p.q_out_stride) & 3) == 0;
     if (wide)
         qk_norm_rope_kv_insert_fp4_kernel<true><<<(unsigned)grid, kThreads, 0, stream>>>(p);

@@ -6,11 +6,14 @@
 // page (0: the page is free).  New pages are the lowest-numbered free ones, so the result of a call
 // depends on its inputs alone; integer sums are the only atomics.
 //
-// Every operator is two launches.  A planning kernel, one cluster of eight CTAs, does the index work
-// (counts, ranks and sums over the reference counts and rows, with a cluster barrier between dependent
-// steps: no launch, no wait on global memory) and writes which pages are copied where; a second kernel
-// over the whole GPU moves the pages of every layer.  The second kernel is bound by HBM (each
-// byte read and written once), the first by the latency of its steps (a few microseconds).
+// Every operator is two launches: a planning kernel does the index work (counts, ranks and sums over the
+// reference counts and rows) and writes which pages are copied where; a second kernel over the whole GPU
+// moves the pages of every layer.  The second is bound by HBM (each byte read and written once), the first by
+// the latency of its dependent steps, so it takes as few trips to global memory as it can: in a pool of up to
+// 16384 pages one CTA does it, with the counts, the rows' numbers and the free list in shared memory; larger
+// ones take a cluster of eight CTAs with a cluster barrier between the steps and the numbers in the workspace.
+// A short list of pages to copy needs no plan: one launch.
+#include <algorithm>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -23,6 +26,10 @@ constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kCluster * kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
+constexpr int kCopyUnroll = 8;         // 16-byte pieces a thread holds: a page of 64 entries of 400 bytes in one round
+constexpr int kSmallPages = 16384;     // the one-CTA plans: pages,
+constexpr int kSmallRows = 1024;       // rows before and after,
+constexpr int kSmallCells = 1 << 16;   // and cells of the table
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -258,6 +265,141 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     }
 }
 
+// The same plan by one CTA, for small pools and tables.
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const ForkParams p)
+{
+    extern __shared__ int sm[];
+    __shared__ int wsum[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int B = p.pool.num_blocks, page = p.pool.page, M = p.max_blocks;
+    int *refs = sm, *refs_new = sm + B, *free_list = sm + 2 * B;
+    int *first = sm + 3 * B, *kids = first + p.rows, *lens = kids + p.rows, *parent = lens + p.rows, *off = parent + p.rows_out;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the copy kernel waits for this grid itself)
+
+    for (int i = tid; i < B; i += kPlanThreads)
+        refs[i] = refs_new[i] = p.refs[i];
+    for (int i = tid; i < p.rows; i += kPlanThreads) {
+        first[i] = INT32_MAX;
+        kids[i] = 0;
+        lens[i] = p.lens[i];
+    }
+    for (int r = tid; r < p.rows_out; r += kPlanThreads) {
+        const int par = p.parent[r];
+        if (par >= p.rows)
+            atomicOr(p.status, kStatusBadIndex);
+        parent[r] = par >= 0 && par < p.rows ? par : -1;
+    }
+    __syncthreads();
+    for (int r = tid; r < p.rows_out; r += kPlanThreads)
+        if (parent[r] >= 0)
+            atomicMin(&first[parent[r]], r);
+    int num_free = 0, total;
+    for (int i0 = 0; i0 < B; i0 += kPlanThreads) {   // (its barriers also end the loop above)
+        const int i = i0 + tid;
+        const bool f = i < B && refs[i] == 0;
+        const int at = num_free + cta_scan(f, wsum, &total);
+        if (f)
+            free_list[at] = i;
+        num_free += total;
+    }
+    __syncthreads();
+
+    // whether a row takes a page of its own for page j of its parent (which is v)
+    auto takes = [&](int r, int par, int full, int j, int v) { return j >= full && !(first[par] == r && refs[v] == 1); };
+    for (int r = warp; r < p.rows_out; r += kPlanThreads / 32) {
+        const int par = parent[r];
+        int need = 0;
+        if (par >= 0) {
+            const int len = lens[par], np = pages_of(len, page, M), full = p.share ? min(np, max(len, 0) / page) : 0;
+            const int32_t *src = p.table + (int64_t)par * p.table_stride;
+            for (int j = full + lane; j < np; j += 32) {   // (shared pages take nothing)
+                const int v = src[j];
+                need += v >= 0 && v < B && takes(r, par, full, j, v);
+            }
+            need = __reduce_add_sync(0xffffffffu, need);
+        }
+        if (lane == 0)
+            off[r] = need;
+    }
+    __syncthreads();
+    const int need = tid < p.rows_out ? off[tid] : 0;   // (one row to a thread: kSmallRows)
+    const int before = cta_scan(need, wsum, &total);
+    const int wanted = min(total, num_free);
+    if (tid < p.rows_out)
+        off[tid] = need > 0 && before + need > num_free ? -1 : before;
+    if (tid == 0)
+        *p.num_copies = wanted;
+    for (int i = tid; i < wanted; i += kPlanThreads)   // (a row that gets no pages leaves its share unused)
+        p.copies[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+
+    for (int r = warp; r < p.rows_out; r += kPlanThreads / 32) {
+        const int par = parent[r];
+        const bool ok = par >= 0 && off[r] >= 0;
+        const int len = ok ? min(lens[par], (int)min((int64_t)M * page, (int64_t)INT32_MAX)) : 0;
+        const int np = pages_of(len, page, M), full = p.share ? min(np, max(len, 0) / page) : 0;
+        if (lane == 0) {
+            p.lens_out[r] = max(len, 0);
+            if (par >= 0 && (!ok || lens[par] > (int64_t)M * page))
+                atomicOr(p.status, kStatusBadIndex);
+            if (ok)
+                atomicAdd(&kids[par], 1);
+        }
+        const int32_t *src = p.table + (int64_t)max(par, 0) * p.table_stride;
+        int32_t *dst = p.table_out + (int64_t)r * p.table_out_stride;
+        int at = off[r];
+        for (int j0 = 0; j0 < M; j0 += 32) {
+            const int j = j0 + lane;
+            int v = -1;
+            bool take = false;
+            if (j < np) {
+                v = src[j];
+                if (v < 0 || v >= B) {
+                    atomicOr(p.status, kStatusBadIndex);
+                    v = -1;
+                } else {
+                    take = takes(r, par, full, j, v);
+                }
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, take);
+            if (take) {
+                const int k = at + __popc(m & ((1u << lane) - 1u)), q = free_list[k];
+                p.copies[k] = make_int4(v, q, entries_of(len, page, j), 0);
+                refs_new[q] = 1;
+                v = q;
+            }
+            at += __popc(m);
+            if (j < M)
+                dst[j] = v;
+        }
+        // a row that finds no pages: its bad cells are flagged as those of any row
+        if (par >= 0 && !ok) {
+            const int npf = pages_of(lens[par], page, M);
+            for (int j = lane; j < npf; j += 32)
+                if (src[j] < 0 || src[j] >= B)
+                    atomicOr(p.status, kStatusBadIndex);
+        }
+    }
+    __syncthreads();
+    for (int i = warp; i < p.rows; i += kPlanThreads / 32) {
+        const int len = lens[i], np = pages_of(len, page, M), full = p.share ? min(np, max(len, 0) / page) : 0;
+        const int c = kids[i], f = first[i];
+        const bool has = f != INT32_MAX && off[f] >= 0;
+        const int32_t *src = p.table + (int64_t)i * p.table_stride;
+        for (int j = lane; j < np; j += 32) {
+            const int v = src[j];
+            if (v < 0 || v >= B)
+                continue;
+            const int d = j < full ? c - 1 : (has && refs[v] == 1 ? 0 : -1);   // (the first child kept it)
+            if (d != 0)
+                atomicAdd(&refs_new[v], d);
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < B; i += kPlanThreads)
+        p.refs_out[i] = refs_new[i];
+}
+
 // ---- compact -------------------------------------------------------------------------------------
 
 // With L live pages (count > 0), the k-th live page at or past L moves to the k-th free page below L.
@@ -330,10 +472,64 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     }
 }
 
+// The same plan by one CTA, for small pools.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_small_kernel(const CompactParams p)
+{
+    extern __shared__ int sm[];
+    __shared__ int wsum[32];
+    const int tid = threadIdx.x;
+    const int B = p.pool.num_blocks;
+    int *refs = sm, *src = sm + B, *dst = src + (B + 1) / 2;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    int mine = 0, L, below;
+    for (int i = tid; i < B; i += kPlanThreads) {
+        const int v = p.refs[i];
+        refs[i] = v;
+        mine += v > 0;
+    }
+    cta_scan(mine, wsum, &L);
+    mine = 0;
+    for (int i = tid; i < L; i += kPlanThreads)
+        mine += refs[i] > 0;
+    cta_scan(mine, wsum, &below);
+    const int moves = L - below;
+    int running = 0, total;
+    for (int i0 = 0; i0 < B; i0 += kPlanThreads) {
+        const int i = i0 + tid;
+        const int v = i < B ? refs[i] : 0;
+        const bool live = v > 0;
+        const int r = running + cta_scan(live, wsum, &total);   // live pages before page i
+        running += total;
+        if (i >= B)
+            continue;
+        if (live && i >= L) {
+            src[r - below] = i;
+        } else {
+            p.page_map[i] = live ? i : -1;
+            if (!live && i < L)
+                dst[i - r] = i;
+            else
+                p.refs_out[i] = live ? v : 0;
+        }
+    }
+    if (tid == 0) {
+        *p.num_live = L;
+        *p.num_copies = moves;
+    }
+    __syncthreads();
+    for (int k = tid; k < moves; k += kPlanThreads) {
+        p.copies[k] = make_int4(src[k], dst[k], p.pool.page, 0);
+        p.page_map[src[k]] = dst[k];
+        p.refs_out[dst[k]] = refs[src[k]];
+        p.refs_out[src[k]] = 0;
+    }
+}
+
 // ---- copies of listed pages ----------------------------------------------------------------------
 
 // A target that is listed twice receives its last pair.  In one pool, a pair whose source is also a
-// target of the call is refused (the page might be read before or after it is written).
+// target of the call is refused (the page might be read before or after it is written).  More pairs than
+// a CTA has threads are checked through a claim on each target; fewer by the moving kernel itself.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) copy_plan_kernel(const CopyPagesParams p)
 {
     const int gtid = cluster_rank() * kPlanThreads + threadIdx.x;
@@ -353,8 +549,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         const int s = p.src_pages[i], d = p.dst_pages[i];
         if (good(s, d))
             atomicMax(&p.claim[d], i);
-        else
-            atomicOr(p.status, kStatusBadIndex);
     }
 }
 
@@ -402,6 +596,11 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
         }
     }
     const int n = p.copies != nullptr ? *p.num_copies : p.num_pages;
+    // a few listed pages are checked against each other here, a pair to a thread, without a plan
+    int2 pair = make_int2(-1, -1);
+    if (p.copies == nullptr && p.claim == nullptr && tid < n)
+        pair = make_int2(p.src_pages[tid], p.dst_pages[tid]);
+    const bool pair_good = pair.x >= 0 && pair.x < p.src.num_blocks && pair.y >= 0 && pair.y < p.dst.num_blocks;
     const int64_t units = (int64_t)n * p.dst.num_layers;
     const int64_t page_bytes = (int64_t)p.dst.page * p.dst.entry_bytes;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -411,27 +610,34 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
             c = p.copies[i];
         } else {
             c = make_int4(p.src_pages[i], p.dst_pages[i], p.dst.page, 0);
-            if (c.x < 0 || c.x >= p.src.num_blocks || c.y < 0 || c.y >= p.dst.num_blocks || p.claim[c.y] != i)
-                continue;
-            if (p.one_pool && p.claim[c.x] != -1) {
-                if (tid == 0 && layer == 0)
+            const bool good = c.x >= 0 && c.x < p.src.num_blocks && c.y >= 0 && c.y < p.dst.num_blocks;
+            bool later, target;   // a later pair has this target; the source is a target of the call
+            if (p.claim != nullptr) {
+                later = good && p.claim[c.y] != i;
+                target = good && p.one_pool && p.claim[c.x] != -1;
+            } else {
+                later = __syncthreads_or(pair_good && tid > i && pair.y == c.y);
+                target = __syncthreads_or(pair_good && p.one_pool && pair.y == c.x);
+            }
+            if (!good || later || target) {
+                if ((!good || (target && !later)) && tid == 0 && layer == 0)
                     atomicOr(p.status, kStatusBadIndex);
                 continue;
             }
         }
         const uint4 *s = reinterpret_cast<const uint4 *>(p.src.base + layer * p.src.layer_stride + c.x * page_bytes);
         uint4 *d = reinterpret_cast<uint4 *>(p.dst.base + layer * p.dst.layer_stride + c.y * page_bytes);
-        const int64_t pieces = (int64_t)c.z * p.dst.entry_bytes / 16;
-        for (int64_t i0 = 0; i0 < pieces; i0 += 4 * kCopyThreads) {
-            uint4 v[4];
+        const int pieces = (int)((int64_t)c.z * p.dst.entry_bytes / 16);
+        for (int i0 = 0; i0 < pieces; i0 += kCopyUnroll * kCopyThreads) {
+            uint4 v[kCopyUnroll];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kCopyUnroll; ++k)
                 if (i0 + k * kCopyThreads + tid < pieces)
-                    v[k] = s[i0 + k * kCopyThreads + tid];
+                    v[k] = __ldcs(s + i0 + k * kCopyThreads + tid);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kCopyUnroll; ++k)
                 if (i0 + k * kCopyThreads + tid < pieces)
-                    d[i0 + k * kCopyThreads + tid] = v[k];
+                    __stcs(d + i0 + k * kCopyThreads + tid, v[k]);
         }
     }
 }
@@ -439,7 +645,7 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
 cudaError_t launch_move(const MoveParams &m, int sms, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sms * 4));
+    cfg.gridDim = dim3((unsigned)(sms * 3));
     cfg.blockDim = dim3(kCopyThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -454,8 +660,18 @@ cudaError_t launch_move(const MoveParams &m, int sms, cudaStream_t stream)
 
 cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t stream)
 {
-    fork_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (p.pool.num_blocks <= kSmallPages && p.rows <= kSmallRows && p.rows_out <= kSmallRows &&
+        (int64_t)std::max(p.rows, p.rows_out) * p.max_blocks <= kSmallCells) {
+        const int bytes = 4 * (3 * p.pool.num_blocks + 3 * p.rows + 2 * p.rows_out);
+        e = set_smem_once(reinterpret_cast<const void *>(fork_plan_small_kernel), bytes, kAttrForkSmall);
+        if (e != cudaSuccess)
+            return e;
+        fork_plan_small_kernel<<<1, kPlanThreads, bytes, stream>>>(p);
+    } else {
+        fork_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+    }
+    e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     MoveParams m{};
@@ -467,8 +683,17 @@ cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t stream)
 
 cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t stream)
 {
-    compact_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (p.pool.num_blocks <= kSmallPages) {
+        const int bytes = 8 * p.pool.num_blocks + 8;
+        e = set_smem_once(reinterpret_cast<const void *>(compact_plan_small_kernel), bytes, kAttrCompactSmall);
+        if (e != cudaSuccess)
+            return e;
+        compact_plan_small_kernel<<<1, kPlanThreads, bytes, stream>>>(p);
+    } else {
+        compact_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+    }
+    e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     MoveParams m{};
@@ -489,17 +714,20 @@ cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t stream)
 
 cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t stream)
 {
-    copy_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess)
-        return e;
+    const bool few = p.num_pages <= kCopyThreads;   // (7 pages in four layers: 3.1 against 5.0 us)
+    if (!few) {
+        copy_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess)
+            return e;
+    }
     MoveParams m{};
     m.dst = p.dst;
     m.src = p.src;
     m.src_pages = p.src_pages;
     m.dst_pages = p.dst_pages;
     m.num_pages = p.num_pages;
-    m.claim = p.claim;
+    m.claim = few ? nullptr : p.claim;
     m.one_pool = p.one_pool;
     m.status = p.status;
     return launch_move(m, sms, stream);
