@@ -423,19 +423,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             int slots = load_slots(0), slots_next = load_slots(8);
             auto slot_of = [&](int b) { return __shfl_sync(0xffffffffu, slots, 4 * (b & 7) + (lane & 3)); };
             auto entry = [&](int slot) { return p.kv + (int64_t)(slot >= 0 ? slot : 0) * kEntry4Bytes; };
-            uint4 pre[2], prope;   // the entry of the block ahead
-            uint32_t psc[2];
-            auto load_piece = [&](const uint8_t *e, int m) {
-                pre[m] = ld16(e + 128 * m + 16 * piece);
-                psc[m] = __ldg(e + kScale4Offset + 8 * m + piece);
+            // the entry of the block ahead; lanes 4 i .. 4 i + 3 (i < 4) hold word i of the rows' scale bytes
+            uint4 pre[2], prope;
+            uint32_t psc = 0u;
+            auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld16(e + 128 * m + 16 * piece); };
+            auto load_rest = [&](const uint8_t *e) {
+                prope = ld16(e + kRope4Offset + 16 * runit);
+                if (lane < 16)
+                    psc = __ldg(reinterpret_cast<const uint32_t *>(e + kScale4Offset) + (lane >> 2));
             };
-            auto load_rope = [&](const uint8_t *e) { prope = ld16(e + kRope4Offset + 16 * runit); };
             const int slot0 = slot_of(0);
             bool pre_ok = slot0 >= 0;
             if (pre_ok) {
                 load_piece(entry(slot0), 0);
                 load_piece(entry(slot0), 1);
-                load_rope(entry(slot0));
+                load_rest(entry(slot0));
             }
             if (n > 0 || p.ctas_per_unit == 0) {
                 if (n > 0)   // S^T of the last segment's last block is done with its Q
@@ -457,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 const int slot1 = slot_of(b + 1);
                 const bool ok_next = slot1 >= 0;
                 const uint8_t *en = entry(slot1);   // the next block's entry goes into the registers as they are used up
+                uint32_t se[2];   // the scales of this lane's pieces
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    se[m] = (__shfl_sync(0xffffffffu, psc, 4 * (2 * m + (piece >> 2)) + (lane & 3)) >> (8 * (piece & 3))) & 0xFFu;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {   // dims 256 m + 32 piece ..
                     if (g >= 2)   // P.V of the block before the last is done with these chunks
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     const uint32_t cb = tile + (uint32_t)(4 * m + (piece >> 1)) * kChunkBytes;
                     const uint32_t u = 4u * (uint32_t)(piece & 1);
                     if (pre_ok) {
-                        dequant32_store(pre[m], psc[m], cb, u, x7);
+                        dequant32_store(pre[m], se[m], cb, u, x7);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         mbar_arrive(bar_grp + 16 * x + 8 * m);
                 }
                 if (ok_next)
-                    load_rope(en);
+                    load_rest(en);
                 pre_ok = ok_next;
             }
         }
