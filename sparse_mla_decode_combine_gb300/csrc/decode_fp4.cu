@@ -18,10 +18,10 @@
 // which bounds a long list.  (One 128-key tile, whose steps form a chain, took 8.5 k.)
 //   - a thread holds its eighth of a row's next entry in registers, loaded as those of the present block are
 //     used up; whole entries are prefetched to L2 two blocks before that;
-//   - the softmax keeps a reference maximum per head from the unit's first block and exchanges maxima between
-//     warps again only when a logit exceeds it by 2^40: P and the sums are floating-point numbers, whose
-//     relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.  The
-//     usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
+//   - the softmax takes the logits of the unit's first key as references, and exchanges maxima between warps only
+//     when a logit exceeds its head's reference by 40 (in log2 units): P and the sums are floating-point numbers,
+//     whose relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.
+//     The usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
 //
 // Work.  A persistent CTA per multiprocessor takes an equal run of the blocks of all units (the end of one unit,
 // whole units, the start of another), so lists of any lengths fill the machine; with one unit per CTA, 256 equal
@@ -180,21 +180,22 @@ __device__ __forceinline__ int run_start(int c, int W, int G)   // floor(c W / G
 __device__ __forceinline__ int run_of(int w, int W, int G) { return (int)(((long long)(w + 1) * G - 1) / W); }
 
 // The queries of 64 heads -> swizzled K-major B operand, in the tile's order of dims (zeros for heads that do not
-// exist), by worker wid of 512.
+// exist), by worker wid of 512, kBatch pieces in flight.
+template <int kBatch>
 __device__ __forceinline__ void store_q(const Decode4Params &p, int t, int h0, uint32_t sQ, int wid)
 {
     const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride + h0 * kDim);
     const int pieces = min(kNH, p.num_heads - h0) * (kDim / 8);
 #pragma unroll 1
-    for (int j0 = 0; j0 < kQLoads; j0 += 3) {
-        uint4 v[3];
+    for (int j0 = 0; j0 < kQLoads; j0 += kBatch) {
+        uint4 v[kBatch];
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
             const int i = wid + kWorkers * (j0 + j);
             v[j] = i < pieces ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
             const int i = wid + kWorkers * (j0 + j);
             const int h = i / (kDim / 8), c = i % (kDim / 8);
             const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
@@ -203,6 +204,35 @@ __device__ __forceinline__ void store_q(const Decode4Params &p, int t, int h0, u
                              __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
             else
                 st_shared_v4(a, v[j].x, v[j].y, v[j].z, v[j].w);
+        }
+    }
+}
+
+// O^T from TMEM to the output (times the heads' factors) or to a part of it, 16 heads of a value tile at a time, by
+// warp `rank` of the `warps` that share the quadrant.
+__device__ __forceinline__ void write_o(const Decode4Params &p, int t, int h0, float *part, const float *fin,
+                                        uint32_t lane_base, int quad, int lane, int rank, int warps)
+{
+    const int slices = min(kNH, p.num_heads - h0) / 16;   // (heads that exist: a multiple of 16)
+    const int vrow = quad * 32 + lane;                    // this lane's row of a value tile,
+    const int dv0 = (vrow & ~7) | ((vrow >> 1) & 3) | ((vrow & 1) << 2);   // and its value dim (the tile's order of dims)
+#pragma unroll 1
+    for (int i = rank; i < 4 * slices; i += warps) {
+        const int m = i / slices, hc = 16 * (i % slices), dv = kDvTile * m + dv0;
+        uint32_t y[16];
+        tmem_ld16(lane_base + kColO + 64 * m + hc, y);
+        tmem_ld_wait();
+        if (part == nullptr) {
+            uint16_t *o = p.out + ((int64_t)t * p.num_heads + h0 + hc) * kLatent + dv;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const __nv_bfloat16 v = __float2bfloat16_rn(__uint_as_float(y[j]) * fin[hc + j]);
+                o[j * kLatent] = *reinterpret_cast<const uint16_t *>(&v);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                __stcg(part + (hc + j) * kLatent + dv, __uint_as_float(y[j]));
         }
     }
 }
@@ -257,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     // the queries are there already, and where the unit is known they are read while the lists are made.
     if (p.ctas_per_unit > 0 && is_worker) {
         const int unit = blockIdx.x / p.ctas_per_unit;
-        store_q(p, unit % p.num_tokens, unit / p.num_tokens * kNH, sQ, tid - 32 * kDequantWarp0);
+        store_q<kQLoads>(p, unit % p.num_tokens, unit / p.num_tokens * kNH, sQ, tid - 32 * kDequantWarp0);
     }
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -442,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             if (n > 0 || p.ctas_per_unit == 0) {
                 if (n > 0)   // S^T of the last segment's last block is done with its Q
                     mbar_wait(bar_s + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
-                store_q(p, t, h0, sQ, wid);
+                store_q<3>(p, t, h0, sQ, wid);
             }
             fence_async_smem();
             __syncwarp();
@@ -494,6 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     load_rest(en);
                 pre_ok = ok_next;
             }
+            if (p.ctas_per_unit > 0) {   // the CTA's only segment: its output is written by all
+                named_bar(4, 32 * kSoftmaxWarps + kWorkers);   // (the factors are there)
+                mbar_wait(bar_pv + 32 * ((g - 1) & 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
+                after_sync();
+                write_o(p, t, h0, seg.nb == blocks_of(seg.len) ? nullptr : p.parts + (size_t)(2 * blockIdx.x) * kPartFloats,
+                        fin, lane_base, quad, lane, 2 + (ww >> 2), 6);
+            }
         }
     } else {
         // ---- softmax and epilogue
@@ -502,8 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         const float c2 = p.scale * 1.4426950408889634f;   // logits in log2 units per raw dot product
         const int hw = 32 * ((warp - 1) >> 2);            // first of this warp's 32 heads; its 16 keys are the quadrant's
         const int slice_bar = 2 + ((warp - 1) >> 2);      // the four warps of these heads
-        const int vrow = quad * 32 + lane;                // this lane's row of a value tile,
-        const int dv0 = (vrow & ~7) | ((vrow >> 1) & 3) | ((vrow & 1) << 2);   // and its value dim (the tile's order of dims)
         // this lane's keys are srow and srow + 8; its heads, j = 0..7:
         const int srow = 16 * quad + (lane >> 2);
         const int sh = hw + 2 * (lane & 3);
@@ -527,8 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 const bool kv[2] = {valid[x * kBK + srow] != 0, valid[x * kBK + srow + 8] != 0};   // (not past the list's end)
                 float ref[8];
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    const float2 m = *reinterpret_cast<const float2 *>(smax + head(j));
+                for (int j = 0; j < 8; j += 2) {   // (in the first block they are 0, and may be being set)
+                    const float2 m = b > 0 ? *reinterpret_cast<const float2 *>(smax + head(j)) : make_float2(0.f, 0.f);
                     ref[j] = m.x;
                     ref[j + 1] = m.y;
                 }
@@ -545,6 +580,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         v[r][j] = kv[r] ? fmaf(__uint_as_float(s[j >> 2][4 * ((j >> 1) & 1) + 2 * r + (j & 1)]), c2, -ref[j]) : -INFINITY;
+                if (b == 0 && valid[x * kBK] != 0) {
+                    // any logit will do as a reference: those of the segment's first key
+                    if (srow == 0) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            smax[head(j)] = fabsf(v[0][j]) < INFINITY ? v[0][j] : 0.f;
+                    }
+                    named_bar(slice_bar, 128);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        v[0][j] -= smax[head(j)];
+                        v[1][j] -= smax[head(j)];
+                    }
+                    fresh = false;
+                }
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -576,8 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         }
                     }
                     named_bar(slice_bar, 128);   // the references and factors are written, and red is free again
-                    if (!fresh) {
-                        // (b > 0: no key was seen before otherwise) P.V of the block before has to be complete
+                    if (b > 0 && !fresh) {   // O^T holds something: P.V of the block before has to be complete
                         mbar_wait(bar_pv + 32 * (x ^ 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
                         after_sync();
 #pragma unroll 1
@@ -655,33 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             named_bar(1, kAll);
             mbar_wait(bar_pv + 32 * ((g - 1) & 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
             after_sync();
-            // ---- O^T out of TMEM: the output, or the part (this warp: its quadrant of every value tile, 32 heads)
-#pragma unroll 1
-            for (int m = 0; m < 4; ++m) {
-                const int dv = kDvTile * m + dv0;
-                if (hw >= nhv)   // nhv is a multiple of 16
-                    break;
-                uint32_t y[2][16];
-                tmem_ld16(lane_base + kColO + 64 * m + hw, y[0]);
-                tmem_ld16(lane_base + kColO + 64 * m + hw + 16, y[1]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int hc = hw + 16 * i;
-                    if (hc >= nhv)
-                        break;
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const __nv_bfloat16 o = __float2bfloat16_rn(__uint_as_float(y[i][j]) * fin[hc + j]);
-                            p.out[((int64_t)t * p.num_heads + h0 + hc + j) * kLatent + dv] = *reinterpret_cast<const uint16_t *>(&o);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            __stcg(part + (hc + j) * kLatent + dv, __uint_as_float(y[i][j]));
-                    }
-                }
+            // ---- O^T out of TMEM (alone: two warps to a quadrant; with the dequant's six)
+            if (p.ctas_per_unit > 0) {
+                named_bar(4, kAll + kWorkers);
+                write_o(p, t, h0, whole ? nullptr : part, fin, lane_base, quad, lane, (warp - 1) >> 2, 6);
+            } else {
+                write_o(p, t, h0, whole ? nullptr : part, fin, lane_base, quad, lane, (warp - 1) >> 2, 2);
             }
             before_sync();
             __syncwarp();

@@ -227,6 +227,52 @@ def test_same_call_twice_is_the_same():
     assert torch.equal(a, b) and torch.equal(la, lb)
 
 
+def test_many_units_are_the_same_every_time():
+    """256 units of up to 700 keys, several to a CTA and split between CTAs: twenty calls give the same bits."""
+    need_gpu()
+    rng = np.random.default_rng(90)
+    w = to_fp4(synth.make_workload(name="many", seed=91, heads=128, req_seq_lens=rng.integers(1, 1500, 128), topk_width=600,
+                                   window=100, sink=True))
+    d = synth.to_device(w, "cuda")
+    a, la = pkg.sparse_mla_decode_fp4(**d)
+    for _ in range(20):
+        b, lb = pkg.sparse_mla_decode_fp4(**d)
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    compare(a[::17], la[::17], fp4.decode(w, list(range(0, 128, 17))))
+
+
+@pytest.mark.parametrize("tokens,heads", [(1, 16), (75, 64), (77, 64), (40, 128), (1300, 16)])
+def test_numbers_of_units(tokens, heads):
+    """Few units (shared evenly), more than half as many as multiprocessors (equal runs of blocks), and so many that runs
+    end between units; some tokens are empty."""
+    need_gpu()
+    rng = np.random.default_rng(tokens)
+    seqs = rng.integers(0, 400, tokens)
+    seqs[rng.random(tokens) < 0.1] = 0
+    if tokens == 1:
+        seqs[:] = 390
+    w = to_fp4(synth.make_workload(name=f"{tokens} tokens", seed=92, heads=heads, req_seq_lens=seqs, topk_width=260, window=70,
+                                   sink=False))
+    check(w, sorted(set(rng.integers(0, tokens, 60).tolist()) | {0, tokens - 1}))
+
+
+def test_logits_far_above_the_first_keys():
+    """Later keys' logits exceed the references, which are the first key's, by far more than the range that is left to
+    them, again and again: the references rise and what was summed falls."""
+    need_gpu()
+    w = synth.make_workload(name="rising", seed=93, heads=64, req_seq_lens=[900, 500], topk_width=0, window=600, sink=True)
+    w = to_fp4(w)
+    cache = w.kv_cache.copy()
+    for r in range(2):                                              # the rope part grows with the position
+        for pos in range(int(w.seq_lens[r])):
+            e = cache[w.block_table[r, pos // 64], pos % 64]
+            e[256:384] = synth.bf16_bits(np.full(64, 2.0 ** (pos / 100.0))).view(np.uint8)
+    q = w.q.copy()
+    q[..., 512:] = synth.bf16_bits(np.full(64, 1.0))[0]
+    w = dataclasses.replace(w, kv_cache=cache, q=q, softmax_scale=1.0)
+    check(w)
+
+
 def test_refusals():
     need_gpu()
     size = pkg.dsv4_sparse_mla_decode_fp4_workspace_size
