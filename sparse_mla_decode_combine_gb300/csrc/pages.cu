@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = p.pool.num_blocks, page = p.pool.page, M = p.max_blocks;
     int *refs = sm, *refs_new = sm + B, *free_list = sm + 2 * B;
-    int *first = sm + 3 * B, *kids = first + p.rows, *lens = kids + p.rows, *parent = lens + p.rows, *off = parent + p.rows_out;
+    int *first = sm + 3 * B, *kids = first + p.rows, *lens = kids + p.rows, *nps = lens + p.rows, *fulls = nps + p.rows;   // [rows]
+    int *parent = fulls + p.rows, *off = parent + p.rows_out;                                                        // [rows_out]
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the copy kernel waits for this grid itself)
 
     for (int i = tid; i < B; i += kPlanThreads)
@@ -281,7 +282,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
     for (int i = tid; i < p.rows; i += kPlanThreads) {
         first[i] = INT32_MAX;
         kids[i] = 0;
-        lens[i] = p.lens[i];
+        const int len = p.lens[i];   // (the divisions are done here, a row to a thread, and not by every row's warp)
+        lens[i] = len;
+        nps[i] = pages_of(len, page, M);
+        fulls[i] = p.share ? min(nps[i], max(len, 0) / page) : 0;
     }
     for (int r = tid; r < p.rows_out; r += kPlanThreads) {
         const int par = p.parent[r];
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
         const int par = parent[r];
         int need = 0;
         if (par >= 0) {
-            const int len = lens[par], np = pages_of(len, page, M), full = p.share ? min(np, max(len, 0) / page) : 0;
+            const int np = nps[par], full = fulls[par];
             const int32_t *src = p.table + (int64_t)par * p.table_stride;
             for (int j = full + lane; j < np; j += 32) {   // (shared pages take nothing)
                 const int v = src[j];
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
         const int par = parent[r];
         const bool ok = par >= 0 && off[r] >= 0;
         const int len = ok ? min(lens[par], (int)min((int64_t)M * page, (int64_t)INT32_MAX)) : 0;
-        const int np = pages_of(len, page, M), full = p.share ? min(np, max(len, 0) / page) : 0;
+        const int np = ok ? nps[par] : 0, full = ok ? fulls[par] : 0;
         if (lane == 0) {
             p.lens_out[r] = max(len, 0);
             if (par >= 0 && (!ok || lens[par] > (int64_t)M * page))
@@ -374,15 +378,14 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
         }
         // a row that finds no pages: its bad cells are flagged as those of any row
         if (par >= 0 && !ok) {
-            const int npf = pages_of(lens[par], page, M);
-            for (int j = lane; j < npf; j += 32)
+            for (int j = lane; j < nps[par]; j += 32)
                 if (src[j] < 0 || src[j] >= B)
                     atomicOr(p.status, kStatusBadIndex);
         }
     }
     __syncthreads();
     for (int i = warp; i < p.rows; i += kPlanThreads / 32) {
-        const int len = lens[i], np = pages_of(len, page, M), full = p.share ? min(np, max(len, 0) / page) : 0;
+        const int np = nps[i], full = fulls[i];
         const int c = kids[i], f = first[i];
         const bool has = f != INT32_MAX && off[f] >= 0;
         const int32_t *src = p.table + (int64_t)i * p.table_stride;
@@ -663,7 +666,7 @@ cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t stream)
     cudaError_t e;
     if (p.pool.num_blocks <= kSmallPages && p.rows <= kSmallRows && p.rows_out <= kSmallRows &&
         (int64_t)std::max(p.rows, p.rows_out) * p.max_blocks <= kSmallCells) {
-        const int bytes = 4 * (3 * p.pool.num_blocks + 3 * p.rows + 2 * p.rows_out);
+        const int bytes = 4 * (3 * p.pool.num_blocks + 5 * p.rows + 2 * p.rows_out);
         e = set_smem_once(reinterpret_cast<const void *>(fork_plan_small_kernel), bytes, kAttrForkSmall);
         if (e != cudaSuccess)
             return e;
