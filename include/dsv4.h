@@ -183,7 +183,7 @@ DSV4_API dsv4_status dsv4_selftest_wait_timeout(int64_t cycles, dsv4_stream_t st
  *
  * Arguments:
  *   q, q_out         BF16 [num_tokens, num_heads, 576], token strides in elements (even, >=
- *                    num_heads * 576); q_out may be q.  Both 4-byte aligned.
+ *                    num_heads * 576); q_out may be q (with its stride).  Both 4-byte aligned.
  *   num_heads        1..128; q_norm_weight fp32 [576] or NULL (all ones); eps >= 0.
  *   kv               BF16 [num_tokens, 576] (512 latent, then 64 rope), token stride even, >= 576.
  *   positions, slot_mapping  int64 [num_tokens].
@@ -464,7 +464,7 @@ DSV4_API size_t dsv4_sparse_mla_decode_fp4_workspace_size(int32_t num_tokens, in
  *
  * Arguments:
  *   q, q_out         BF16 [num_tokens, num_heads, 576], token strides in elements (even, >=
- *                    num_heads * 576); q_out may be q.  Both 4-byte aligned.
+ *                    num_heads * 576); q_out may be q (with its stride).  Both 4-byte aligned.
  *   num_heads        1..128; q_norm_weight fp32 [576] or NULL (all ones); eps >= 0.
  *   kv_norm_dims     0 (the key is not normalised), 512 (its latent) or 576 (all of it);
  *                    kv_norm_weight fp32 [kv_norm_dims] or NULL (all ones).

@@ -386,6 +386,12 @@ def _opt(dev: int, t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]
     return None if t is None else _on(dev, t, dtype, name)
 
 
+def _workspace(dev: int, t: torch.Tensor) -> int:
+    if not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    return _on(dev, t, torch.uint8, "workspace")
+
+
 # the current stream's handle without a Stream object (most of a small call's host time, otherwise)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -446,7 +452,7 @@ def dsv4_sparse_mla_decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, block_ta
         _opt(dev, req_idx, i32, "req_idx"), _on(dev, topk_idx, i32, "topk_idx"), _row_stride(topk_idx, "topk_idx", T, K), K,
         _opt(dev, topk_lens, i32, "topk_lens"), _on(dev, seq_lens, i32, "seq_lens"), T, H, int(window),
         _opt(dev, sink, torch.float32, "sink"), float(softmax_scale), _on(dev, out, bf16, "out"),
-        _opt(dev, lse, torch.float32, "lse"), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), st)
+        _opt(dev, lse, torch.float32, "lse"), _workspace(dev, workspace), workspace.numel(), st)
 
 
 def dsv4_qk_norm_rope_kv_insert_fp4(q: torch.Tensor, q_out: torch.Tensor, kv: torch.Tensor, positions: torch.Tensor,
@@ -522,7 +528,7 @@ def dsv4_cache_fork_rows(cache: torch.Tensor, block_table: torch.Tensor, seq_len
         _on(dev, block_table_out, i32, "block_table_out"), _row_stride(block_table_out, "block_table_out", Ro, M),
         _on(dev, seq_lens_out, i32, "seq_lens_out"), _on(dev, ref_counts, i32, "ref_counts"),
         _on(dev, ref_counts_out, i32, "ref_counts_out"), 1 if share else 0,
-        _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), st)
+        _workspace(dev, workspace), workspace.numel(), st)
 
 
 def dsv4_cache_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
@@ -546,7 +552,7 @@ def dsv4_cache_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens:
         _on(dev, seq_lens, i32, "seq_lens"), R, M, _on(dev, block_table_out, i32, "block_table_out"),
         _row_stride(block_table_out, "block_table_out", R, M), _on(dev, ref_counts, i32, "ref_counts"),
         _on(dev, ref_counts_out, i32, "ref_counts_out"), _on(dev, page_map, i32, "page_map"),
-        _on(dev, num_live, i32, "num_live"), _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(), st)
+        _on(dev, num_live, i32, "num_live"), _workspace(dev, workspace), workspace.numel(), st)
 
 
 def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_pages: torch.Tensor,
@@ -566,7 +572,7 @@ def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_
     i32 = torch.int32
     return lib.dsv4_cache_copy_pages(
         dp, dls, dB, sp, sls, sB, L, page, entry, _on(dev, src_pages, i32, "src_pages"),
-        _on(dev, dst_pages, i32, "dst_pages"), n, _on(dev, workspace, torch.uint8, "workspace"), workspace.numel(),
+        _on(dev, dst_pages, i32, "dst_pages"), n, _workspace(dev, workspace), workspace.numel(),
         st)
 
 

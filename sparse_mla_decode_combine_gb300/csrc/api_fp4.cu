@@ -230,6 +230,9 @@ extern "C" DSV4_API dsv4_status dsv4_qk_norm_rope_kv_insert_fp4(
         !aligned(kv, 4) || (k_out != nullptr && (!aligned(k_out, 4) || (k_out_token_stride & 1) != 0)) ||
         (num_slots > 0 && !aligned(kv_cache, 16)))
         return DSV4_ERR_INVALID_ARG;
+    // queries in place keep their rows' places; a key's blocks are read again after the first of k_out are written
+    if ((q_out == q && num_tokens > 1 && q_out_token_stride != q_token_stride) || k_out == kv)
+        return DSV4_ERR_INVALID_ARG;
     Insert4Params p{};
     if (device_info(&p.status, nullptr) != cudaSuccess)
         return DSV4_ERR_CUDA;

@@ -13,15 +13,21 @@
 //
 // Pipeline over two K tiles.  While the workers do the softmax of block b in one tile, S^T of block b + 1 runs
 // from the other; while they write block b + 2 over block b (behind P.V of b, half the value dims at a time),
-// P.V of b runs.  What the tensor cores read (a product of M 128 or 64 x N 64 x K 16 takes 6 or 4 KB of
-// operands) and what the workers write share 128 B a cycle of shared memory: about 5 k cycles for 128 keys,
-// which bounds a long list.  (One 128-key tile, whose steps form a chain, took 8.5 k.)
+// P.V of b runs.  (In one 128-key tile, whose steps form a chain, the
+// lists' work of 128 tokens x 128 heads took 180 us where the first form with two tiles took 168.)
 //   - a thread holds its eighth of a row's next entry in registers, loaded as those of the present block are
-//     used up; whole entries are prefetched to L2 two blocks before that;
+//     used up (two blocks ahead in registers: 140 against 135 us below; whole entries prefetched to L2: slower too);
 //   - the softmax takes the logits of the unit's first key as references, and exchanges maxima between warps only
 //     when a logit exceeds its head's reference by 40 (in log2 units): P and the sums are floating-point numbers,
 //     whose relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.
 //     The usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
+//
+// What bounds it.  128 tokens x 128 heads x 2176 keys: 127 us in this kernel (135 with the lists and the join), 0.61 PFLOP/s,
+// DRAM at 19 % of its peak, the tensor pipe busy 38 % of the time, shared memory's data path about 60 % besides the operands
+// that the products read.  A 64-key block takes 4.1 k cycles: the dequant warps spend 1.4 k of them on conversion and
+// swizzled stores, 1.1 k waiting for the gathered entries, 0.4 k for P.V, and the rest between; the two issuing warps and the
+// softmax wait for one another about half the time.  (With half of the dequant left out: 127 us in all, so two CTAs of a
+// 128-head token that shared it would gain 5 % at most; without P.V: 120.)
 //
 // Work.  A persistent CTA per multiprocessor takes an equal run of the blocks of all units (the end of one unit,
 // whole units, the start of another), so lists of any lengths fill the machine; with one unit per CTA, 256 equal

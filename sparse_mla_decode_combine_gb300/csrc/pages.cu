@@ -11,7 +11,9 @@
 // moves the pages of every layer.  The second is bound by HBM (each byte read and written once), the first by
 // the latency of its dependent steps, so it takes as few trips to global memory as it can: in a pool of up to
 // 16384 pages one CTA does it, with the counts, the rows' numbers and the free list in shared memory; larger
-// ones take a cluster of eight CTAs with a cluster barrier between the steps and the numbers in the workspace.
+// ones take a cluster of eight CTAs with a cluster barrier between the steps and the numbers in the workspace
+// (333 pages: 5.7 us for a compaction against 9.3; a fork of 64 rows: 9.7 against 14.2).  A compaction that moves
+// 418 MB takes 140 us where the bytes alone take 123 at the measured 6794 GB/s.
 // A short list of pages to copy needs no plan: one launch.
 #include <algorithm>
 #include <cuda_runtime.h>
@@ -717,7 +719,7 @@ cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t stream)
 
 cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t stream)
 {
-    const bool few = p.num_pages <= kCopyThreads;   // (7 pages in four layers: 3.1 against 5.0 us)
+    const bool few = p.num_pages <= kCopyThreads;   // (7 pages in four layers: 2.4 against 5.0 us)
     if (!few) {
         copy_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
         const cudaError_t e = cudaGetLastError();

@@ -297,3 +297,5 @@ def test_refusals():
         call(seq_lens=d["seq_lens"][:1])
     with pytest.raises(TypeError):
         call(q=d["q"].half())
+    with pytest.raises(ValueError):
+        call(workspace=torch.empty((ws.numel() // 16, 32), dtype=torch.uint8, device="cuda")[:, :16])

@@ -225,3 +225,9 @@ def test_refusals():
         call(slot_mapping=i.int())
     with pytest.raises(ValueError):
         call(k_out=kv[:, :512])
+    assert call(k_out=kv) == pkg.DSV4_ERR_INVALID_ARG
+    wide = torch.zeros((2, 3, 576), dtype=torch.bfloat16, device="cuda")[:, :2]
+    flat = torch.as_strided(wide, (2, 2, 576), (1152, 576, 1))
+    assert call(q=wide, q_out=flat) == pkg.DSV4_ERR_INVALID_ARG   # in place, but rows in other places
+    assert call(q=wide, q_out=wide) == pkg.DSV4_OK
+    assert pkg.dsv4_get_device_status() == pkg.DSV4_OK

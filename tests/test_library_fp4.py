@@ -38,12 +38,15 @@ def test_decode(lib):
 
 def test_insert(lib):
     #       q, qs, qo, qos, T, H, qw, kw, n, eps, kv, kvs, pos, slot, cs, maxp, cache, slots, ko, kos, st
-    good = [P, 1152, P, 1152, 1, 2, None, None, 512, 1e-6, P, 576, P, P, P, 8, P, 4, P, 576, None]
+    good = [P, 1152, P, 1152, 1, 2, None, None, 512, 1e-6, P, 576, P, P, P, 8, P, 4, ctypes.c_void_p(512), 576, None]
     call = lib.dsv4_qk_norm_rope_kv_insert_fp4
     each(call, good, [(5, 0), (5, 129), (9, float("nan")), (9, -1.0), (1, 1153), (1, 1150), (3, 1150), (11, 577), (11, 574),
                       (15, 0), (8, 64), (8, 575), (17, -1), (19, 577), (19, 100), (18, ctypes.c_void_p(2)), (0, None),
                       (10, ctypes.c_void_p(258)), (16, ctypes.c_void_p(8)), (12, None), (4, -1)], BAD)
     each(call, good, [(4, 0)], OK)
+    each(call, good, [(18, P)], BAD)                       # k_out is kv
+    good[4] = 2
+    each(call, good, [(3, 1154), (1, 1154)], BAD)          # queries in place with another stride
 
 
 def test_pages(lib):
