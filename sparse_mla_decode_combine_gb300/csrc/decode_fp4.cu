@@ -289,14 +289,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     }
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    // Only the lists come from the previous kernel, which began after everything before it in the stream had ended:
-    // the queries are there already, and where the unit is known they are read while the lists are made.
+    // Only the lists come from the previous kernel, which let this one begin after everything before it in the stream had
+    // ended: the queries are there already, and where the unit is known they are read while the lists are made.
     if (p.ctas_per_unit > 0 && is_worker) {
         const int unit = blockIdx.x / p.ctas_per_unit;
         store_q<kQLoads>(p, unit % p.num_tokens, unit / p.num_tokens * kNH, sQ, tid - 32 * kDequantWarp0);
     }
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    griddep_wait();
 
     // ---- this CTA's blocks
     Walk walk;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     after_sync();
     const uint32_t tmem = *tmem_slot;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the joining kernel waits for this grid itself)
+    griddep_launch();   // (the joining kernel waits for this grid itself)
     const int quad = warp & 3;                            // TMEM lane quadrant of this warp
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     Segment seg;
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4P
     const int t = unit % p.num_tokens, h0 = unit / p.num_tokens * kNH;
     const int h = kJoinHeads * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;   // head of the group
     const float sk = p.sink != nullptr ? p.sink[h0 + h] : -INFINITY;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    griddep_wait();
     const int2 join = __ldcg(p.joins + unit);   // (slot of the first part, parts); zeros for a unit of one part
     int first = 2 * unit * p.ctas_per_unit, most = p.ctas_per_unit;
     if (p.ctas_per_unit == 0) {
@@ -831,23 +831,11 @@ cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp4_kernel), kSmemBytes, kAttrFp4);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t r = cudaLaunchKernelEx(&cfg, decode_fp4_kernel, p);
+    const cudaError_t r = launch_dependent(decode_fp4_kernel, dim3((unsigned)p.grid), kThreads, kSmemBytes, stream, p);
     if (r != cudaSuccess || !p.split)
         return r;
-    cfg.gridDim = dim3((unsigned)p.num_tokens * (unsigned)p.groups, (unsigned)(std::min(p.num_heads, kNH) / kJoinHeads));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    return p.ctas_per_unit > 0 ? cudaLaunchKernelEx(&cfg, join_parts_kernel<4>, p) : cudaLaunchKernelEx(&cfg, join_parts_kernel<2>, p);
+    const dim3 grid((unsigned)p.num_tokens * (unsigned)p.groups, (unsigned)(std::min(p.num_heads, kNH) / kJoinHeads));
+    return launch_dependent(p.ctas_per_unit > 0 ? join_parts_kernel<4> : join_parts_kernel<2>, grid, kJoinThreads, 0, stream, p);
 }
 
 }  // namespace dsv4

@@ -16,6 +16,31 @@ constexpr int kRope4Offset = 256;
 constexpr int kScale4Offset = 384;
 constexpr int kScale4Block = 32;
 
+// A launch that may begin while the kernel before it in the stream ends (its CTAs are set up by then; 1 to 2 us a launch
+// in a stream of small kernels).  The kernel waits for that one with griddep_wait() before it touches memory, and only
+// then lets its own dependent begin: what that one reads ahead of its own wait was complete before this kernel.
+template <typename Params>
+cudaError_t launch_dependent(void (*kernel)(const Params), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const Params &p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 struct Insert4Params {
     const uint32_t *q;          // BF16 pairs
     int64_t q_stride;           // pairs per token

@@ -332,6 +332,7 @@ __device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int la
 template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kv_insert_fp4_kernel(const Insert4Params p)
 {
+    griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int quads = (p.num_heads + 3) / 4;
@@ -354,11 +355,8 @@ cudaError_t launch_qk_norm_rope_kv_insert_fp4(const Insert4Params &p, cudaStream
     const bool wide = (((reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.q_out) |
                          reinterpret_cast<uintptr_t>(p.q_w) | reinterpret_cast<uintptr_t>(p.cos_sin)) & 15u) == 0) &&
                       ((p.q_stride | p.q_out_stride) & 3) == 0;
-    if (wide)
-        qk_norm_rope_kv_insert_fp4_kernel<true><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-    else
-        qk_norm_rope_kv_insert_fp4_kernel<false><<<(unsigned)grid, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(wide ? qk_norm_rope_kv_insert_fp4_kernel<true> : qk_norm_rope_kv_insert_fp4_kernel<false>,
+                            dim3((unsigned)grid), kThreads, 0, stream, p);
 }
 
 }  // namespace dsv4

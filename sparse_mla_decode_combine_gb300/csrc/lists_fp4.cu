@@ -48,7 +48,8 @@ __device__ __forceinline__ unsigned insert(unsigned long long *tab, int bits, in
 
 __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params p)
 {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the decode waits for this grid itself)
+    griddep_wait();
+    griddep_launch();   // (the decode waits for this grid itself; the queries it reads ahead of that are there)
     extern __shared__ unsigned long long tab[];
     __shared__ int wsum[kPassLoads][kWarps];
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -196,8 +197,7 @@ cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream)
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(lists_fp4_kernel), q.smem_bytes, kAttrFp4Lists);
     if (e != cudaSuccess)
         return e;
-    lists_fp4_kernel<<<p.num_tokens, kThreads, q.smem_bytes, stream>>>(q);
-    return cudaGetLastError();
+    return launch_dependent(lists_fp4_kernel, dim3((unsigned)p.num_tokens), kThreads, (size_t)q.smem_bytes, stream, q);
 }
 
 }  // namespace dsv4

@@ -110,7 +110,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     const int rank = cluster_rank(), tid = threadIdx.x, lane = tid & 31;
     const int gtid = rank * kPlanThreads + tid, gwarp = gtid >> 5;
     const int B = p.pool.num_blocks, page = p.pool.page;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the copy kernel waits for this grid itself)
+    griddep_wait();
+    griddep_launch();   // (the moving kernel waits for this grid itself)
 
     // ---- the free pages of this CTA's part of the pool, and the rows' empty counters
     const int part = (B + kCluster - 1) / kCluster;
@@ -277,7 +278,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
     int *refs = sm, *refs_new = sm + B, *free_list = sm + 2 * B;
     int *first = sm + 3 * B, *kids = first + p.rows, *lens = kids + p.rows, *nps = lens + p.rows, *fulls = nps + p.rows;   // [rows]
     int *parent = fulls + p.rows, *off = parent + p.rows_out;                                                        // [rows_out]
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the copy kernel waits for this grid itself)
+    griddep_wait();
+    griddep_launch();   // (the moving kernel waits for this grid itself)
 
     for (int i = tid; i < B; i += kPlanThreads)
         refs[i] = refs_new[i] = p.refs[i];
@@ -414,7 +416,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     __shared__ int count[2];
     const int rank = cluster_rank(), tid = threadIdx.x;
     const int B = p.pool.num_blocks;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
+    griddep_launch();
 
     const int part = (B + kCluster - 1) / kCluster;
     const int lo = min(B, rank * part), hi = min(B, lo + part);
@@ -488,7 +491,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_small_kernel(const 
     const int B = p.pool.num_blocks;
     const int per = (B + kPlanThreads - 1) / kPlanThreads | 1;   // (odd: no bank conflicts between the threads' runs)
     int *refs = sm, *map = sm + B, *src = map + B, *dst = src + (B + 1) / 2;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
+    griddep_launch();
     for (int i = tid; i < B; i += kPlanThreads)
         refs[i] = p.refs[i];
     __syncthreads();
@@ -539,7 +543,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
 {
     const int gtid = cluster_rank() * kPlanThreads + threadIdx.x;
     constexpr int kStep = kCluster * kPlanThreads;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    griddep_wait();
+    griddep_launch();
     auto good = [&](int s, int d) { return s >= 0 && s < p.src.num_blocks && d >= 0 && d < p.dst.num_blocks; };
     for (int i = gtid; i < p.num_pages; i += kStep) {
         const int s = p.src_pages[i], d = p.dst_pages[i];
@@ -583,7 +588,7 @@ struct MoveParams {
 
 __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MoveParams p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    griddep_wait();
     const int tid = threadIdx.x;
     if (p.table != nullptr) {
         const int64_t cells = (int64_t)p.rows * p.max_blocks;
@@ -649,16 +654,7 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
 
 cudaError_t launch_move(const MoveParams &m, int sms, cudaStream_t stream)
 {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sms * 3));
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, move_pages_kernel, m);
+    return launch_dependent(move_pages_kernel, dim3((unsigned)(sms * 3)), kCopyThreads, 0, stream, m);
 }
 
 }  // namespace
@@ -672,11 +668,10 @@ cudaError_t launch_fork(const ForkParams &p, int sms, cudaStream_t stream)
         e = set_smem_once(reinterpret_cast<const void *>(fork_plan_small_kernel), bytes, kAttrForkSmall);
         if (e != cudaSuccess)
             return e;
-        fork_plan_small_kernel<<<1, kPlanThreads, bytes, stream>>>(p);
+        e = launch_dependent(fork_plan_small_kernel, dim3(1), kPlanThreads, (size_t)bytes, stream, p);
     } else {
-        fork_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+        e = launch_dependent(fork_plan_kernel, dim3(kCluster), kPlanThreads, 0, stream, p);
     }
-    e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     MoveParams m{};
@@ -694,11 +689,10 @@ cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t stream)
         e = set_smem_once(reinterpret_cast<const void *>(compact_plan_small_kernel), bytes, kAttrCompactSmall);
         if (e != cudaSuccess)
             return e;
-        compact_plan_small_kernel<<<1, kPlanThreads, bytes, stream>>>(p);
+        e = launch_dependent(compact_plan_small_kernel, dim3(1), kPlanThreads, (size_t)bytes, stream, p);
     } else {
-        compact_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
+        e = launch_dependent(compact_plan_kernel, dim3(kCluster), kPlanThreads, 0, stream, p);
     }
-    e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
     MoveParams m{};
@@ -721,8 +715,7 @@ cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t st
 {
     const bool few = p.num_pages <= kCopyThreads;   // (7 pages in four layers: 2.4 against 5.0 us)
     if (!few) {
-        copy_plan_kernel<<<kCluster, kPlanThreads, 0, stream>>>(p);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_dependent(copy_plan_kernel, dim3(kCluster), kPlanThreads, 0, stream, p);
         if (e != cudaSuccess)
             return e;
     }
