@@ -39,7 +39,7 @@ bool plan4(int num_tokens, int num_heads, int topk_width, int window, int sms, P
     pl->list_w = topk_width + window;
     pl->groups = (num_heads + 63) / 64;
     const int tile = decode_fp4_block_keys();
-    if ((long long)num_tokens * pl->groups * ((pl->list_w + tile - 1) / tile) > INT_MAX)
+    if ((long long)num_tokens * pl->groups * std::max(1, (pl->list_w + tile - 1) / tile) > INT_MAX)
         return false;
     // Half as many units as multiprocessors or fewer: each unit is shared by as many CTAs as there are for it (two
     // blocks or more to each).  Otherwise every multiprocessor's CTA takes an equal run of all blocks, which splits units

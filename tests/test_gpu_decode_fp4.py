@@ -276,6 +276,7 @@ def test_logits_far_above_the_first_keys():
 def test_refusals():
     need_gpu()
     size = pkg.dsv4_sparse_mla_decode_fp4_workspace_size
+    assert size(1 << 30, 128, 0, 0) == 0 and size(1 << 20, 16, 8192, 1 << 20) == 0      # more blocks than 2^31 - 1
     assert size(0, 16, 0, 0) > 0 and size(4, 64, 512, 128) >= 4 * 4 * 640 and size(2, 64, 0, 8193) > 0
     w = to_fp4(small(1))
     d = synth.to_device(w, "cuda")
