@@ -184,7 +184,8 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
     l.out = static_cast<uint16_t *>(out);
     l.lse = lse;
     l.status = status;
-    if (launch_lists_fp4(l, cs) != cudaSuccess)
+    l.smem_bytes = lists_fp4_smem_bytes(topk_width);
+    if (pl.ctas_per_unit == 0 && launch_lists_fp4(l, cs) != cudaSuccess)   // (else the decode makes them)
         return DSV4_ERR_CUDA;
     Decode4Params p{};
     p.groups = pl.groups;
@@ -205,6 +206,7 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(
     p.scale = softmax_scale;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
+    p.lists = l;
     p.status = status;
     return launch_decode_fp4(p, cs) == cudaSuccess ? DSV4_OK : DSV4_ERR_CUDA;
 }

@@ -46,7 +46,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
-#include "fp4.h"
+#include "lists_fp4.cuh"
 #include "tcgen05.cuh"
 
 namespace dsv4 {
@@ -60,6 +60,7 @@ constexpr int kDequantWarps = 16;        // warps 9-24: also Q's layout and the 
 constexpr int kPvWarp = 25;              // issues P.V
 constexpr int kThreads = 832;
 constexpr int kWorkers = 32 * kDequantWarps;
+constexpr int kListThreads = kThreads - kWorkers;   // make a list while the others bring Q
 constexpr int kBK = 64;                  // keys per block = MMA M of the logits
 constexpr int kDvTile = 128;             // value dims per tile = MMA M of P.V
 constexpr int kNH = 64;                  // heads per CTA = MMA N
@@ -90,6 +91,7 @@ constexpr int kSmallBytes = 1984;
 constexpr int kSmemBytes = kQBytes + 2 * kKBytes + kSmallBytes + 1024;   // + alignment slack
 constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                     // 9 16-byte Q pieces per worker
 static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
+static_assert(2 * kKBytes >= 16 * kMaxTopkWidth + 4 * lists::kPassLoads * kListThreads / 32, "a list's sets fit the K tiles");
 constexpr int kPartFloats = kNH * kLatent + 2 * kNH;   // a part in the workspace: O [64][512], then (m, l) [64]
 
 // instruction descriptors (kind::f16): D f32, A/B bf16, N = 64
@@ -243,6 +245,11 @@ __device__ __forceinline__ void write_o(const Decode4Params &p, int t, int h0, f
     }
 }
 
+struct SyncLists {   // the threads that make a list
+    __device__ __forceinline__ void operator()() const { named_bar(5, kListThreads); }
+    __device__ __forceinline__ bool any(bool v) const { return named_bar_or(5, kListThreads, v); }
+};
+
 __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Params p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -289,29 +296,43 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     }
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    // Only the lists come from the previous kernel, which let this one begin after everything before it in the stream had
-    // ended: the queries are there already, and where the unit is known they are read while the lists are made.
-    if (p.ctas_per_unit > 0 && is_worker) {
-        const int unit = blockIdx.x / p.ctas_per_unit;
-        store_q<kQLoads>(p, unit % p.num_tokens, unit / p.num_tokens * kNH, sQ, tid - 32 * kDequantWarp0);
-    }
-
     griddep_wait();
 
     // ---- this CTA's blocks
     Walk walk;
     int W = 0, G = 1, w0 = 0;
-    if (p.ctas_per_unit > 0) {   // an equal share of one unit
+    if (p.ctas_per_unit > 0) {   // an equal share of one unit, whose list is made here
         const int unit = blockIdx.x / p.ctas_per_unit, s = blockIdx.x % p.ctas_per_unit;
         walk.t = unit % p.num_tokens;
         walk.h0 = unit / p.num_tokens * kNH;
         walk.start = 0;
-        walk.len = __ldcg(p.lens + walk.t);
+        if (is_worker) {
+            store_q<kQLoads>(p, walk.t, walk.h0, sQ, tid - 32 * kDequantWarp0);
+        } else {   // (CTAs that share a token write the same slots to the same places)
+            const int ltid = warp < kDequantWarp0 ? tid : tid - kWorkers;
+            uint8_t *tab = gbase + kQBytes;   // (the K tiles' place)
+            const int len = lists::build<kListThreads>(p.lists, walk.t, ltid, reinterpret_cast<unsigned long long *>(tab),
+                                                       reinterpret_cast<int *>(tab + p.lists.smem_bytes), SyncLists());
+            if (ltid == 0)
+                first[0] = len;
+        }
+        before_sync();
+        __syncthreads();
+        walk.len = first[0];
         W = blocks_of(walk.len);
         G = max(1, min(p.ctas_per_unit, (W + kMinBlocks - 1) / kMinBlocks));
         walk.w = s < G ? run_start(s, W, G) : W;
         walk.w1 = s < G ? run_start(s + 1, W, G) : W;
-        before_sync();
+        if (s == 0 && G == 1 && tid == 0)
+            p.joins[unit] = make_int2(0, 0);
+        if (s == 0 && W == 0) {   // a token without a key
+            const int nhv = min(kNH, p.num_heads - walk.h0);
+            const int64_t row = (int64_t)walk.t * p.num_heads + walk.h0;
+            for (int i = tid; i < nhv * kLatent / 8; i += kThreads)
+                *reinterpret_cast<uint4 *>(p.out + row * kLatent + 8 * i) = make_uint4(0, 0, 0, 0);
+            if (p.lse != nullptr && tid < nhv)
+                p.lse[row + tid] = p.sink != nullptr ? p.sink[walk.h0 + tid] : -INFINITY;
+        }
     } else {                     // an equal run of the blocks of all units
         const int per = (p.num_tokens + kThreads - 1) / kThreads;
         const int t0 = min(p.num_tokens, tid * per), t1 = min(p.num_tokens, t0 + per);

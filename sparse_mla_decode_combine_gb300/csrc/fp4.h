@@ -91,9 +91,17 @@ struct Lists4Params {
     int32_t num_heads;
     uint16_t *out;
     float *lse;
-    int32_t smem_bytes;        // (set by the launch)
+    int32_t smem_bytes;        // shared memory for the sets: lists_fp4_smem_bytes(topk_width)
     unsigned *status;
 };
+// the hash set of a row; as a bitmap at least 262144 positions (131072 bytes at the widest rows)
+inline int lists_fp4_smem_bytes(int topk_width)
+{
+    int bytes = 32768;
+    while (bytes < 16 * topk_width)
+        bytes *= 2;
+    return bytes;
+}
 cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream);
 
 struct Decode4Params {
@@ -114,7 +122,8 @@ struct Decode4Params {
     int32_t ctas_per_unit;     // CTAs that share each unit; 0: every CTA takes an equal run of the blocks of all units
     bool split;                // whether several CTAs may share a unit
     float *parts;              // [2 * grid] partial results of units that several CTAs share
-    int2 *joins;               // [groups * T] such a unit's first part and their number, zeroed by the list kernel
+    int2 *joins;               // [groups * T] such a unit's first part and their number, zeros for units that are not shared
+    Lists4Params lists;        // ctas_per_unit > 0: the CTAs make their token's list themselves
     unsigned *status;
 };
 cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream);

@@ -1,178 +1,31 @@
-// lists_fp4.cu -- the cache slots that each token of a 4-bit decode attends to.
-//
-// The combine of dsv4_combine_topk_swa_indices (kept top-k entries in input order, then the window
-// ascending; entries that are not causal, lie in the window or repeat an earlier one are dropped), with
-// every kept position taken through the block table to its cache slot:
-//   slots[t][0 .. L) = block_table[row][p / page] * page + p % page  (-1 for a page out of range, which is
-//   flagged),  lens[t] = L.   Entries from L on are not written.
+// lists_fp4.cu -- a kernel of its own for the lists of cache slots (lists_fp4.cuh), one CTA per token: for decodes whose
+// CTAs take runs of the blocks of many tokens, and so need every token's length before they begin.
 //
 // A token without a key gets its outputs here: zeros, and the sink (or -inf) as its lse.
-//
-// One CTA per token.  The steps are dependent latencies (row, set, block table, store), so each is one round for rows
-// of up to 2048 entries, four to a thread, and loads that do not depend on one another are issued together.
-// Repeats are looked for in a bitmap of the positions (one 32-bit shared-memory OR an entry).  Only a row that has one,
-// or positions past the bitmap, goes through a hash set of 64-bit slots, (position << 32) | smallest top-k index, at
-// most half full, which says which of the repeats comes first: its 64-bit compare-and-swaps alone took 7 us for 2048
-// entries.  Ballots over up to four passes of the row give the output order.
-#include <algorithm>
-#include <climits>
 #include <cmath>
 
-#include "fp4.h"
+#include "lists_fp4.cuh"
 
 namespace dsv4 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kPassLoads = 4;
-constexpr unsigned long long kEmpty = ~0ull;
 
-__device__ __forceinline__ unsigned hash_pos(int v, int bits) { return ((unsigned)v * 0x9E3779B1u) >> (32 - bits); }
-
-__device__ __forceinline__ unsigned insert(unsigned long long *tab, int bits, int v, int i)
-{
-    const unsigned long long want = ((unsigned long long)(unsigned)v << 32) | (unsigned)i;
-    unsigned h = hash_pos(v, bits);
-    while (true) {   // (the set is at most half full)
-        const unsigned long long prev = atomicCAS(&tab[h], kEmpty, want);
-        if (prev == kEmpty)
-            return h;
-        if ((unsigned)(prev >> 32) == (unsigned)v) {
-            atomicMin(&tab[h], want);
-            return h;
-        }
-        h = (h + 1u) & ((1u << bits) - 1u);
-    }
-}
+struct SyncAll {
+    __device__ __forceinline__ void operator()() const { __syncthreads(); }
+    __device__ __forceinline__ bool any(bool v) const { return __syncthreads_or(v); }
+};
 
 __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params p)
 {
     griddep_wait();
-    griddep_launch();   // (the decode waits for this grid itself; the queries it reads ahead of that are there)
+    griddep_launch();   // (the decode waits for this grid itself)
     extern __shared__ unsigned long long tab[];
-    __shared__ int wsum[kPassLoads][kWarps];
-    const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t *trow = p.topk + (int64_t)t * p.topk_stride;
-    int tv[kPassLoads];
-#pragma unroll
-    for (int u = 0; u < kPassLoads; ++u)
-        tv[u] = u * kThreads + tid < p.topk_width ? __ldg(trow + u * kThreads + tid) : -1;
-    const int seq_len = p.seq_lens[t];
-    const int row = p.req_idx != nullptr ? p.req_idx[t] : t;
-    int n = p.topk_width;
-    if (p.topk_lens != nullptr) {
-        n = p.topk_lens[t];
-        n = n < 0 ? 0 : (n > p.topk_width ? p.topk_width : n);
-    }
+    __shared__ int wsum[lists::kPassLoads * kThreads / 32];
+    const int t = blockIdx.x, tid = threadIdx.x;
     if (tid < p.groups)
         p.joins[tid * gridDim.x + t] = make_int2(0, 0);
-    const int npass = (n + kThreads - 1) / kThreads;
-    const bool row_ok = row >= 0 && row < p.num_reqs;
-    const int32_t *bt_row = p.block_table + (int64_t)(row_ok ? row : 0) * p.bt_stride;
-    // window [win_lo, pos]; the top-k survivors are the first occurrences of positions in [0, win_lo)
-    const int pos = seq_len - 1;   // seq_len <= 0: nothing is visible
-    const long long lo = (long long)pos - p.window + 1;
-    const int win_lo = lo < 0 ? 0 : (int)lo;
-    const int swa = seq_len > 0 ? pos - win_lo + 1 : 0;
-    int32_t *out = p.slots + (int64_t)t * p.list_w;
-    auto slot_of = [&](int v) {
-        const int blk = v / p.page;
-        const int phys = row_ok && blk < p.max_blocks ? __ldg(bt_row + blk) : -1;
-        if (phys < 0 || phys >= p.num_blocks) {
-            atomicOr(p.status, kStatusBadIndex);
-            return -1;
-        }
-        return phys * p.page + (v - blk * p.page);
-    };
-#pragma unroll
-    for (int u = 0; u < kPassLoads; ++u)   // entries that are not selectable: -1
-        tv[u] = u * kThreads + tid < n && tv[u] >= 0 && tv[u] < win_lo ? tv[u] : -1;
-
-    // ---- is any position listed twice?
-    unsigned *seen = reinterpret_cast<unsigned *>(tab);
-    bool hashed = win_lo > p.smem_bytes * 8;
-    if (!hashed) {
-        for (int i = tid; i < (win_lo + 31) / 32; i += kThreads)
-            seen[i] = 0u;
-        __syncthreads();
-        bool twice = false;
-#pragma unroll
-        for (int u = 0; u < kPassLoads; ++u)
-            if (tv[u] >= 0)
-                twice |= (atomicOr(&seen[tv[u] >> 5], 1u << (tv[u] & 31)) >> (tv[u] & 31)) & 1u;
-#pragma unroll 1
-        for (int i = kPassLoads * kThreads + tid; i < n; i += kThreads) {
-            const int v = __ldg(trow + i);
-            if (v >= 0 && v < win_lo)
-                twice |= (atomicOr(&seen[v >> 5], 1u << (v & 31)) >> (v & 31)) & 1u;
-        }
-        hashed = __syncthreads_or(twice);
-    }
-    // the entries' slots do not depend on which of them are kept
-    int sv[kPassLoads];
-#pragma unroll
-    for (int u = 0; u < kPassLoads; ++u)
-        sv[u] = tv[u] >= 0 ? slot_of(tv[u]) : -1;
-    int bits = 6;
-    while ((1 << bits) < 2 * n)
-        ++bits;
-    unsigned hs[kPassLoads];
-    if (hashed) {
-        for (int i = tid; i < 1 << bits; i += kThreads)
-            tab[i] = kEmpty;
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kPassLoads; ++u)
-            hs[u] = tv[u] >= 0 ? insert(tab, bits, tv[u], u * kThreads + tid) : 0u;
-#pragma unroll 1
-        for (int i = kPassLoads * kThreads + tid; i < n; i += kThreads) {
-            const int v = __ldg(trow + i);
-            if (v >= 0 && v < win_lo)
-                insert(tab, bits, v, i);
-        }
-        __syncthreads();
-    }
-    int total = 0;
-#pragma unroll 1
-    for (int pg = 0; pg < npass; pg += kPassLoads) {
-        unsigned bal[kPassLoads];
-        int vg[kPassLoads];
-#pragma unroll
-        for (int u = 0; u < kPassLoads; ++u) {
-            const int i = (pg + u) * kThreads + tid;
-            int v = pg == 0 ? tv[u] : (i < n ? __ldg(trow + i) : -1);
-            v = v < win_lo ? v : -1;
-            vg[u] = v;
-            bool keep = v >= 0;
-            if (keep && hashed) {
-                unsigned h = hs[u];
-                if (pg != 0) {
-                    h = hash_pos(v, bits);
-                    while ((unsigned)(tab[h] >> 32) != (unsigned)v)
-                        h = (h + 1u) & ((1u << bits) - 1u);
-                }
-                keep = (unsigned)tab[h] == (unsigned)i;
-            }
-            bal[u] = __ballot_sync(0xffffffffu, keep);
-            if (lane == 0)
-                wsum[u][warp] = __popc(bal[u]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kPassLoads; ++u) {
-            const int x = lane < kWarps ? wsum[u][lane] : 0;
-            const int before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
-            const int rank = total + before + __popc(bal[u] & ((1u << lane) - 1u));
-            total += __reduce_add_sync(0xffffffffu, x);
-            if ((bal[u] >> lane) & 1u)
-                out[rank] = pg == 0 ? sv[u] : slot_of(vg[u]);
-        }
-        __syncthreads();   // wsum is rewritten by the next group of passes
-    }
-    for (int k = tid; k < swa; k += kThreads)
-        out[total + k] = slot_of(win_lo + k);
-    const int len = total + swa;
+    const int len = lists::build<kThreads>(p, t, tid, tab, wsum, SyncAll());
     if (tid == 0)
         p.lens[t] = len;
     if (len == 0) {
@@ -189,15 +42,10 @@ cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream)
 {
     if (p.num_tokens <= 0)
         return cudaSuccess;
-    int bits = 6;
-    while ((1 << bits) < 2 * p.topk_width)
-        ++bits;
-    Lists4Params q = p;
-    q.smem_bytes = std::max(8 << bits, 32768);   // the hash set; as a bitmap at least 262144 positions
-    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(lists_fp4_kernel), q.smem_bytes, kAttrFp4Lists);
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(lists_fp4_kernel), p.smem_bytes, kAttrFp4Lists);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(lists_fp4_kernel, dim3((unsigned)p.num_tokens), kThreads, (size_t)q.smem_bytes, stream, q);
+    return launch_dependent(lists_fp4_kernel, dim3((unsigned)p.num_tokens), kThreads, (size_t)p.smem_bytes, stream, p);
 }
 
 }  // namespace dsv4
