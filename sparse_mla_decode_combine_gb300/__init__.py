@@ -382,23 +382,35 @@ def _on(dev: int, t: torch.Tensor, dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def _opt(dev: int, t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
-    return None if t is None else _on(dev, t, dtype, name)
+def _vec(dev: int, t: Optional[torch.Tensor], dtype, n: int, name: str) -> Optional[int]:
+    """The pointer of a contiguous tensor of n values on device `dev` (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: must be {n} contiguous values on the current CUDA device")
+    return t.data_ptr()
 
 
 def _workspace(dev: int, t: torch.Tensor) -> int:
-    if not t.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-    return _on(dev, t, torch.uint8, "workspace")
+    if t.dtype is not torch.uint8:
+        raise TypeError(f"workspace: expected {torch.uint8}, got {t.dtype}")
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace: must be contiguous, on the current CUDA device")
+    return t.data_ptr()
 
 
 # the current stream's handle without a Stream object (most of a small call's host time, otherwise)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _device_and_stream(stream):
     """The current device's number, and the stream's handle (that device's current one for None)."""
-    dev = torch.cuda.current_device()
+    dev = _current_device() if _current_device is not None and torch.cuda.is_initialized() else torch.cuda.current_device()
     if stream is None:
         return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
     return dev, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -406,7 +418,7 @@ def _device_and_stream(stream):
 
 def _row_stride(t: torch.Tensor, name: str, rows: int, width: int) -> int:
     """The stride of dim 0 (of a single row: any that is wide enough); rows must not overlap."""
-    s = t.stride(0)
+    s = t.stride()[0]
     if s < width:
         if rows > 1:
             raise ValueError(f"{name}: rows must not overlap")
@@ -432,27 +444,21 @@ def dsv4_sparse_mla_decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, block_ta
     blocks, page, entry = kv_cache.shape
     R, M = block_table.shape
     Tk, K = topk_idx.shape
-    if D != 576 or (H > 1 and q.stride(1) != 576):
+    if D != 576 or (H > 1 and q.stride()[1] != 576):
         raise ValueError("q: heads must be contiguous rows of 576")
     if entry != 400 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache: must be contiguous, with entries of 400 bytes")
-    if out.shape != (T, H, 512) or not out.is_contiguous():
-        raise ValueError("out: must be contiguous [tokens, heads, 512]")
-    if lse is not None and (lse.shape != (T, H) or not lse.is_contiguous()):
-        raise ValueError("lse: must be contiguous [tokens, heads]")
-    if Tk != T or seq_lens.shape != (T,) or (topk_lens is not None and topk_lens.shape != (T,)) or \
-            (req_idx is not None and req_idx.shape != (T,)):
-        raise ValueError("topk_idx, topk_lens, seq_lens, req_idx: must have a row for each token")
-    if sink is not None and sink.shape != (H,):
-        raise ValueError("sink: must have a value for each head")
-    i32, bf16 = torch.int32, torch.bfloat16
+    if Tk != T:
+        raise ValueError("topk_idx: must have a row for each token")
+    i32, f32 = torch.int32, torch.float32
     return lib.dsv4_sparse_mla_decode_fp4(
-        _on(dev, q, bf16, "q"), _row_stride(q, "q", T, H * 576), _on(dev, kv_cache, torch.uint8, "kv_cache"), blocks, page,
-        _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M), M, R,
-        _opt(dev, req_idx, i32, "req_idx"), _on(dev, topk_idx, i32, "topk_idx"), _row_stride(topk_idx, "topk_idx", T, K), K,
-        _opt(dev, topk_lens, i32, "topk_lens"), _on(dev, seq_lens, i32, "seq_lens"), T, H, int(window),
-        _opt(dev, sink, torch.float32, "sink"), float(softmax_scale), _on(dev, out, bf16, "out"),
-        _opt(dev, lse, torch.float32, "lse"), _workspace(dev, workspace), workspace.numel(), st)
+        _on(dev, q, torch.bfloat16, "q"), _row_stride(q, "q", T, H * 576), _on(dev, kv_cache, torch.uint8, "kv_cache"),
+        blocks, page, _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M), M, R,
+        _vec(dev, req_idx, i32, T, "req_idx"), _on(dev, topk_idx, i32, "topk_idx"),
+        _row_stride(topk_idx, "topk_idx", T, K), K, _vec(dev, topk_lens, i32, T, "topk_lens"),
+        _vec(dev, seq_lens, i32, T, "seq_lens"), T, H, int(window), _vec(dev, sink, f32, H, "sink"), float(softmax_scale),
+        _vec(dev, out, torch.bfloat16, T * H * 512, "out"), _vec(dev, lse, f32, T * H, "lse"), _workspace(dev, workspace),
+        workspace.numel(), st)
 
 
 def dsv4_qk_norm_rope_kv_insert_fp4(q: torch.Tensor, q_out: torch.Tensor, kv: torch.Tensor, positions: torch.Tensor,
@@ -466,29 +472,25 @@ def dsv4_qk_norm_rope_kv_insert_fp4(q: torch.Tensor, q_out: torch.Tensor, kv: to
     lib = _lib or load_library()
     dev, st = _device_and_stream(stream)
     T, H, D = q.shape
-    bf16, i64, f32 = torch.bfloat16, torch.int64, torch.float32
-    if D != 576 or q_out.shape != (T, H, D) or (H > 1 and (q.stride(1) != 576 or q_out.stride(1) != 576)):
+    bf16, f32 = torch.bfloat16, torch.float32
+    if D != 576 or q_out.shape != (T, H, D) or (H > 1 and (q.stride()[1] != 576 or q_out.stride()[1] != 576)):
         raise ValueError("q, q_out: heads must be contiguous rows of 576, and the shapes the same")
     if kv.shape != (T, 576) or (k_out is not None and k_out.shape != (T, 576)):
         raise ValueError("kv, k_out: must be [tokens, 576]")
-    if positions.shape != (T,) or slot_mapping.shape != (T,):
-        raise ValueError("positions, slot_mapping: must have a value for each token")
     max_pos, width = cos_sin_cache.shape
-    if width != 64 or not cos_sin_cache.is_contiguous():
-        raise ValueError("cos_sin_cache: must be contiguous [max_position, 64]")
+    if width != 64:
+        raise ValueError("cos_sin_cache: must be [max_position, 64]")
     if kv_cache.shape[-1] != 400 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache: must be contiguous, with entries of 400 bytes")
-    if (q_norm_weight is not None and q_norm_weight.shape != (576,)) or \
-            (kv_norm_weight is not None and kv_norm_weight.shape != (kv_norm_dims,)):
-        raise ValueError("norm weights: must have a value for each normalised dim")
     return lib.dsv4_qk_norm_rope_kv_insert_fp4(
         _on(dev, q, bf16, "q"), _row_stride(q, "q", T, H * 576), _on(dev, q_out, bf16, "q_out"),
-        _row_stride(q_out, "q_out", T, H * 576), T, H, _opt(dev, q_norm_weight, f32, "q_norm_weight"),
-        _opt(dev, kv_norm_weight, f32, "kv_norm_weight"), int(kv_norm_dims), float(eps), _on(dev, kv, bf16, "kv"),
-        _row_stride(kv, "kv", T, 576), _on(dev, positions, i64, "positions"), _on(dev, slot_mapping, i64, "slot_mapping"),
-        _on(dev, cos_sin_cache, f32, "cos_sin_cache"), max_pos, _on(dev, kv_cache, torch.uint8, "kv_cache"),
-        kv_cache.numel() // 400, _opt(dev, k_out, bf16, "k_out"),
-        0 if k_out is None else _row_stride(k_out, "k_out", T, 576), st)
+        _row_stride(q_out, "q_out", T, H * 576), T, H, _vec(dev, q_norm_weight, f32, 576, "q_norm_weight"),
+        _vec(dev, kv_norm_weight, f32, kv_norm_dims, "kv_norm_weight"), int(kv_norm_dims), float(eps),
+        _on(dev, kv, bf16, "kv"), _row_stride(kv, "kv", T, 576), _vec(dev, positions, torch.int64, T, "positions"),
+        _vec(dev, slot_mapping, torch.int64, T, "slot_mapping"), _vec(dev, cos_sin_cache, f32, 64 * max_pos, "cos_sin_cache"),
+        max_pos, _on(dev, kv_cache, torch.uint8, "kv_cache"), kv_cache.numel() // 400,
+        None if k_out is None else _on(dev, k_out, bf16, "k_out"), 0 if k_out is None else _row_stride(k_out, "k_out", T, 576),
+        st)
 
 
 def _pool(dev: int, cache: torch.Tensor, name: str):
@@ -518,17 +520,15 @@ def dsv4_cache_fork_rows(cache: torch.Tensor, block_table: torch.Tensor, seq_len
     i32 = torch.int32
     R, M = block_table.shape
     (Ro,) = parent.shape
-    if seq_lens.shape != (R,) or seq_lens_out.shape != (Ro,) or block_table_out.shape != (Ro, M):
-        raise ValueError("block_table_out, seq_lens, seq_lens_out: must have a row for each row, and max_blocks cells")
-    if ref_counts.shape != (B,) or ref_counts_out.shape != (B,):
-        raise ValueError("ref_counts, ref_counts_out: must have a count for each page")
+    if block_table_out.shape != (Ro, M):
+        raise ValueError("block_table_out: must have a row for each parent, and max_blocks cells")
     return lib.dsv4_cache_fork_rows(
         ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M),
-        _on(dev, seq_lens, i32, "seq_lens"), R, _on(dev, parent, i32, "parent"), Ro, M,
+        _vec(dev, seq_lens, i32, R, "seq_lens"), R, _vec(dev, parent, i32, Ro, "parent"), Ro, M,
         _on(dev, block_table_out, i32, "block_table_out"), _row_stride(block_table_out, "block_table_out", Ro, M),
-        _on(dev, seq_lens_out, i32, "seq_lens_out"), _on(dev, ref_counts, i32, "ref_counts"),
-        _on(dev, ref_counts_out, i32, "ref_counts_out"), 1 if share else 0,
-        _workspace(dev, workspace), workspace.numel(), st)
+        _vec(dev, seq_lens_out, i32, Ro, "seq_lens_out"), _vec(dev, ref_counts, i32, B, "ref_counts"),
+        _vec(dev, ref_counts_out, i32, B, "ref_counts_out"), 1 if share else 0, _workspace(dev, workspace),
+        workspace.numel(), st)
 
 
 def dsv4_cache_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
@@ -543,16 +543,14 @@ def dsv4_cache_compact(cache: torch.Tensor, block_table: torch.Tensor, seq_lens:
     ptr, L, ls, B, page, entry = _pool(dev, cache, "cache")
     i32 = torch.int32
     R, M = block_table.shape
-    if seq_lens.shape != (R,) or block_table_out.shape != (R, M):
-        raise ValueError("seq_lens, block_table_out: must have a row for each row of block_table")
-    if ref_counts.shape != (B,) or ref_counts_out.shape != (B,) or page_map.shape != (B,) or num_live.shape != (1,):
-        raise ValueError("ref_counts, ref_counts_out, page_map: must have a value for each page, num_live one value")
+    if block_table_out.shape != (R, M):
+        raise ValueError("block_table_out: must have the shape of block_table")
     return lib.dsv4_cache_compact(
         ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M),
-        _on(dev, seq_lens, i32, "seq_lens"), R, M, _on(dev, block_table_out, i32, "block_table_out"),
-        _row_stride(block_table_out, "block_table_out", R, M), _on(dev, ref_counts, i32, "ref_counts"),
-        _on(dev, ref_counts_out, i32, "ref_counts_out"), _on(dev, page_map, i32, "page_map"),
-        _on(dev, num_live, i32, "num_live"), _workspace(dev, workspace), workspace.numel(), st)
+        _vec(dev, seq_lens, i32, R, "seq_lens"), R, M, _on(dev, block_table_out, i32, "block_table_out"),
+        _row_stride(block_table_out, "block_table_out", R, M), _vec(dev, ref_counts, i32, B, "ref_counts"),
+        _vec(dev, ref_counts_out, i32, B, "ref_counts_out"), _vec(dev, page_map, i32, B, "page_map"),
+        _vec(dev, num_live, i32, 1, "num_live"), _workspace(dev, workspace), workspace.numel(), st)
 
 
 def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_pages: torch.Tensor,
@@ -566,14 +564,10 @@ def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_
     sp, sL, sls, sB, spage, sentry = _pool(dev, src_cache, "src_cache")
     if (sL, spage, sentry) != (L, page, entry):
         raise ValueError("dst_cache, src_cache: must have the same layers, page and entry sizes")
-    (n,) = src_pages.shape
-    if dst_pages.shape != (n,):
-        raise ValueError("src_pages, dst_pages: must have the same length")
-    i32 = torch.int32
+    n, i32 = src_pages.numel(), torch.int32
     return lib.dsv4_cache_copy_pages(
-        dp, dls, dB, sp, sls, sB, L, page, entry, _on(dev, src_pages, i32, "src_pages"),
-        _on(dev, dst_pages, i32, "dst_pages"), n, _workspace(dev, workspace), workspace.numel(),
-        st)
+        dp, dls, dB, sp, sls, sB, L, page, entry, _vec(dev, src_pages, i32, n, "src_pages"),
+        _vec(dev, dst_pages, i32, n, "dst_pages"), n, _workspace(dev, workspace), workspace.numel(), st)
 
 
 def dsv4_get_device_status(stream=None) -> int:

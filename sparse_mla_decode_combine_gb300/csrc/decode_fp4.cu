@@ -2,7 +2,8 @@
 //
 // Operation (per token t, head h, over the token's combined list of positions):
 //   s_p = scale * q_h . k_p (576 dims),  lse_h = ln(sum_p e^{s_p} + e^{sink_h}),  out_h = sum_p e^{s_p - lse_h} v_p
-// The lists of cache slots come from the list kernel (lists_fp4.cu) ahead of this one in the stream.
+// The lists of cache slots come from the list kernel (lists_fp4.cu) ahead of this one in the stream, or, with few units, are
+// made here by the ten warps that do not bring Q (a launch less: 10.7 against 12.4 us for 2 tokens x 16 heads in a loop of calls).
 //
 // Contraction.  All heads share one key set, so a (token, 64 heads) unit is a pair of dense products, run
 // transposed (keys and value dims on the M side of the tensor tile):
@@ -13,8 +14,8 @@
 //
 // Pipeline over two K tiles.  While the workers do the softmax of block b in one tile, S^T of block b + 1 runs
 // from the other; while they write block b + 2 over block b (behind P.V of b, half the value dims at a time),
-// P.V of b runs.  (In one 128-key tile, whose steps form a chain, the
-// lists' work of 128 tokens x 128 heads took 180 us where the first form with two tiles took 168.)
+// P.V of b runs.  (In one 128-key tile, whose steps form a chain, 128 tokens x 128 heads took 180 us where the first
+// form with two tiles took 168.)
 //   - a thread holds its eighth of a row's next entry in registers, loaded as those of the present block are
 //     used up (two blocks ahead in registers: 140 against 135 us below; whole entries prefetched to L2: slower too);
 //   - the softmax takes the logits of the unit's first key as references, and exchanges maxima between warps only
@@ -22,14 +23,17 @@
 //     whose relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.
 //     The usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
 //
-// What bounds it.  128 tokens x 128 heads x 2176 keys: 127 us in this kernel (135 with the lists and the join), 0.61 PFLOP/s,
-// DRAM at 19 % of its peak, the tensor pipe busy 38 % of the time, shared memory's data path about 60 % besides the operands
-// that the products read.  A 64-key block takes 4.1 k cycles: the dequant warps spend 1.4 k of them on conversion and
-// swizzled stores, 1.1 k waiting for the gathered entries, 0.4 k for P.V, and the rest between; the two issuing warps and the
-// softmax wait for one another about half the time.  (With half of the dequant left out: 127 us in all, so two CTAs of a
-// 128-head token that shared it would gain 5 % at most; without P.V: 120.)
+// What bounds it.  128 tokens x 128 heads x 2176 keys: 127 us in this kernel (134 with the lists and the join), 0.61 PFLOP/s,
+// DRAM at 19 % of its peak, the tensor pipe busy 38 % of the time, issue slots 53 %.  A 64-key block takes 3.7 k cycles where
+// the loop runs freely (4.1 k with the units' ends), and its steps are a chain over twice that, since its tile is one of two: the
+// dequant 3.0 k to its last chunk, S^T 1.2 k after that, the softmax 1.7 k, P.V 1.4 k to the first chunks' release.  S^T of one block and P.V of
+// the other meet and then take 116 of the 128 bytes a cycle of shared memory; letting either go first, or issuing both
+// from one warp (a product takes it about 50 cycles), was slower: 140 and 159 us.  The dequant warps are busy for all of a block's
+// time too, 1.4 k of it with conversion and stores and 1.1 k waiting for scale bytes and entries, so neither side alone
+// is worth much: half of the dequant left out gives 127 us in all, no P.V 120, no gather 118.
 //
-// Work.  A persistent CTA per multiprocessor takes an equal run of the blocks of all units (the end of one unit,
+// Work.  With up to half as many units as multiprocessors, as many CTAs as there are for it share each unit evenly.  Otherwise a
+// persistent CTA per multiprocessor takes an equal run of the blocks of all units (the end of one unit,
 // whole units, the start of another), so lists of any lengths fill the machine; with one unit per CTA, 256 equal
 // units on 152 multiprocessors take two full waves.  26 warps: warp 0 issues S^T, warp 25 P.V, warps 1-8 do the
 // softmax and the epilogue, warps 9-24 bring Q and the K tiles; the roles meet only at mbarriers, so the first blocks
