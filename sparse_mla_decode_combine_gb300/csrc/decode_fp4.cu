@@ -64,7 +64,8 @@ constexpr int kDequantWarps = 16;        // warps 9-24: also Q's layout and the 
 constexpr int kPvWarp = 25;              // issues P.V
 constexpr int kThreads = 832;
 constexpr int kWorkers = 32 * kDequantWarps;
-constexpr int kListThreads = kThreads - kWorkers;   // make a list while the others bring Q
+constexpr int kListThreads = kThreads - kWorkers;   // make a list while the others bring Q,
+constexpr int kListLoads = 4;            // each with so many of its entries in flight: 1280 in all
 constexpr int kBK = 64;                  // keys per block = MMA M of the logits
 constexpr int kDvTile = 128;             // value dims per tile = MMA M of P.V
 constexpr int kNH = 64;                  // heads per CTA = MMA N
@@ -95,7 +96,8 @@ constexpr int kSmallBytes = 1984;
 constexpr int kSmemBytes = kQBytes + 2 * kKBytes + kSmallBytes + 1024;   // + alignment slack
 constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                     // 9 16-byte Q pieces per worker
 static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
-static_assert(2 * kKBytes >= 16 * kMaxTopkWidth + 4 * lists::kPassLoads * kListThreads / 32, "a list's sets fit the K tiles");
+static_assert(2 * kKBytes >= 32768 + 4 * kListLoads * kListThreads / 32, "a list's sets fit the K tiles");
+static_assert(16 * kListLoads * kListThreads <= 32768, "the rows of lists made here");
 constexpr int kPartFloats = kNH * kLatent + 2 * kNH;   // a part in the workspace: O [64][512], then (m, l) [64]
 
 // instruction descriptors (kind::f16): D f32, A/B bf16, N = 64
@@ -254,6 +256,12 @@ struct SyncLists {   // the threads that make a list
     __device__ __forceinline__ bool any(bool v) const { return named_bar_or(5, kListThreads, v); }
 };
 
+// CTAs that share a unit of W blocks evenly
+__device__ __forceinline__ int shares_of(const Decode4Params &p, int W) { return max(1, min(p.ctas_per_unit, (W + kMinBlocks - 1) / kMinBlocks)); }
+
+// kShared: few units, each shared evenly by p.ctas_per_unit CTAs, which make its token's list themselves (p.own_lists) unless
+// the rows are wide; otherwise every CTA takes an equal run of the blocks of all units.  (In one kernel the second kind took 2 % longer: registers.)
+template <bool kShared>
 __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Params p)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -300,36 +308,46 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     }
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    griddep_wait();
-
     // ---- this CTA's blocks
     Walk walk;
     int W = 0, G = 1, w0 = 0;
-    if (p.ctas_per_unit > 0) {   // an equal share of one unit, whose list is made here
+    if constexpr (kShared) {   // an equal share of one unit
         const int unit = blockIdx.x / p.ctas_per_unit, s = blockIdx.x % p.ctas_per_unit;
         walk.t = unit % p.num_tokens;
         walk.h0 = unit / p.num_tokens * kNH;
         walk.start = 0;
+        if (p.own_lists)
+            griddep_wait();
         if (is_worker) {
+            // (where a list kernel is ahead, it let this one begin after everything before it in the stream had ended: the
+            // queries are there, and come in while the lists are made)
             store_q<kQLoads>(p, walk.t, walk.h0, sQ, tid - 32 * kDequantWarp0);
-        } else {   // (CTAs that share a token write the same slots to the same places)
+        } else if (p.own_lists) {
             const int ltid = warp < kDequantWarp0 ? tid : tid - kWorkers;
+            // Every CTA of a token writes the slots of its top-k entries, the same ones to the same places, and those of the
+            // window's part that it needs.
             uint8_t *tab = gbase + kQBytes;   // (the K tiles' place)
-            const int len = lists::build<kListThreads>(p.lists, walk.t, ltid, reinterpret_cast<unsigned long long *>(tab),
-                                                       reinterpret_cast<int *>(tab + p.lists.smem_bytes), SyncLists());
+            const int len = lists::build<kListThreads, kListLoads>(
+                p.lists, walk.t, ltid, reinterpret_cast<unsigned long long *>(tab),
+                reinterpret_cast<int *>(tab + p.lists.smem_bytes), SyncLists(), [&](int n) {
+                    const int blocks = blocks_of(n), g = shares_of(p, blocks);
+                    return s < g ? make_int2(run_start(s, blocks, g) * kBK, run_start(s + 1, blocks, g) * kBK) : make_int2(n, n);
+                });
             if (ltid == 0)
                 first[0] = len;
         }
+        if (!p.own_lists)
+            griddep_wait();
         before_sync();
         __syncthreads();
-        walk.len = first[0];
+        walk.len = p.own_lists ? first[0] : __ldcg(p.lens + walk.t);
         W = blocks_of(walk.len);
-        G = max(1, min(p.ctas_per_unit, (W + kMinBlocks - 1) / kMinBlocks));
+        G = shares_of(p, W);
         walk.w = s < G ? run_start(s, W, G) : W;
         walk.w1 = s < G ? run_start(s + 1, W, G) : W;
-        if (s == 0 && G == 1 && tid == 0)
+        if (p.own_lists && s == 0 && G == 1 && tid == 0)
             p.joins[unit] = make_int2(0, 0);
-        if (s == 0 && W == 0) {   // a token without a key
+        if (p.own_lists && s == 0 && W == 0) {   // a token without a key
             const int nhv = min(kNH, p.num_heads - walk.h0);
             const int64_t row = (int64_t)walk.t * p.num_heads + walk.h0;
             for (int i = tid; i < nhv * kLatent / 8; i += kThreads)
@@ -338,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 p.lse[row + tid] = p.sink != nullptr ? p.sink[walk.h0 + tid] : -INFINITY;
         }
     } else {                     // an equal run of the blocks of all units
+        griddep_wait();
         const int per = (p.num_tokens + kThreads - 1) / kThreads;
         const int t0 = min(p.num_tokens, tid * per), t1 = min(p.num_tokens, t0 + per);
         int mine = 0;
@@ -500,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 load_piece(entry(slot0), 1);
                 load_rest(entry(slot0));
             }
-            if (n > 0 || p.ctas_per_unit == 0) {
+            if (n > 0 || !kShared) {
                 if (n > 0)   // S^T of the last segment's last block is done with its Q
                     mbar_wait(bar_s + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
                 store_q<3>(p, t, h0, sQ, wid);
@@ -555,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     load_rest(en);
                 pre_ok = ok_next;
             }
-            if (p.ctas_per_unit > 0) {   // the CTA's only segment: its output is written by all
+            if (kShared) {   // the CTA's only segment: its output is written by all
                 named_bar(4, 32 * kSoftmaxWarps + kWorkers);   // (the factors are there)
                 mbar_wait(bar_pv + 32 * ((g - 1) & 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
                 after_sync();
@@ -711,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 const int slot = walk.start > w0 ? 1 : 0;   // (the unit begins in this run, or with it or before it)
                 part = p.parts + (size_t)(2 * blockIdx.x + slot) * kPartFloats;
                 if (seg.kb == 0 && wid == 0) {   // its first part says how many there are, and which
-                    const int n = p.ctas_per_unit > 0 ? G : run_of(walk.start + blocks_of(seg.len) - 1, W, G) - (int)blockIdx.x + 1;
+                    const int n = kShared ? G : run_of(walk.start + blocks_of(seg.len) - 1, W, G) - (int)blockIdx.x + 1;
                     p.joins[h0 / kNH * p.num_tokens + t] = make_int2(2 * blockIdx.x + slot, n);
                 }
             }
@@ -736,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             mbar_wait(bar_pv + 32 * ((g - 1) & 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
             after_sync();
             // ---- O^T out of TMEM (alone: two warps to a quadrant; with the dequant's six)
-            if (p.ctas_per_unit > 0) {
+            if (kShared) {
                 named_bar(4, kAll + kWorkers);
                 write_o(p, t, h0, whole ? nullptr : part, fin, lane_base, quad, lane, (warp - 1) >> 2, 6);
             } else {
@@ -845,6 +864,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4P
 }  // namespace
 
 int decode_fp4_block_keys() { return kBK; }
+int decode_fp4_own_list_width() { return kListLoads * kListThreads; }
 size_t decode_fp4_part_bytes() { return sizeof(float) * (size_t)kPartFloats; }
 
 cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
@@ -853,14 +873,16 @@ cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
         return cudaSuccess;
     if (p.groups != (p.num_heads + kNH - 1) / kNH || p.grid < 1)
         return cudaErrorInvalidValue;
-    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(decode_fp4_kernel), kSmemBytes, kAttrFp4);
+    const bool shared = p.ctas_per_unit > 0;
+    const auto kernel = shared ? decode_fp4_kernel<true> : decode_fp4_kernel<false>;
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), kSmemBytes, shared ? kAttrFp4Shared : kAttrFp4);
     if (e != cudaSuccess)
         return e;
-    const cudaError_t r = launch_dependent(decode_fp4_kernel, dim3((unsigned)p.grid), kThreads, kSmemBytes, stream, p);
+    const cudaError_t r = launch_dependent(kernel, dim3((unsigned)p.grid), kThreads, kSmemBytes, stream, p);
     if (r != cudaSuccess || !p.split)
         return r;
     const dim3 grid((unsigned)p.num_tokens * (unsigned)p.groups, (unsigned)(std::min(p.num_heads, kNH) / kJoinHeads));
-    return launch_dependent(p.ctas_per_unit > 0 ? join_parts_kernel<4> : join_parts_kernel<2>, grid, kJoinThreads, 0, stream, p);
+    return launch_dependent(shared ? join_parts_kernel<4> : join_parts_kernel<2>, grid, kJoinThreads, 0, stream, p);
 }
 
 }  // namespace dsv4

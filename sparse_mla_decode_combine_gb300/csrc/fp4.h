@@ -123,11 +123,13 @@ struct Decode4Params {
     bool split;                // whether several CTAs may share a unit
     float *parts;              // [2 * grid] partial results of units that several CTAs share
     int2 *joins;               // [groups * T] such a unit's first part and their number, zeros for units that are not shared
-    Lists4Params lists;        // ctas_per_unit > 0: the CTAs make their token's list themselves
+    bool own_lists;            // (ctas_per_unit > 0) the CTAs make their token's list themselves:
+    Lists4Params lists;
     unsigned *status;
 };
 cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream);
 int decode_fp4_block_keys();
+int decode_fp4_own_list_width();   // widest top-k rows of which the decode makes the lists itself
 size_t decode_fp4_part_bytes();
 
 // ---- page operators

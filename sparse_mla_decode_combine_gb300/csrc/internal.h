@@ -92,7 +92,7 @@ struct DecodeParams {
 // (device, kernel slot); later calls with no larger size touch no CUDA state, so a
 // call made after the first one on a device is safe inside stream capture.
 enum AttrSlot { kAttrCombine = 0, kAttrTc, kAttrTcLong, kAttrTcUnion, kAttrTcUnionLong, kAttrUnion, kAttrTopk,
-                kAttrTopkCluster, kAttrFp4, kAttrFp4Lists, kAttrForkSmall,
+                kAttrTopkCluster, kAttrFp4, kAttrFp4Shared, kAttrFp4Lists, kAttrForkSmall,
                 kAttrCompactSmall, kAttrSlots };
 cudaError_t set_smem_once(const void *kernel, int bytes, AttrSlot slot);
 

@@ -10,6 +10,7 @@ namespace dsv4 {
 namespace {
 
 constexpr int kThreads = 512;
+constexpr int kLoads = 4;   // entries of a row that a thread has in flight: 2048 in all
 
 struct SyncAll {
     __device__ __forceinline__ void operator()() const { __syncthreads(); }
@@ -21,11 +22,11 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
     griddep_wait();
     griddep_launch();   // (the decode waits for this grid itself)
     extern __shared__ unsigned long long tab[];
-    __shared__ int wsum[lists::kPassLoads * kThreads / 32];
+    __shared__ int wsum[kLoads * kThreads / 32];
     const int t = blockIdx.x, tid = threadIdx.x;
     if (tid < p.groups)
         p.joins[tid * gridDim.x + t] = make_int2(0, 0);
-    const int len = lists::build<kThreads>(p, t, tid, tab, wsum, SyncAll());
+    const int len = lists::build<kThreads, kLoads>(p, t, tid, tab, wsum, SyncAll(), [](int len) { return make_int2(0, len); });
     if (tid == 0)
         p.lens[t] = len;
     if (len == 0) {
