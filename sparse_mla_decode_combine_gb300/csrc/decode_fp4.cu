@@ -79,7 +79,8 @@ constexpr uint32_t kColS = 0;            // S^T: 64 columns for each of the two 
 constexpr uint32_t kColO = 128;          // O^T: 4 tiles x 64 columns
 constexpr float kExceedLog2 = 40.f;
 constexpr int kJoinHeads = 4;            // heads per CTA of the joining kernel, a warp each
-constexpr int kJoinThreads = 32 * kJoinHeads;
+constexpr int kJoinSplit = 8;            // warps to a head where it may have kJoinMany parts or more
+constexpr int kJoinMany = 8;
 constexpr int kMinBlocks = 2;            // per CTA: below that, joining costs more than the blocks
 
 // small shared region (after Q and the two K tiles)
@@ -775,20 +776,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         tmem_free(tmem, kTmemCols);
 }
 
-// Joins the parts of the units that several CTAs shared, a warp to a head, in the order of the parts:
+// Joins the parts of the units that several CTAs shared, in the order of the parts:
 //   m = max(max_c m_c, sink), Z = sum_c l_c e^{m_c - m} + e^{sink - m},
 //   out = sum_c e^{m_c - m} O_c / Z  (BF16),  lse = m + ln Z
-// The parts come from L2, kJoinBatch at a time with every load in flight: four where few CTAs share each unit (latency
-// is all there is; they are read before it is known how many of them had work), two where runs of blocks end inside
-// units (two parts are usual, and more registers would leave fewer warps: 8 against 10.5 us for 151 split units).  (Joined inside the decode, by the CTA of a unit that finished last, the 256
+// A warp to a head, or kSplit of them, each with a run of the parts, where there may be many (one token over 131072 keys, 152
+// parts: 75 us in all with one warp, 42 with eight; 17 parts: 19.6 and 17.8; four parts: 20.6 and 24.8).  The parts come from L2, kJoinBatch at a time with every load in flight:
+// four where few CTAs share each unit (latency is all there is; they are read before it is known how many of them had
+// work), two where runs of blocks end inside units (two parts are usual, and more registers would leave fewer warps: 8
+// against 10.5 us for 151 split units).  (Joined inside the decode, by the CTA of a unit that finished last, the 256
 // threads that are free there hold too few bytes in flight: a unit took 25 us.)
-template <int kJoinBatch>
-__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4Params p)
+template <int kJoinBatch, int kSplit>
+__global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) join_parts_kernel(const Decode4Params p)
 {
-    const int unit = blockIdx.x;
+    const int unit = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = unit % p.num_tokens, h0 = unit / p.num_tokens * kNH;
-    const int h = kJoinHeads * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;   // head of the group
-    const float sk = p.sink != nullptr ? p.sink[h0 + h] : -INFINITY;
+    const int h = kSplit == 1 ? kJoinHeads * blockIdx.y + warp : blockIdx.y;   // head of the group
     griddep_wait();
     const int2 join = __ldcg(p.joins + unit);   // (slot of the first part, parts); zeros for a unit of one part
     int first = 2 * unit * p.ctas_per_unit, most = p.ctas_per_unit;
@@ -796,19 +798,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4P
         first = join.x;
         most = join.y;
     }
+    const int share = (most + kSplit - 1) / kSplit, lo = kSplit == 1 ? 0 : warp * share, hi = min(most, lo + share);
+    const float sk = p.sink != nullptr && (kSplit == 1 || warp == 0) ? p.sink[h0 + h] : -INFINITY;
     float M = sk, Z = sk == -INFINITY ? 0.f : 1.f;
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = 0; c0 < most; c0 += kJoinBatch) {
+    for (int c0 = lo; c0 < hi; c0 += kJoinBatch) {
         float2 ml[kJoinBatch];
         float4 o[kJoinBatch][4];
 #pragma unroll
         for (int c = 0; c < kJoinBatch; ++c) {
             // the first part may be its CTA's second; the others are their CTAs' first
             const float *pc = p.parts + (size_t)(c0 + c == 0 ? first : 2 * (first / 2 + c0 + c)) * kPartFloats;
-            if (c0 + c < most) {
+            if (c0 + c < hi) {
                 ml[c] = __ldcg(reinterpret_cast<const float2 *>(pc + kNH * kLatent + 2 * h));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -820,7 +824,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4P
         float m = M;
 #pragma unroll
         for (int c = 0; c < kJoinBatch; ++c) {
-            if (c0 + c >= join.y)
+            if (c0 + c >= min(hi, join.y))
                 ml[c] = make_float2(-INFINITY, 0.f);
             m = fmaxf(m, ml[c].x);
         }
@@ -851,13 +855,42 @@ __global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const Decode4P
     }
     if (join.y == 0)
         return;
+    if (kSplit > 1) {   // the warps' sums, in the order of their runs, by warp k to the dims 128 k ..
+        __shared__ float2 mz[kSplit];
+        __shared__ float4 sums[kSplit][kLatent / 4];
+        if (lane == 0)
+            mz[warp] = make_float2(M, Z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            sums[warp][32 * k + lane] = acc[k];
+        __syncthreads();
+        if (warp >= 4)
+            return;
+        float m = -INFINITY;
+        for (int i = 0; i < kSplit; ++i)
+            m = fmaxf(m, mz[i].x);
+        M = m;
+        Z = 0.f;
+        acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < kSplit; ++i) {
+            if (mz[i].x == -INFINITY)   // (a run without keys)
+                continue;
+            const float w = expf(mz[i].x - m);
+            const float4 o = sums[i][32 * warp + lane];
+            Z = fmaf(mz[i].y, w, Z);
+            acc[0].x = fmaf(w, o.x, acc[0].x);
+            acc[0].y = fmaf(w, o.y, acc[0].y);
+            acc[0].z = fmaf(w, o.z, acc[0].z);
+            acc[0].w = fmaf(w, o.w, acc[0].w);
+        }
+    }
     const float f = Z > 0.f || Z != Z ? 1.f / Z : 0.f;   // (no key and no sink: zeros)
     const int64_t row = (int64_t)t * p.num_heads + h0 + h;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint2 *>(p.out + row * kLatent + 128 * k + 4 * lane) =
+    for (int k = 0; k < (kSplit == 1 ? 4 : 1); ++k)
+        *reinterpret_cast<uint2 *>(p.out + row * kLatent + 128 * (kSplit == 1 ? k : warp) + 4 * lane) =
             make_uint2(pack_bf16x2(acc[k].x * f, acc[k].y * f), pack_bf16x2(acc[k].z * f, acc[k].w * f));
-    if (lane == 0 && p.lse != nullptr)
+    if (lane == 0 && (kSplit == 1 || warp == 0) && p.lse != nullptr)
         p.lse[row] = M == -INFINITY ? -INFINITY : M + logf(Z);
 }
 
@@ -881,8 +914,11 @@ cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
     const cudaError_t r = launch_dependent(kernel, dim3((unsigned)p.grid), kThreads, kSmemBytes, stream, p);
     if (r != cudaSuccess || !p.split)
         return r;
-    const dim3 grid((unsigned)p.num_tokens * (unsigned)p.groups, (unsigned)(std::min(p.num_heads, kNH) / kJoinHeads));
-    return launch_dependent(shared ? join_parts_kernel<4> : join_parts_kernel<2>, grid, kJoinThreads, 0, stream, p);
+    const unsigned units = (unsigned)p.num_tokens * (unsigned)p.groups, heads = (unsigned)std::min(p.num_heads, kNH);
+    if (p.ctas_per_unit >= kJoinMany)
+        return launch_dependent(join_parts_kernel<2, kJoinSplit>, dim3(units, heads), 32 * kJoinSplit, 0, stream, p);
+    return launch_dependent(shared ? join_parts_kernel<4, 1> : join_parts_kernel<2, 1>, dim3(units, heads / kJoinHeads),
+                            32 * kJoinHeads, 0, stream, p);
 }
 
 }  // namespace dsv4

@@ -256,6 +256,22 @@ def test_numbers_of_units(tokens, heads):
     check(w, sorted(set(rng.integers(0, tokens, 60).tolist()) | {0, tokens - 1}))
 
 
+@pytest.mark.parametrize("tokens,heads,topk,window,seq", [(1, 16, 0, 20000, 20000), (1, 64, 2048, 128, 9000), (3, 128, 1280, 100, 5000),
+                                                         (3, 32, 1281, 100, 5000), (2, 16, 0, 1024, 900)])
+def test_few_tokens_shared_by_many(tokens, heads, topk, window, seq):
+    """One to three tokens, each shared by up to all multiprocessors: parts without keys, long windows, rows of one round of
+    loads and of more, with and without repeats."""
+    need_gpu()
+    rng = np.random.default_rng(topk)
+    seqs = [seq] + rng.integers(0, seq, tokens - 1).tolist()
+    w = to_fp4(synth.make_workload(name="few", seed=94, heads=heads, req_seq_lens=seqs, topk_width=topk, window=window, sink=True))
+    check(w)
+    if topk:
+        rows = w.topk_idx.copy()
+        rows[:, 1::3] = rows[:, 0::3][:, :rows[:, 1::3].shape[1]]      # every third entry again
+        check(dataclasses.replace(w, topk_idx=rows))
+
+
 def test_logits_far_above_the_first_keys():
     """Later keys' logits exceed the references, which are the first key's, by far more than the range that is left to
     them, again and again: the references rise and what was summed falls."""
