@@ -23,8 +23,8 @@
 //     whose relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.
 //     The usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
 //
-// What bounds it.  128 tokens x 128 heads x 2176 keys: 127 us in this kernel (134 with the lists and the join), 0.61 PFLOP/s,
-// DRAM at 19 % of its peak, the tensor pipe busy 38 % of the time, issue slots 53 %.  A 64-key block takes 3.7 k cycles where
+// What bounds it.  128 tokens x 128 heads x 2176 keys: 124 us in this kernel (132 with the lists and the join), 0.63 PFLOP/s,
+// DRAM at 20 % of its peak, the tensor pipe busy 40 % of the time, issue slots 54 %.  A 64-key block takes 3.7 k cycles where
 // the loop runs freely (4.1 k with the units' ends), and its steps are a chain over twice that, since its tile is one of two: the
 // dequant 3.0 k to its last chunk, S^T 1.2 k after that, the softmax 1.7 k, P.V 1.4 k to the first chunks' release.  S^T of one block and P.V of
 // the other meet and then take 116 of the 128 bytes a cycle of shared memory; letting either go first, or issuing both
