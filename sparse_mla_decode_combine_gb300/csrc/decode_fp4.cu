@@ -508,8 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             uint4 pre[2], prope;
             uint32_t psc = 0u;
             auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld16(e + 128 * m + 16 * piece); };
-            auto load_rest = [&](const uint8_t *e) {
-                prope = ld16(e + kRope4Offset + 16 * runit);
+            auto load_scales = [&](const uint8_t *e) {
                 if (lane < 16)
                     psc = __ldg(reinterpret_cast<const uint32_t *>(e + kScale4Offset) + (lane >> 2));
             };
@@ -518,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             if (pre_ok) {
                 load_piece(entry(slot0), 0);
                 load_piece(entry(slot0), 1);
-                load_rest(entry(slot0));
+                load_scales(entry(slot0));
+                prope = ld16(entry(slot0) + kRope4Offset + 16 * runit);
             }
             if (n > 0 || !kShared) {
                 if (n > 0)   // S^T of the last segment's last block is done with its Q
@@ -544,6 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
                     se[m] = (__shfl_sync(0xffffffffu, psc, 4 * (2 * m + (piece >> 2)) + (lane & 3)) >> (8 * (piece & 3))) & 0xFFu;
+                if (ok_next)
+                    load_scales(en);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {   // dims 256 m + 32 piece ..
                     if (g >= 2)   // P.V of the block before the last is done with these chunks
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         mbar_arrive(bar_grp + 16 * x + 8 * m);
                 }
                 if (ok_next)
-                    load_rest(en);
+                    prope = ld16(en + kRope4Offset + 16 * runit);
                 pre_ok = ok_next;
             }
             if (kShared) {   // the CTA's only segment: its output is written by all
@@ -630,7 +632,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        v[r][j] = kv[r] ? fmaf(__uint_as_float(s[j >> 2][4 * ((j >> 1) & 1) + 2 * r + (j & 1)]), c2, -ref[j]) : -INFINITY;
+                        v[r][j] = fmaf(__uint_as_float(s[j >> 2][4 * ((j >> 1) & 1) + 2 * r + (j & 1)]), c2, -ref[j]);
+                if (!__all_sync(0xffffffffu, kv[0] && kv[1])) {   // (few blocks have rows without a key: 132.5 -> 131.6 us)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            v[r][j] = kv[r] ? v[r][j] : -INFINITY;
+                }
                 if (b == 0 && valid[x * kBK] != 0) {
                     // any logit will do as a reference: those of the segment's first key
                     if (srow == 0) {
