@@ -22,6 +22,8 @@
 //     when a logit exceeds its head's reference by 40 (in log2 units): P and the sums are floating-point numbers,
 //     whose relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.
 //     The usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
+//     Where few units are shared, the output is divided by the sum of the weights as rounded to BF16, so that a key that
+//     has most of the weight loses nothing by its rounding (the lse keeps the exact sum; 1 % of the time of a small batch).
 //
 // What bounds it.  128 tokens x 128 heads x 2176 keys: 124 us in this kernel (132 with the lists and the join), 0.63 PFLOP/s,
 // DRAM at 20 % of its peak, the tensor pipe busy 40 % of the time, issue slots 54 %.  A 64-key block takes 3.7 k cycles where
@@ -93,13 +95,14 @@ constexpr int kOffTmem = 1808;           // u32
 constexpr int kOffAbort = 1812;          // int
 constexpr int kOffStart = 1816;          // int [8]: the unit at the run's start, its first block and the next unit's; at its end
 constexpr int kOffScan = 1848;           // int [26]
-constexpr int kSmallBytes = 1984;
+constexpr int kOffRed2 = 1984;           // float [4][64]: the rounded weights' row sums at the end
+constexpr int kSmallBytes = 3008;
 constexpr int kSmemBytes = kQBytes + 2 * kKBytes + kSmallBytes + 1024;   // + alignment slack
 constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                     // 9 16-byte Q pieces per worker
 static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
 static_assert(2 * kKBytes >= 32768 + 4 * kListLoads * kListThreads / 32, "a list's sets fit the K tiles");
 static_assert(16 * kListLoads * kListThreads <= 32768, "the rows of lists made here");
-constexpr int kPartFloats = kNH * kLatent + 2 * kNH;   // a part in the workspace: O [64][512], then (m, l) [64]
+constexpr int kPartFloats = kNH * kLatent + 4 * kNH;   // a part in the workspace: O [64][512], then (m, l, l of rounded weights, -) [64]
 
 // instruction descriptors (kind::f16): D f32, A/B bf16, N = 64
 constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kNH >> 3) << 17);
@@ -278,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     const uint32_t sK = base + kQBytes;           // two K tiles; P^T takes a tile's rope chunk once its S^T is done
     uint8_t *small = gbase + kQBytes + 2 * kKBytes;
     float *red = reinterpret_cast<float *>(small + kOffRed);
+    float *red2 = reinterpret_cast<float *>(small + kOffRed2);
     float *smax = reinterpret_cast<float *>(small + kOffMax);
     float *fin = reinterpret_cast<float *>(small + kOffFin);
     uint8_t *valid = small + kOffValid;
@@ -607,6 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 l[j] = 0.f;
+            float lr[kShared ? 8 : 1];                        // the same of the weights as P.V takes them, rounded to BF16
+#pragma unroll
+            for (int j = 0; j < (kShared ? 8 : 0); ++j)
+                lr[j] = 0.f;
             bool fresh = true;                                // no key has been seen: the references are not set
 
             for (int b = 0; b < seg.nb; ++b, ++g) {
@@ -678,6 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);   // (-inf: every logit is NaN)
                         const float fall = fresh ? 1.f : exp2_approx(-up);
                         l[j] *= fall;
+                        if constexpr (kShared)
+                            lr[j] *= fall;
                         v[0][j] -= up;
                         v[1][j] -= up;
                         if (quad == 0 && lane < 4) {
@@ -712,8 +722,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         const float p0 = exp2_approx(v[r][j]), p1 = exp2_approx(v[r][j + 1]);
                         l[j] += p0;
                         l[j + 1] += p1;
-                        st_shared_u32(sK + x * kKBytes + 8u * kChunkBytes + sw128(srow + 8 * r, (hw >> 3) + (j >> 1)) + 4u * (lane & 3),
-                                      pack_bf16x2(p0, p1));
+                        const uint32_t pk = pack_bf16x2(p0, p1);
+                        if constexpr (kShared) {
+                            lr[j] += __uint_as_float(pk << 16);
+                            lr[j + 1] += __uint_as_float(pk & 0xFFFF0000u);
+                        }
+                        st_shared_u32(sK + x * kKBytes + 8u * kChunkBytes + sw128(srow + 8 * r, (hw >> 3) + (j >> 1)) + 4u * (lane & 3), pk);
                     }
                 fence_async_smem();
                 before_sync();
@@ -730,6 +744,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     l[j] += __shfl_xor_sync(0xffffffffu, l[j], d);
                 if (lane < 4)
                     red[quad * kNH + head(j)] = l[j];
+                if constexpr (kShared) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1)
+                        lr[j] += __shfl_xor_sync(0xffffffffu, lr[j], d);
+                    if (lane < 4)
+                        red2[quad * kNH + head(j)] = lr[j];
+                }
             }
             if (quad == 0)
                 smax[hw + lane] = fresh ? -INFINITY : smax[hw + lane] * 0.6931471805599453f;
@@ -747,18 +768,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             if (wid < kNH) {
                 const int h = wid;
                 const float lsum = (red[h] + red[kNH + h]) + (red[2 * kNH + h] + red[3 * kNH + h]);
+                const float lround = kShared ? (red2[h] + red2[kNH + h]) + (red2[2 * kNH + h] + red2[3 * kNH + h]) : lsum;
                 const float ms = smax[h];
                 if (whole) {
                     const float sk = p.sink != nullptr && h < nhv ? p.sink[h0 + h] : -INFINITY;
                     const float M = fmaxf(ms, sk);
                     const float e = ms == -INFINITY ? 0.f : expf(ms - M);
-                    const float Z = (ms == -INFINITY ? 0.f : lsum * e) + (sk == -INFINITY ? 0.f : expf(sk - M));
-                    fin[h] = ms == -INFINITY ? 0.f : e / Z;
+                    const float zs = sk == -INFINITY ? 0.f : expf(sk - M);
+                    const float Z = (ms == -INFINITY ? 0.f : lsum * e) + zs;
+                    fin[h] = ms == -INFINITY ? 0.f : e / (kShared ? lround * e + zs : Z);
                     if (p.lse != nullptr && h < nhv)
                         p.lse[(int64_t)t * p.num_heads + h0 + h] = M == -INFINITY ? -INFINITY : M + logf(Z);
                 } else {
-                    part[kNH * kLatent + 2 * h] = ms;
-                    part[kNH * kLatent + 2 * h + 1] = ms == -INFINITY ? 0.f : lsum;
+                    *reinterpret_cast<float4 *>(part + kNH * kLatent + 4 * h) =
+                        ms == -INFINITY ? make_float4(ms, 0.f, 0.f, 0.f) : make_float4(ms, lsum, lround, 0.f);
                 }
             }
             named_bar(1, kAll);
@@ -794,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 // work), two where runs of blocks end inside units (two parts are usual, and more registers would leave fewer warps: 8
 // against 10.5 us for 151 split units).  (Joined inside the decode, by the CTA of a unit that finished last, the 256
 // threads that are free there hold too few bytes in flight: a unit took 25 us.)
-template <int kJoinBatch, int kSplit>
+template <int kJoinBatch, int kSplit, bool kShared>
 __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) join_parts_kernel(const Decode4Params p)
 {
     const int unit = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -809,20 +832,23 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
     }
     const int share = (most + kSplit - 1) / kSplit, lo = kSplit == 1 ? 0 : warp * share, hi = min(most, lo + share);
     const float sk = p.sink != nullptr && (kSplit == 1 || warp == 0) ? p.sink[h0 + h] : -INFINITY;
-    float M = sk, Z = sk == -INFINITY ? 0.f : 1.f;
+    float M = sk, Z = sk == -INFINITY ? 0.f : 1.f, Zr = Z;   // (Zr: with the weights as rounded)
     float4 acc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c0 = lo; c0 < hi; c0 += kJoinBatch) {
         float2 ml[kJoinBatch];
+        float lr[kJoinBatch];
         float4 o[kJoinBatch][4];
 #pragma unroll
         for (int c = 0; c < kJoinBatch; ++c) {
             // the first part may be its CTA's second; the others are their CTAs' first
             const float *pc = p.parts + (size_t)(c0 + c == 0 ? first : 2 * (first / 2 + c0 + c)) * kPartFloats;
             if (c0 + c < hi) {
-                ml[c] = __ldcg(reinterpret_cast<const float2 *>(pc + kNH * kLatent + 2 * h));
+                ml[c] = __ldcg(reinterpret_cast<const float2 *>(pc + kNH * kLatent + 4 * h));
+                if (kShared)
+                    lr[c] = __ldcg(pc + kNH * kLatent + 4 * h + 2);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     o[c][k] = __ldcg(reinterpret_cast<const float4 *>(pc + h * kLatent + 128 * k + 4 * lane));
@@ -839,6 +865,8 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
         }
         const float fall = M == -INFINITY ? 0.f : expf(M - m);
         Z *= fall;
+        if (kShared)
+            Zr *= fall;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             acc[k].x *= fall;
@@ -852,6 +880,8 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
                 continue;
             const float w = expf(ml[c].x - m);
             Z = fmaf(ml[c].y, w, Z);
+            if (kShared)
+                Zr = fmaf(lr[c], w, Zr);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 acc[k].x = fmaf(w, o[c][k].x, acc[k].x);
@@ -865,10 +895,10 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
     if (join.y == 0)
         return;
     if (kSplit > 1) {   // the warps' sums, in the order of their runs, by warp k to the dims 128 k ..
-        __shared__ float2 mz[kSplit];
+        __shared__ float4 mz[kSplit];
         __shared__ float4 sums[kSplit][kLatent / 4];
         if (lane == 0)
-            mz[warp] = make_float2(M, Z);
+            mz[warp] = make_float4(M, Z, Zr, 0.f);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             sums[warp][32 * k + lane] = acc[k];
@@ -879,7 +909,7 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
         for (int i = 0; i < kSplit; ++i)
             m = fmaxf(m, mz[i].x);
         M = m;
-        Z = 0.f;
+        Z = Zr = 0.f;
         acc[0] = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i = 0; i < kSplit; ++i) {
             if (mz[i].x == -INFINITY)   // (a run without keys)
@@ -887,13 +917,16 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
             const float w = expf(mz[i].x - m);
             const float4 o = sums[i][32 * warp + lane];
             Z = fmaf(mz[i].y, w, Z);
+            Zr = fmaf(mz[i].z, w, Zr);
             acc[0].x = fmaf(w, o.x, acc[0].x);
             acc[0].y = fmaf(w, o.y, acc[0].y);
             acc[0].z = fmaf(w, o.z, acc[0].z);
             acc[0].w = fmaf(w, o.w, acc[0].w);
         }
     }
-    const float f = Z > 0.f || Z != Z ? 1.f / Z : 0.f;   // (no key and no sink: zeros)
+    if (!kShared)
+        Zr = Z;
+    const float f = Zr > 0.f || Zr != Zr ? 1.f / Zr : 0.f;   // (no key and no sink: zeros)
     const int64_t row = (int64_t)t * p.num_heads + h0 + h;
 #pragma unroll
     for (int k = 0; k < (kSplit == 1 ? 4 : 1); ++k)
@@ -925,8 +958,8 @@ cudaError_t launch_decode_fp4(const Decode4Params &p, cudaStream_t stream)
         return r;
     const unsigned units = (unsigned)p.num_tokens * (unsigned)p.groups, heads = (unsigned)std::min(p.num_heads, kNH);
     if (p.ctas_per_unit >= kJoinMany)
-        return launch_dependent(join_parts_kernel<2, kJoinSplit>, dim3(units, heads), 32 * kJoinSplit, 0, stream, p);
-    return launch_dependent(shared ? join_parts_kernel<4, 1> : join_parts_kernel<2, 1>, dim3(units, heads / kJoinHeads),
+        return launch_dependent(join_parts_kernel<2, kJoinSplit, true>, dim3(units, heads), 32 * kJoinSplit, 0, stream, p);
+    return launch_dependent(shared ? join_parts_kernel<4, 1, true> : join_parts_kernel<2, 1, false>, dim3(units, heads / kJoinHeads),
                             32 * kJoinHeads, 0, stream, p);
 }
 

@@ -289,6 +289,28 @@ def test_logits_far_above_the_first_keys():
     check(w)
 
 
+def test_one_key_has_nearly_all_the_weight():
+    """With few tokens the output is divided by the sum of the weights as they were rounded for the product, so the rounding d
+    (2^-8 at most) of the one key's weight cancels: what is left of it is d times the other keys' share e of all weight, times
+    the distance of the values, 2 V, and the same again for their own roundings; then fp32's sums (2^-18 V) and the output's
+    own rounding, 2^-8 of the value."""
+    need_gpu()
+    w = to_fp4(synth.make_workload(name="peak", seed=95, heads=16, req_seq_lens=[300, 40], topk_width=0, window=300, sink=False))
+    cache = w.kv_cache.copy()
+    cache[..., 256:384] = 0
+    for r in range(2):
+        cache[w.block_table[r, 0], 20, 256:384] = synth.bf16_bits(np.full(64, 0.25)).view(np.uint8)
+    q = np.zeros_like(w.q)
+    q[..., 512:] = synth.bf16_bits(0.8 + 0.05 * np.arange(16))[None, :, None]      # logits 12.8 to 24.8, all others 0
+    w = dataclasses.replace(w, kv_cache=cache, q=q, softmax_scale=1.0)
+    ref = fp4.decode(w)
+    out, lse, _ = run(w)
+    compare(out, lse, ref)
+    V = np.abs(fp4.dequant(cache)[:, :512]).max()
+    tol = 2.0 ** -8 * np.abs(ref[0]) + (4 * 300 * np.exp(-12.7) * 2.0 ** -8 + 2.0 ** -18) * V
+    assert np.all(np.abs(out.double().cpu().numpy() - ref[0]) <= tol)
+
+
 def test_refusals():
     need_gpu()
     size = pkg.dsv4_sparse_mla_decode_fp4_workspace_size
