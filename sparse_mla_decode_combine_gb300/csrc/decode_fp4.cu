@@ -3,7 +3,8 @@
 // Operation (per token t, head h, over the token's combined list of positions):
 //   s_p = scale * q_h . k_p (576 dims),  lse_h = ln(sum_p e^{s_p} + e^{sink_h}),  out_h = sum_p e^{s_p - lse_h} v_p
 // The lists of cache slots come from the list kernel (lists_fp4.cu) ahead of this one in the stream, or, with few units, are
-// made here by the ten warps that do not bring Q (a launch less: 10.7 against 12.4 us for 2 tokens x 16 heads in a loop of calls).
+// made here by the ten warps that do not bring Q (a launch less: 10.7 against 12.4 us for 2 tokens x 16 heads in a loop of
+// calls).
 //
 // Contraction.  All heads share one key set, so a (token, 64 heads) unit is a pair of dense products, run
 // transposed (keys and value dims on the M side of the tensor tile):
@@ -28,11 +29,11 @@
 // What bounds it.  128 tokens x 128 heads x 2176 keys: 124 us in this kernel (132 with the lists and the join), 0.63 PFLOP/s,
 // DRAM at 20 % of its peak, the tensor pipe busy 40 % of the time, issue slots 54 %.  A 64-key block takes 3.7 k cycles where
 // the loop runs freely (4.1 k with the units' ends), and its steps are a chain over twice that, since its tile is one of two: the
-// dequant 3.0 k to its last chunk, S^T 1.2 k after that, the softmax 1.7 k, P.V 1.4 k to the first chunks' release.  S^T of one block and P.V of
-// the other meet and then take 116 of the 128 bytes a cycle of shared memory; letting either go first, or issuing both
-// from one warp (a product takes it about 50 cycles), was slower: 140 and 159 us.  The dequant warps are busy for all of a block's
-// time too, 1.4 k of it with conversion and stores and 1.1 k waiting for scale bytes and entries, so neither side alone
-// is worth much: half of the dequant left out gives 127 us in all, no P.V 120, no gather 118.
+// dequant 3.0 k to its last chunk, S^T 1.2 k after that, the softmax 1.7 k, P.V 1.4 k to the first chunks' release.  S^T of
+// one block and P.V of the other meet and then take 116 of the 128 bytes a cycle of shared memory; letting either go first,
+// or issuing both from one warp (a product takes it about 50 cycles), was slower: 140 and 159 us.  The dequant warps are
+// busy for all of a block's time too, 1.4 k of it with conversion and stores and 1.1 k waiting for scale bytes and entries,
+// so neither side alone is worth much: half of the dequant left out gives 127 us in all, no P.V 120, no gather 118.
 //
 // Work.  With up to half as many units as multiprocessors, as many CTAs as there are for it share each unit evenly.  Otherwise a
 // persistent CTA per multiprocessor takes an equal run of the blocks of all units (the end of one unit,
@@ -64,6 +65,7 @@ constexpr int kSoftmaxWarps = 8;         // warps 1-8 (warp 0 issues S^T)
 constexpr int kDequantWarp0 = 9;
 constexpr int kDequantWarps = 16;        // warps 9-24: also Q's layout and the epilogue
 constexpr int kPvWarp = 25;              // issues P.V
+constexpr int kTmemWarp = 24;            // takes and frees the tensor memory (a warp that makes no list)
 constexpr int kThreads = 832;
 constexpr int kWorkers = 32 * kDequantWarps;
 constexpr int kListThreads = kThreads - kWorkers;   // make a list while the others bring Q,
@@ -102,7 +104,8 @@ constexpr int kQLoads = kNH * (kDim / 8) / kWorkers;                     // 9 16
 static_assert(kNH * (kDim / 8) % kWorkers == 0, "Q pieces per worker");
 static_assert(2 * kKBytes >= 32768 + 4 * kListLoads * kListThreads / 32, "a list's sets fit the K tiles");
 static_assert(16 * kListLoads * kListThreads <= 32768, "the rows of lists made here");
-constexpr int kPartFloats = kNH * kLatent + 4 * kNH;   // a part in the workspace: O [64][512], then (m, l, l of rounded weights, -) [64]
+// a part in the workspace: O [64][512], then (m, l, l of the rounded weights, -) [64]
+constexpr int kPartFloats = kNH * kLatent + 4 * kNH;
 
 // instruction descriptors (kind::f16): D f32, A/B bf16, N = 64
 constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kNH >> 3) << 17);
@@ -261,10 +264,14 @@ struct SyncLists {   // the threads that make a list
 };
 
 // CTAs that share a unit of W blocks evenly
-__device__ __forceinline__ int shares_of(const Decode4Params &p, int W) { return max(1, min(p.ctas_per_unit, (W + kMinBlocks - 1) / kMinBlocks)); }
+__device__ __forceinline__ int shares_of(const Decode4Params &p, int W)
+{
+    return max(1, min(p.ctas_per_unit, (W + kMinBlocks - 1) / kMinBlocks));
+}
 
 // kShared: few units, each shared evenly by p.ctas_per_unit CTAs, which make its token's list themselves (p.own_lists) unless
-// the rows are wide; otherwise every CTA takes an equal run of the blocks of all units.  (In one kernel the second kind took 2 % longer: registers.)
+// the rows are wide; otherwise every CTA takes an equal run of the blocks of all units.  (In one kernel the second kind took
+// 2 % longer: registers.)
 template <bool kShared>
 __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Params p)
 {
@@ -311,7 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
-    if (warp == 0)
+    // (tensor memory is taken when no kernel but this library's own list kernel can still be running ahead of this one)
+    const bool own_lists = kShared && p.own_lists;
+    if (own_lists)
+        griddep_wait();
+    if (warp == kTmemWarp)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     // ---- this CTA's blocks
     Walk walk;
@@ -321,13 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         walk.t = unit % p.num_tokens;
         walk.h0 = unit / p.num_tokens * kNH;
         walk.start = 0;
-        if (p.own_lists)
-            griddep_wait();
         if (is_worker) {
             // (where a list kernel is ahead, it let this one begin after everything before it in the stream had ended: the
             // queries are there, and come in while the lists are made)
             store_q<kQLoads>(p, walk.t, walk.h0, sQ, tid - 32 * kDequantWarp0);
-        } else if (p.own_lists) {
+        } else if (own_lists) {
             const int ltid = warp < kDequantWarp0 ? tid : tid - kWorkers;
             // Every CTA of a token writes the slots of its top-k entries, the same ones to the same places, and those of the
             // window's part that it needs.
@@ -341,18 +350,18 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             if (ltid == 0)
                 first[0] = len;
         }
-        if (!p.own_lists)
+        if (!own_lists)
             griddep_wait();
         before_sync();
         __syncthreads();
-        walk.len = p.own_lists ? first[0] : __ldcg(p.lens + walk.t);
+        walk.len = own_lists ? first[0] : __ldcg(p.lens + walk.t);
         W = blocks_of(walk.len);
         G = shares_of(p, W);
         walk.w = s < G ? run_start(s, W, G) : W;
         walk.w1 = s < G ? run_start(s + 1, W, G) : W;
-        if (p.own_lists && s == 0 && G == 1 && tid == 0)
+        if (own_lists && s == 0 && G == 1 && tid == 0)
             p.joins[unit] = make_int2(0, 0);
-        if (p.own_lists && s == 0 && W == 0) {   // a token without a key
+        if (own_lists && s == 0 && W == 0) {   // a token without a key
             const int nhv = min(kNH, p.num_heads - walk.h0);
             const int64_t row = (int64_t)walk.t * p.num_heads + walk.h0;
             for (int i = tid; i < nhv * kLatent / 8; i += kThreads)
@@ -804,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
     before_sync();
     __syncthreads();
     after_sync();
-    if (warp == 0)
+    if (warp == kTmemWarp)
         tmem_free(tmem, kTmemCols);
 }
 
@@ -812,8 +821,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 //   m = max(max_c m_c, sink), Z = sum_c l_c e^{m_c - m} + e^{sink - m},
 //   out = sum_c e^{m_c - m} O_c / Z  (BF16),  lse = m + ln Z
 // A warp to a head, or kSplit of them, each with a run of the parts, where there may be many (one token over 131072 keys, 152
-// parts: 75 us in all with one warp, 42 with eight; 17 parts: 19.6 and 17.8; four parts: 20.6 and 24.8).  The parts come from L2, kJoinBatch at a time with every load in flight:
-// four where few CTAs share each unit (latency is all there is; they are read before it is known how many of them had
+// parts: 75 us in all with one warp, 42 with eight; 17 parts: 19.6 and 17.8; four parts: 20.6 and 24.8).  The parts come from
+// L2, kJoinBatch at a time with every load in flight: four where few CTAs share each unit (latency is all there is; they are read before it is known how many of them had
 // work), two where runs of blocks end inside units (two parts are usual, and more registers would leave fewer warps: 8
 // against 10.5 us for 151 split units).  (Joined inside the decode, by the CTA of a unit that finished last, the 256
 // threads that are free there hold too few bytes in flight: a unit took 25 us.)
