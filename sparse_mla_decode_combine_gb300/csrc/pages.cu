@@ -28,7 +28,7 @@ constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kCluster * kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 8;         // 16-byte pieces a thread holds: a page of 64 entries of 400 bytes in one round
+constexpr int kCopyUnroll = 8;         // 16-byte pieces a thread holds: a page of 64 entries of 400 bytes in one round of a CTA
 constexpr int kSmallPages = 16384;     // the one-CTA plans: pages,
 constexpr int kSmallRows = 1024;       // rows before and after,
 constexpr int kSmallCells = 1 << 16;   // and cells of the table
@@ -586,6 +586,10 @@ struct MoveParams {
     unsigned *status;
 };
 
+// kGroup threads to a page, kCopyThreads / kGroup pages at a time to a CTA: as few as hold a page in one round of kCopyUnroll
+// pieces each, so that a CTA has some 25 KB in flight whatever the size of a page (8000 pages of 6400 bytes in four layers: 5.7
+// TB/s, with a whole CTA to a page 3.5).  Two to three CTAs a multiprocessor are level; more disturb DRAM.
+template <int kGroup>
 __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MoveParams p)
 {
     griddep_wait();
@@ -606,14 +610,17 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
         }
     }
     const int n = p.copies != nullptr ? *p.num_copies : p.num_pages;
+    constexpr int kGroups = kCopyThreads / kGroup;
+    const int gid = tid % kGroup;
     // a few listed pages are checked against each other here, a pair to a thread, without a plan
+    const bool check = kGroups == 1 && p.copies == nullptr && p.claim == nullptr;
     int2 pair = make_int2(-1, -1);
-    if (p.copies == nullptr && p.claim == nullptr && tid < n)
+    if (check && tid < n)
         pair = make_int2(p.src_pages[tid], p.dst_pages[tid]);
     const bool pair_good = pair.x >= 0 && pair.x < p.src.num_blocks && pair.y >= 0 && pair.y < p.dst.num_blocks;
     const int64_t units = (int64_t)n * p.dst.num_layers;
     const int64_t page_bytes = (int64_t)p.dst.page * p.dst.entry_bytes;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    for (int64_t u = (int64_t)blockIdx.x * kGroups + tid / kGroup; u < units; u += (int64_t)gridDim.x * kGroups) {
         const int i = (int)(u / p.dst.num_layers), layer = (int)(u % p.dst.num_layers);
         int4 c;
         if (p.copies != nullptr) {
@@ -622,15 +629,15 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
             c = make_int4(p.src_pages[i], p.dst_pages[i], p.dst.page, 0);
             const bool good = c.x >= 0 && c.x < p.src.num_blocks && c.y >= 0 && c.y < p.dst.num_blocks;
             bool later, target;   // a later pair has this target; the source is a target of the call
-            if (p.claim != nullptr) {
-                later = good && p.claim[c.y] != i;
-                target = good && p.one_pool && p.claim[c.x] != -1;
-            } else {
+            if (check) {
                 later = __syncthreads_or(pair_good && tid > i && pair.y == c.y);
                 target = __syncthreads_or(pair_good && p.one_pool && pair.y == c.x);
+            } else {
+                later = good && p.claim[c.y] != i;
+                target = good && p.one_pool && p.claim[c.x] != -1;
             }
             if (!good || later || target) {
-                if ((!good || (target && !later)) && tid == 0 && layer == 0)
+                if ((!good || (target && !later)) && gid == 0 && layer == 0)
                     atomicOr(p.status, kStatusBadIndex);
                 continue;
             }
@@ -638,23 +645,28 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
         const uint4 *s = reinterpret_cast<const uint4 *>(p.src.base + layer * p.src.layer_stride + c.x * page_bytes);
         uint4 *d = reinterpret_cast<uint4 *>(p.dst.base + layer * p.dst.layer_stride + c.y * page_bytes);
         const int pieces = (int)((int64_t)c.z * p.dst.entry_bytes / 16);
-        for (int i0 = 0; i0 < pieces; i0 += kCopyUnroll * kCopyThreads) {
+        for (int i0 = 0; i0 < pieces; i0 += kCopyUnroll * kGroup) {
             uint4 v[kCopyUnroll];
 #pragma unroll
             for (int k = 0; k < kCopyUnroll; ++k)
-                if (i0 + k * kCopyThreads + tid < pieces)
-                    v[k] = __ldcs(s + i0 + k * kCopyThreads + tid);
+                if (i0 + k * kGroup + gid < pieces)
+                    v[k] = __ldcs(s + i0 + k * kGroup + gid);
 #pragma unroll
             for (int k = 0; k < kCopyUnroll; ++k)
-                if (i0 + k * kCopyThreads + tid < pieces)
-                    __stcs(d + i0 + k * kCopyThreads + tid, v[k]);
+                if (i0 + k * kGroup + gid < pieces)
+                    __stcs(d + i0 + k * kGroup + gid, v[k]);
         }
     }
 }
 
 cudaError_t launch_move(const MoveParams &m, int sms, cudaStream_t stream)
 {
-    return launch_dependent(move_pages_kernel, dim3((unsigned)(sms * 3)), kCopyThreads, 0, stream, m);
+    const int64_t pieces = (int64_t)m.dst.page * m.dst.entry_bytes / 16;
+    const bool check = m.copies == nullptr && m.claim == nullptr;   // (by whole CTAs)
+    const auto kernel = check || pieces > kCopyUnroll * 128 ? move_pages_kernel<256>
+                        : pieces > kCopyUnroll * 64         ? move_pages_kernel<128>
+                                                            : move_pages_kernel<64>;
+    return launch_dependent(kernel, dim3((unsigned)(sms * 3)), kCopyThreads, 0, stream, m);
 }
 
 }  // namespace

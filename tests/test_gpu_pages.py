@@ -211,6 +211,17 @@ def test_copy_two_pools(entry, page, layers, n):
     check_copy(dst, src, rng.integers(0, 23, n), rng.permutation(40)[:n], False)
 
 
+@pytest.mark.parametrize("page", [1, 511, 512, 513, 1024, 1025, 2048, 2049, 4100])
+@pytest.mark.parametrize("n", [3, 300])
+def test_copy_page_sizes(page, n):
+    """Pages of 16-byte entries around the sizes where more threads share a page, or take it in several rounds."""
+    need_gpu()
+    rng = np.random.default_rng(page)
+    dst = rng.integers(0, 256, (2, 400, page, 16)).astype(np.uint8)
+    src = rng.integers(0, 256, (2, 310, page, 16)).astype(np.uint8)
+    check_copy(dst, src, rng.integers(0, 310, n), rng.permutation(400)[:n], False)
+
+
 def test_copy_repeats_conflicts_and_bad_pages():
     need_gpu()
     rng = np.random.default_rng(71)
