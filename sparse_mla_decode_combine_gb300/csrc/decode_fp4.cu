@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     mbar_arrive(bar_p + 8 * x);
             }
 
-            // ---- the segment's row sums and maxima (natural-log units, -inf for a segment without keys)
+            // ---- the segment's row sums and references (natural-log units)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
 #pragma unroll
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 }
             }
             if (quad == 0)
-                smax[hw + lane] = fresh ? -INFINITY : smax[hw + lane] * 0.6931471805599453f;
+                smax[hw + lane] *= 0.6931471805599453f;
             named_bar(1, kAll);
             const bool whole = seg.nb == blocks_of(seg.len);
             float *part = nullptr;   // this CTA's part of a split unit
@@ -778,7 +778,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 const int h = wid;
                 const float lsum = (red[h] + red[kNH + h]) + (red[2 * kNH + h] + red[3 * kNH + h]);
                 const float lround = kShared ? (red2[h] + red2[kNH + h]) + (red2[2 * kNH + h] + red2[3 * kNH + h]) : lsum;
-                const float ms = smax[h];
+                // (no key, or logits of -inf alone: as a segment without keys.  With a reference that some logit has, or had
+                // and was raised above, the sum is about 1 or more)
+                const float ms = lsum == 0.f ? -INFINITY : smax[h];
                 if (whole) {
                     const float sk = p.sink != nullptr && h < nhv ? p.sink[h0 + h] : -INFINITY;
                     const float M = fmaxf(ms, sk);
