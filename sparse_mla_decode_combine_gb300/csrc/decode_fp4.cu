@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 #pragma unroll
             for (int j = 0; j < (kShared ? 8 : 0); ++j)
                 lr[j] = 0.f;
-            bool fresh = true;                                // no key has been seen: the references are not set
+            uint32_t unset = 0xFFu;                           // bit j: head j has no reference (no logit above -inf so far)
 
             for (int b = 0; b < seg.nb; ++b, ++g) {
                 const uint32_t x = g & 1u, ph = (g >> 1) & 1u;
@@ -658,26 +658,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                             v[r][j] = kv[r] ? v[r][j] : -INFINITY;
                 }
                 if (b == 0 && valid[x * kBK] != 0) {
-                    // any logit will do as a reference: those of the segment's first key
+                    // any finite logit will do as a reference: those of the segment's first key
                     if (srow == 0) {
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
-                            smax[head(j)] = fabsf(v[0][j]) < INFINITY ? v[0][j] : 0.f;
+                            smax[head(j)] = v[0][j];
                     }
                     named_bar(slice_bar, 128);
+                    unset = 0u;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        v[0][j] -= smax[head(j)];
-                        v[1][j] -= smax[head(j)];
+                        const float m = smax[head(j)];
+                        const bool ok = fabsf(m) < INFINITY;
+                        v[0][j] -= ok ? m : 0.f;
+                        v[1][j] -= ok ? m : 0.f;
+                        unset |= ok ? 0u : 1u << j;   // (this block's maxima replace it below)
                     }
-                    fresh = false;
                 }
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     top = fmaxf(top, fmaxf(v[0][j], v[1][j]));
-                if (named_bar_or(slice_bar, 128, (fresh && (kv[0] || kv[1])) || top > kExceedLog2)) {
-                    // the block's maxima, by the four warps of these heads, become the references where they are larger
+                if (named_bar_or(slice_bar, 128, (unset != 0u && (kv[0] || kv[1])) || top > kExceedLog2)) {
+                    // the block's maxima, by the four warps of these heads, become the references where they are larger or
+                    // there is none (logits below 2^-126 of one that is too high would vanish, all of a head's among them)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         float mx = fmaxf(v[0][j], v[1][j]);
@@ -692,20 +696,22 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     for (int j = 0; j < 8; ++j) {
                         const int h = head(j);
                         const float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
-                        const float up = m == -INFINITY ? 0.f : fresh ? m : fmaxf(m, 0.f);   // (-inf: every logit is NaN)
-                        const float fall = fresh ? 1.f : exp2_approx(-up);
+                        const bool none = (unset >> j) & 1u;
+                        const float up = m == -INFINITY ? 0.f : none ? m : fmaxf(m, 0.f);   // (-inf: every logit is that or NaN)
+                        const float fall = none ? 1.f : exp2_approx(-up);
+                        unset &= m == -INFINITY ? ~0u : ~(1u << j);
                         l[j] *= fall;
                         if constexpr (kShared)
                             lr[j] *= fall;
                         v[0][j] -= up;
                         v[1][j] -= up;
                         if (quad == 0 && lane < 4) {
-                            smax[h] += up;
+                            smax[h] = none ? up : smax[h] + up;
                             fin[h] = fall;
                         }
                     }
                     named_bar(slice_bar, 128);   // the references and factors are written, and red is free again
-                    if (b > 0 && !fresh) {   // O^T holds something: P.V of the block before has to be complete
+                    if (b > 0) {   // O^T holds something: P.V of the block before has to be complete
                         mbar_wait(bar_pv + 32 * (x ^ 1u) + 24, ((g - 1) >> 1) & 1u, abort_flag, p.status);
                         after_sync();
 #pragma unroll 1
@@ -721,7 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         }
                         tmem_st_wait();
                     }
-                    fresh = false;
                 }
                 // P = 2^v -> BF16 P^T rows srow and srow + 8
 #pragma unroll
@@ -779,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                 const float lsum = (red[h] + red[kNH + h]) + (red[2 * kNH + h] + red[3 * kNH + h]);
                 const float lround = kShared ? (red2[h] + red2[kNH + h]) + (red2[2 * kNH + h] + red2[3 * kNH + h]) : lsum;
                 // (no key, or logits of -inf alone: as a segment without keys.  With a reference that some logit has, or had
-                // and was raised above, the sum is about 1 or more)
+                // and was raised to another's, the sum is about 1 or more)
                 const float ms = lsum == 0.f ? -INFINITY : smax[h];
                 if (whole) {
                     const float sk = p.sink != nullptr && h < nhv ? p.sink[h0 + h] : -INFINITY;

@@ -10,7 +10,7 @@ import torch
 
 import sparse_mla_decode_combine_gb300 as pkg
 import synth
-from fp4_util import run, to_fp4
+from fp4_util import compare, run, to_fp4
 from gpu_util import need_gpu
 from oracle import fp4
 
@@ -43,6 +43,13 @@ def workload(tokens, heads, keys, dead, sink, low=-200.0):
     return w, dataclasses.replace(w, topk_idx=live)
 
 
+def check(w, live):
+    out, lse, st = run(w)
+    assert st == pkg.DSV4_OK
+    idx = sorted({0, 1, w.num_tokens // 2, w.num_tokens - 1})
+    compare(out[idx], lse[idx], fp4.decode(live, idx), w.name)
+
+
 @pytest.mark.parametrize("sink", [False, True])
 @pytest.mark.parametrize("tokens,heads", [FEW, MANY, SPLIT])
 @pytest.mark.parametrize("keys", [1, 64, 200])
@@ -53,3 +60,27 @@ def test_every_logit_is_minus_infinity(tokens, heads, keys, sink):
     out, lse, st = run(w)
     want = np.tile(w.sink if sink else np.full(heads, -np.inf, np.float32), (tokens, 1))
     assert st == pkg.DSV4_OK and not out.any() and np.array_equal(lse.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("tokens,heads", [FEW, MANY, SPLIT])
+@pytest.mark.parametrize("dead", [[0], range(64), range(130), [0, 64, 128, 199], range(199), [100]])
+def test_some_logits_are_minus_infinity(tokens, heads, dead, sink):
+    """The first key, all of the first blocks, or keys behind them: the logits that are left lie 200 and more below 0, so no
+    reference but one of their own keeps their weights in fp32's range."""
+    need_gpu()
+    check(*workload(tokens, heads, 200, dead, sink))
+
+
+@pytest.mark.parametrize("tokens,heads", [FEW, MANY])
+def test_the_first_key_is_left_out_and_the_next_is_minus_infinity(tokens, heads):
+    """A page out of range at the list's start (no key, flagged), then logits of -inf, then finite ones."""
+    need_gpu()
+    w, live = workload(tokens, heads, 200, range(64, 100), False)
+    table = w.block_table.copy()
+    table[:, 0] = -1
+    w, live = (dataclasses.replace(x, block_table=table) for x in (w, live))
+    out, lse, st = run(w)
+    assert st == pkg.DSV4_ERR_BAD_INDEX
+    idx = [0, w.num_tokens - 1]
+    compare(out[idx], lse[idx], fp4.decode(live, idx))
