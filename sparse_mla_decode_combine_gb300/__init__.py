@@ -595,7 +595,9 @@ def _allocating_on(stream):
     """A context in which what is allocated belongs to the stream that the call runs on."""
     if stream is None or isinstance(stream, torch.cuda.Stream):
         return torch.cuda.stream(stream)
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)))
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    # (ExternalStream(0) is one of torch's own streams, not the legacy default stream that the handle 0 means)
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle != 0 else torch.cuda.default_stream())
 
 
 def workspace_for_fp4(num_tokens: int, num_heads: int, topk_width: int, window: int, device=None) -> torch.Tensor:
