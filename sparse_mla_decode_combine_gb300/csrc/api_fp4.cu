@@ -103,7 +103,7 @@ size_t pool_bytes(int num_layers, int64_t layer_stride, int num_blocks, int page
 
 size_t table_bytes(int rows, int64_t stride, int max_blocks)
 {
-    return rows > 0 ? 4 * ((size_t)(rows - 1) * (size_t)stride + (size_t)max_blocks) : 0;
+    return rows > 0 && max_blocks > 0 ? 4 * ((size_t)(rows - 1) * (size_t)stride + (size_t)max_blocks) : 0;
 }
 
 }  // namespace
