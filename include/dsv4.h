@@ -503,7 +503,8 @@ DSV4_API dsv4_status dsv4_qk_norm_rope_kv_insert_fp4(
  * The operators below run on the device alone: they can be captured, and no length, count or page number
  * passes through the host.  A page number outside [0, num_blocks), or a length past max_blocks *
  * page_block, in a row that is read sets DSV4_ERR_BAD_INDEX in the device status word; the cell becomes
- * -1, the length is cut.  ref_counts must count every row of the table that is given.
+ * -1, the length is cut (the compact writes no lengths: it reads the row as far as the table goes).
+ * ref_counts must count every row of the table that is given.
  *
  * workspace: at least dsv4_cache_pages_workspace_size(num_rows, num_rows_out, num_blocks) bytes (the
  * compact and the copies need no rows: 0, 0), 256-byte aligned, not used by anything else until the

@@ -222,6 +222,7 @@ def compact(cache, table, lens, refs):
             cache[:, to[b]] = cache[:, b]
     tout, bad = np.full(table.shape, -1, np.int32), 0
     for r in range(len(lens)):
+        bad += lens[r] > M * page
         for j in range(pages(lens[r], page, M)):
             v = int(table[r, j])
             tout[r, j] = to[v] if 0 <= v < B else -1

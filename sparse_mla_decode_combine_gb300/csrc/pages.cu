@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
 {
     griddep_wait();
     const int tid = threadIdx.x;
-    if (p.table != nullptr) {
+    if (p.rows > 0) {
         const int64_t cells = (int64_t)p.rows * p.max_blocks;
         for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + tid; i < cells; i += (int64_t)gridDim.x * kCopyThreads) {
             const int r = (int)(i / p.max_blocks), j = (int)(i % p.max_blocks);
@@ -608,6 +608,9 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
             }
             p.table_out[(int64_t)r * p.table_out_stride + j] = v;
         }
+        for (int r = blockIdx.x * kCopyThreads + tid; r < p.rows; r += gridDim.x * kCopyThreads)
+            if (p.lens[r] > (int64_t)p.max_blocks * p.dst.page)
+                atomicOr(p.status, kStatusBadIndex);
     }
     const int n = p.copies != nullptr ? *p.num_copies : p.num_pages;
     constexpr int kGroups = kCopyThreads / kGroup;
@@ -712,7 +715,7 @@ cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t stream)
     m.copies = p.copies;
     m.num_copies = p.num_copies;
     m.page_map = p.page_map;
-    m.table = p.rows > 0 ? p.table : nullptr;
+    m.table = p.table;
     m.table_stride = p.table_stride;
     m.lens = p.lens;
     m.rows = p.rows;
