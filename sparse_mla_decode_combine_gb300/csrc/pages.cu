@@ -595,10 +595,16 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
     griddep_wait();
     const int tid = threadIdx.x;
     if (p.rows > 0) {
-        const int64_t cells = (int64_t)p.rows * p.max_blocks;
+        const int width = max(p.max_blocks, 1);   // (a row without cells has a length to look at)
+        const int64_t cells = (int64_t)p.rows * width;
         for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + tid; i < cells; i += (int64_t)gridDim.x * kCopyThreads) {
-            const int r = (int)(i / p.max_blocks), j = (int)(i % p.max_blocks);
-            const int np = pages_of(p.lens[r], p.dst.page, p.max_blocks);
+            const int r = (int)(i / width), j = (int)(i % width);
+            const int len = p.lens[r];
+            if (j == 0 && len > (int64_t)p.max_blocks * p.dst.page)
+                atomicOr(p.status, kStatusBadIndex);
+            if (j >= p.max_blocks)
+                continue;
+            const int np = pages_of(len, p.dst.page, p.max_blocks);
             int v = -1;
             if (j < np) {
                 v = p.table[(int64_t)r * p.table_stride + j];
@@ -608,9 +614,6 @@ __global__ void __launch_bounds__(kCopyThreads) move_pages_kernel(const MovePara
             }
             p.table_out[(int64_t)r * p.table_out_stride + j] = v;
         }
-        for (int r = blockIdx.x * kCopyThreads + tid; r < p.rows; r += gridDim.x * kCopyThreads)
-            if (p.lens[r] > (int64_t)p.max_blocks * p.dst.page)
-                atomicOr(p.status, kStatusBadIndex);
     }
     const int n = p.copies != nullptr ? *p.num_copies : p.num_pages;
     constexpr int kGroups = kCopyThreads / kGroup;
