@@ -199,10 +199,12 @@ def fork(cache, table, lens, refs, parent, share):
                 tout[r, j] = v
                 if how == "kept":
                     kept.add((par, j))
-    for i in range(len(lens)):
+    for i in range(len(lens)):                # every row of the table is read, for the references that it gives up or keeps
         L = min(max(int(lens[i]), 0), M * page)
+        bad += lens[i] > M * page
         for j in range(pages(L, page, M)):
             v = int(table[i, j])
+            bad += not 0 <= v < B
             if 0 <= v < B:
                 rout[v] += kids.get(i, 0) - 1 if share and (j + 1) * page <= L else 0 if (i, j) in kept else -1
     return cache, tout, lout, rout, bad

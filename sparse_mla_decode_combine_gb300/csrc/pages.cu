@@ -257,10 +257,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         const bool has = f != INT32_MAX && p.offset[f] >= 0;
         const int32_t *src = p.table + (int64_t)i * p.table_stride;
         const int32_t *kept = p.table_out + (int64_t)(has ? f : 0) * p.table_out_stride;
+        if (len > (int64_t)p.max_blocks * page && lane == 0)   // (rows that nobody descends from are read here alone)
+            atomicOr(p.status, kStatusBadIndex);
         for (int j = lane; j < np; j += 32) {
             const int v = src[j];
-            if (v < 0 || v >= B)
+            if (v < 0 || v >= B) {
+                atomicOr(p.status, kStatusBadIndex);
                 continue;
+            }
             const int d = j < full ? c - 1 : (has && kept[j] == v ? 0 : -1);
             if (d != 0)
                 atomicAdd(&p.refs_out[v], d);
@@ -290,6 +294,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
         lens[i] = len;
         nps[i] = pages_of(len, page, M);
         fulls[i] = p.share ? min(nps[i], max(len, 0) / page) : 0;
+        if (len > (int64_t)M * page)
+            atomicOr(p.status, kStatusBadIndex);
     }
     for (int r = tid; r < p.rows_out; r += kPlanThreads) {
         const int par = p.parent[r];
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
         const int np = ok ? nps[par] : 0, full = ok ? fulls[par] : 0;
         if (lane == 0) {
             p.lens_out[r] = max(len, 0);
-            if (par >= 0 && (!ok || lens[par] > (int64_t)M * page))
+            if (par >= 0 && !ok)
                 atomicOr(p.status, kStatusBadIndex);
             if (ok)
                 atomicAdd(&kids[par], 1);
@@ -362,12 +368,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
             bool take = false;
             if (j < np) {
                 v = src[j];
-                if (v < 0 || v >= B) {
-                    atomicOr(p.status, kStatusBadIndex);
+                if (v < 0 || v >= B)
                     v = -1;
-                } else {
+                else
                     take = takes(r, par, full, j, v);
-                }
             }
             const unsigned m = __ballot_sync(0xffffffffu, take);
             if (take) {
@@ -380,12 +384,6 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
             if (j < M)
                 dst[j] = v;
         }
-        // a row that finds no pages: its bad cells are flagged as those of any row
-        if (par >= 0 && !ok) {
-            for (int j = lane; j < nps[par]; j += 32)
-                if (src[j] < 0 || src[j] >= B)
-                    atomicOr(p.status, kStatusBadIndex);
-        }
     }
     __syncthreads();
     for (int i = warp; i < p.rows; i += kPlanThreads / 32) {
@@ -393,10 +391,12 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_small_kernel(const For
         const int c = kids[i], f = first[i];
         const bool has = f != INT32_MAX && off[f] >= 0;
         const int32_t *src = p.table + (int64_t)i * p.table_stride;
-        for (int j = lane; j < np; j += 32) {
+        for (int j = lane; j < np; j += 32) {   // (every cell of every row: bad ones are flagged here)
             const int v = src[j];
-            if (v < 0 || v >= B)
+            if (v < 0 || v >= B) {
+                atomicOr(p.status, kStatusBadIndex);
                 continue;
+            }
             const int d = j < full ? c - 1 : (has && refs[v] == 1 ? 0 : -1);   // (the first child kept it)
             if (d != 0)
                 atomicAdd(&refs_new[v], d);
