@@ -10,10 +10,9 @@
 //
 // Arithmetic.  Queries: fp32, one rounding to BF16.  The key's codes are those of the exactly computed
 // key: a 4-bit step is a quarter of the value or more, so a value that fp32 puts on the wrong side of a
-// rounding border would be off by all of it.  The key is computed in fp32 too, to within 15 roundings (2^-20: a
-// sum of squares of 16 terms a lane and five levels, halved by the root; root, reciprocal and two products),
-// with a check whether any value of a block, or its maximum, lies that near to a border; the blocks that have
-// one (about one in two hundred) are done again in fp64.
+// rounding border would be off by all of it.  The key is computed in fp32 too, with a check whether any value of a
+// block, or its maximum, lies so near to a border that roundings could decide (kNear); the pairs of blocks that have one
+// (about one in 3500 of normal keys) are done again in fp64.
 //
 // Work.  A warp per four heads of a token, a warp per key.  Eight lanes share a head, each with nine 16-byte pieces
 // (8 values) of its 1152 bytes, so a load or store covers 128 contiguous bytes of four heads, the sum of squares takes
@@ -35,7 +34,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPairs = kDim / 2;   // 288 BF16 pairs per head; pairs 256.. are the rope part
-constexpr float kNear = 0x1p-20f;
+// What a key's value may be off by in fp32, in roundings of 2^-24 of it.  Over 576 dims: the sum of squares 17 to a lane (of
+// 18 products the first is exact) and 5 levels, the mean 1, eps 1, adding it 1: 25, halved by the root; the root, its
+// reciprocal and two products 4: 16.5.  (512 dims: 15 by the same count, dividing by them is exact.)  The comparison's own
+// product rounds once more: 17.5 in all, below 20.  (The window of exponent_of: 16 steps of 2^-23 at 1.5, 21 roundings.)
+constexpr float kNear = 0x1.4p-20f;
 
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t v)
 {
@@ -70,7 +73,7 @@ __device__ __forceinline__ T half_warp_max(T v)
 }
 
 // Smallest integer e with 6 * 2^e >= amax (0 for amax 0), clamped to [-127, 125]: k - 2 for amax in [2^k, 1.5 * 2^k],
-// k - 1 from there to 2^(k+1).  *near: amax is within about 2^-20 of the border 1.5 * 2^k, or too small to tell.
+// k - 1 from there to 2^(k+1).  *near: amax is within 21 roundings of the border 1.5 * 2^k, or too small to tell.
 __device__ __forceinline__ int exponent_of(float amax, bool *near)
 {
     const int bits = __float_as_int(amax), m = bits & 0x7FFFFF;
