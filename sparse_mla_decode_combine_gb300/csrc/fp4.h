@@ -33,7 +33,10 @@ cudaError_t launch_dependent(void (*kernel)(const Params), dim3 grid, int thread
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+    if (e != cudaSuccess)
+        (void)cudaGetLastError();   // (returned here: a later call of this library must not find it as its own)
+    return e;
 }
 
 #ifdef __CUDACC__
