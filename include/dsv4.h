@@ -476,7 +476,9 @@ DSV4_API size_t dsv4_sparse_mla_decode_fp4_workspace_size(int32_t num_tokens, in
  *   positions, slot_mapping  int64 [num_tokens].
  *   cos_sin_cache    fp32 [max_position, 64]: 32 cosines, then 32 sines per position.
  *   kv_cache         uint8 [num_slots, 400], 16-byte aligned.
- *   k_out            BF16 [num_tokens, 576], token stride even, >= 576; or NULL.  Not kv itself.
+ *   k_out            BF16 [num_tokens, 576], token stride even, >= 576; or NULL.
+ * But for q_out = q, a row of q_out or k_out shares no byte with a row of q, kv or the other output (rows may
+ * lie between those of another array); such calls are refused.
  * A negative slot writes no entry (a padding token; its queries and k_out are computed).  A slot >=
  * num_slots, or a position outside [0, max_position), writes no entry and sets DSV4_ERR_BAD_INDEX in
  * the device status word; at such a position nothing is rotated.  Two tokens of a call must not name

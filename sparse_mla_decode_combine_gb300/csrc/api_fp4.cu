@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstdlib>
 
 #include "../../include/dsv4.h"
 #include "fp4.h"
@@ -21,6 +22,19 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb)
 {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+// whether any of the `rows` rows of wa bytes from a on, sa bytes apart, shares a byte with one of b's (rows that lie between
+// the other array's, as in a buffer that holds queries and keys side by side, do not)
+bool rows_overlap(const void *a, int64_t sa, int64_t wa, const void *b, int64_t sb, int64_t wb, int64_t rows)
+{
+    if (!overlap(a, (size_t)((rows - 1) * sa + wa), b, (size_t)((rows - 1) * sb + wb)))
+        return false;
+    if (sa != sb || rows == 1)
+        return true;
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    const int64_t k = d / sa - (d % sa < 0 ? 1 : 0), r = d - k * sa;   // row j of b begins r bytes into row j + k of a
+    return (r < wa && std::llabs(k) < rows) || (r + wb > sa && std::llabs(k + 1) < rows);
 }
 
 // ---- the decode's workspace: the tokens' slot lists, their lengths, and the parts of split units
@@ -237,8 +251,16 @@ extern "C" DSV4_API dsv4_status dsv4_qk_norm_rope_kv_insert_fp4(
         !aligned(kv, 4) || (k_out != nullptr && (!aligned(k_out, 4) || (k_out_token_stride & 1) != 0)) ||
         (num_slots > 0 && !aligned(kv_cache, 16)))
         return DSV4_ERR_INVALID_ARG;
-    // queries in place keep their rows' places; a key's blocks are read again after the first of k_out are written
-    if ((q_out == q && num_tokens > 1 && q_out_token_stride != q_token_stride) || k_out == kv)
+    // queries in place keep their rows' places; a key's blocks are read again after the first of k_out are written, and other
+    // rows that share bytes would be read before or after they are written
+    if (q_out == q ? num_tokens > 1 && q_out_token_stride != q_token_stride
+                   : rows_overlap(q, 2 * q_token_stride, 2 * row, q_out, 2 * q_out_token_stride, 2 * row, num_tokens))
+        return DSV4_ERR_INVALID_ARG;
+    const int64_t key = 2 * kDim;
+    if (rows_overlap(kv, 2 * kv_token_stride, key, q_out, 2 * q_out_token_stride, 2 * row, num_tokens) ||
+        (k_out != nullptr && (rows_overlap(kv, 2 * kv_token_stride, key, k_out, 2 * k_out_token_stride, key, num_tokens) ||
+                              rows_overlap(q, 2 * q_token_stride, 2 * row, k_out, 2 * k_out_token_stride, key, num_tokens) ||
+                              rows_overlap(q_out, 2 * q_out_token_stride, 2 * row, k_out, 2 * k_out_token_stride, key, num_tokens))))
         return DSV4_ERR_INVALID_ARG;
     Insert4Params p{};
     if (device_info(&p.status, nullptr) != cudaSuccess)
