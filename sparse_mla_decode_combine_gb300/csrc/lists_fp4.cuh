@@ -67,7 +67,7 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
     const bool row_ok = row >= 0 && row < p.num_reqs;
     const int32_t *bt_row = p.block_table + (int64_t)(row_ok ? row : 0) * p.bt_stride;
     // window [win_lo, pos]; the top-k survivors are the first occurrences of positions in [0, win_lo)
-    const int pos = seq_len - 1;   // seq_len <= 0: nothing is visible
+    const int pos = max(seq_len, 0) - 1;   // seq_len <= 0: nothing is visible
     const long long lo = (long long)pos - p.window + 1;
     const int win_lo = lo < 0 ? 0 : (int)lo;
     const int swa = seq_len > 0 ? pos - win_lo + 1 : 0;
