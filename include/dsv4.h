@@ -422,6 +422,12 @@ DSV4_API size_t dsv4_sparse_mla_decode_mtp_union_workspace_size(int32_t num_toke
  * No page has a 4-bit cache: this is the decode of dsv4_sparse_mla_decode (same lists, same
  * formulas, same outputs) with the entry above, which takes 61 % of the bytes.  The dequantised
  * keys are exact in BF16 (a product past its range becomes an infinity, as rounding to BF16 does).
+ * The softmax's weights are rounded to BF16 for their product with the values, as there.  With few tokens
+ * (num_tokens * ceil(num_heads / 64) up to half the multiprocessors) the output is divided by the sum of the
+ * rounded weights, so that the rounding of a key that has most of the weight cancels; with more by that of
+ * the exact ones: a token's last bits depend on the size of its batch.  The lse is that of the exact weights.
+ * Weights are held relative to a logit that may lie 40 ln 2 below the largest, so the fp32 sums over a list of
+ * up to 2^24 keys stay in range for latent values below 2^64; larger ones may become infinite.
  *
  * Arguments: those of dsv4_sparse_mla_decode, with
  *   kv_cache        uint8 [num_blocks, page_block, 400], 16-byte aligned (num_blocks may be 0);

@@ -21,7 +21,8 @@
 //     used up (two blocks ahead in registers: 140 against 135 us below; whole entries prefetched to L2: slower too);
 //   - the softmax takes the logits of the unit's first key as references, and exchanges maxima between warps only
 //     when a logit exceeds its head's reference by 40 (in log2 units): P and the sums are floating-point numbers,
-//     whose relative precision does not depend on the reference, and 2^40 is far from fp32's and BF16's range.
+//     whose relative precision does not depend on the reference, and 2^40 leaves fp32's sums of 2^24 keys room for
+//     values up to 2^64 (those of normalised keys are about 1).
 //     The usual block needs one barrier that ORs a predicate.  Row sums stay in registers.
 //     Where few units are shared, the output is divided by the sum of the weights as rounded to BF16, so that a key that
 //     has most of the weight loses nothing by its rounding (the lse keeps the exact sum; 1 % of the time of a small batch).

@@ -8,7 +8,7 @@ import torch
 
 import sparse_mla_decode_combine_gb300 as pkg
 import synth
-from fp4_util import run, to_fp4
+from fp4_util import compare, run, to_fp4
 from gpu_util import need_gpu
 from oracle import fp4
 
@@ -68,3 +68,28 @@ def test_the_nan_scale_stays_in_its_token(tokens, heads):
     assert bool(torch.isfinite(alone).all())
     assert torch.equal(out[good], alone[good]) and torch.equal(lse[good], alone_lse[good])
     assert bool(torch.isnan(out[~good]).all()) and bool(torch.isnan(lse[~good]).all())
+
+
+@pytest.mark.parametrize("tokens,heads", [(2, 64), (90, 128)])
+@pytest.mark.parametrize("step", [0.03, 0.5])
+def test_latents_up_to_2_to_the_64_beside_rising_logits(tokens, heads, step):
+    """The largest magnitudes for which the sums are promised to stay finite, with logits that rise over the list to just below
+    the range that is left above the first one's (0.03 a key), or past it many times (0.5)."""
+    need_gpu()
+    keys = 900
+    w = to_fp4(synth.make_workload(name="large", seed=102, heads=heads, req_seq_lens=[keys] * tokens, topk_width=0, window=keys,
+                                   sink=False))
+    cache = w.kv_cache.copy()
+    cache[..., 384:] = 127 + 61                            # 6 * 2^61 < 2^64
+    rope = np.zeros((*cache.shape[:2], 64))
+    for t in range(tokens):
+        for i in range(-(-keys // w.page)):
+            rope[w.block_table[t, i], :, 0] = step * (64 * i + np.arange(64))
+    cache[..., 256:384] = synth.bf16_bits(rope).astype("<u2").view(np.uint8).reshape(*cache.shape[:2], 128)
+    q = np.zeros(w.q.shape)
+    q[..., 512] = 1.0
+    w = dataclasses.replace(w, kv_cache=cache, q=synth.bf16_bits(q), softmax_scale=1.0)
+    out, lse, st = run(w)
+    assert st == pkg.DSV4_OK
+    idx = [0, tokens // 2, tokens - 1]
+    compare(out[idx], lse[idx], fp4.decode(w, idx), w.name)
