@@ -116,7 +116,7 @@ constexpr uint32_t kIdescPV = kIdescBase | ((uint32_t)(kDvTile >> 4) << 24) | (1
 // 16 bytes of an entry.  Entries start at odd multiples of 16 bytes as often as at even ones, so a row's 64-byte
 // pieces share 32-byte sectors with their neighbours: L1 keeps them for the next piece (8 % of the kernel's time
 // against loads that do not allocate there).
-__device__ __forceinline__ uint4 ld16(const void *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
+__device__ __forceinline__ uint4 ld16(const void *p) { return __ldca(reinterpret_cast<const uint4 *>(p)); }
 
 // 32 E2M1 codes times 2^(se - 127) -> 32 BF16 values, exactly, into the four 16-byte units u .. u + 3 (xored with x)
 // of the row at shared address rb.
@@ -214,7 +214,7 @@ __device__ __forceinline__ void store_q(const Decode4Params &p, int t, int h0, u
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             const int i = wid + kWorkers * (j0 + j);
-            v[j] = i < pieces ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
+            v[j] = i < pieces ? __ldca(q + i) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
             auto load_piece = [&](const uint8_t *e, int m) { pre[m] = ld16(e + 128 * m + 16 * piece); };
             auto load_scales = [&](const uint8_t *e) {
                 if (lane < 16)
-                    psc = __ldg(reinterpret_cast<const uint32_t *>(e + kScale4Offset) + (lane >> 2));
+                    psc = __ldca(reinterpret_cast<const uint32_t *>(e + kScale4Offset) + (lane >> 2));
             };
             const int slot0 = slot_of(0);
             bool pre_ok = slot0 >= 0;

@@ -130,14 +130,14 @@ __device__ __noinline__ uint32_t exact_codes(const Insert4Params &p, int t, int 
     const int nj = p.kv_norm_dims / 64;
     double ss = 0.0;
     for (int i = 0; i < nj; ++i) {
-        const float2 v = unpack_bf16x2(__ldg(a + 32 * i));
+        const float2 v = unpack_bf16x2(__ldca(a + 32 * i));
         ss = fma((double)v.x, (double)v.x, fma((double)v.y, (double)v.y, ss));
     }
     const double root = sqrt(warp_sum(ss) / (double)p.kv_norm_dims + p.eps);
-    const float2 v = unpack_bf16x2(__ldg(a + 32 * j));
+    const float2 v = unpack_bf16x2(__ldca(a + 32 * j));
     const int d = 2 * (lane + 32 * j);
-    const double y0 = (double)v.x / root * (p.kv_w ? (double)__ldg(p.kv_w + d) : 1.0);
-    const double y1 = (double)v.y / root * (p.kv_w ? (double)__ldg(p.kv_w + d + 1) : 1.0);
+    const double y0 = (double)v.x / root * (p.kv_w ? (double)__ldca(p.kv_w + d) : 1.0);
+    const double y1 = (double)v.y / root * (p.kv_w ? (double)__ldca(p.kv_w + d + 1) : 1.0);
     const double a0 = isnan(y0) ? 0.0 : fabs(y0), a1 = isnan(y1) ? 0.0 : fabs(y1);
     const int e = exponent_of(half_warp_max(a0 > a1 ? a0 : a1));
     return code_of(ldexp(y0, -e)) | code_of(ldexp(y1, -e)) << 4 | (uint32_t)(e + 127) << 8;
@@ -148,9 +148,9 @@ template <bool kWide>
 __device__ __forceinline__ uint4 load4(const void *a)
 {
     if (kWide)
-        return __ldg(reinterpret_cast<const uint4 *>(a));
+        return __ldca(reinterpret_cast<const uint4 *>(a));
     const uint32_t *b = static_cast<const uint32_t *>(a);
-    return make_uint4(__ldg(b), __ldg(b + 1), __ldg(b + 2), __ldg(b + 3));
+    return make_uint4(__ldca(b), __ldca(b + 1), __ldca(b + 2), __ldca(b + 3));
 }
 
 __device__ __forceinline__ float4 as_floats(const uint4 &v)
@@ -244,8 +244,8 @@ __device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int la
     const bool rot = pos >= 0 && pos < p.max_pos;
     float c = 1.f, s = 0.f;   // this lane's rope pair i = lane
     if (rot) {
-        c = __ldg(p.cos_sin + pos * 64 + lane);
-        s = __ldg(p.cos_sin + pos * 64 + 32 + lane);
+        c = __ldca(p.cos_sin + pos * 64 + lane);
+        s = __ldca(p.cos_sin + pos * 64 + 32 + lane);
     } else if (lane == 0) {
         atomicOr(p.status, kStatusBadIndex);
     }
@@ -256,7 +256,7 @@ __device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int la
     uint32_t x[9];
 #pragma unroll
     for (int j = 0; j < 9; ++j)
-        x[j] = __ldg(p.kv + t * p.kv_stride + lane + 32 * j);
+        x[j] = __ldca(p.kv + t * p.kv_stride + lane + 32 * j);
     const int nj = p.kv_norm_dims / 64;   // pairs lane + 32 j with j < nj are normalised
     float r = 1.f;
     if (nj > 0) {
@@ -281,8 +281,8 @@ __device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int la
             y0 *= r;
             y1 *= r;
             if (p.kv_w != nullptr) {
-                y0 *= __ldg(p.kv_w + 2 * (lane + 32 * j));
-                y1 *= __ldg(p.kv_w + 2 * (lane + 32 * j) + 1);
+                y0 *= __ldca(p.kv_w + 2 * (lane + 32 * j));
+                y1 *= __ldca(p.kv_w + 2 * (lane + 32 * j) + 1);
             }
         }
         bool near;
@@ -312,7 +312,7 @@ __device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int la
         if (wild) {   // (as the latent: from the fp64 root)
             double ss = 0.0;
             for (int i = 0; i < 9; ++i) {
-                const float2 u = unpack_bf16x2(__ldg(p.kv + t * p.kv_stride + lane + 32 * i));
+                const float2 u = unpack_bf16x2(__ldca(p.kv + t * p.kv_stride + lane + 32 * i));
                 ss = fma((double)u.x, (double)u.x, fma((double)u.y, (double)u.y, ss));
             }
             const double root = sqrt(warp_sum(ss) / (double)kDim + p.eps);
@@ -320,8 +320,8 @@ __device__ __forceinline__ void insert_key(const Insert4Params &p, int t, int la
             v = make_float2((float)((double)u.x / root), (float)((double)u.y / root));
         }
         if (p.kv_w != nullptr) {
-            v.x *= __ldg(p.kv_w + kLatent + 2 * lane);
-            v.y *= __ldg(p.kv_w + kLatent + 2 * lane + 1);
+            v.x *= __ldca(p.kv_w + kLatent + 2 * lane);
+            v.y *= __ldca(p.kv_w + kLatent + 2 * lane + 1);
         }
     }
     const uint32_t rope = pack_rn_bf16x2(v.x * c - v.y * s, v.x * s + v.y * c);

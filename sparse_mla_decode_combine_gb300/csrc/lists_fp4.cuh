@@ -55,7 +55,7 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
     int tv[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u)
-        tv[u] = u * kThreads + tid < p.topk_width ? __ldg(trow + u * kThreads + tid) : -1;
+        tv[u] = u * kThreads + tid < p.topk_width ? __ldca(trow + u * kThreads + tid) : -1;
     const int seq_len = p.seq_lens[t];
     const int row = p.req_idx != nullptr ? p.req_idx[t] : t;
     int n = p.topk_width;
@@ -72,7 +72,7 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
     const int win_lo = lo < 0 ? 0 : (int)lo;
     const int swa = seq_len > 0 ? pos - win_lo + 1 : 0;
     int32_t *out = p.slots + (int64_t)t * p.list_w;
-    auto page_at = [&](int blk) { return row_ok && blk < p.max_blocks ? __ldg(bt_row + blk) : -1; };   // (-1: outside the table)
+    auto page_at = [&](int blk) { return row_ok && blk < p.max_blocks ? __ldca(bt_row + blk) : -1; };   // (-1: outside the table)
     auto slot_in = [&](int phys, int at) {
         if (phys < 0 || phys >= p.num_blocks) {
             atomicOr(p.status, kStatusBadIndex);
@@ -102,7 +102,7 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
                 twice |= (atomicOr(&seen[tv[u] >> 5], 1u << (tv[u] & 31)) >> (tv[u] & 31)) & 1u;
 #pragma unroll 1
         for (int i = kLoads * kThreads + tid; i < n; i += kThreads) {
-            const int v = __ldg(trow + i);
+            const int v = __ldca(trow + i);
             if (v >= 0 && v < win_lo)
                 twice |= (atomicOr(&seen[v >> 5], 1u << (v & 31)) >> (v & 31)) & 1u;
         }
@@ -126,7 +126,7 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
             hs[u] = tv[u] >= 0 ? insert(tab, bits, tv[u], u * kThreads + tid) : 0u;
 #pragma unroll 1
         for (int i = kLoads * kThreads + tid; i < n; i += kThreads) {
-            const int v = __ldg(trow + i);
+            const int v = __ldca(trow + i);
             if (v >= 0 && v < win_lo)
                 insert(tab, bits, v, i);
         }
@@ -142,7 +142,7 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
             if (pg + u >= npass)
                 break;
             const int i = (pg + u) * kThreads + tid;
-            int v = pg == 0 ? tv[u] : (i < n ? __ldg(trow + i) : -1);
+            int v = pg == 0 ? tv[u] : (i < n ? __ldca(trow + i) : -1);
             v = v < win_lo ? v : -1;
             vg[u] = v;
             bool keep = v >= 0;
