@@ -11,8 +11,8 @@
 // moves the pages of every layer.  The second is bound by HBM (each byte read and written once), the first by
 // the latency of its dependent steps, so it takes as few trips to global memory as it can: in a pool of up to
 // 16384 pages one CTA does it, with the counts, the rows' numbers and the free list in shared memory; larger
-// ones take a cluster of eight CTAs with a cluster barrier between the steps and the numbers in the workspace
-// (333 pages: 5.7 us for a compaction against 9.3; a fork of 64 rows: 9.7 against 14.2).  A compaction that moves
+// ones take a cluster of eight CTAs with a cluster barrier between the steps and the numbers in the workspace,
+// and so do forks of many rows or wide tables, whose cells 32 warps read too slowly.  A compaction that moves
 // 418 MB takes 140 us where the bytes alone take 123 at the measured 6794 GB/s.
 // A short list of pages to copy needs no plan: one launch.
 #include <algorithm>
@@ -29,9 +29,13 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kCluster * kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;         // 16-byte pieces a thread holds: a page of 64 entries of 400 bytes in one round of a CTA
-constexpr int kSmallPages = 16384;     // the one-CTA plans: pages,
-constexpr int kSmallRows = 1024;       // rows before and after,
-constexpr int kSmallCells = 1 << 16;   // and cells of the table
+// The one-CTA plans, against those of eight CTAs, in us with a move of little.  Compact: 333 pages 4.8 / 8.3, 8192 pages
+// 8.6 / 10.0, 12000 pages 10.3 / 11.3, 16384 pages 12.4 / 12.1.  Fork, rows x cells: of 4096 pages 64 x 64 9.2 / 13.2, 128 x 64
+// 12.6 / 13.6, 160 x 64 14.3 / 13.1, 64 x 256 10.8 / 12.9, 96 x 256 13.2 / 12.8; of 16384 pages 64 x 256 15.4 / 16.5, 128 x 8
+// 14.7 / 14.1, 64 x 1024 22.0 / 18.3, 1024 x 8 57 / 25.
+constexpr int kSmallPages = 16384;     // pages,
+constexpr int kSmallRows = 128;        // rows before and after (at most one to a thread),
+constexpr int kSmallCells = 1 << 14;   // and cells of the table
 
 __device__ __forceinline__ void cluster_sync()
 {
