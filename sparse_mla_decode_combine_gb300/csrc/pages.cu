@@ -28,6 +28,7 @@ constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kCluster * kPlanThreads / 32;
 constexpr int kCopyThreads = 256;
+constexpr int kFewSmall = 2048;        // small pages that are copied without a plan
 constexpr int kCopyUnroll = 8;         // 16-byte pieces a thread holds: a page of 64 entries of 400 bytes in one round of a CTA
 // The one-CTA plans, against those of eight CTAs, in us with a move of little.  Compact: 333 pages 4.8 / 8.3, 8192 pages
 // 8.6 / 10.0, 12000 pages 10.3 / 11.3, 16384 pages 12.4 / 12.1.  Fork, rows x cells: of 4096 pages 64 x 64 9.2 / 13.2, 128 x 64
@@ -541,8 +542,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_small_kernel(const 
 // ---- copies of listed pages ----------------------------------------------------------------------
 
 // A target that is listed twice receives its last pair.  In one pool, a pair whose source is also a
-// target of the call is refused (the page might be read before or after it is written).  More pairs than
-// a CTA has threads are checked through a claim on each target; fewer by the moving kernel itself.
+// target of the call is refused (the page might be read before or after it is written).  Long lists are
+// checked through a claim on each target; short ones (launch_copy_pages) by the moving kernel itself, a pair to a thread.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) copy_plan_kernel(const CopyPagesParams p)
 {
     const int gtid = cluster_rank() * kPlanThreads + threadIdx.x;
@@ -735,7 +736,13 @@ cudaError_t launch_compact(const CompactParams &p, int sms, cudaStream_t stream)
 
 cudaError_t launch_copy_pages(const CopyPagesParams &p, int sms, cudaStream_t stream)
 {
-    const bool few = p.num_pages <= kCopyThreads;   // (7 pages in four layers: 2.4 against 5.0 us)
+    // A short list goes without a plan (8 pages of 25600 bytes in 1, 8 and 40 layers: 2.1, 2.2 and 3.4 us, with it 4.0, 4.1 and
+    // 5.3; 256 pages: 3.4, 13.9 and 84 against 5.7, 17.9 and 91).  Pages that would not take a whole CTA then do, with two
+    // barriers each: up to about 2048 of them, over all layers, that still costs less than the plan (6400 bytes, 256 pages in 8
+    // layers: 5.5 against 6.8, in 40: 33 against 21; 400 bytes: 5.2 against 5.0, and 18.7 against 8.5).
+    const int64_t pieces = (int64_t)p.dst.page * p.dst.entry_bytes / 16;
+    const bool few = p.num_pages <= kCopyThreads &&
+                     (pieces > kCopyUnroll * 128 || (int64_t)p.num_pages * p.dst.num_layers <= kFewSmall);
     if (!few) {
         const cudaError_t e = launch_dependent(copy_plan_kernel, dim3(kCluster), kPlanThreads, 0, stream, p);
         if (e != cudaSuccess)

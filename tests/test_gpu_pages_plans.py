@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from gpu_util import need_gpu
-from test_gpu_pages import check_compact, check_fork, pool
+from test_gpu_pages import check_compact, check_copy, check_fork, pool
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +25,17 @@ def test_compact(blocks):
     spare = np.flatnonzero(refs == 0)
     refs[spare[rng.random(len(spare)) < 0.4]] = 3
     check_compact(cache, table, lens, refs, in_place=blocks % 2 == 0)
+
+
+@pytest.mark.parametrize("layers,n", [(8, 256), (9, 227), (9, 228), (8, 257), (2049, 1), (1, 256)])
+@pytest.mark.parametrize("page", [1, 1025])
+@pytest.mark.parametrize("one_pool", [True, False])
+def test_copies(layers, n, page, one_pool):
+    """Short lists with and without a plan; targets that are named twice, sources that are targets, pages out of range."""
+    need_gpu()
+    rng = np.random.default_rng(layers + n)
+    blocks = 300 if page == 1 else 30
+    dst = rng.integers(0, 256, (min(layers, 100) if page > 1 else layers, blocks, page, 16)).astype(np.uint8)
+    src = dst if one_pool else rng.integers(0, 256, dst.shape).astype(np.uint8)
+    s, d = rng.integers(-1, blocks + 1, n), rng.integers(0, blocks + 1, n)
+    check_copy(dst, src, s, d, one_pool)
