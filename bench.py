@@ -21,7 +21,8 @@ streams double-buffered against the calls (as a serving loop overlaps them), 64 
 
 Other ops, timed the same way on their own workloads: --op topk-select (top-k selection from
 indexer scores), --op combine-compressed (the compressed-region combine), --op
-qnorm-rope-insert (fused query norm/RoPE and FP8 KV insert).
+qnorm-rope-insert (fused query norm/RoPE and FP8 KV insert), --op fp4-and-pages (the 4-bit cache's
+decode and insert and the page operators, every case of perf/operators.py and five more shapes of the decode).
 N > 1: every rank decodes its own batch on its own GPU (no data-path
 collective; weak scaling).
 
@@ -68,7 +69,8 @@ def parse_args():
     ap.add_argument("--no-e2e", action="store_true")
     ap.add_argument("--no-per-workload", action="store_true",
                     help="time only --workload (the default line also times all five decode workloads)")
-    ap.add_argument("--op", choices=["decode", "combine-compressed", "topk-select", "qnorm-rope-insert", "mtp-union"],
+    ap.add_argument("--op", choices=["decode", "combine-compressed", "topk-select", "qnorm-rope-insert", "mtp-union",
+                                     "fp4-and-pages"],
                     default="decode", help="decode (the headline), or one of the steps around it on its own")
     ap.add_argument("--topk-workload", choices=["long-batch", "long-decode"], default="long-batch",
                     help="top-k selection workload (synth.topk_config)")
@@ -756,6 +758,65 @@ def run_mtp_union(args):
     return 0
 
 
+def run_fp4_and_pages(args):
+    """The 4-bit cache's operators and the page operators: each case captured, twelve calls to a graph that is replayed ("graph_us"
+    a call), and called in a loop through the Python binding from an idle start ("loop_us"), over three prepared inputs in turn
+    (the small cases' inputs stay in L2).  240 calls a case, or fewer with --steps."""
+    import torch
+    import perf.operators as ops
+    from sparse_mla_decode_combine_gb300 import build as pkg_build
+    pkg_build.build()
+    torch.cuda.set_device(0)
+    props = torch.cuda.get_device_properties(0)
+    ops.own = True
+    cases = ops.listed()
+    heavy = next(c for c in cases if c["name"] == "decode-heavy")
+    cases += [dict(heavy, name=f"decode-{h}-heads", heads=h) for h in (16, 32, 64)]
+    cases += [dict(heavy, name="decode-one-token", tokens=1, heads=16),
+              dict(heavy, name="decode-one-token-long", tokens=1, heads=16, topk=64, window=131008, seq_lo=200000, seq_hi=200000,
+                   sink=False)]
+    sampler = ClockSampler(str(getattr(props, "uuid", "")))
+    sampler.start()
+    time.sleep(0.2)
+    hbm_peak, flops_peak, _, peak_src = peaks()
+    n = max(1, min(args.steps, 240) // 12)
+
+    def timed(run, calls):
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        torch.cuda.synchronize()
+        ev[0].record()
+        run()
+        ev[1].record()
+        torch.cuda.synchronize()
+        return ev[0].elapsed_time(ev[1]) / calls * 1e3
+
+    rows, t0 = {}, time.time()
+    for c in cases:
+        states = [ops.prepare(c, k) for k in range(3)]
+        for i in range(max(6, min(args.warmup, 30))):
+            ops.run(states[i % 3])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(12):
+                ops.run(states[i % 3])
+        for _ in range(3):
+            graph.replay()
+        g = timed(lambda: [graph.replay() for _ in range(n)], 12 * n)
+        for _ in range(2):   # (the first loop after a graph warms up the host)
+            loop = timed(lambda: [ops.run(states[i % 3]) for i in range(12 * n)], 12 * n)
+        w = ops.work(c)
+        by, fl = w["bytes"] / (hbm_peak * 1e9) * 1e6, w["flops"] / (flops_peak * 1e12) * 1e6
+        rows[c["name"]] = {"graph_us": g, "loop_us": loop, "floor_us": max(by, fl), "floor_bound": "hbm" if by > fl else "flops",
+                           "frac": max(by, fl) / g}
+        del states, graph
+        torch.cuda.empty_cache()
+    t1 = time.time()
+    sampler.stop()
+    print(json.dumps({"op": "fp4-and-pages", "metric": "microseconds a call", "unit": "us", "higher_is_better": False, "n_gpus": 1,
+                      "data": "synthetic", "peak_source": peak_src, "cases": rows, "clocks": sampler.summary(t0, t1)}), flush=True)
+    return 0
+
+
 def run_combine_compressed(args):
     """The compressed-region combine on its own: 64 requests x 4 tokens (speculative verify
     shape), top-k 2048 of a 4x-compressed region, window 128, rows of 2304 entries. Bytes per
@@ -1033,6 +1094,10 @@ def main():
         if args.impl == "reference" or int(os.environ.get("RANK", "0")) != 0:
             return 0
         return run_combine_compressed(args)
+    if args.op == "fp4-and-pages":
+        if args.impl == "reference" or int(os.environ.get("RANK", "0")) != 0:
+            return 0
+        return run_fp4_and_pages(args)
     if args.op == "mtp-union":
         if args.impl == "reference" or int(os.environ.get("RANK", "0")) != 0:
             return 0
