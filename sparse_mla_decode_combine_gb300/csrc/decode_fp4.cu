@@ -86,7 +86,7 @@ constexpr float kExceedLog2 = 40.f;
 constexpr int kJoinHeads = 4;            // heads per CTA of the joining kernel, a warp each
 constexpr int kJoinSplit = 8;            // warps to a head where it may have kJoinMany parts or more
 constexpr int kJoinMany = 8;
-constexpr int kMinBlocks = 2;            // per CTA: below that, joining costs more than the blocks
+constexpr int kMinBlocks = 2;            // per CTA (with 1: 1 x 16 heads, 256 keys 11.8 -> 10.8 us, 16 x 64, 640 keys 16.7 -> 18.6)
 
 // small shared region (after Q and the two K tiles)
 constexpr int kOffRed = 0;               // float [4][64]: per-quadrant head maxima, or row sums at the end
@@ -828,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 // Joins the parts of the units that several CTAs shared, in the order of the parts:
 //   m = max(max_c m_c, sink), Z = sum_c l_c e^{m_c - m} + e^{sink - m},
 //   out = sum_c e^{m_c - m} O_c / Z  (BF16),  lse = m + ln Z
-// A warp to a head, or kSplit of them, each with a run of the parts, where there may be many (one token over 131072 keys, 152
-// parts: 75 us in all with one warp, 42 with eight; 17 parts: 19.6 and 17.8; four parts: 20.6 and 24.8).  The parts come from
+// A warp to a head, or kSplit of them, each with a run of the parts, where there may be many (one token x 16 heads over 131072
+// keys, 152 parts: 81 us in all with one warp, 45.5 with eight; 17 parts: 16.8 and 15.0; four parts: 20.6 and 24.8).  The parts come from
 // L2, kJoinBatch at a time with every load in flight: four where few CTAs share each unit (latency is all there is; they are read before it is known how many of them had
 // work), two where runs of blocks end inside units (two parts are usual, and more registers would leave fewer warps: 8
 // against 10.5 us for 151 split units).  (Joined inside the decode, by the CTA of a unit that finished last, the 256

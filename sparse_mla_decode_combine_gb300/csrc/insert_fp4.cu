@@ -17,7 +17,7 @@
 // Work.  A warp per four heads of a token, a warp per key.  Eight lanes share a head, each with nine 16-byte pieces
 // (8 values) of its 1152 bytes, so a load or store covers 128 contiguous bytes of four heads, the sum of squares takes
 // three shuffles for all four, and no lane is idle; all loads of a warp are in flight before any use.  Bound by HBM:
-// every query is read and written once (8191 tokens x 64 heads: 182 us, 1.24 GB, the rate of a copy; 128 x 128: 7.9 us).
+// every query is read and written once (8191 tokens x 64 heads: 183 us, 1.23 GB, the rate of a copy; 128 x 128: 7.4 us).
 // (Pairs of 4 bytes to a lane and a warp to a head took 477 us; queries whose rows are not 16-byte aligned still go by
 // fours of such loads.)  The keys' warps come first: their fp64 chain is the longest.
 #include <climits>
@@ -159,7 +159,7 @@ __device__ __forceinline__ float4 as_floats(const uint4 &v)
 }
 
 // The queries stream through: written so that they leave L2 first, they do not push out what else the step keeps
-// there (128 tokens x 128 heads: 7.9 against 11.4 us with the inputs of other calls in L2; 8191 x 64: the same).
+// there (128 tokens x 128 heads: 7.4 against 11.4 us with the inputs of other calls in L2; 8191 x 64: the same).
 template <bool kWide>
 __device__ __forceinline__ void store4(uint32_t *a, const uint32_t (&v)[4])
 {
