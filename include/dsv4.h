@@ -438,7 +438,8 @@ DSV4_API size_t dsv4_sparse_mla_decode_mtp_union_workspace_size(int32_t num_toke
  *                   thread blocks share a token, their parts (264 KB a multiprocessor at most).
  * One to three launches: the lists (few tokens: made by the decode), the decode, and a join where thread
  * blocks share a token.  Results do not depend on timing.  A token whose list is empty gets out = 0 and
- * lse = the sink (-inf without one), as does a head whose logits are all -inf.
+ * lse = the sink (-inf without one), as does a head whose logits are all -inf; a sink of +inf gives
+ * out = 0 and lse = +inf.
  * Returns DSV4_OK, DSV4_ERR_INVALID_ARG, DSV4_ERR_UNSUPPORTED (num_heads, topk_width) or DSV4_ERR_CUDA.
  */
 DSV4_API dsv4_status dsv4_sparse_mla_decode_fp4(const void *q, int64_t q_token_stride, const void *kv_cache,

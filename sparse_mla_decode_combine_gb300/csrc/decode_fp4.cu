@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                     const float sk = p.sink != nullptr && h < nhv ? p.sink[h0 + h] : -INFINITY;
                     const float M = fmaxf(ms, sk);
                     const float e = ms == -INFINITY ? 0.f : expf(ms - M);
-                    const float zs = sk == -INFINITY ? 0.f : expf(sk - M);
+                    const float zs = sk == -INFINITY ? 0.f : sk == M ? 1.f : expf(sk - M);   // (a sink of +inf takes all)
                     const float Z = (ms == -INFINITY ? 0.f : lsum * e) + zs;
                     fin[h] = ms == -INFINITY ? 0.f : e / (kShared ? lround * e + zs : Z);
                     if (p.lse != nullptr && h < nhv)
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
                 ml[c] = make_float2(-INFINITY, 0.f);
             m = fmaxf(m, ml[c].x);
         }
-        const float fall = M == -INFINITY ? 0.f : expf(M - m);
+        const float fall = M == m ? 1.f : expf(M - m);   // (both may be a sink of +inf, or -inf while all sums are 0)
         Z *= fall;
         if (kShared)
             Zr *= fall;
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
         for (int i = 0; i < kSplit; ++i) {
             if (mz[i].x == -INFINITY)   // (a run without keys)
                 continue;
-            const float w = expf(mz[i].x - m);
+            const float w = mz[i].x == m ? 1.f : expf(mz[i].x - m);
             const float4 o = sums[i][32 * warp + lane];
             Z = fmaf(mz[i].y, w, Z);
             Zr = fmaf(mz[i].z, w, Zr);

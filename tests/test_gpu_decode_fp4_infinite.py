@@ -84,3 +84,23 @@ def test_the_first_key_is_left_out_and_the_next_is_minus_infinity(tokens, heads)
     assert st == pkg.DSV4_ERR_BAD_INDEX
     idx = [0, w.num_tokens - 1]
     compare(out[idx], lse[idx], fp4.decode(live, idx))
+
+
+@pytest.mark.parametrize("tokens,heads", [FEW, MANY, SPLIT, (1, 16)])
+def test_a_sink_of_plus_infinity_takes_all_of_the_weight(tokens, heads):
+    """lse = +inf and out = 0 for its heads, however the work is split; the other heads are what they are without it."""
+    need_gpu()
+    keys = 1500 if tokens == 1 else 200
+    w, _ = workload(tokens, heads, keys, [], True, low=0.0)
+    seqs = w.seq_lens.copy()
+    if tokens > 2:
+        seqs[2] = 0
+    w = dataclasses.replace(w, seq_lens=seqs)
+    plain, plain_lse, _ = run(w)
+    sink = w.sink.copy()
+    sink[::5] = np.inf
+    out, lse, st = run(dataclasses.replace(w, sink=sink))
+    top = torch.from_numpy(np.isinf(sink)).cuda()
+    assert st == pkg.DSV4_OK
+    assert not out[:, top].any() and bool(torch.isposinf(lse[:, top]).all())
+    assert torch.equal(out[:, ~top], plain[:, ~top]) and torch.equal(lse[:, ~top], plain_lse[:, ~top])
