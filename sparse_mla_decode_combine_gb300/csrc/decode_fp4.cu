@@ -742,7 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                             lr[j] += __uint_as_float(pk << 16);
                             lr[j + 1] += __uint_as_float(pk & 0xFFFF0000u);
                         }
-                        st_shared_u32(sK + x * kKBytes + 8u * kChunkBytes + sw128(srow + 8 * r, (hw >> 3) + (j >> 1)) + 4u * (lane & 3), pk);
+                        st_shared_u32(sK + x * kKBytes + 8u * kChunkBytes + sw128(srow + 8 * r, (hw >> 3) + (j >> 1)) +
+                                          4u * (lane & 3),
+                                      pk);
                     }
                 fence_async_smem();
                 before_sync();
@@ -829,9 +831,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
 //   m = max(max_c m_c, sink), Z = sum_c l_c e^{m_c - m} + e^{sink - m},
 //   out = sum_c e^{m_c - m} O_c / Z  (BF16),  lse = m + ln Z
 // A warp to a head, or kSplit of them, each with a run of the parts, where there may be many (one token x 16 heads over 131072
-// keys, 152 parts: 81 us in all with one warp, 45.5 with eight; 17 parts: 16.8 and 15.0; four parts: 20.6 and 24.8).  The parts come from
-// L2, kJoinBatch at a time with every load in flight: four where few CTAs share each unit (latency is all there is; they are read before it is known how many of them had
-// work), two where runs of blocks end inside units (two parts are usual, and more registers would leave fewer warps: 8
+// keys, 152 parts: 81 us in all with one warp, 45.5 with eight; 17 parts: 16.8 and 15.0; four parts: 20.6 and 24.8).  The parts
+// come from L2, kJoinBatch at a time with every load in flight: four where few CTAs share each unit (latency is all there is; they
+// are read before it is known how many of them had work), two where runs of blocks end inside units (two parts are usual, and more registers would leave fewer warps: 8
 // against 10.5 us for 151 split units).  (Joined inside the decode, by the CTA of a unit that finished last, the 256
 // threads that are free there hold too few bytes in flight: a unit took 25 us.)
 template <int kJoinBatch, int kSplit, bool kShared>

@@ -17,7 +17,8 @@ pytestmark = pytest.mark.gpu
 
 def two_keys(tokens, heads):
     """Tokens over keys 0 and 1; queries are zero but for -1 in dim 96 and 1 in dim 200."""
-    w = to_fp4(synth.make_workload(name="two keys", seed=101, heads=heads, req_seq_lens=[2] * tokens, topk_width=0, window=2, sink=False))
+    w = to_fp4(synth.make_workload(name="two keys", seed=101, heads=heads, req_seq_lens=[2] * tokens, topk_width=0, window=2,
+                                   sink=False))
     cache = w.kv_cache.copy()
     cache[:, :, 256:384] = 0
     q = np.zeros(w.q.shape)

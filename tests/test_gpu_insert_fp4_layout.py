@@ -18,9 +18,12 @@ def test_queries_in_place_beside_keys(T, H):
     cs = torch.randn((16, 64), generator=g, device="cuda")
     pos, slots = torch.arange(T, device="cuda") % 16, torch.randperm(T, generator=g, device="cuda")
     caches = [torch.zeros((T, 400), dtype=torch.uint8, device="cuda") for _ in range(2)]
-    kept, q2, k2 = kv.clone(), torch.empty((T, H, 576), dtype=torch.bfloat16, device="cuda"), torch.empty_like(ko, memory_format=torch.contiguous_format)
+    kept = kv.clone()
+    q2 = torch.empty((T, H, 576), dtype=torch.bfloat16, device="cuda")
+    k2 = torch.empty((T, 576), dtype=torch.bfloat16, device="cuda")
     pkg.check(pkg.dsv4_qk_norm_rope_kv_insert_fp4(q.clone(), q2, kept, pos, slots, cs, caches[0], k2))
     pkg.check(pkg.dsv4_qk_norm_rope_kv_insert_fp4(q, q, kv, pos, slots, cs, caches[1], ko))
     assert torch.equal(q, q2) and torch.equal(ko, k2) and torch.equal(kv, kept) and torch.equal(*caches)
-    assert pkg.dsv4_qk_norm_rope_kv_insert_fp4(q, q, kv, pos, slots, cs, caches[1], row[:, H * 576 + 2:(H + 1) * 576 + 2]) == pkg.DSV4_ERR_INVALID_ARG
+    across = row[:, H * 576 + 2:(H + 1) * 576 + 2]
+    assert pkg.dsv4_qk_norm_rope_kv_insert_fp4(q, q, kv, pos, slots, cs, caches[1], across) == pkg.DSV4_ERR_INVALID_ARG
     assert pkg.dsv4_get_device_status() == pkg.DSV4_OK
