@@ -91,7 +91,7 @@ constexpr int kMinBlocks = 2;            // per CTA (with 1: 1 x 16 heads, 256 k
 // small shared region (after Q and the two K tiles)
 constexpr int kOffRed = 0;               // float [4][64]: per-quadrant head maxima, or row sums at the end
 constexpr int kOffMax = 1024;            // float [64]: reference maximum per head (log2 units; natural ones at the end)
-constexpr int kOffFin = 1280;            // float [64]: the factor of a rescale; at the end the output's, or a split's row sum
+constexpr int kOffFin = 1280;            // float [64]: the root of a rescale's factor; at the end the output's, or a split's row sum
 constexpr int kOffValid = 1536;          // uint8 [2][64]: rows of a K tile that hold a key
 constexpr int kOffBars = 1664;           // u64: bar_s[2], bar_p[2], bar_grp[2][2], bar_pv[2][4], bar_q, bar_o
 constexpr int kOffTmem = 1808;           // u32
@@ -699,11 +699,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                         const float m = fmaxf(fmaxf(red[h], red[kNH + h]), fmaxf(red[2 * kNH + h], red[3 * kNH + h]));
                         const bool none = (unset >> j) & 1u;
                         const float up = m == -INFINITY ? 0.f : none ? m : fmaxf(m, 0.f);   // (-inf: every logit is that or NaN)
-                        const float fall = none ? 1.f : exp2_approx(-up);
+                        // (half of the fall, taken twice: what it is taken from may be 2^40 and more, so that the whole of
+                        // it, below 2^-126, would lose weights that are not)
+                        const float fall = none ? 1.f : exp2_approx(-0.5f * up);
                         unset &= m == -INFINITY ? ~0u : ~(1u << j);
-                        l[j] *= fall;
+                        l[j] = l[j] * fall * fall;
                         if constexpr (kShared)
-                            lr[j] *= fall;
+                            lr[j] = lr[j] * fall * fall;
                         v[0][j] -= up;
                         v[1][j] -= up;
                         if (quad == 0 && lane < 4) {
@@ -723,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
                             tmem_ld_wait();
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                y[j] = __float_as_uint(__uint_as_float(y[j]) * fin[hc + j]);
+                                y[j] = __float_as_uint(__uint_as_float(y[j]) * fin[hc + j] * fin[hc + j]);
                             tmem_st16(lane_base + kColO + 64 * (m >> 1) + hc, y);
                         }
                         tmem_st_wait();
@@ -827,6 +829,23 @@ __global__ void __launch_bounds__(kThreads, 1) decode_fp4_kernel(const Decode4Pa
         tmem_free(tmem, kTmemCols);
 }
 
+// e^x times sums that may be 2^40 and more: where it is small (x is the same in a warp) half of it goes into them first, since
+// by itself it could go below 2^-126 and lose weights that fp32 holds.  Returns what is left to multiply by.
+template <int kVecs>
+__device__ __forceinline__ float exp_of(float x, float &z, float &zr, float4 (&o)[kVecs])
+{
+    if (x < -60.f) {
+        x *= 0.5f;
+        const float h = expf(x);
+        z *= h;
+        zr *= h;
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k)
+            o[k] = make_float4(o[k].x * h, o[k].y * h, o[k].z * h, o[k].w * h);
+    }
+    return expf(x);
+}
+
 // Joins the parts of the units that several CTAs shared, in the order of the parts:
 //   m = max(max_c m_c, sink), Z = sum_c l_c e^{m_c - m} + e^{sink - m},
 //   out = sum_c e^{m_c - m} O_c / Z  (BF16),  lse = m + ln Z
@@ -858,7 +877,7 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
         acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c0 = lo; c0 < hi; c0 += kJoinBatch) {
         float2 ml[kJoinBatch];
-        float lr[kJoinBatch];
+        float lr[kJoinBatch] = {};
         float4 o[kJoinBatch][4];
 #pragma unroll
         for (int c = 0; c < kJoinBatch; ++c) {
@@ -882,7 +901,8 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
                 ml[c] = make_float2(-INFINITY, 0.f);
             m = fmaxf(m, ml[c].x);
         }
-        const float fall = M == m ? 1.f : expf(M - m);   // (both may be a sink of +inf, or -inf while all sums are 0)
+        // (both may be a sink of +inf, or -inf while all sums are 0)
+        const float fall = M == m ? 1.f : exp_of(M - m, Z, Zr, acc);
         Z *= fall;
         if (kShared)
             Zr *= fall;
@@ -897,7 +917,7 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
         for (int c = 0; c < kJoinBatch; ++c) {
             if (ml[c].x == -INFINITY)   // no part, or one without keys
                 continue;
-            const float w = expf(ml[c].x - m);
+            const float w = exp_of(ml[c].x - m, ml[c].y, lr[c], o[c]);
             Z = fmaf(ml[c].y, w, Z);
             if (kShared)
                 Zr = fmaf(lr[c], w, Zr);
@@ -933,14 +953,14 @@ __global__ void __launch_bounds__(kSplit == 1 ? 32 * kJoinHeads : 32 * kSplit) j
         for (int i = 0; i < kSplit; ++i) {
             if (mz[i].x == -INFINITY)   // (a run without keys)
                 continue;
-            const float w = mz[i].x == m ? 1.f : expf(mz[i].x - m);
-            const float4 o = sums[i][32 * warp + lane];
-            Z = fmaf(mz[i].y, w, Z);
-            Zr = fmaf(mz[i].z, w, Zr);
-            acc[0].x = fmaf(w, o.x, acc[0].x);
-            acc[0].y = fmaf(w, o.y, acc[0].y);
-            acc[0].z = fmaf(w, o.z, acc[0].z);
-            acc[0].w = fmaf(w, o.w, acc[0].w);
+            float4 z = mz[i], o[1] = {sums[i][32 * warp + lane]};
+            const float w = z.x == m ? 1.f : exp_of(z.x - m, z.y, z.z, o);
+            Z = fmaf(z.y, w, Z);
+            Zr = fmaf(z.z, w, Zr);
+            acc[0].x = fmaf(w, o[0].x, acc[0].x);
+            acc[0].y = fmaf(w, o[0].y, acc[0].y);
+            acc[0].z = fmaf(w, o[0].z, acc[0].z);
+            acc[0].w = fmaf(w, o[0].w, acc[0].w);
         }
     }
     if (!kShared)
