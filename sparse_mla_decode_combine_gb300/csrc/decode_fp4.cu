@@ -27,7 +27,7 @@
 //     Where few units are shared, the output is divided by the sum of the weights as rounded to BF16, so that a key that
 //     has most of the weight loses nothing by its rounding (the lse keeps the exact sum; 1 % of the time of a small batch).
 //
-// What bounds it.  128 tokens x 128 heads x 2176 keys: 124 us in this kernel (132 with the lists and the join), 0.63 PFLOP/s,
+// What bounds it.  128 tokens x 128 heads x 2176 keys: 122 us in this kernel (131 with the lists and the join), 0.63 PFLOP/s,
 // DRAM at 20 % of its peak, the tensor pipe busy 40 % of the time, issue slots 54 %.  A 64-key block takes 3.7 k cycles where
 // the loop runs freely (4.1 k with the units' ends), and its steps are a chain over twice that, since its tile is one of two: the
 // dequant 3.0 k to its last chunk, S^T 1.2 k after that, the softmax 1.7 k, P.V 1.4 k to the first chunks' release.  S^T of
