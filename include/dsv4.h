@@ -594,6 +594,131 @@ DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_st
                                            void *workspace, size_t workspace_bytes, dsv4_stream_t stream);
 
 /*
+ * ---- between two decode steps -----------------------------------------------------------------
+ *
+ * dsv4_verify_drafts -- which of the drafted tokens stand, and the token after them, from given random numbers.
+ *
+ * The decode's batches of several query tokens a request (vllm #43385 "[ROCm] [DSv4] [Perf] Support DeepSeek v4 MTP") end
+ * in this step; the pages print no rule for it.  This is the one that leaves the tokens with the target's distribution.
+ * Request b has rows [query_start_loc[b], query_start_loc[b + 1]) - query_start_loc[0] of target probabilities, one for
+ * each of its k drafted tokens and one for the token after them.  Draft j of it is
+ * row query_start_loc[b] - query_start_loc[0] - b + j of draft_tokens and draft_probs.  With p_j, q_j the probabilities,
+ * d_j the drafted tokens and u_j = uniform[row j]:
+ *   a         = the number of leading drafts with u_j * q_j(d_j) < p_j(d_j)   (q_j(d_j) = 1 without draft_probs)
+ *   w         = p_k when a = k; max(p_a - q_a, 0), or without draft_probs p_a without d_a, when a < k (p_a itself where
+ *               that leaves nothing)
+ *   token     = the lowest i with w_0 + .. + w_i > u_k * (w_0 + .. + w_{vocab - 1})
+ * A greedy request (greedy[b] != 0) accepts while d_j is the index of the largest value of row j (the lowest of equal ones,
+ * NaN below every number) and then takes that of row a; its rows may be logits.  One row (k = 0) is plain sampling.
+ *   tokens[b]       = d_0 .. d_{a-1}, token, then -1
+ *   num_accepted[b] = a
+ *   seq_lens_out[b] = seq_lens[b] - (k - a)   (the cache's entries of the drafts that do not stand are dropped)
+ * Products and comparisons are exact; sums are held to 2^-46 of themselves or better.  Probabilities are finite (they
+ * need not sum to 1); negative values and NaN count as 0.
+ *
+ * Arguments:
+ *   target_probs     fp32, or BF16 when probs_bf16 != 0, [num_rows, vocab], row stride target_stride (>= vocab).
+ *   draft_probs      the same type, [num_drafts, vocab], row stride draft_stride; or NULL.
+ *   vocab            1 .. 2^22.
+ *   draft_tokens     int32 [num_drafts]; one outside [0, vocab) is turned down and sets DSV4_ERR_BAD_INDEX in the device
+ *                    status word.
+ *   query_start_loc  int32 [num_reqs + 1], increasing: every request has a row or more; num_reqs <= 2^24.
+ *   uniform          fp32 [num_rows] in [0, 1).
+ *   greedy           uint8 [num_reqs] or NULL (none is).
+ *   tokens           int32 [num_reqs, tokens_width], row stride tokens_stride; tokens_width >= k + 1.
+ *   num_accepted     int32 [num_reqs].
+ *   seq_lens, seq_lens_out  int32 [num_reqs], both or neither; may be one array.
+ * A request without a row, with rows or drafts outside the arrays, or with more of them than tokens_width gets -1 and
+ * a = 0 (its length is kept); one without a positive value gets a token of -1.  Both set DSV4_ERR_BAD_INDEX in the device
+ * status word.  Nothing is allocated.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_verify_drafts(const void *target_probs, int64_t target_stride, const void *draft_probs,
+                                        int64_t draft_stride, int32_t probs_bf16, int32_t vocab,
+                                        const int32_t *draft_tokens, int32_t num_drafts, const int32_t *query_start_loc,
+                                        int32_t num_reqs, int32_t num_rows, const float *uniform, const uint8_t *greedy,
+                                        int32_t *tokens, int64_t tokens_stride, int32_t tokens_width,
+                                        int32_t *num_accepted, const int32_t *seq_lens, int32_t *seq_lens_out,
+                                        dsv4_stream_t stream);
+
+/*
+ * dsv4_sparse_mla_key_weights -- add the attention weight that a decode step gave each key to its place in a table.
+ *
+ *   weights[row][p] += sum over heads h of e^{s_p - lse[t][h]}
+ * for each token t, with row, the positions p of its list K_t and the logits s_p as in dsv4_sparse_mla_decode (8-bit
+ * entries) or dsv4_sparse_mla_decode_fp4 (4-bit ones), and the lse that it returned.  A head whose lse is -inf gives
+ * nothing.  Tokens of one row are added in ascending order, one rounding to fp32 each.  Several layers may be added to
+ * one table, a call each.
+ *
+ * Arguments: those of the decode, with
+ *   entry_bytes     656 or 400 (others: DSV4_ERR_UNSUPPORTED): kv_cache uint8 [num_blocks, page_block, entry_bytes];
+ *   lse             fp32 [num_tokens, num_heads];
+ *   weights         fp32 [num_reqs, weights_width], row stride weights_stride; weights_width >= max_blocks * page_block;
+ *   workspace       at least dsv4_sparse_mla_key_weights_workspace_size(...) bytes, 256-byte aligned, not used by
+ *                   anything else until the work enqueued by this call has finished.
+ * Block-table entries and rows out of range are data errors, as in the decode; such keys are left out.
+ * Returns DSV4_OK, DSV4_ERR_INVALID_ARG, DSV4_ERR_UNSUPPORTED (num_heads, topk_width, entry_bytes) or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_sparse_mla_key_weights(
+    const void *q, int64_t q_token_stride, const void *kv_cache, int32_t num_blocks, int32_t page_block,
+    int32_t entry_bytes, const int32_t *block_table, int64_t bt_stride, int32_t max_blocks, int32_t num_reqs,
+    const int32_t *req_idx, const int32_t *topk_idx, int64_t topk_stride, int32_t topk_width, const int32_t *topk_lens,
+    const int32_t *seq_lens, int32_t num_tokens, int32_t num_heads, int32_t window, const float *lse,
+    float softmax_scale, float *weights, int64_t weights_stride, int32_t weights_width, void *workspace,
+    size_t workspace_bytes, dsv4_stream_t stream);
+
+/* Bytes of device workspace dsv4_sparse_mla_key_weights needs; 0 for arguments it rejects. */
+DSV4_API size_t dsv4_sparse_mla_key_weights_workspace_size(int32_t num_tokens, int32_t num_heads, int32_t topk_width,
+                                                           int32_t window);
+
+/*
+ * dsv4_cache_evict -- cut long rows of a cache to a budget of entries, by accumulated attention weight.
+ *
+ * The pool, block table, lengths and reference counts are those of the page operators above.  A row of n > limit entries
+ * keeps its first `first` entries, its last `recent` ones and, of those between, the heaviest: budget in all, in their
+ * order (larger weight first, then the lower position; -0 is +0, NaN below every number).  Shorter rows are not changed.
+ * Entries move down within the row in every layer.  A decode of the row afterwards takes its length as the number of
+ * entries left; they keep the rotation of the positions that they were inserted with.
+ *
+ * Page j of a row that is cut
+ *   stays    when it is full and all of its entries stay where they are, shared or not;
+ *   is written in place  otherwise, when its count on entry is 1;
+ *   is replaced  else, by a free page (count 1) that receives all of its entries.
+ * Pages past the new end, and those replaced, lose a reference.  Pages that are free on entry are taken lowest first, in
+ * the order of (row, page); pages that this call frees are not taken by it.  A row that would need pages past the last
+ * free one stays as it was and sets DSV4_ERR_BAD_INDEX in the device status word.
+ *
+ * Arguments: the pool; block_table, seq_lens [num_rows], ref_counts: the state before the call (ref_counts must count
+ * every row of the table);
+ *   weights          fp32 [num_rows, weights_width], row stride weights_stride; weights_width >= max_blocks * page_block.
+ *   budget, limit    1 <= budget <= limit; first, recent >= 0, first + recent <= budget.
+ *   block_table_out  int32 [num_rows, max_blocks], row stride bt_out_stride; every cell is written (-1 after a row's
+ *                    pages).  Must not overlap block_table.
+ *   seq_lens_out     int32 [num_rows].  Must not overlap seq_lens.
+ *   ref_counts_out   int32 [num_blocks]; may be ref_counts.
+ *   weights_out      fp32 [num_rows, weights_width], row stride weights_out_stride: the kept entries' weights, then 0;
+ *                    may be weights (with the same stride).
+ *   workspace        at least dsv4_cache_evict_workspace_size(...) bytes, 256-byte aligned, not used by anything else
+ *                    until the call's work has finished.
+ * max_blocks <= 2^20, num_blocks <= 2^30.  A page number outside [0, num_blocks) in a row that is read becomes -1, entries
+ * on such pages are not moved, a length past max_blocks * page_block is cut; both set DSV4_ERR_BAD_INDEX.  Nothing is
+ * allocated; the call can be captured.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.
+ */
+DSV4_API dsv4_status dsv4_cache_evict(void *cache, int32_t num_layers, int64_t layer_stride, int32_t num_blocks,
+                                      int32_t page_block, int32_t entry_bytes, const int32_t *block_table,
+                                      int64_t bt_stride, const int32_t *seq_lens, int32_t num_rows, int32_t max_blocks,
+                                      const float *weights, int64_t weights_stride, int32_t weights_width,
+                                      int32_t budget, int32_t limit, int32_t first, int32_t recent,
+                                      int32_t *block_table_out, int64_t bt_out_stride, int32_t *seq_lens_out,
+                                      const int32_t *ref_counts, int32_t *ref_counts_out, float *weights_out,
+                                      int64_t weights_out_stride, void *workspace, size_t workspace_bytes,
+                                      dsv4_stream_t stream);
+
+/* Bytes of device workspace dsv4_cache_evict needs; 0 for arguments it rejects. */
+DSV4_API size_t dsv4_cache_evict_workspace_size(int32_t num_rows, int32_t max_blocks, int32_t num_blocks,
+                                                int32_t num_layers, int32_t page_block, int32_t entry_bytes,
+                                                int32_t budget);
+
+/*
  * dsv4_get_device_status -- synchronise `stream`, then read and clear the current
  * device's sticky status word.
  *

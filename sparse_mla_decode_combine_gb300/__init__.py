@@ -36,7 +36,8 @@ EXPORTED = ("dsv4_combine_topk_swa_indices", "dsv4_combine_topk_swa_indices_comp
             "dsv4_sparse_mla_decode_mtp_union_workspace_size", "dsv4_sparse_mla_decode_fp4",
             "dsv4_sparse_mla_decode_fp4_workspace_size", "dsv4_qk_norm_rope_kv_insert_fp4",
             "dsv4_cache_pages_workspace_size", "dsv4_cache_fork_rows", "dsv4_cache_compact", "dsv4_cache_copy_pages",
-            "dsv4_get_device_status")
+            "dsv4_verify_drafts", "dsv4_sparse_mla_key_weights", "dsv4_sparse_mla_key_weights_workspace_size",
+            "dsv4_cache_evict", "dsv4_cache_evict_workspace_size", "dsv4_get_device_status")
 
 
 class Dsv4Error(RuntimeError):
@@ -112,6 +113,18 @@ def load_library():
                                        ctypes.c_size_t, P]
     lib.dsv4_cache_copy_pages.restype = ctypes.c_int
     lib.dsv4_cache_copy_pages.argtypes = [P, i64, i32, P, i64, i32, i32, i32, i32, P, P, i32, P, ctypes.c_size_t, P]
+    lib.dsv4_verify_drafts.restype = ctypes.c_int
+    lib.dsv4_verify_drafts.argtypes = [P, i64, P, i64, i32, i32, P, i32, P, i32, i32, P, P, P, i64, i32, P, P, P, P]
+    lib.dsv4_sparse_mla_key_weights_workspace_size.restype = ctypes.c_size_t
+    lib.dsv4_sparse_mla_key_weights_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.dsv4_sparse_mla_key_weights.restype = ctypes.c_int
+    lib.dsv4_sparse_mla_key_weights.argtypes = [P, i64, P, i32, i32, i32, P, i64, i32, i32, P, P, i64, i32, P, P, i32, i32,
+                                                i32, P, ctypes.c_float, P, i64, i32, P, ctypes.c_size_t, P]
+    lib.dsv4_cache_evict_workspace_size.restype = ctypes.c_size_t
+    lib.dsv4_cache_evict_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.dsv4_cache_evict.restype = ctypes.c_int
+    lib.dsv4_cache_evict.argtypes = [P, i32, i64, i32, i32, i32, P, i64, P, i32, i32, P, i64, i32, i32, i32, i32, i32, P,
+                                     i64, P, P, P, P, i64, P, ctypes.c_size_t, P]
     lib.dsv4_get_device_status.restype = ctypes.c_int
     lib.dsv4_get_device_status.argtypes = [P]
     _lib = lib
@@ -570,6 +583,112 @@ def dsv4_cache_copy_pages(dst_cache: torch.Tensor, src_cache: torch.Tensor, src_
         _vec(dev, dst_pages, i32, n, "dst_pages"), n, _workspace(dev, workspace), workspace.numel(), st)
 
 
+# ----------------------------------------------------------------------------
+# between two decode steps
+# ----------------------------------------------------------------------------
+def dsv4_verify_drafts(target_probs: torch.Tensor, draft_probs: Optional[torch.Tensor], draft_tokens: torch.Tensor,
+                       query_start_loc: torch.Tensor, uniform: torch.Tensor, tokens: torch.Tensor,
+                       num_accepted: torch.Tensor, greedy: Optional[torch.Tensor] = None,
+                       seq_lens: Optional[torch.Tensor] = None, seq_lens_out: Optional[torch.Tensor] = None,
+                       stream=None) -> int:
+    """Which drafted tokens stand, and the token after them (see include/dsv4.h).  target_probs float32 or bf16
+    [rows, vocab]; draft_probs the same type [drafts, vocab] or None; draft_tokens int32 [drafts]; query_start_loc int32
+    [requests + 1]; uniform float32 [rows]; tokens int32 [requests, >= most drafts + 1]; num_accepted int32 [requests];
+    greedy uint8 [requests] or None; seq_lens, seq_lens_out int32 [requests], both or neither (may be one tensor)."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    N, V = target_probs.shape
+    Nd = draft_tokens.numel()
+    R, W = tokens.shape
+    dtype, i32 = target_probs.dtype, torch.int32
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
+        raise TypeError(f"target_probs: expected torch.float32 or torch.bfloat16, got {dtype}")
+    if draft_probs is not None and draft_probs.shape != (Nd, V):
+        raise ValueError("draft_probs: must have a row for each drafted token, of the width of target_probs")
+    return lib.dsv4_verify_drafts(
+        _on(dev, target_probs, dtype, "target_probs"), _row_stride(target_probs, "target_probs", N, V),
+        None if draft_probs is None else _on(dev, draft_probs, dtype, "draft_probs"),
+        0 if draft_probs is None else _row_stride(draft_probs, "draft_probs", Nd, V), 1 if dtype is torch.bfloat16 else 0, V,
+        _vec(dev, draft_tokens, i32, Nd, "draft_tokens"), Nd, _vec(dev, query_start_loc, i32, R + 1, "query_start_loc"), R, N,
+        _vec(dev, uniform, torch.float32, N, "uniform"), _vec(dev, greedy, torch.uint8, R, "greedy"),
+        _on(dev, tokens, i32, "tokens"), _row_stride(tokens, "tokens", R, W), W, _vec(dev, num_accepted, i32, R, "num_accepted"),
+        _vec(dev, seq_lens, i32, R, "seq_lens"), _vec(dev, seq_lens_out, i32, R, "seq_lens_out"), st)
+
+
+def dsv4_sparse_mla_key_weights_workspace_size(num_tokens: int, num_heads: int, topk_width: int, window: int) -> int:
+    return int(load_library().dsv4_sparse_mla_key_weights_workspace_size(num_tokens, num_heads, topk_width, window))
+
+
+def dsv4_sparse_mla_key_weights(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
+                                req_idx: Optional[torch.Tensor], topk_idx: torch.Tensor,
+                                topk_lens: Optional[torch.Tensor], seq_lens: torch.Tensor, window: int,
+                                lse: torch.Tensor, softmax_scale: float, weights: torch.Tensor, workspace: torch.Tensor,
+                                stream=None) -> int:
+    """weights[row, p] += the attention weight that the tokens of a decode gave key p of their row (see include/dsv4.h).
+    kv_cache uint8 [num_blocks, page, 656 or 400]; lse float32 [T, H], as the decode returned it; weights float32
+    [requests, >= max_blocks * page]; workspace uint8 [>= dsv4_sparse_mla_key_weights_workspace_size(...)]; the other
+    arguments as in the decode."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    T, H, D = q.shape
+    blocks, page, entry = kv_cache.shape
+    R, M = block_table.shape
+    Tk, K = topk_idx.shape
+    Rw, W = weights.shape
+    if D != 576 or (H > 1 and q.stride()[1] != 576):
+        raise ValueError("q: heads must be contiguous rows of 576")
+    if not kv_cache.is_contiguous():
+        raise ValueError("kv_cache: must be contiguous")
+    if Tk != T:
+        raise ValueError("topk_idx: must have a row for each token")
+    if Rw != R:
+        raise ValueError("weights: must have a row for each row of block_table")
+    i32, f32 = torch.int32, torch.float32
+    return lib.dsv4_sparse_mla_key_weights(
+        _on(dev, q, torch.bfloat16, "q"), _row_stride(q, "q", T, H * 576), _on(dev, kv_cache, torch.uint8, "kv_cache"),
+        blocks, page, entry, _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M), M, R,
+        _vec(dev, req_idx, i32, T, "req_idx"), _on(dev, topk_idx, i32, "topk_idx"),
+        _row_stride(topk_idx, "topk_idx", T, K), K, _vec(dev, topk_lens, i32, T, "topk_lens"),
+        _vec(dev, seq_lens, i32, T, "seq_lens"), T, H, int(window), _vec(dev, lse, f32, T * H, "lse"), float(softmax_scale),
+        _on(dev, weights, f32, "weights"), _row_stride(weights, "weights", Rw, W), W, _workspace(dev, workspace),
+        workspace.numel(), st)
+
+
+def dsv4_cache_evict_workspace_size(num_rows: int, max_blocks: int, num_blocks: int, num_layers: int, page_block: int,
+                                    entry_bytes: int, budget: int) -> int:
+    return int(load_library().dsv4_cache_evict_workspace_size(num_rows, max_blocks, num_blocks, num_layers, page_block,
+                                                              entry_bytes, budget))
+
+
+def dsv4_cache_evict(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor,
+                     weights: torch.Tensor, budget: int, limit: int, first: int, recent: int,
+                     block_table_out: torch.Tensor, seq_lens_out: torch.Tensor, ref_counts_out: torch.Tensor,
+                     weights_out: torch.Tensor, workspace: torch.Tensor, stream=None) -> int:
+    """Rows of more than `limit` entries are cut to `budget`: the first `first`, the last `recent` and the heaviest between
+    (see include/dsv4.h).  cache uint8 [layers, pages, page, entry bytes]; block_table, block_table_out int32
+    [rows, max_blocks]; seq_lens, seq_lens_out int32 [rows]; ref_counts, ref_counts_out int32 [pages] and weights,
+    weights_out float32 [rows, >= max_blocks * page] (each pair may be one tensor); workspace uint8 [>=
+    dsv4_cache_evict_workspace_size(rows, max_blocks, pages, layers, page, entry bytes, budget)]."""
+    lib = _lib or load_library()
+    dev, st = _device_and_stream(stream)
+    ptr, L, ls, B, page, entry = _pool(dev, cache, "cache")
+    i32, f32 = torch.int32, torch.float32
+    R, M = block_table.shape
+    Rw, W = weights.shape
+    if block_table_out.shape != (R, M):
+        raise ValueError("block_table_out: must have the shape of block_table")
+    if Rw != R or weights_out.shape != (R, W):
+        raise ValueError("weights, weights_out: must have a row for each row of block_table, and the same shape")
+    return lib.dsv4_cache_evict(
+        ptr, L, ls, B, page, entry, _on(dev, block_table, i32, "block_table"), _row_stride(block_table, "block_table", R, M),
+        _vec(dev, seq_lens, i32, R, "seq_lens"), R, M, _on(dev, weights, f32, "weights"), _row_stride(weights, "weights", R, W),
+        W, int(budget), int(limit), int(first), int(recent), _on(dev, block_table_out, i32, "block_table_out"),
+        _row_stride(block_table_out, "block_table_out", R, M), _vec(dev, seq_lens_out, i32, R, "seq_lens_out"),
+        _vec(dev, ref_counts, i32, B, "ref_counts"), _vec(dev, ref_counts_out, i32, B, "ref_counts_out"),
+        _on(dev, weights_out, f32, "weights_out"), _row_stride(weights_out, "weights_out", R, W), _workspace(dev, workspace),
+        workspace.numel(), st)
+
+
 def dsv4_get_device_status(stream=None) -> int:
     return int(load_library().dsv4_get_device_status(_stream(stream)))
 
@@ -609,6 +728,21 @@ def workspace_for_fp4(num_tokens: int, num_heads: int, topk_width: int, window: 
 
 def workspace_for_cache_pages(num_rows: int, num_rows_out: int, num_blocks: int, device=None) -> torch.Tensor:
     n = dsv4_cache_pages_workspace_size(num_rows, num_rows_out, num_blocks)
+    if n == 0:
+        raise Dsv4Error(DSV4_ERR_INVALID_ARG, "workspace size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def workspace_for_key_weights(num_tokens: int, num_heads: int, topk_width: int, window: int, device=None) -> torch.Tensor:
+    n = dsv4_sparse_mla_key_weights_workspace_size(num_tokens, num_heads, topk_width, window)
+    if n == 0:
+        raise Dsv4Error(DSV4_ERR_INVALID_ARG, "workspace size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def workspace_for_cache_evict(num_rows: int, max_blocks: int, num_blocks: int, num_layers: int, page_block: int,
+                              entry_bytes: int, budget: int, device=None) -> torch.Tensor:
+    n = dsv4_cache_evict_workspace_size(num_rows, max_blocks, num_blocks, num_layers, page_block, entry_bytes, budget)
     if n == 0:
         raise Dsv4Error(DSV4_ERR_INVALID_ARG, "workspace size")
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
@@ -673,6 +807,50 @@ def cache_compact(cache, block_table, seq_lens, ref_counts, workspace=None, stre
         check(dsv4_cache_compact(cache, block_table, seq_lens, ref_counts, table, refs, page_map, live, workspace, stream),
               "dsv4_cache_compact")
     return table, refs, page_map, live
+
+
+def verify_drafts(target_probs, draft_probs, draft_tokens, query_start_loc, uniform, max_drafts, greedy=None, seq_lens=None,
+                  stream=None):
+    """Allocating wrapper of dsv4_verify_drafts; returns (tokens, num_accepted), and the new seq_lens where they are given."""
+    R, dev = query_start_loc.numel() - 1, target_probs.device
+    with _allocating_on(stream):
+        tokens = torch.empty((R, max_drafts + 1), dtype=torch.int32, device=dev)
+        accepted = torch.empty((R,), dtype=torch.int32, device=dev)
+        lens = None if seq_lens is None else torch.empty_like(seq_lens)
+        check(dsv4_verify_drafts(target_probs, draft_probs, draft_tokens, query_start_loc, uniform, tokens, accepted, greedy,
+                                 seq_lens, lens, stream), "dsv4_verify_drafts")
+    return (tokens, accepted) if lens is None else (tokens, accepted, lens)
+
+
+def sparse_mla_key_weights(q, kv_cache, block_table, req_idx, topk_idx, topk_lens, seq_lens, window, lse, softmax_scale,
+                           weights=None, workspace=None, stream=None):
+    """Allocating wrapper of dsv4_sparse_mla_key_weights; returns weights (zeros before the call when not given)."""
+    T, H, _ = q.shape
+    with _allocating_on(stream):
+        if weights is None:
+            weights = torch.zeros((block_table.shape[0], block_table.shape[1] * kv_cache.shape[1]), dtype=torch.float32,
+                                  device=q.device)
+        if workspace is None:
+            workspace = workspace_for_key_weights(T, H, topk_idx.shape[1], window, q.device)
+        check(dsv4_sparse_mla_key_weights(q, kv_cache, block_table, req_idx, topk_idx, topk_lens, seq_lens, window, lse,
+                                          softmax_scale, weights, workspace, stream), "dsv4_sparse_mla_key_weights")
+    return weights
+
+
+def cache_evict(cache, block_table, seq_lens, ref_counts, weights, budget, limit=None, first=0, recent=0, workspace=None,
+                stream=None):
+    """Allocating wrapper of dsv4_cache_evict (limit: the budget when not given); returns (block_table, seq_lens,
+    ref_counts, weights) after the call.  The cache is written in place."""
+    L, B, page, entry = cache.shape
+    dev = cache.device
+    with _allocating_on(stream):
+        table, lens, refs = (torch.empty(t.shape, dtype=torch.int32, device=dev) for t in (block_table, seq_lens, ref_counts))
+        out = torch.empty(weights.shape, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = workspace_for_cache_evict(*block_table.shape, B, L, page, entry, budget, dev)
+        check(dsv4_cache_evict(cache, block_table, seq_lens, ref_counts, weights, budget, budget if limit is None else limit,
+                               first, recent, table, lens, refs, out, workspace, stream), "dsv4_cache_evict")
+    return table, lens, refs, out
 
 
 def combine_topk_swa_indices(topk_idx, topk_lens, seq_lens, window, combined_width=None, stream=None):

@@ -98,6 +98,7 @@ struct Lists4Params {
     float *lse;
     int32_t smem_bytes;        // shared memory for the sets: lists_fp4_smem_bytes(topk_width)
     unsigned *status;
+    int32_t *positions;        // [T, list_w] (launch_lists_positions)
 };
 // the hash set of a row; as a bitmap at least 262144 positions (131072 bytes at the widest rows)
 inline int lists_fp4_smem_bytes(int topk_width)
@@ -108,6 +109,8 @@ inline int lists_fp4_smem_bytes(int topk_width)
     return bytes;
 }
 cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream);
+// slots, positions and lengths alone (no joins, no outputs of tokens without a key)
+cudaError_t launch_lists_positions(const Lists4Params &p, cudaStream_t stream);
 
 struct Decode4Params {
     const uint16_t *q;

@@ -93,7 +93,7 @@ struct DecodeParams {
 // call made after the first one on a device is safe inside stream capture.
 enum AttrSlot { kAttrCombine = 0, kAttrTc, kAttrTcLong, kAttrTcUnion, kAttrTcUnionLong, kAttrUnion, kAttrTopk,
                 kAttrTopkCluster, kAttrFp4, kAttrFp4Shared, kAttrFp4Lists, kAttrForkSmall,
-                kAttrCompactSmall, kAttrSlots };
+                kAttrCompactSmall, kAttrPositions, kAttrKeyWeights, kAttrSlots };
 cudaError_t set_smem_once(const void *kernel, int bytes, AttrSlot slot);
 
 // Device address of the status word and the SM count of the current device (either may be null).

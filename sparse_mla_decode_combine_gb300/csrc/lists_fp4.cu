@@ -37,7 +37,29 @@ __global__ void __launch_bounds__(kThreads) lists_fp4_kernel(const Lists4Params 
     }
 }
 
+// The lists with their positions, for a kernel that returns something per key.
+__global__ void __launch_bounds__(kThreads) lists_positions_kernel(const Lists4Params p)
+{
+    griddep_wait();
+    griddep_launch();   // (the next kernel waits for this grid itself)
+    extern __shared__ unsigned long long tab[];
+    __shared__ int wsum[kLoads * kThreads / 32];
+    const int t = blockIdx.x;
+    const int len = lists::build<kThreads, kLoads, true>(p, t, threadIdx.x, tab, wsum, SyncAll(),
+                                                         [](int len) { return make_int2(0, len); });
+    if (threadIdx.x == 0)
+        p.lens[t] = len;
+}
+
 }  // namespace
+
+cudaError_t launch_lists_positions(const Lists4Params &p, cudaStream_t stream)
+{
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(lists_positions_kernel), p.smem_bytes, kAttrPositions);
+    if (e != cudaSuccess)
+        return e;
+    return launch_dependent(lists_positions_kernel, dim3((unsigned)p.num_tokens), kThreads, (size_t)p.smem_bytes, stream, p);
+}
 
 cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream)
 {

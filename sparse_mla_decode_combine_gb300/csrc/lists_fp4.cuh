@@ -45,7 +45,8 @@ __device__ __forceinline__ unsigned insert(unsigned long long *tab, int bits, in
 // Token t's list, by kThreads threads (tid: this one's number; whole warps); returns its length.  tab: p.smem_bytes of
 // shared memory, wsum: kLoads * kThreads / 32 ints of it.  sync() is a barrier of these threads, sync.any(v) one that
 // tells them whether any has v.  range(length) says from which entry to which the window's part of the list is wanted.
-template <int kThreads, int kLoads, typename Sync, typename Range>
+// kPositions: p.positions receives the entries' positions beside their slots.
+template <int kThreads, int kLoads, bool kPositions = false, typename Sync, typename Range>
 __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsigned long long *tab, int *wsum, const Sync &sync,
                                      const Range &range)
 {
@@ -72,6 +73,7 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
     const int win_lo = lo < 0 ? 0 : (int)lo;
     const int swa = seq_len > 0 ? pos - win_lo + 1 : 0;
     int32_t *out = p.slots + (int64_t)t * p.list_w;
+    int32_t *out_pos = kPositions ? p.positions + (int64_t)t * p.list_w : nullptr;
     auto page_at = [&](int blk) { return row_ok && blk < p.max_blocks ? __ldca(bt_row + blk) : -1; };   // (-1: outside the table)
     auto slot_in = [&](int phys, int at) {
         if (phys < 0 || phys >= p.num_blocks) {
@@ -168,8 +170,11 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
             const int before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
             const int rank = total + before + __popc(bal[u] & ((1u << lane) - 1u));
             total += __reduce_add_sync(0xffffffffu, x);
-            if ((bal[u] >> lane) & 1u)
+            if ((bal[u] >> lane) & 1u) {
                 out[rank] = pg == 0 ? sv[u] : slot_of(vg[u]);
+                if (kPositions)
+                    out_pos[rank] = vg[u];
+            }
         }
         sync();   // wsum is rewritten by the next group of passes
     }
@@ -177,6 +182,9 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
     const int2 part = range(len);
     const int i1 = min(part.y, len);
     int i = max(part.x, total) + tid;
+    if (kPositions)
+        for (int k = i; k < i1; k += kThreads)
+            out_pos[k] = win_lo + (k - total);
     for (; i + 3 * kThreads < i1; i += 4 * kThreads) {   // the window, four loads in flight
         int phys[4], at[4];
 #pragma unroll

@@ -56,7 +56,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity)
 
 // The rest of a wait whose first try failed: bounded; after any timeout in the CTA (abort flag set)
 // waits return at once, so the CTA still reaches its end.
-__device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status)
+static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag, unsigned *status)
 {
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
