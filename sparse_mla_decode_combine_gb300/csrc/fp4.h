@@ -98,7 +98,9 @@ struct Lists4Params {
     float *lse;
     int32_t smem_bytes;        // shared memory for the sets: lists_fp4_smem_bytes(topk_width)
     unsigned *status;
-    int32_t *positions;        // [T, list_w] (launch_lists_positions)
+    // launch_lists_positions alone:
+    int32_t *positions;        // [T, list_w]
+    int32_t *sole;             // [T] 1: no other token with keys names this one's row
 };
 // the hash set of a row; as a bitmap at least 262144 positions (131072 bytes at the widest rows)
 inline int lists_fp4_smem_bytes(int topk_width)

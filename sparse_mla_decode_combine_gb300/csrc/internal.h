@@ -93,7 +93,8 @@ struct DecodeParams {
 // call made after the first one on a device is safe inside stream capture.
 enum AttrSlot { kAttrCombine = 0, kAttrTc, kAttrTcLong, kAttrTcUnion, kAttrTcUnionLong, kAttrUnion, kAttrTopk,
                 kAttrTopkCluster, kAttrFp4, kAttrFp4Shared, kAttrFp4Lists, kAttrForkSmall,
-                kAttrCompactSmall, kAttrPositions, kAttrKeyWeights, kAttrSlots };
+                kAttrCompactSmall, kAttrPositions, kAttrKeyWeights,
+                kAttrSlots = kAttrKeyWeights + 8 };   // (key weights: four numbers of heads, two formats)
 cudaError_t set_smem_once(const void *kernel, int bytes, AttrSlot slot);
 
 // Device address of the status word and the SM count of the current device (either may be null).

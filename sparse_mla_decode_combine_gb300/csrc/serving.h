@@ -45,6 +45,7 @@ struct KeyWeightsParams {
     const int32_t *slots;      // [T, list_w] cache slots (-1: no key), the positions that they hold, how many a token has
     const int32_t *positions;
     const int32_t *lens;
+    const int32_t *sole;       // [T] not 0: no other token with keys names this one's row
     int32_t list_w;
     int32_t num_tokens;
     int32_t num_heads;
@@ -52,12 +53,12 @@ struct KeyWeightsParams {
     int32_t num_reqs;
     const float *lse;          // [T, H]
     float scale;
-    float *got;                // [T, list_w] what each key of a token received
+    float *got;                // [T, list_w] what each key of a token that is not sole received
     float *weights;            // [num_reqs, weights_width]
     int64_t weights_stride;
-    int32_t grid;
     unsigned *status;
 };
+int key_weights_block_keys();
 cudaError_t launch_key_weights(const KeyWeightsParams &p, int sms, cudaStream_t stream);
 
 struct EvictParams {
