@@ -34,7 +34,7 @@ size_t span4(int rows, int64_t stride, int64_t width)
 // ---- the key weights' workspace: the tokens' slots, positions and lengths, and what each key received
 struct WeightsPlan {
     int list_w;
-    size_t off_positions, off_got, off_lens, off_sole, total;
+    size_t off_positions, off_got, off_lens, off_later, total;
 };
 
 bool weights_plan(int num_tokens, int num_heads, int topk_width, int window, WeightsPlan *pl)
@@ -51,8 +51,8 @@ bool weights_plan(int num_tokens, int num_heads, int topk_width, int window, Wei
     pl->off_positions = lists;
     pl->off_got = 2 * lists;
     pl->off_lens = 3 * lists;
-    pl->off_sole = align_up(pl->off_lens + 4 * (size_t)num_tokens, 256);
-    pl->total = std::max<size_t>(256, align_up(pl->off_sole + 4 * (size_t)num_tokens, 256));
+    pl->off_later = align_up(pl->off_lens + 4 * (size_t)num_tokens, 256);
+    pl->total = std::max<size_t>(256, align_up(pl->off_later + 4 * (size_t)num_tokens, 256));
     return true;
 }
 
@@ -210,7 +210,7 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_key_weights(
     l.slots = reinterpret_cast<int32_t *>(ws);
     l.positions = reinterpret_cast<int32_t *>(ws + pl.off_positions);
     l.lens = reinterpret_cast<int32_t *>(ws + pl.off_lens);
-    l.sole = reinterpret_cast<int32_t *>(ws + pl.off_sole);
+    l.later = reinterpret_cast<int32_t *>(ws + pl.off_later);
     l.list_w = pl.list_w;
     l.status = status;
     l.smem_bytes = lists_fp4_smem_bytes(topk_width);
@@ -224,7 +224,7 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_key_weights(
     p.slots = l.slots;
     p.positions = l.positions;
     p.lens = l.lens;
-    p.sole = l.sole;
+    p.later = l.later;
     p.list_w = pl.list_w;
     p.num_tokens = num_tokens;
     p.num_heads = num_heads;

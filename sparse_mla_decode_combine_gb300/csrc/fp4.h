@@ -100,7 +100,7 @@ struct Lists4Params {
     unsigned *status;
     // launch_lists_positions alone:
     int32_t *positions;        // [T, list_w]
-    int32_t *sole;             // [T] 1: no other token with keys names this one's row
+    int32_t *later;            // [T] 1: a token with keys before this one names its row
 };
 // the hash set of a row; as a bitmap at least 262144 positions (131072 bytes at the widest rows)
 inline int lists_fp4_smem_bytes(int topk_width)

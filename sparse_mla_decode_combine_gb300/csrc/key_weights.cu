@@ -7,16 +7,19 @@
 //
 // Contraction.  S[128 keys x H heads] = K_tile[128 x 576] . Q^T, keys on the M side, so that a key's logits lie in one lane of
 // tensor memory and its sum over the heads is a thread's own loop.  Q of a token (H x 576 in BF16, up to 144 KB) stays in
-// shared memory; the keys come through a ring of 16-KB stages, one 64-dim column chunk of 128 keys each, dequantised to
-// BF16 on the way (exactly).
+// shared memory.  The entries come whole, by asynchronous 16-byte copies whose neighbours are neighbours in memory (bulk copies
+// of an entry each take some 80 cycles), into a ring of 16-key units for each quadrant; a thread takes 64 dims of its key out of one, dequantises
+// them to BF16 (exactly) and writes them to tensor memory, from where the product reads them: written to shared memory
+// instead, the keys' stores and the products' reads of both operands (and loads to registers, whose pieces of 16 or 32
+// bytes a row take a pass of L1 each) kept L1 busy for 80 % of the time.
 //
-// Roles (21 warps): warp 0 issues the products, a chunk's four as it comes; warps 1-4 read a finished block out of one of two
-// accumulators, a quadrant each, while the next block is computed; warps 5-20 bring Q and the keys: two groups of eight
-// take the even and the odd chunks (the rope chunk in turn), a thread half a row of a chunk, whose bytes it loaded a block
-// ahead.  A persistent CTA per multiprocessor takes an equal run of the blocks of all tokens.
+// Roles (23 warps): warp 0 issues the products; warps 1-4 read a finished block out of one of two accumulators, a quadrant
+// each, while the next block is computed; warps 5 and 6 issue the copies; warps 7-22 bring Q and dequantise, in four sets that
+// take every fourth 64-dim chunk, a warp a quadrant.  A persistent CTA per multiprocessor takes an equal run of the blocks
+// of all tokens.
 //
-// Tokens of one row are added in ascending order, one rounding each, so the result does not depend on timing: a token
-// whose row no other token of the call names is added by the epilogue, the others by a second kernel.
+// Tokens of one row are added in ascending order, one rounding each, so the result does not depend on timing: the first
+// token with keys that names a row is added by the epilogue, the others by a second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -31,60 +34,116 @@ namespace {
 using namespace tc;
 
 constexpr int kEpilogueWarps = 4;        // warps 1-4
-constexpr int kKeyWarp0 = 5;
-constexpr int kKeyWarps = 16;            // warps 5-20, in two groups
+constexpr int kCopyWarp0 = 5;
+constexpr int kCopyWarps = 2;            // warps 5 and 6, two quadrants each
+constexpr int kKeyWarp0 = kCopyWarp0 + kCopyWarps;
+constexpr int kKeyWarps = 16;            // warps 7-22, in four sets
+constexpr int kSets = kKeyWarps / 4;
 constexpr int kThreads = 32 * (kKeyWarp0 + kKeyWarps);
 constexpr int kBK = 128;                 // keys per block = MMA M
 constexpr int kChunks = 9;               // 576 dims / 64
-constexpr int kStageBytes = kBK * 128;   // 16384
-constexpr int kAddThreads = 512;
-constexpr int kAddSlices = 16;
+constexpr int kSlots = 8;                // chunks in tensor memory, 32 columns each
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColKeys = 256;       // (two accumulators of up to 128 columns before them)
+constexpr int kMaxDepth = 4;             // units of a quadrant's ring
+constexpr int kAddThreads = 256;
+constexpr int kAddSlices = 8;
 
-// N heads: Q takes 1152 N bytes; the stages fill what is left of 227 KB, up to a whole block
-__host__ __device__ constexpr int stages_of(int heads) { return heads == 128 ? 5 : 9; }
+// the small region after Q and the units
+constexpr int kOffLse = 0;               // float [128]: the token's lse in log2 units; before that int [23]: a sum over the warps
+constexpr int kOffBars = 512;            // u64: raw_full[16], raw_empty[16], full[8], empty[8], d_full[2], d_empty[2], q
+constexpr int kOffTmem = 944;            // u32
+constexpr int kOffAbort = 948;           // int
+constexpr int kOffStart = 952;           // int [2]: the token at the run's start, and its first block
+constexpr int kSmallBytes = 1024;
+static_assert(kOffBars + 8 * (8 * kMaxDepth + 2 * kSlots + 5) <= kOffTmem && 4 * (kThreads / 32) <= kOffBars, "small region");
 
-// the small region after Q and the stages
-constexpr int kOffLse = 0;               // float [128]: the token's lse in log2 units
-constexpr int kOffBars = 512;            // u64: full[9], empty[9], d_full[2], d_empty[2], q
-constexpr int kOffTmem = 704;            // u32
-constexpr int kOffAbort = 708;           // int
-constexpr int kOffStart = 712;           // int [2]: the unit at the run's start, and its first block
-constexpr int kOffScan = 720;            // int [21]
-constexpr int kSmallBytes = 832;
+// N heads: Q takes 1152 N bytes; units of 16 entries fill what is left of 227 KB
+template <int kH, bool kFour>
+struct Shape {
+    static constexpr int kEntry = kFour ? kEntry4Bytes : kEntryBytes;
+    static constexpr int kUnitBytes = 16 * kEntry;
+    static constexpr int kRoom = (232448 - kSmallBytes - kH * kDim * 2) / (4 * kUnitBytes);
+    static constexpr int kDepth = kRoom < kMaxDepth ? kRoom : kMaxDepth;
+    static constexpr int kSmem = kH * kDim * 2 + 4 * kDepth * kUnitBytes + kSmallBytes;
+    // (a block's chunks are consumed in all four quadrants together, so a whole block has to fit)
+    static_assert(kDepth >= 2, "units");
+};
 
-template <int kH>
-constexpr int smem_bytes() { return kH * kDim * 2 + stages_of(kH) * kStageBytes + kSmallBytes + 1024; }
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
 
-__device__ __forceinline__ uint4 ld16(const void *p) { return __ldca(reinterpret_cast<const uint4 *>(p)); }
+__device__ __forceinline__ uint32_t lds8(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
 
-// 32 E2M1 codes times 2^(se - 127) -> 32 BF16 values, exactly, into the 16-byte units u .. u + 3 (xored with x) of the row
-// at shared address rb, in the order e0 e4 e1 e5 e2 e6 e3 e7 of each eight (a code and the one four after it lie 16 bits
-// apart, so one shift puts both at their places in a BF16 pair).  A code's exponent and mantissa bits at the low end of
-// the BF16 exponent are its value times 2^-126; one multiply by 2^(se - 1) gives the value.  Scales past 2 (se > 128,
-// whose factor has no BF16 form) take a second multiply, 255 (NaN) among them.
-__device__ __forceinline__ void store32_e2m1(const uint4 &v, uint32_t se, uint32_t rb, uint32_t u, uint32_t x)
+// A (BF16 pairs, K along the columns) from tensor memory, B from shared memory
+__device__ __forceinline__ void mma_bf16_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accum)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accum), "r"(leader)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+                 "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+                 "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+
+// 16 bytes from global to shared memory, past L1
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// one arrival of this thread (counted at the mbarrier's set-up) when its copies so far are complete
+__device__ __forceinline__ void arrive_copied(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 E2M1 codes times 2^(se - 127) -> 32 BF16 values, exactly, as pairs in the order (e0 e4) (e1 e5) (e2 e6) (e3 e7) of each
+// eight (a code and the one four after it lie 16 bits apart, so one shift puts both at their places in a BF16 pair).  A
+// code's exponent and mantissa bits at the low end of the BF16 exponent are its value times 2^-126; one multiply by
+// 2^(se - 1) gives the value.  Scales past 2 (se > 128, whose factor has no BF16 form) take a second multiply, 255 (NaN)
+// among them.
+__device__ __forceinline__ void dequant32_e2m1(const uint4 &v, uint32_t se, uint32_t *o)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t f = (min(se, 128u) + 126u) << 7;
     f |= f << 16;
-    uint32_t g = se == 255u ? 0x7FC0u : (se - 1u) << 7;   // 2^(se - 128), where se > 128
-    g |= g << 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t h = w[i] >> 8;
-        uint32_t o[4] = {((w[i] << 6) & 0x01C001C0u) | ((w[i] << 12) & 0x80008000u),
-                         ((w[i] << 2) & 0x01C001C0u) | ((w[i] << 8) & 0x80008000u),
-                         ((h << 6) & 0x01C001C0u) | ((w[i] << 4) & 0x80008000u),
-                         ((h << 2) & 0x01C001C0u) | (w[i] & 0x80008000u)};
+        o[4 * i] = ((w[i] << 6) & 0x01C001C0u) | ((w[i] << 12) & 0x80008000u);
+        o[4 * i + 1] = ((w[i] << 2) & 0x01C001C0u) | ((w[i] << 8) & 0x80008000u);
+        o[4 * i + 2] = ((h << 6) & 0x01C001C0u) | ((w[i] << 4) & 0x80008000u);
+        o[4 * i + 3] = ((h << 2) & 0x01C001C0u) | (w[i] & 0x80008000u);
+    }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = mul_bf16x2(o[k], f);
-        if (se > 128u) {
+    for (int i = 0; i < 16; ++i)
+        o[i] = mul_bf16x2(o[i], f);
+    if (se > 128u) {
+        uint32_t g = se == 255u ? 0x7FC0u : (se - 1u) << 7;   // 2^(se - 128)
+        g |= g << 16;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                o[k] = mul_bf16x2(o[k], g);
-        }
-        st_shared_v4(rb + (((u + i) ^ x) << 4), o[0], o[1], o[2], o[3]);
+        for (int i = 0; i < 16; ++i)
+            o[i] = mul_bf16x2(o[i], g);
     }
 }
 
@@ -96,17 +155,15 @@ __device__ __forceinline__ uint32_t convert2_e4m3(uint32_t two, float scale)
     return pack_bf16x2(f.x * scale, f.y * scale);
 }
 
-// the form of store16_e4m3 for pieces with the NaN code or a scale past 2^7, out of line
-static __device__ __noinline__ void store16_e4m3_convert(uint4 v, uint32_t se, uint32_t a0, uint32_t a1)
+__device__ __forceinline__ float scale_of(uint32_t se)   // 2^(se - 127); 255: NaN
 {
-    const float sc = se == 255u ? __int_as_float(0x7FC00000) : se == 0u ? __int_as_float(0x00400000) : __int_as_float((int)(se << 23));
-    st_shared_v4(a0, convert2_e4m3(v.x, sc), convert2_e4m3(v.x >> 16, sc), convert2_e4m3(v.y, sc), convert2_e4m3(v.y >> 16, sc));
-    st_shared_v4(a1, convert2_e4m3(v.z, sc), convert2_e4m3(v.z >> 16, sc), convert2_e4m3(v.w, sc), convert2_e4m3(v.w >> 16, sc));
+    return se == 255u ? __int_as_float(0x7FC00000) : se == 0u ? __int_as_float(0x00400000) : __int_as_float((int)(se << 23));
 }
 
-// 16 E4M3 codes times 2^(se - 127) -> 16 BF16, elements 0-7 to shared address a0 and 8-15 to a1.  A code s.eeee.mmm placed
-// as the BF16 pattern s.0000eeee.mmm0000 is its value times 2^-120; one multiply by 2^(se - 7) gives the value.
-__device__ __forceinline__ void store16_e4m3(const uint4 &v, uint32_t se, uint32_t a0, uint32_t a1)
+// 16 E4M3 codes times 2^(se - 127) -> 16 BF16 values as pairs.  A code s.eeee.mmm placed as the BF16 pattern
+// s.0000eeee.mmm0000 is its value times 2^-120; one multiply by 2^(se - 7) gives the value.  Pieces with the NaN code, or a scale
+// past 2^7, take the hardware's conversion.
+__device__ __forceinline__ void dequant16_e4m3(const uint4 &v, uint32_t se, uint32_t *o)
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t odd = se > 134u ? 1u : 0u;
@@ -114,18 +171,19 @@ __device__ __forceinline__ void store16_e4m3(const uint4 &v, uint32_t se, uint32
     for (int i = 0; i < 4; ++i)
         odd |= ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // a byte with magnitude 0x7F
     if (odd != 0u) {
-        store16_e4m3_convert(v, se, a0, a1);
+        const float sc = scale_of(se);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = convert2_e4m3(w[i >> 1] >> (16 * (i & 1)), sc);
         return;
     }
-    uint32_t f = (se + 120u) << 7, o[8];
+    uint32_t f = (se + 120u) << 7;
     f |= f << 16;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t t = __byte_perm(w[i >> 1], 0u, i & 1 ? 0x3424 : 0x1404);   // [0, c, 0, c']
         o[i] = mul_bf16x2((t & 0x80008000u) | ((t & 0x7F007F00u) >> 4), f);
     }
-    st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-    st_shared_v4(a1, o[4], o[5], o[6], o[7]);
 }
 
 __device__ __forceinline__ int blocks_of(int len) { return (len + kBK - 1) / kBK; }
@@ -163,31 +221,35 @@ __device__ __forceinline__ bool next_segment(Walk &k, const KeyWeightsParams &p,
 template <int kH, bool kFour>
 __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeightsParams p)
 {
-    extern __shared__ uint8_t smem_raw[];
-    constexpr int kStages = stages_of(kH);
+    using S = Shape<kH, kFour>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];   // (the swizzled tiles of Q start on 1024-byte boundaries)
+    constexpr int kDepth = S::kDepth;
     constexpr int kQChunkBytes = kH * 128;
-    constexpr uint32_t kTmemCols = kH < 16 ? 32 : 2 * kH;
     // instruction descriptor (kind::f16): D f32, A/B bf16, both K-major
     constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kH >> 3) << 17) | ((uint32_t)(kBK >> 4) << 24);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;   // the swizzled tiles start on 1024-byte boundaries
-    const uint32_t sQ = base, sK = base + kChunks * kQChunkBytes;
-    uint8_t *small = smem_raw + (base - raw) + kChunks * kQChunkBytes + kStages * kStageBytes;
+    const uint32_t sQ = smem_u32(smem_raw), sRaw = sQ + kChunks * kQChunkBytes;
+    uint8_t *small = smem_raw + kChunks * kQChunkBytes + 4 * kDepth * S::kUnitBytes;
     float *slse = reinterpret_cast<float *>(small + kOffLse);
-    const uint32_t bar_full = smem_u32(small + kOffBars);      // [stage] written (a group's eight warps)
-    const uint32_t bar_empty = bar_full + 8 * 9;               // [stage] read by its products
-    const uint32_t bar_dfull = bar_full + 8 * 18;              // [2] the block's products are complete
-    const uint32_t bar_dempty = bar_full + 8 * 20;             // [2] read by the epilogue
-    const uint32_t bar_q = bar_full + 8 * 22;                  // Q of the segment written
+    const uint32_t bar_raw_full = smem_u32(small + kOffBars);  // [quadrant][unit] its entries are there
+    const uint32_t bar_raw_empty = bar_raw_full + 32 * kMaxDepth;  // [quadrant][unit] dequantised (its nine chunks)
+    const uint32_t bar_full = bar_raw_empty + 32 * kMaxDepth;  // [slot] the chunk is in tensor memory (a set's four warps)
+    const uint32_t bar_empty = bar_full + 8 * kSlots;          // [slot] read by its products
+    const uint32_t bar_dfull = bar_empty + 8 * kSlots;         // [2] the block's products are complete
+    const uint32_t bar_dempty = bar_dfull + 16;                // [2] read by the epilogue
+    const uint32_t bar_q = bar_dfull + 32;                     // Q of the segment written
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(small + kOffAbort);
     int *first = reinterpret_cast<int *>(small + kOffStart);
-    int *scan = reinterpret_cast<int *>(small + kOffScan);
+    int *scan = reinterpret_cast<int *>(small + kOffLse);
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(bar_full + 8 * i, kKeyWarps / 2);
+        for (int i = 0; i < 4 * kMaxDepth; ++i) {
+            mbar_init(bar_raw_full + 8 * i, 32);
+            mbar_init(bar_raw_empty + 8 * i, kChunks);
+        }
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(bar_full + 8 * i, 4);
             mbar_init(bar_empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -249,10 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
     uint32_t g = 0;     // blocks since the kernel began
 
     if (warp == 0) {
-        // ---- the products: K-major operands advance 32 B per 16 dims and one chunk per 64
+        // ---- the products: K-major operands advance 32 B, or eight columns, per 16 dims
         const uint32_t leader = elect_one();
-        const uint64_t da = sdesc(sK, 16, 1024), db = sdesc(sQ, 16, 1024);
-        uint32_t stage = 0, phase = 0;
+        const uint64_t db = sdesc(sQ, 16, 1024);
+        uint32_t at = 0;   // chunks since the kernel began
         for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
             mbar_wait(bar_q, n & 1u, abort_flag, p.status);
             for (int b = 0; b < seg.nb; ++b, ++g) {
@@ -261,24 +323,22 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                     mbar_wait(bar_dempty + 8 * x, ((g >> 1) - 1) & 1u, abort_flag, p.status);
                     after_sync();
                 }
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    mbar_wait(bar_full + 8 * stage, phase, abort_flag, p.status);
+#pragma unroll 3
+                for (int c = 0; c < kChunks; ++c, ++at) {
+                    const uint32_t slot = at % kSlots;
+                    mbar_wait(bar_full + 8 * slot, (at / kSlots) & 1u, abort_flag, p.status);
                     after_sync();
-                    const uint64_t a = da + (uint64_t)((stage * kStageBytes) >> 4), bq = db + (uint64_t)((c * kQChunkBytes) >> 4);
+                    const uint64_t bq = db + (uint64_t)((c * kQChunkBytes) >> 4);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_bf16(leader, tmem + kH * x, a + (uint64_t)(2 * k), bq + (uint64_t)(2 * k), kIdesc, (c != 0 || k != 0) ? 1u : 0u);
-                    commit(leader, bar_empty + 8 * stage);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                        mma_bf16_ts(leader, tmem + kH * x, tmem + kColKeys + 32 * slot + 8 * k, bq + (uint64_t)(2 * k), kIdesc,
+                                    (c != 0 || k != 0) ? 1u : 0u);
+                    commit(leader, bar_empty + 8 * slot);
                 }
                 commit(leader, bar_dfull + 8 * x);
             }
         }
-    } else if (warp < kKeyWarp0) {
+    } else if (warp <= kEpilogueWarps) {
         // ---- sums over the heads: lane l of quadrant q has key 32 q + l of the block
         const int quad = warp & 3, row = 32 * quad + lane;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -286,24 +346,26 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
         while (next_segment(walk, p, seg)) {
             const int t = seg.t;
             const int r = p.req_idx != nullptr ? __ldcg(p.req_idx + t) : t;
-            const bool sole = __ldcg(p.sole + t) != 0;
+            const bool first_of = __ldcg(p.later + t) == 0;
             named_bar(1, 32 * kEpilogueWarps);   // (slse has been read)
             if (row < kH) {
                 const float l = __ldcg(p.lse + (int64_t)t * kH + row);
                 slse[row] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;   // (a head without weight)
             }
             named_bar(1, 32 * kEpilogueWarps);
+            // the place of a block's key (-1: none), read a block ahead
+            const int64_t list = (int64_t)t * p.list_w;
+            auto load_place = [&](int b) {
+                const int i = (seg.kb + b) * kBK + row;
+                return b < seg.nb && i < seg.len && __ldcg(p.slots + list + i) >= 0 ? (first_of ? __ldcg(p.positions + list + i) : i) : -1;
+            };
+            float *out = first_of ? p.weights + (int64_t)max(r, 0) * p.weights_stride : p.got + list;
+            int place_next = load_place(0);
             for (int b = 0; b < seg.nb; ++b, ++g) {
                 const uint32_t x = g & 1u;
-                const int i = (seg.kb + b) * kBK + row;
-                const int64_t at = (int64_t)t * p.list_w + i;
-                float *place = nullptr;
-                float had = 0.f;
-                if (i < seg.len && __ldcg(p.slots + at) >= 0) {
-                    place = sole ? p.weights + (int64_t)r * p.weights_stride + __ldcg(p.positions + at) : p.got + at;
-                    if (sole)
-                        had = __ldcg(place);
-                }
+                const int place = place_next;
+                const float had = first_of && place >= 0 ? __ldcg(out + place) : 0.f;
+                place_next = load_place(b + 1);
                 mbar_wait(bar_dfull + 8 * x, (g >> 1) & 1u, abort_flag, p.status);
                 after_sync();
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -325,60 +387,64 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar_dempty + 8 * x);
-                if (place != nullptr)
-                    __stcg(place, had + ((sum[0] + sum[1]) + (sum[2] + sum[3])));
+                if (place >= 0)
+                    __stcg(out + place, had + ((sum[0] + sum[1]) + (sum[2] + sum[3])));
             }
         }
-    } else {
-        // ---- Q and the keys.  A thread has dims [32 half, 32 half + 32) of row `row` of its group's chunks
-        const int kw = warp - kKeyWarp0, group = kw >> 3, gid = 32 * (kw & 7) + lane;
-        const int row = gid >> 1, half = gid & 1;
-        const uint32_t rb = (uint32_t)(row >> 3) * 1024u + (uint32_t)(row & 7) * 128u, x7 = (uint32_t)(row & 7);
-        constexpr int kPieces = kFour ? 1 : 2;           // 16-byte pieces of 32 values
-        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
-            const int t = seg.t;
-            const int32_t *list = p.slots + (int64_t)t * p.list_w;
-            auto load_slot = [&](int b) {
-                const int i = (seg.kb + b) * kBK + row;
+    } else if (warp < kKeyWarp0) {
+        // ---- the entries of two quadrants.  A lane holds the slot of its row of each (rows without a key keep what was there:
+        // nobody reads their sums).  Every unit of a ring is filled by one warp, so it is never two phases behind its barrier
+        constexpr int kPieces = S::kEntry / 16;
+        const int quad0 = 2 * (warp - kCopyWarp0);
+        uint32_t unit = 0, round = 0;   // the next unit of the two rings, and how often they have been filled
+        while (next_segment(walk, p, seg)) {
+            const int32_t *list = p.slots + (int64_t)seg.t * p.list_w;
+            auto load_slot = [&](int b, int quad) {
+                const int i = ((seg.kb + b) * 4 + quad) * 32 + lane;
                 return b < seg.nb && i < seg.len ? __ldcg(list + i) : -1;
             };
-            auto entry_of = [&](int slot) { return p.kv + (int64_t)max(slot, 0) * (kFour ? kEntry4Bytes : kEntryBytes); };
-            // the entry of the block ahead: pieces of chunks group, group + 2, ..; rope in the blocks of this group's turn
-            uint4 pre[4][kPieces], rope[4], scales;
-            auto load_piece = [&](const uint8_t *e, int i) {
-                const int chunk = group + 2 * i;
-#pragma unroll
-                for (int k = 0; k < kPieces; ++k)
-                    pre[i][k] = ld16(e + (kFour ? 32 * chunk + 16 * half : 64 * chunk + 32 * half + 16 * k));
-            };
-            auto load_scales = [&](const uint8_t *e) {
-                if (kFour)
-                    scales = ld16(e + kScale4Offset);
-                else
-                    scales.x = __ldca(reinterpret_cast<const uint32_t *>(e + kScaleOffset));
-            };
-            auto load_rope = [&](const uint8_t *e) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    rope[i] = ld16(e + (kFour ? kRope4Offset : kRopeOffset) + 64 * half + 16 * i);
-            };
-            int slot = load_slot(0), slot_next = load_slot(1);
-            if (slot >= 0) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    load_piece(entry_of(slot), i);
-                load_scales(entry_of(slot));
-                if ((int)(g & 1u) == group)
-                    load_rope(entry_of(slot));
-            }
-            if (n > 0)   // the products of the last segment are done with its Q
-                mbar_wait(bar_dfull + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
-            {
-                const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)t * p.q_token_stride);
-                constexpr int kLoads = (kH * (kDim / 8) + 32 * kKeyWarps - 1) / (32 * kKeyWarps);
-                constexpr int kBatch = kLoads < 6 ? kLoads : 6;
+            int next[2] = {load_slot(0, quad0), load_slot(0, quad0 + 1)};
+            for (int b = 0; b < seg.nb; ++b) {
+                const int slot[2] = {next[0], next[1]};
+                next[0] = load_slot(b + 1, quad0);
+                next[1] = load_slot(b + 1, quad0 + 1);
 #pragma unroll 1
-                for (int j0 = 0; j0 < kLoads; j0 += kBatch) {
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t at_unit = (quad0 + j) * kDepth + unit;
+                        if (round > 0)
+                            mbar_wait(bar_raw_empty + 8 * at_unit, (round - 1) & 1u, abort_flag, p.status);
+                        const uint32_t dst = sRaw + at_unit * S::kUnitBytes + 16 * lane;
+#pragma unroll
+                        for (int i = 0; i < (16 * kPieces + 31) / 32; ++i) {
+                            const int at = 32 * i + lane, e = at / kPieces;   // piece `at` of the unit, of entry e
+                            const int from = __shfl_sync(0xffffffffu, slot[j], 16 * half + (e & 15));
+                            if (from >= 0 && e < 16)
+                                copy16(dst + 512 * i, p.kv + (int64_t)from * S::kEntry + 16 * (at - e * kPieces));
+                        }
+                        arrive_copied(bar_raw_full + 8 * at_unit);
+                    }
+                    if (++unit == kDepth) {
+                        unit = 0;
+                        ++round;
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        // ---- Q and the keys: lane l of quadrant q has key 32 q + l of the block, its set every kSets-th chunk
+        const int kw = warp - kKeyWarp0, set = kw >> 2, quad = warp & 3;
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + kColKeys;
+        uint32_t at = set;       // this set's next chunk, of block at / kChunks
+        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
+            {
+                const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)seg.t * p.q_token_stride);
+                constexpr int kQLoads = (kH * (kDim / 8) + 32 * kKeyWarps - 1) / (32 * kKeyWarps);
+                constexpr int kBatch = kQLoads < 9 ? kQLoads : 9;
+#pragma unroll 1
+                for (int j0 = 0; j0 < kQLoads; j0 += kBatch) {
                     uint4 v[kBatch];
 #pragma unroll
                     for (int j = 0; j < kBatch; ++j) {
@@ -386,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                         if (i < kH * (kDim / 8))
                             v[j] = __ldca(q + i);
                     }
+                    if (n > 0 && j0 == 0)   // the products of the last segment are done with its Q
+                        mbar_wait(bar_dfull + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
 #pragma unroll
                     for (int j = 0; j < kBatch; ++j) {
                         const int i = 32 * kKeyWarps * (j0 + j) + 32 * kw + lane;
@@ -393,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                             break;
                         const int h = i / (kDim / 8), c = i % (kDim / 8);
                         const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
-                        if (kFour && c < kLatent / 8)   // (the order of the latent dims that store32_e2m1 gives)
+                        if (kFour && c < kLatent / 8)   // (the order of the latent dims that dequant32_e2m1 gives)
                             st_shared_v4(a, __byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
                                          __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
                         else
@@ -406,60 +474,52 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             if (lane == 0)
                 mbar_arrive(bar_q);
 
-            for (int b = 0; b < seg.nb; ++b, ++g) {
-                const bool ok = slot >= 0, ok_next = slot_next >= 0;
-                const uint8_t *next = entry_of(slot_next);
-                const uint4 sc = scales;
-                if (ok_next)
-                    load_scales(next);
-                // a stage for chunk c: wait until its last products are complete, and then tell that it is written
-                auto begin = [&](int c) {
-                    const uint32_t at = g * kChunks + c, stage = at % kStages;
-                    if (at >= kStages)
-                        mbar_wait(bar_empty + 8 * stage, ((at / kStages) & 1u) ^ 1u, abort_flag, p.status);
-                    return stage;
-                };
-                auto end = [&](uint32_t stage) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar_full + 8 * stage);
-                };
+            g += (uint32_t)seg.nb;
+            for (; at < g * kChunks; at += kSets) {
+                const uint32_t blk = at / kChunks, c = at - blk * kChunks;
+                // both units of the quadrant's half blocks, and this lane's entry in its own
+                const uint32_t u0 = 2 * blk, u1 = 2 * blk + 1;
+                const uint32_t unit0 = quad * kDepth + u0 % kDepth, unit1 = quad * kDepth + u1 % kDepth;
+                mbar_wait(bar_raw_full + 8 * unit0, (u0 / kDepth) & 1u, abort_flag, p.status);
+                mbar_wait(bar_raw_full + 8 * unit1, (u1 / kDepth) & 1u, abort_flag, p.status);
+                const uint32_t e = sRaw + (lane < 16 ? unit0 : unit1) * S::kUnitBytes + (lane & 15) * S::kEntry;
+                uint32_t o[32];
+                if (c == kChunks - 1) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t stage = begin(group + 2 * i);
-                    const uint32_t a = sK + stage * kStageBytes + rb;
-                    if (!ok) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            st_shared_v4(a + (((4 * half + k) ^ x7) << 4), 0u, 0u, 0u, 0u);
-                    } else if (kFour) {
-                        const uint32_t word = i == 0 ? sc.x : i == 1 ? sc.y : i == 2 ? sc.z : sc.w;
-                        store32_e2m1(pre[i][0], (word >> (8 * (2 * group + half))) & 255u, a, 4 * half, x7);
-                    } else {
-                        const uint32_t se = (sc.x >> (8 * i)) & 255u;
-#pragma unroll
-                        for (int k = 0; k < kPieces; ++k)
-                            store16_e4m3(pre[i][k], se, a + (((4 * half + 2 * k) ^ x7) << 4), a + (((4 * half + 2 * k + 1) ^ x7) << 4));
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 v = lds16(e + (kFour ? kRope4Offset : kRopeOffset) + 16 * i);
+                        o[4 * i] = v.x;
+                        o[4 * i + 1] = v.y;
+                        o[4 * i + 2] = v.z;
+                        o[4 * i + 3] = v.w;
                     }
-                    if (ok_next)
-                        load_piece(next, i);
-                    end(stage);
-                }
-                if ((int)(g & 1u) == group) {
-                    const uint32_t stage = begin(8);
-                    const uint32_t a = sK + stage * kStageBytes + rb;
+                } else if (kFour) {
+                    const uint4 v0 = lds16(e + 32 * c), v1 = lds16(e + 32 * c + 16);
+                    const uint32_t s0 = lds8(e + kScale4Offset + 2 * c), s1 = lds8(e + kScale4Offset + 2 * c + 1);
+                    dequant32_e2m1(v0, s0, o);
+                    dequant32_e2m1(v1, s1, o + 16);
+                } else {
+                    const uint32_t se = lds8(e + kScaleOffset + (c >> 1));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 v = ok ? rope[i] : make_uint4(0u, 0u, 0u, 0u);
-                        st_shared_v4(a + (((4 * half + i) ^ x7) << 4), v.x, v.y, v.z, v.w);
-                    }
-                    end(stage);
-                } else if (ok_next) {
-                    load_rope(next);
+                    for (int i = 0; i < 4; ++i)
+                        dequant16_e4m3(lds16(e + 64 * c + 16 * i), se, o + 8 * i);
                 }
-                slot = slot_next;
-                slot_next = load_slot(b + 2);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_raw_empty + 8 * unit0);
+                    mbar_arrive(bar_raw_empty + 8 * unit1);
+                }
+                const uint32_t slot = at % kSlots;
+                if (at >= kSlots) {
+                    mbar_wait(bar_empty + 8 * slot, ((at / kSlots) & 1u) ^ 1u, abort_flag, p.status);
+                    after_sync();
+                }
+                tmem_st32(lane_base + 32 * slot, o);
+                tmem_st_wait();
+                before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_full + 8 * slot);
             }
         }
     }
@@ -470,23 +530,59 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
         tmem_free(tmem, kTmemCols);
 }
 
-// Tokens that share a row, one after the other; positions are dealt out to the slices in runs of 256.
+// The tokens after a row's first one, in order.  One of them: the slices share its list.  Several: one after the other, positions
+// dealt out to the slices in runs of 256.
 __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const KeyWeightsParams p)
 {
+    __shared__ int tokens[kAddThreads], wcount[kAddThreads / 32];
     griddep_wait();
     griddep_launch();
-    const int r = blockIdx.y, slice = blockIdx.x, tid = threadIdx.x;
+    const int r = blockIdx.y, slice = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float *row = p.weights + (int64_t)r * p.weights_stride;
-    for (int t = 0; t < p.num_tokens; ++t) {
-        if (p.req_idx[t] != r || __ldcg(p.sole + t) != 0)
-            continue;
+    constexpr int kDeep = 4;
+    auto add = [&](int t, int i0, int step, bool deal) {
         const int len = __ldcg(p.lens + t);
-        for (int i = tid; i < len; i += kAddThreads) {
-            const int pos = __ldcg(p.positions + (int64_t)t * p.list_w + i);
-            if ((pos >> 8) % kAddSlices == slice && __ldcg(p.slots + (int64_t)t * p.list_w + i) >= 0)
-                row[pos] += __ldcg(p.got + (int64_t)t * p.list_w + i);
+        const int64_t at = (int64_t)t * p.list_w;
+        for (; i0 < len; i0 += kDeep * step) {
+            int pos[kDeep];
+            float got[kDeep];
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u) {
+                const int i = i0 + u * step;
+                const bool in = i < len && __ldcg(p.slots + at + i) >= 0;
+                pos[u] = in ? __ldcg(p.positions + at + i) : -1;
+                got[u] = in ? __ldcg(p.got + at + i) : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u)
+                if (pos[u] >= 0 && (!deal || (pos[u] >> 8) % kAddSlices == slice))
+                    __stcg(row + pos[u], __ldcg(row + pos[u]) + got[u]);
         }
-        __syncthreads();   // the next token's sums come on top
+    };
+    for (int t0 = 0; t0 < p.num_tokens; t0 += kAddThreads) {
+        const int t = t0 + tid;
+        const bool mine = t < p.num_tokens && p.req_idx[t] == r && __ldcg(p.later + t) != 0;
+        const unsigned m = __ballot_sync(0xffffffffu, mine);
+        if (lane == 0)
+            wcount[warp] = __popc(m);
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < kAddThreads / 32; ++w) {
+            before += w < warp ? wcount[w] : 0;
+            all += wcount[w];
+        }
+        if (mine)
+            tokens[before + __popc(m & ((1u << lane) - 1u))] = t;
+        __syncthreads();
+        const bool deal = all > 1 || p.num_tokens > kAddThreads;   // (else it is the row's only one)
+        for (int k = 0; k < all; ++k) {
+            if (deal)
+                add(tokens[k], tid, kAddThreads, true);
+            else
+                add(tokens[k], slice * kAddThreads + tid, kAddSlices * kAddThreads, false);
+            __syncthreads();   // the next token's sums come on top
+        }
+        __syncthreads();
     }
 }
 
@@ -495,10 +591,10 @@ cudaError_t launch(const KeyWeightsParams &p, int sms, cudaStream_t stream)
 {
     const auto kernel = key_weights_kernel<kH, kFour>;
     constexpr int kSlot = kAttrKeyWeights + (kH == 16 ? 0 : kH == 32 ? 1 : kH == 64 ? 2 : 3) + (kFour ? 4 : 0);
-    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), smem_bytes<kH>(), (AttrSlot)kSlot);
+    const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), Shape<kH, kFour>::kSmem, (AttrSlot)kSlot);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(kernel, dim3((unsigned)sms), kThreads, smem_bytes<kH>(), stream, p);
+    return launch_dependent(kernel, dim3((unsigned)sms), kThreads, Shape<kH, kFour>::kSmem, stream, p);
 }
 
 template <bool kFour>

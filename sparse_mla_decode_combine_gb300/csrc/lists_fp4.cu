@@ -47,16 +47,16 @@ __global__ void __launch_bounds__(kThreads) lists_positions_kernel(const Lists4P
     const int t = blockIdx.x;
     const int len = lists::build<kThreads, kLoads, true>(p, t, threadIdx.x, tab, wsum, SyncAll(),
                                                          [](int len) { return make_int2(0, len); });
-    bool other = false;
+    bool later = false;
     if (p.req_idx != nullptr) {
         const int r = p.req_idx[t];
-        for (int i = threadIdx.x; i < p.num_tokens; i += kThreads)
-            other |= i != t && p.req_idx[i] == r && p.seq_lens[i] > 0;
+        for (int i = threadIdx.x; i < t; i += kThreads)
+            later |= p.req_idx[i] == r && p.seq_lens[i] > 0;
     }
-    other = __syncthreads_or(other);
+    later = __syncthreads_or(later);
     if (threadIdx.x == 0) {
         p.lens[t] = len;
-        p.sole[t] = other ? 0 : 1;
+        p.later[t] = later ? 1 : 0;
     }
 }
 

@@ -45,7 +45,7 @@ struct KeyWeightsParams {
     const int32_t *slots;      // [T, list_w] cache slots (-1: no key), the positions that they hold, how many a token has
     const int32_t *positions;
     const int32_t *lens;
-    const int32_t *sole;       // [T] not 0: no other token with keys names this one's row
+    const int32_t *later;      // [T] not 0: a token with keys before this one names its row
     int32_t list_w;
     int32_t num_tokens;
     int32_t num_heads;
@@ -53,7 +53,7 @@ struct KeyWeightsParams {
     int32_t num_reqs;
     const float *lse;          // [T, H]
     float scale;
-    float *got;                // [T, list_w] what each key of a token that is not sole received
+    float *got;                // [T, list_w] what each key of such a later token received
     float *weights;            // [num_reqs, weights_width]
     int64_t weights_stride;
     unsigned *status;
