@@ -392,36 +392,53 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             }
         }
     } else if (warp < kKeyWarp0) {
-        // ---- the entries of two quadrants.  A lane holds the slot of its row of each (rows without a key keep what was there:
-        // nobody reads their sums).  Every unit of a ring is filled by one warp, so it is never two phases behind its barrier
+        // ---- the entries of two quadrants, four lanes to a row (rows without a key keep what was there: nobody reads their
+        // sums): a lane has the rows lane / 4, + 8, + 16 and + 24 of a quadrant, whose addresses are all that it computes (with
+        // consecutive lanes at consecutive pieces, a division and a shuffle each, the two warps were what the others waited
+        // for).  Every unit of a ring is filled by one warp, so it is never two phases behind its barrier
         constexpr int kPieces = S::kEntry / 16;
         const int quad0 = 2 * (warp - kCopyWarp0);
+        const uint8_t *kv = p.kv + 16 * (lane & 3);
+        const uint32_t dst0 = sRaw + (lane >> 2) * S::kEntry + 16 * (lane & 3);
         uint32_t unit = 0, round = 0;   // the next unit of the two rings, and how often they have been filled
         while (next_segment(walk, p, seg)) {
             const int32_t *list = p.slots + (int64_t)seg.t * p.list_w;
-            auto load_slot = [&](int b, int quad) {
-                const int i = ((seg.kb + b) * 4 + quad) * 32 + lane;
-                return b < seg.nb && i < seg.len ? __ldcg(list + i) : -1;
+            int next[2][4];
+            auto load_slots = [&](int b) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = ((seg.kb + b) * 4 + quad0 + j) * 32 + 8 * k + (lane >> 2);
+                        next[j][k] = b < seg.nb && i < seg.len ? __ldcg(list + i) : -1;
+                    }
             };
-            int next[2] = {load_slot(0, quad0), load_slot(0, quad0 + 1)};
+            load_slots(0);
             for (int b = 0; b < seg.nb; ++b) {
-                const int slot[2] = {next[0], next[1]};
-                next[0] = load_slot(b + 1, quad0);
-                next[1] = load_slot(b + 1, quad0 + 1);
-#pragma unroll 1
+                int slot[2][4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    slot[i >> 2][i & 3] = next[i >> 2][i & 3];
+                load_slots(b + 1);
+#pragma unroll
                 for (int half = 0; half < 2; ++half) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t at_unit = (quad0 + j) * kDepth + unit;
                         if (round > 0)
                             mbar_wait(bar_raw_empty + 8 * at_unit, (round - 1) & 1u, abort_flag, p.status);
-                        const uint32_t dst = sRaw + at_unit * S::kUnitBytes + 16 * lane;
 #pragma unroll
-                        for (int i = 0; i < (16 * kPieces + 31) / 32; ++i) {
-                            const int at = 32 * i + lane, e = at / kPieces;   // piece `at` of the unit, of entry e
-                            const int from = __shfl_sync(0xffffffffu, slot[j], 16 * half + (e & 15));
-                            if (from >= 0 && e < 16)
-                                copy16(dst + 512 * i, p.kv + (int64_t)from * S::kEntry + 16 * (at - e * kPieces));
+                        for (int k = 0; k < 2; ++k) {
+                            const int from = slot[j][2 * half + k];
+                            if (from < 0)
+                                continue;
+                            const uint8_t *src = kv + (int64_t)from * S::kEntry;
+                            const uint32_t dst = dst0 + at_unit * S::kUnitBytes + 8 * k * S::kEntry;
+#pragma unroll
+                            for (int i = 0; i < kPieces / 4; ++i)
+                                copy16(dst + 64 * i, src + 64 * i);
+                            if ((lane & 3) < kPieces % 4)
+                                copy16(dst + kPieces / 4 * 64, src + kPieces / 4 * 64);
                         }
                         arrive_copied(bar_raw_full + 8 * at_unit);
                     }
