@@ -214,7 +214,7 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_key_weights(
     l.list_w = pl.list_w;
     l.status = status;
     l.smem_bytes = lists_fp4_smem_bytes(topk_width);
-    if (launch_lists_positions(l, cs) != cudaSuccess)
+    if (launch_lists_positions(l, sms, cs) != cudaSuccess)
         return DSV4_ERR_CUDA;
     KeyWeightsParams p{};
     p.q = static_cast<const uint16_t *>(q);

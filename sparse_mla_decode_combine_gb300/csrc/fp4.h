@@ -112,7 +112,7 @@ inline int lists_fp4_smem_bytes(int topk_width)
 }
 cudaError_t launch_lists_fp4(const Lists4Params &p, cudaStream_t stream);
 // slots, positions and lengths alone (no joins, no outputs of tokens without a key)
-cudaError_t launch_lists_positions(const Lists4Params &p, cudaStream_t stream);
+cudaError_t launch_lists_positions(const Lists4Params &p, int sms, cudaStream_t stream);
 
 struct Decode4Params {
     const uint16_t *q;

@@ -111,6 +111,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // one arrival of this thread (counted at the mbarrier's set-up) when its copies so far are complete
 __device__ __forceinline__ void arrive_copied(uint32_t bar)
 {
@@ -447,6 +449,18 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                         ++round;
                     }
                 }
+                // a block's units are free when all of its chunks are dequantised, so the next block's copies begin late: its
+                // entries wait in L2 (every 128-byte line of one: it starts and ends on 16-byte boundaries)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int from = next[i >> 2][i & 3];
+                    if (from >= 0) {
+                        const uint8_t *src = p.kv + (int64_t)from * S::kEntry + 128 * (lane & 3);
+                        prefetch_l2(src);
+                        if (512 + 128 * (lane & 3) < S::kEntry)
+                            prefetch_l2(src + 512);
+                    }
+                }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -455,6 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
         const int kw = warp - kKeyWarp0, set = kw >> 2, quad = warp & 3;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + kColKeys;
         uint32_t at = set;       // this set's next chunk, of block at / kChunks
+        auto prefetch_q = [&](int t) {
+            const uint8_t *q = reinterpret_cast<const uint8_t *>(p.q + (int64_t)t * p.q_token_stride);
+            for (int i = 32 * kw + lane; i < (kH * kDim * 2 + 127) / 128; i += 32 * kKeyWarps)
+                prefetch_l2(q + 128 * i);
+        };
         for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
             {
                 const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)seg.t * p.q_token_stride);
@@ -490,6 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_q);
+            if (walk.w < walk.w1)   // the next token's
+                prefetch_q(seg.t + 1);
 
             g += (uint32_t)seg.nb;
             for (; at < g * kChunks; at += kSets) {

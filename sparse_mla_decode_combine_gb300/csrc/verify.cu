@@ -15,6 +15,11 @@
 // What is decided next to a border has to be right, so the sums are held in about 48 bits: a weight is the exact
 // difference of two floats as (high, low), and a thread's running sum is such a pair too (Knuth's two-sum); sums of tiles
 // and the search are in 64 bits.  Products u q are exact there.
+//
+// What bounds it.  Large batches: HBM, and the 17 additions a pair of values takes (half of the time at the measured rate of
+// both).  Loads of a thread's next 16 values of each row are issued before any is used: with a load, its use and the next
+// load one behind the other, 256 requests of 151937 took 217 us.  One request: the chain of dependent loads (row numbers,
+// tokens, probabilities, the row, the tile again) and the cluster's barrier.
 #include <cuda_bf16.h>
 #include <limits.h>
 #include <math.h>
@@ -27,8 +32,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kTile = 1024;          // values per tile, or a multiple of it where a CTA's part has more than kMaxTiles
-constexpr int kMaxTiles = 512;
+constexpr int kDeep = 16;            // values of a row that a thread has in flight
+constexpr int kMinTile = 256;        // values whose sum is held for the search
+constexpr int kMaxTiles = 1024;      // of a CTA
+constexpr int kEach = 4;             // values of the tile that a thread looks at
 
 __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ float value(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -57,24 +64,35 @@ struct Sum {   // hi + lo
     float hi, lo;
 };
 
-__device__ __forceinline__ void add(Sum &s, float x)   // exact but for the rounding of the low parts' sum
+// x + e (e far below x) into the sum; exact but for the rounding of the low parts
+__device__ __forceinline__ void add(Sum &s, float x, float e)
 {
     const float t = __fadd_rn(s.hi, x);
     const float b = __fsub_rn(t, s.hi);
-    s.lo = __fadd_rn(s.lo, __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(x, b)));
+    const float r = __fadd_rn(__fsub_rn(s.hi, __fsub_rn(t, b)), __fsub_rn(x, b));
+    s.lo = __fadd_rn(s.lo, __fadd_rn(r, e));
     s.hi = t;
 }
 
-// max(p - q, 0) of a value, exactly, into the sum
-__device__ __forceinline__ void add_weight(Sum &s, float p, float q)
+// max(p - q, 0), exactly, into the sum (q >= 0)
+__device__ __forceinline__ void add_difference(Sum &s, float p, float q)
 {
-    const float d = __fsub_rn(p, q);
-    if (!(d > 0.f))   // (the difference's sign is exact; NaN has no weight)
-        return;
-    const float b = __fsub_rn(d, p);
+    const float d = __fsub_rn(p, q), b = __fsub_rn(d, p);
     const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b));
-    add(s, d);
-    s.lo = __fadd_rn(s.lo, e);
+    const bool some = d > 0.f;   // (the rounded difference has the exact one's sign; NaN has no weight)
+    add(s, some ? d : 0.f, some ? e : 0.f);
+}
+
+__device__ __forceinline__ double scan32(double x, int lane, int width)   // inclusive sum over lanes 0 .. width - 1
+{
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+        if (d < width) {
+            const double y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d)
+                x += y;
+        }
+    return x;
 }
 
 // A request's row of weights: p, less the draft's q, or without the drafted token
@@ -82,38 +100,52 @@ template <typename T>
 struct Row {
     const T *p, *q;
     int point;         // this value has no weight (-1: none)
-    __device__ __forceinline__ void load(int i, float &x, float &y) const
+    // the sum over [t0, t1), by the lanes of a warp
+    template <bool kQ>
+    __device__ __forceinline__ double sum(int t0, int t1, int lane) const
     {
-        x = value(p[i]);
-        y = q != nullptr ? fmaxf(value(q[i]), 0.f) : 0.f;   // (NaN: 0)
-    }
-    __device__ __forceinline__ double weight(int i) const
-    {
-        float x, y;
-        load(i, x, y);
-        const double d = (double)x - (double)y;
-        return d > 0.0 && i != point ? d : 0.0;
+        Sum s = {0.f, 0.f};
+        for (int i0 = t0 + lane; i0 < t1; i0 += 32 * kDeep) {
+            T x[kDeep], y[kDeep];
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u) {
+                const int i = min(i0 + 32 * u, t1 - 1);
+                x[u] = p[i];
+                if (kQ)
+                    y[u] = q[i];
+            }
+#pragma unroll
+            for (int u = 0; u < kDeep; ++u) {
+                const int i = i0 + 32 * u;
+                const float v = i < t1 && i != point ? value(x[u]) : 0.f;
+                if (kQ)
+                    add_difference(s, v, fmaxf(value(y[u]), 0.f));   // (q of NaN: 0)
+                else
+                    add(s, fmaxf(v, 0.f), 0.f);
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            const float hi = __shfl_xor_sync(0xffffffffu, s.hi, d), lo = __shfl_xor_sync(0xffffffffu, s.lo, d);
+            add(s, hi, lo);
+        }
+        return (double)s.hi + (double)s.lo;
     }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p)
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const VerifyParams p)
 {
     __shared__ double tile_sum[kMaxTiles];
     __shared__ double totals[kMaxCluster];                    // the cluster's parts of the row
     __shared__ unsigned long long bests[2][kMaxCluster];      // greedy: (order key of the value, ~index)
     __shared__ unsigned long long wbest[kWarps];
     __shared__ double wscan[kWarps];
-    __shared__ int found, last_positive, chosen;
+    __shared__ double want, start;
+    __shared__ int owner, chosen, found, last_positive;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = p.cluster, b = blockIdx.x / C;
-    const uint32_t rank = C > 1 ? cluster_rank() : 0u;
-    auto sync_all = [&]() {
-        if (C > 1)
-            cluster_barrier();
-        else
-            __syncthreads();
-    };
+    const int rank = C > 1 ? (int)cluster_rank() : 0;
     const T *target = static_cast<const T *>(p.target), *draft = static_cast<const T *>(p.draft);
     const int V = p.vocab;
     griddep_wait();
@@ -140,28 +172,26 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p)
     const bool greedy = p.greedy != nullptr && p.greedy[b] != 0;
     // this CTA's part of a row
     const int part = ((V + C - 1) / C + p.tile - 1) / p.tile * p.tile;
-    const int lo = min(V, (int)rank * part), hi = min(V, lo + part);
+    const int lo = min(V, rank * part), hi = min(V, lo + part);
 
     int a = 0;
-    int token = -1;      // of a greedy request
     if (greedy) {
+        int token;
         for (int j = 0;; ++j) {   // row j: its largest value, the lowest index of equal ones
             const T *row = target + (int64_t)(row0 + j) * p.target_stride;
             float best = -INFINITY;
             int at = INT_MAX;
-            constexpr int kDeep = 8;
-            for (int i0 = lo; i0 < hi; i0 += kDeep * kThreads) {
-                float x[kDeep];
+            for (int i0 = lo + tid; i0 < hi; i0 += kDeep * kThreads) {
+                T x[kDeep];
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u)
+                    x[u] = row[min(i0 + u * kThreads, hi - 1)];
 #pragma unroll
                 for (int u = 0; u < kDeep; ++u) {
-                    const int i = i0 + u * kThreads + tid;
-                    x[u] = i < hi ? value(row[i]) : -INFINITY;
-                }
-#pragma unroll
-                for (int u = 0; u < kDeep; ++u) {
-                    const int i = i0 + u * kThreads + tid;
-                    if (i < hi && (x[u] > best || (x[u] == best && at == INT_MAX))) {
-                        best = x[u];
+                    const int i = i0 + u * kThreads;
+                    const float v = value(x[u]);
+                    if (i < hi && (v > best || (v == best && at == INT_MAX))) {
+                        best = v;
                         at = i;
                     }
                 }
@@ -223,154 +253,141 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p)
         }
         if (bad)
             atomicOr(p.status, kStatusBadIndex);
-        const double u = p.uniform[row0 + k];
         Row<T> row;
         row.p = target + (int64_t)(row0 + a) * p.target_stride;
         row.q = a < k && draft != nullptr ? draft + (int64_t)(d0 + a) * p.draft_stride : nullptr;
         row.point = a < k && draft == nullptr ? p.tokens[d0 + a] : -1;
+        const int tiles = (hi - lo + p.tile - 1) / p.tile;
         for (int turn = 0;; ++turn) {
             // ---- the sums of this CTA's tiles, a tile to a warp
-            const int tiles = (hi - lo + p.tile - 1) / p.tile;
             for (int t = warp; t < tiles; t += kWarps) {
                 const int t0 = lo + t * p.tile, t1 = min(hi, t0 + p.tile);
-                Sum s = {0.f, 0.f};
-                for (int i0 = t0; i0 < t1; i0 += 256) {
-                    float x[8], y[8];
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        const int i = i0 + 32 * v + lane;
-                        x[v] = y[v] = 0.f;
-                        if (i < t1)
-                            row.load(i, x[v], y[v]);
-                        if (i == row.point)
-                            x[v] = 0.f;
-                    }
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        add_weight(s, x[v], y[v]);
-                }
-                double w = (double)s.hi + (double)s.lo;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    w += __shfl_xor_sync(0xffffffffu, w, d);
+                const double w = row.q != nullptr ? row.template sum<true>(t0, t1, lane) : row.template sum<false>(t0, t1, lane);
                 if (lane == 0)
                     tile_sum[t] = w;
             }
             __syncthreads();
-            // ---- the row's sum, and what comes before this CTA's part: every warp the same
-            double mine = 0.0;
-            for (int t0 = 0; t0 < tiles; t0 += 32) {
-                double w = t0 + lane < tiles ? tile_sum[t0 + lane] : 0.0;
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1)
-                    w += __shfl_xor_sync(0xffffffffu, w, d);
-                mine += w;
-            }
-            if (tid < C) {
-                if (C > 1)
-                    put_remote(&totals[rank], tid, (unsigned long long)__double_as_longlong(mine));
-                else
-                    totals[0] = mine;
-            }
-            sync_all();
-            double all = 0.0, before = 0.0;
-            int last = -1;       // the last part that has weight
-            for (int r = 0; r < C; ++r) {
-                before += r < (int)rank ? totals[r] : 0.0;
-                all += totals[r];
-                last = totals[r] > 0.0 ? r : last;
-            }
-            if (last < 0 && turn == 0 && a < k) {   // nothing is left of p_a: p_a itself
-                row.q = nullptr;
-                row.point = -1;
-                sync_all();      // (totals have been read by all)
-                continue;
-            }
-            if (last < 0) {
-                if (rank == 0 && tid == 0) {
-                    out[a] = -1;
-                    atomicOr(p.status, kStatusBadIndex);
-                }
-                break;
-            }
-            const double want = u * all;
-            // the first part, tile and value whose sum is above `want`; where rounding leaves none, the last ones with weight
-            double at = 0.0;
-            int owner = last;
-            for (int r = 0; r <= last; ++r) {
-                if (at + totals[r] > want) {
-                    owner = r;
-                    break;
-                }
-                at += totals[r];
-            }
-            if (owner != (int)rank)
-                break;
+            // ---- the sum over the row, the part that holds the wanted sum, and there the tile.  Where rounding leaves no sum
+            // above it, the last part, tile and value with weight are taken
+            const int each = (tiles + 31) / 32, f0 = min(tiles, lane * each), f1 = min(tiles, f0 + each);
+            double mine = 0.0;   // of this lane's run of tiles
             if (warp == 0) {
-                int tile = -1, tail = -1;
-                double run = before, start = before, tail_start = before;
-                for (int t0 = 0; t0 < tiles && tile < 0; t0 += 32) {
-                    const double w = t0 + lane < tiles ? tile_sum[t0 + lane] : 0.0;
-                    double incl = w;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const double y = __shfl_up_sync(0xffffffffu, incl, d);
-                        if (lane >= d)
-                            incl += y;
-                    }
-                    const unsigned above = __ballot_sync(0xffffffffu, w > 0.0 && run + incl > want);
-                    const unsigned some = __ballot_sync(0xffffffffu, w > 0.0);
-                    if (above != 0u) {
-                        const int l = __ffs(above) - 1;
-                        tile = t0 + l;
-                        start = __shfl_sync(0xffffffffu, run + (incl - w), l);
-                    }
-                    if (some != 0u) {
-                        const int l = 31 - __clz(some);
-                        tail = t0 + l;
-                        tail_start = __shfl_sync(0xffffffffu, run + (incl - w), l);
-                    }
-                    run += __shfl_sync(0xffffffffu, incl, 31);
+                for (int t = f0; t < f1; ++t)
+                    mine += tile_sum[t];
+                mine = scan32(mine, lane, 32);
+                const double all = __shfl_sync(0xffffffffu, mine, 31);
+                if (lane < C) {
+                    if (C > 1)
+                        put_remote(&totals[rank], lane, (unsigned long long)__double_as_longlong(all));
+                    else
+                        totals[0] = all;
                 }
-                if (lane == 0) {
-                    chosen = tile >= 0 ? tile : tail;
-                    wscan[0] = tile >= 0 ? start : tail_start;
-                    found = INT_MAX;
-                    last_positive = -1;
+                __syncwarp();
+            }
+            if (C > 1)
+                cluster_barrier();
+            if (warp == 0) {
+                const double t = lane < C ? totals[lane] : 0.0;
+                const double sum = scan32(t, lane, kMaxCluster);
+                const double w = (double)p.uniform[row0 + k] * __shfl_sync(0xffffffffu, sum, kMaxCluster - 1);
+                const unsigned above = __ballot_sync(0xffffffffu, t > 0.0 && sum > w), some = __ballot_sync(0xffffffffu, t > 0.0);
+                const int who = above != 0u ? __ffs(above) - 1 : some != 0u ? 31 - __clz(some) : -1;
+                if (who == rank) {
+                    const double before = __shfl_sync(0xffffffffu, sum - t, who);
+                    // the lanes' runs, then the tiles of one run
+                    const double prev = __shfl_up_sync(0xffffffffu, mine, 1);
+                    double at = before + (lane > 0 ? prev : 0.0), last_at = at, first_at = at;
+                    int first = -1, last = -1;
+                    for (int i = f0; i < f1; ++i) {
+                        const double v = tile_sum[i];
+                        if (v > 0.0) {
+                            last = i;
+                            last_at = at;
+                            if (first < 0 && at + v > w) {
+                                first = i;
+                                first_at = at;
+                            }
+                        }
+                        at += v;
+                    }
+                    const unsigned has = __ballot_sync(0xffffffffu, first >= 0), any = __ballot_sync(0xffffffffu, last >= 0);
+                    const int l = has != 0u ? __ffs(has) - 1 : 31 - __clz(any);
+                    const int tile = __shfl_sync(0xffffffffu, has != 0u ? first : last, l);
+                    const double tile_at = __shfl_sync(0xffffffffu, has != 0u ? first_at : last_at, l);
+                    if (lane == 0) {
+                        chosen = tile;
+                        start = tile_at;
+                        want = w;
+                        found = INT_MAX;
+                        last_positive = -1;
+                    }
                 }
+                if (lane == 0)
+                    owner = who;
             }
             __syncthreads();
+            if (owner < 0 && turn == 0 && a < k) {   // nothing is left of p_a: p_a itself
+                row.q = nullptr;
+                row.point = -1;
+                if (C > 1)
+                    cluster_barrier();   // (totals have been read by all)
+                else
+                    __syncthreads();
+                continue;
+            }
+            if (owner < 0 && rank == 0 && tid == 0) {
+                out[a] = -1;
+                atomicOr(p.status, kStatusBadIndex);
+            }
+            if (owner != rank)
+                break;
+            // ---- the tile, kEach values to a thread at a time
             const int t0 = lo + chosen * p.tile, t1 = min(hi, t0 + p.tile);
-            double run = wscan[0];
-            // ---- the tile, two values to a thread at a time
-            for (int i0 = t0; i0 < t1; i0 += 2 * kThreads) {
-                const int i = i0 + 2 * tid;
-                const double w0 = i < t1 ? row.weight(i) : 0.0, w1 = i + 1 < t1 ? row.weight(i + 1) : 0.0;
-                double incl = w0 + w1;
+            double run = start;
+            const double w = want;
+            for (int i0 = t0; i0 < t1; i0 += kEach * kThreads) {
+                const int i = i0 + kEach * tid;
+                T x[kEach], y[kEach];
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, incl, d);
-                    if (lane >= d)
-                        incl += y;
+                for (int u = 0; u < kEach; ++u) {
+                    x[u] = row.p[min(i + u, t1 - 1)];
+                    if (row.q != nullptr)
+                        y[u] = row.q[min(i + u, t1 - 1)];
                 }
-                __syncthreads();   // (wscan has been read)
+                double v[kEach], sum = 0.0;
+#pragma unroll
+                for (int u = 0; u < kEach; ++u) {
+                    const double d = (double)value(x[u]) - (row.q != nullptr ? (double)fmaxf(value(y[u]), 0.f) : 0.0);
+                    v[u] = i + u < t1 && i + u != row.point && d > 0.0 ? d : 0.0;
+                    sum += v[u];
+                }
+                const double incl = scan32(sum, lane, 32);
                 if (lane == 31)
                     wscan[warp] = incl;
                 __syncthreads();
-                double pre = run + (incl - (w0 + w1));
-                for (int w = 0; w < kWarps; ++w) {
-                    if (w < warp)
-                        pre += wscan[w];
-                    run += wscan[w];
+                const double ws = scan32(lane < kWarps ? wscan[lane] : 0.0, lane, kWarps);
+                const double pre_warp = __shfl_sync(0xffffffffu, ws, warp > 0 ? warp - 1 : 0);
+                double at = run + (warp > 0 ? pre_warp : 0.0) + (incl - sum);
+                int mine_first = INT_MAX, mine_last = -1;
+#pragma unroll
+                for (int u = 0; u < kEach; ++u) {
+                    at += v[u];
+                    if (v[u] > 0.0) {
+                        mine_last = i + u;
+                        if (mine_first == INT_MAX && at > w)
+                            mine_first = i + u;
+                    }
                 }
-                if (w0 > 0.0 && pre + w0 > want)
-                    atomicMin(&found, i);
-                else if (w1 > 0.0 && pre + w0 + w1 > want)
-                    atomicMin(&found, i + 1);
-                if (w0 > 0.0 || w1 > 0.0)
-                    atomicMax(&last_positive, w1 > 0.0 ? i + 1 : i);
+                const int wfirst = __reduce_min_sync(0xffffffffu, mine_first), wlast = __reduce_max_sync(0xffffffffu, mine_last);
+                if (lane == 0) {
+                    if (wfirst != INT_MAX)
+                        atomicMin(&found, wfirst);
+                    if (wlast >= 0)
+                        atomicMax(&last_positive, wlast);
+                }
+                run += __shfl_sync(0xffffffffu, ws, kWarps - 1);
+                __syncthreads();   // (wscan has been read)
             }
-            __syncthreads();
             if (tid == 0)
                 out[a] = found != INT_MAX ? found : last_positive;
             break;
@@ -390,19 +407,23 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p)
 
 }  // namespace
 
-// CTAs per request: as many as there are for it, with four tiles or more to each
+// CTAs per request: two to a multiprocessor or fewer, with a tile for each warp
 int verify_cluster_size(int num_reqs, int vocab, int sms)
 {
     int c = 1;
-    while (c < kMaxCluster && 2ll * c * num_reqs <= 2 * sms && 2 * c * 4 * kTile <= vocab)
+    while (c < kMaxCluster && 2ll * c * num_reqs <= 4 * sms && 2 * c * kWarps * kMinTile / 4 <= vocab)
         c *= 2;
     return c;
 }
 
+// Values per tile: some 64 tiles to a CTA (four to a warp), between kMinTile and what the search looks at in one go
 int verify_tile(int vocab, int cluster)
 {
     const int part = (vocab + cluster - 1) / cluster;
-    return kTile * ((part + kTile * kMaxTiles - 1) / (kTile * kMaxTiles));
+    int tile = kMinTile;
+    while ((tile < kEach * kThreads && part / tile > 64) || part / tile >= kMaxTiles)
+        tile *= 2;
+    return tile;
 }
 
 cudaError_t launch_verify(const VerifyParams &p, bool bf16, cudaStream_t stream)
