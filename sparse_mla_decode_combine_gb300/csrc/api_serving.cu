@@ -62,7 +62,8 @@ struct EvictPlan {
     size_t picked, between, moved, need, offset, free_list, read, ticket, total;
 };
 
-bool evict_plan(int rows, int max_blocks, int num_blocks, int num_layers, int page, int entry_bytes, int budget, EvictPlan *pl)
+bool evict_plan(int rows, int max_blocks, int num_blocks, int num_layers, int page, int entry_bytes, int budget, int weights_width,
+                EvictPlan *pl)
 {
     if (rows < 0 || max_blocks < 0 || max_blocks > kMaxRowPages || num_blocks < 0 || num_blocks > kMaxPages || num_layers < 1 ||
         page < 1 || entry_bytes < 16 || entry_bytes % 16 != 0 || budget < 1 || (long long)max_blocks * page > INT_MAX ||
@@ -72,9 +73,9 @@ bool evict_plan(int rows, int max_blocks, int num_blocks, int num_layers, int pa
     const long long columns = (long long)num_layers * ((entry_bytes + 16383) / 16384);
     if (columns > INT_MAX / 4 || (long long)rows * columns > INT_MAX / 4)
         return false;
-    pl->shape = evict_shape(num_layers, entry_bytes, budget);
-    if ((double)rows * pl->shape.columns * pl->shape.tiles > INT_MAX / 2)
-        return false;
+    pl->shape = evict_shape(num_layers, entry_bytes, budget, weights_width);
+    if ((double)rows * ((double)pl->shape.columns * pl->shape.tiles + pl->shape.weight_tiles + pl->shape.zero_tiles) > INT_MAX / 2)
+        return false;   // (tickets)
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -87,7 +88,7 @@ bool evict_plan(int rows, int max_blocks, int num_blocks, int num_layers, int pa
     pl->need = take(4 * (size_t)rows);
     pl->offset = take(4 * (size_t)rows);
     pl->free_list = take(4 * (size_t)num_blocks);
-    pl->read = take(4 * (size_t)rows * (size_t)pl->shape.columns * (size_t)pl->shape.words);
+    pl->read = take(4 * (size_t)rows * ((size_t)pl->shape.columns * (size_t)pl->shape.words + (size_t)pl->shape.weight_words));
     pl->ticket = take(4);
     pl->total = off;
     return true;
@@ -244,7 +245,7 @@ extern "C" DSV4_API size_t dsv4_cache_evict_workspace_size(int32_t num_rows, int
                                                            int32_t budget)
 {
     EvictPlan pl;
-    return evict_plan(num_rows, max_blocks, num_blocks, num_layers, page_block, entry_bytes, budget, &pl) ? pl.total : 0;
+    return evict_plan(num_rows, max_blocks, num_blocks, num_layers, page_block, entry_bytes, budget, 0, &pl) ? pl.total : 0;
 }
 
 extern "C" DSV4_API dsv4_status dsv4_cache_evict(
@@ -257,7 +258,8 @@ extern "C" DSV4_API dsv4_status dsv4_cache_evict(
 {
     EvictPlan pl;
     if (budget < 1 || limit < budget || first < 0 || recent < 0 || first > budget || recent > budget - first ||
-        !evict_plan(num_rows, max_blocks, num_blocks, num_layers, page_block, entry_bytes, budget, &pl))
+        weights_width < 0 ||
+        !evict_plan(num_rows, max_blocks, num_blocks, num_layers, page_block, entry_bytes, budget, weights_width, &pl))
         return DSV4_ERR_INVALID_ARG;
     if ((num_layers > 1 && (layer_stride % 16 != 0 || layer_stride < (int64_t)num_blocks * page_block * entry_bytes)) ||
         (num_blocks > 0 && (cache == nullptr || !aligned(cache, 16) || ref_counts == nullptr || ref_counts_out == nullptr)))
@@ -322,5 +324,8 @@ extern "C" DSV4_API dsv4_status dsv4_cache_evict(
     p.columns = pl.shape.columns;
     p.tiles = pl.shape.tiles;
     p.words = pl.shape.words;
+    p.weight_tiles = pl.shape.weight_tiles;
+    p.weight_words = pl.shape.weight_words;
+    p.zero_tiles = pl.shape.zero_tiles;
     return launch_evict(p, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DSV4_OK : DSV4_ERR_CUDA;
 }

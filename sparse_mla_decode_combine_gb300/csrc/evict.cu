@@ -5,17 +5,22 @@
 //   kept(i) = i                             i < first
 //             first + picked[i - first]     the picked ones
 //             n - budget + i                the recent ones
-// The selection (topk.cu: radix select over the weights), a plan (pages, lengths, counts), and the moves.
+// Three launches: the selection, a plan (pages, lengths, counts), and the moves.
+//
+// The selection.  Rows of up to 16384 entries between the first and the recent ones: a CTA a row, an entry's weight as an
+// order-preserving 32-bit key in a register, and the bits of the lightest kept key found one after the other by counting (no
+// histograms, whose atomics meet at the many entries of weight 0; 64 rows of 12000 take 6 us where the radix select takes
+// 17).  Longer rows go through the radix select of topk.cu, which shares a row among eight CTAs.
 //
 // The plan.  A page of the new row whose entries all stay where they are and that is full stays, shared or not.  The other
 // pages are written: in place where the row alone holds the page, into a free page (lowest first) otherwise.  Pages past
-// the new end, and those replaced by a free one, lose a reference.
+// the new end, and those replaced by a free one, lose a reference.  One cluster, a thread a cell.
 //
 // The moves go through every layer, in place and in one pass over the bytes.  A row's new entries are cut into tiles; a
 // CTA reads the sources of a tile into registers, says so in a bitmap, waits until the tiles before it whose sources its own
 // writes would overwrite have been read (sources lie at or past their targets, so only earlier tiles can be in the way),
 // and writes.  Tiles are handed out by a ticket in that order, so those that a tile waits for were begun before it and
-// never wait for it; every wait is bounded.
+// never wait for it; every wait is bounded.  The weights go the same way, in tiles of their own.
 #include <algorithm>
 #include <climits>
 
@@ -31,6 +36,10 @@ constexpr int kMoveThreads = 256;
 constexpr int kUnroll = 8;                                  // 16-byte pieces a thread holds
 constexpr int kTileBytes = 16 * kMoveThreads * kUnroll;     // 32 KB
 constexpr int kMaxTile = 512;                               // entries
+constexpr int kWeightTile = kMoveThreads * kUnroll;         // weights
+constexpr int kZeroTile = 4 * kWeightTile;
+constexpr int kSelectThreads = 1024;
+constexpr int kSelectEach = 16;                             // keys of a thread
 constexpr long long kWaitCycles = 4000000000LL;             // about two seconds
 
 __device__ __forceinline__ void cluster_sync()
@@ -107,6 +116,100 @@ __global__ void __launch_bounds__(kMoveThreads) evict_between_kernel(const Evict
         p.between[r] = max(0, length_of(p, r, &over) - p.first - p.recent);
 }
 
+// Larger weight -> larger key; -0 and +0 share a key; NaN below every number.
+__device__ __forceinline__ uint32_t order_key(float x)
+{
+    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+    return x != x ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// The heaviest entries of a row between its first and its recent ones, of up to kEach * kSelectThreads (key u of thread t: entry
+// u * kSelectThreads + t), and the lowest that is not among them.
+template <int kEach>
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p)
+{
+    __shared__ int count[2][32];
+    __shared__ int wsum[32];
+    __shared__ uint32_t cells[32 * kEach];       // (keys above, keys equal) of each warp's 32 entries, in order; then sums
+    __shared__ int lowest;
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_wait();
+    griddep_launch();
+    bool over;
+    const int n = length_of(p, r, &over), k = p.budget - p.first - p.recent;
+    if (n <= p.limit)
+        return;
+    const int len = n - p.first - p.recent;      // > k
+    const float *w = p.weights + (int64_t)r * p.weights_stride + p.first;
+    uint32_t key[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const int i = u * kSelectThreads + tid;
+        key[u] = i < len ? order_key(__ldcg(w + i)) : 0u;
+    }
+    if (tid == 0)
+        lowest = INT_MAX;
+    // ---- the k-th largest key, from its highest bit on.  (Entries past the row count as 0, and are asked about by no candidate:
+    // it has a bit set)
+    uint32_t top = 0u;
+    int more = 0;                                // keys >= top + 1, once all bits are found: those above it
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t want = top | (1u << bit);
+        int c = 0;
+#pragma unroll
+        for (int u = 0; u < kEach; ++u)
+            c += key[u] >= want;
+        c = __reduce_add_sync(0xffffffffu, c);
+        int *slot = count[bit & 1];              // (in turn: one barrier a bit)
+        if (lane == 0)
+            slot[warp] = c;
+        __syncthreads();
+        c = __reduce_add_sync(0xffffffffu, slot[lane]);
+        if (c >= k)
+            top = want;
+        else
+            more = c;                            // (the last one that fell short: its candidate is the least key above the final `top`)
+    }
+    const int take = k - more;                   // of the keys equal to top, the first ones
+    // ---- where each warp's 32 entries begin in the list
+    uint32_t above[kEach], equal[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+        const bool in = u * kSelectThreads + tid < len;
+        above[u] = __ballot_sync(0xffffffffu, in && key[u] > top);
+        equal[u] = __ballot_sync(0xffffffffu, in && key[u] == top);
+        if (lane == 0)
+            cells[32 * u + warp] = (uint32_t)__popc(above[u]) | ((uint32_t)__popc(equal[u]) << 16);
+    }
+    __syncthreads();
+    int total;
+    const uint32_t cell = tid < 32 * kEach ? cells[tid] : 0u;
+    const uint32_t before = (uint32_t)cta_scan((int)cell, wsum, &total);   // (each half below 2^15: no carry between them)
+    if (tid < 32 * kEach)
+        cells[tid] = before;
+    __syncthreads();
+    int32_t *out = p.picked + (int64_t)r * k;
+    int left = INT_MAX;                          // the lowest entry of this thread that is not kept
+#pragma unroll
+    for (int u = kEach - 1; u >= 0; --u) {
+        const int i = u * kSelectThreads + tid;
+        const uint32_t at = cells[32 * u + warp], below = (1u << lane) - 1u;
+        const int a = (int)(at & 0xFFFFu) + __popc(above[u] & below), e = (int)(at >> 16) + __popc(equal[u] & below);
+        const bool kept = ((above[u] >> lane) & 1u) || (((equal[u] >> lane) & 1u) && e < take);
+        if (kept)
+            out[a + min(e, take)] = i;
+        else if (i < len)
+            left = i;
+    }
+    left = __reduce_min_sync(0xffffffffu, left);
+    if (lane == 0)
+        atomicMin(&lowest, left);
+    __syncthreads();
+    if (tid == 0)
+        p.moved[r] = p.first + lowest;
+}
+
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads) evict_plan_kernel(const EvictParams p)
 {
     __shared__ int wsum[32];
@@ -118,14 +221,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     griddep_wait();
     griddep_launch();   // (the moving kernel waits for this grid itself)
 
-    // ---- each row's pages as they stand, -2 for those to take, and the first entry that is written
+    // ---- each row's new length, and the first entry that is written
     for (int r = gwarp; r < p.rows; r += kPlanWarps) {
         bool over;
         const int n = length_of(p, r, &over);
         const bool cut = n > p.limit;
         const int m = cut ? p.budget : n;
         int f = n;
-        if (cut) {   // the lowest i with kept(i) != i (kept(i) - i does not fall), 32 places at a time
+        if (cut && p.selected) {
+            f = min(__ldcg(p.moved + r), m);
+        } else if (cut) {   // the lowest i with kept(i) != i (kept(i) - i does not fall), 32 places at a time
             int a = 0, z = m;
             while (a < z) {
                 const int step = (z - a + 31) / 32, i = a + lane * step;
@@ -136,27 +241,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
             }
             f = a;
         }
-        const int stay = cut ? min(f, m) / page : INT_MAX;   // pages that stay
-        const int np = pages_of(m, page);
-        const int32_t *src = p.table + (int64_t)r * p.table_stride;
-        int32_t *dst = p.table_out + (int64_t)r * p.table_out_stride;
-        int need = 0;
-        for (int j = lane; j < p.max_blocks; j += 32) {
-            int v = -1;
-            if (j < np) {
-                v = src[j];
-                if (v < 0 || v >= B) {
-                    v = -1;
-                } else if (j >= stay && p.refs[v] != 1) {
-                    v = -2;
-                    ++need;
-                }
-            }
-            dst[j] = v;
-        }
-        need = __reduce_add_sync(0xffffffffu, need);
+        __syncwarp();
         if (lane == 0) {
-            p.need[r] = need;
+            p.need[r] = 0;
             p.moved[r] = f;
             p.lens_out[r] = m;
             if (over)
@@ -166,11 +253,36 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     if (p.refs_out != p.refs)
         for (int i = gtid; i < B; i += kStep)
             p.refs_out[i] = p.refs[i];
-    const int64_t words = (int64_t)p.rows * p.columns * p.words;
+    const int64_t words = (int64_t)p.rows * (p.columns * p.words + p.weight_words);
     for (int64_t i = gtid; i < words; i += kStep)
         p.read[i] = 0u;
     if (gtid == 0)
         *p.ticket = 0;
+    cluster_sync();
+
+    // ---- the cells: pages as they stand, -2 for those to take
+    const int64_t cells = (int64_t)p.rows * p.max_blocks;
+    for (int64_t x = gtid; x < cells; x += kStep) {
+        const int r = (int)((unsigned long long)x / (unsigned)p.max_blocks), j = (int)(x - (int64_t)r * p.max_blocks);
+        bool over;
+        const int n = length_of(p, r, &over);
+        const int m = __ldcg(p.lens_out + r);
+        int v = -1;
+        if (j < pages_of(n, page)) {
+            v = p.table[(int64_t)r * p.table_stride + j];
+            if (v < 0 || v >= B) {
+                atomicOr(p.status, kStatusBadIndex);
+                v = -1;
+            }
+        }
+        if (j >= pages_of(m, page)) {
+            v = -1;
+        } else if (v >= 0 && m < n && j >= min(__ldcg(p.moved + r), m) / page && p.refs[v] != 1) {
+            v = -2;
+            atomicAdd(p.need + r, 1);
+        }
+        p.table_out[(int64_t)r * p.table_out_stride + j] = v;
+    }
     cluster_sync();
 
     // ---- where each row's new pages start in the list of free pages (every CTA the same)
@@ -183,11 +295,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
             p.offset[r] = before;
         wanted = min(wanted + total, INT_MAX / 2);
     }
-    int num_free = 0;
-    if (wanted > 0) {   // the free pages' list, lowest first
+    if (wanted > 0) {
+        // ---- the free pages' list, lowest first
         const int part = (B + kCluster - 1) / kCluster;
         const int lo = min(B, rank * part), hi = min(B, lo + part);
-        int mine = 0, before = 0;
+        int mine = 0, before = 0, num_free = 0;
         for (int i = lo + tid; i < hi; i += kPlanThreads)
             mine += p.refs[i] == 0;
         cta_scan(mine, wsum, &total);
@@ -207,100 +319,168 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
                 p.free_list[at] = i;
             before += total;
         }
-    }
-    cluster_sync();
+        cluster_sync();
 
-    // ---- the new pages into the rows; references
-    for (int r = gwarp; r < p.rows; r += kPlanWarps) {
-        bool over;
-        const int n = length_of(p, r, &over);
-        const int need = __ldcg(p.need + r), off = __ldcg(p.offset + r);
-        const int32_t *src = p.table + (int64_t)r * p.table_stride;
-        int32_t *dst = p.table_out + (int64_t)r * p.table_out_stride;
-        const int np_old = pages_of(n, page);
-        const bool cut = n > p.limit;
-        if (cut && need > 0 && need > num_free - off) {   // not enough pages: the row stays as it was
-            for (int j = lane; j < np_old; j += 32) {
-                const int v = src[j];
-                dst[j] = v >= 0 && v < B ? v : -1;
+        // ---- the new pages into the rows that take some
+        for (int r = gwarp; r < p.rows; r += kPlanWarps) {
+            const int need = __ldcg(p.need + r), off = __ldcg(p.offset + r);
+            if (need == 0)
+                continue;
+            bool over;
+            const int n = length_of(p, r, &over);
+            const int32_t *src = p.table + (int64_t)r * p.table_stride;
+            int32_t *dst = p.table_out + (int64_t)r * p.table_out_stride;
+            if (need > num_free - off) {   // not enough pages: the row stays as it was
+                for (int j = lane; j < pages_of(n, page); j += 32) {
+                    const int v = src[j];
+                    dst[j] = v >= 0 && v < B ? v : -1;
+                }
+                if (lane == 0) {
+                    p.moved[r] = n;
+                    p.lens_out[r] = n;
+                    atomicOr(p.status, kStatusBadIndex);
+                }
+                continue;
             }
-            if (lane == 0) {
-                p.moved[r] = n;
-                p.lens_out[r] = n;
-                atomicOr(p.status, kStatusBadIndex);
-            }
-        } else if (cut) {
             const int np = pages_of(p.budget, page);
             int at = off;
-            for (int j0 = 0; j0 < np_old; j0 += 32) {
+            for (int j0 = 0; j0 < np; j0 += 32) {
                 const int j = j0 + lane;
-                const bool take = j < np && dst[j] == -2;
+                const bool take = j < np && __ldcg(dst + j) == -2;
                 const unsigned m = __ballot_sync(0xffffffffu, take);
                 if (take) {
                     const int q = __ldcg(p.free_list + at + __popc(m & ((1u << lane) - 1u)));
                     dst[j] = q;
                     p.refs_out[q] = 1;
+                    atomicSub(&p.refs_out[src[j]], 1);
                 }
                 at += __popc(m);
-                const int v = j < np_old ? src[j] : -1;
-                if (v >= 0 && v < B && (take || j >= np))
-                    atomicSub(&p.refs_out[v], 1);
             }
         }
-        for (int j = lane; j < np_old; j += 32)
-            if (src[j] < 0 || src[j] >= B)
-                atomicOr(p.status, kStatusBadIndex);
+        cluster_sync();   // (rows that stay as they were have their length again)
+    }
+
+    // ---- the pages past the new ends lose a reference
+    for (int64_t x = gtid; x < cells; x += kStep) {
+        const int r = (int)((unsigned long long)x / (unsigned)p.max_blocks), j = (int)(x - (int64_t)r * p.max_blocks);
+        bool over;
+        const int n = length_of(p, r, &over), m = __ldcg(p.lens_out + r);
+        if (m < n && j >= pages_of(m, page) && j < pages_of(n, page)) {
+            const int v = p.table[(int64_t)r * p.table_stride + j];
+            if (v >= 0 && v < B)
+                atomicSub(&p.refs_out[v], 1);
+        }
     }
 }
 
-// Rows' weights (the first tickets, a row each), then the tiles: of all rows and columns the first, then the second, ..
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p)
+// Waits until the tiles [first, tile) of a bitmap have been read, by a warp; false if that took too long.
+__device__ __forceinline__ bool wait_read(const uint32_t *bits, int first, int tile, int lane)
+{
+    bool lost = false;
+    for (int w = first / 32 + lane; first < tile && w <= (tile - 1) / 32; w += 32) {
+        uint32_t want = 0xffffffffu;
+        if (w == first / 32)
+            want &= 0xffffffffu << (first & 31);
+        if (w == tile / 32)
+            want &= (1u << (tile & 31)) - 1u;
+        const long long t0 = clock64();
+        while ((*reinterpret_cast<const volatile uint32_t *>(bits + w) & want) != want)
+            if (clock64() - t0 > kWaitCycles) {
+                lost = true;
+                break;
+            }
+    }
+    __threadfence();
+    return !lost;
+}
+
+// In the order of the tickets: the rows' weights in tiles (of all rows the first, then the second, ..), what has to be zero after
+// them, then the entries' tiles (of all rows and columns the first, then the second, ..).
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p)
 {
     __shared__ int64_t src_at[kMaxTile], dst_at[kMaxTile];   // byte offsets in the layer; -1: not written
     __shared__ int next;
     const int tid = threadIdx.x;
     const int page = p.pool.page, entry = p.pool.entry_bytes;
-    const int64_t per_tile = (int64_t)p.rows * p.columns;
-    const int64_t tickets = p.rows + per_tile * p.tiles;
+    const int per_tile = p.rows * p.columns;
+    const int weight_tickets = p.rows * p.weight_tiles, zero_tickets = p.rows * p.zero_tiles;
+    const int64_t tickets = (int64_t)weight_tickets + zero_tickets + (int64_t)per_tile * p.tiles;
     const int entry_columns = (entry + p.column_bytes - 1) / p.column_bytes;
+    const bool same_weights = p.weights == p.weights_out;
     griddep_wait();
+    if (tid == 0)
+        next = atomicAdd(p.ticket, 1);
     while (true) {
-        __syncthreads();   // (`next`, src_at and dst_at are free)
-        if (tid == 0)
-            next = atomicAdd(p.ticket, 1);
         __syncthreads();
-        const int64_t ticket = next;
+        const int ticket = next;
         if (ticket >= tickets)
             return;
-        if (ticket < p.rows) {   // ---- a row's weights
-            const int r = (int)ticket;
+        __syncthreads();   // (`next` has been read; src_at and dst_at are free)
+        if (tid == 0)      // (the next one is on its way meanwhile)
+            next = atomicAdd(p.ticket, 1);
+        if (ticket < weight_tickets + zero_tickets) {
+            const bool zeros = ticket >= weight_tickets;
+            const int x = zeros ? ticket - weight_tickets : ticket, r = x % p.rows, tile = x / p.rows;
             bool over;
             const int n = length_of(p, r, &over), m = __ldcg(p.lens_out + r);
             const float *src = p.weights + (int64_t)r * p.weights_stride;
             float *dst = p.weights_out + (int64_t)r * p.weights_out_stride;
-            const int f = m < n ? __ldcg(p.moved + r) : n;
-            for (int i0 = 0; i0 < m; i0 += kUnroll * kMoveThreads) {
-                float v[kUnroll];
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int i = i0 + u * kMoveThreads + tid;
-                    v[u] = i < m ? __ldcg(src + (i < f ? i : kept(p, r, n, i))) : 0.f;
+            uint32_t *bits = p.read + (int64_t)p.rows * p.columns * p.words + (int64_t)r * p.weight_words;
+            if (zeros) {   // [m, width), once every source has been read
+                const int i0 = tile * kZeroTile, i1 = min(p.weights_width, i0 + kZeroTile);
+                bool lost = false;
+                if (i1 <= m)
+                    continue;
+                if (same_weights && m < n && i0 < n && tid < 32)
+                    lost = !wait_read(bits, __ldcg(p.moved + r) / kWeightTile, (m - 1) / kWeightTile + 1, tid);
+                if (__syncthreads_or(lost)) {
+                    if (tid == 0)
+                        atomicOr(p.status, kStatusTimeout);
+                    continue;
                 }
-                __syncthreads();   // (in place: sources lie at or past their targets)
+                for (int i = max(m, i0) + tid; i < i1; i += kMoveThreads)
+                    dst[i] = 0.f;
+                continue;
+            }
+            const int i0 = tile * kWeightTile, f = m < n ? __ldcg(p.moved + r) : n;
+            // (a row that is not cut may be longer than a tile for each of the budget's entries)
+            for (int j0 = i0; j0 < m; j0 += p.weight_tiles * kWeightTile) {
+                if (same_weights && j0 + kWeightTile <= f)
+                    continue;   // (nothing moves)
+                float v[kUnroll];
+                float sum = 0.f;
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int i = i0 + u * kMoveThreads + tid;
+                    const int i = j0 + u * kMoveThreads + tid;
+                    v[u] = i < m ? __ldcg(src + (i < f ? i : kept(p, r, n, i))) : 0.f;
+                    sum = fmaxf(sum, v[u]);
+                }
+                bool lost = false;
+                __syncthreads_or(sum > 0.f);   // (takes a value that depends on every load, so that they have all returned)
+                if (same_weights && m < n) {
+                    if (tid == 0) {
+                        __threadfence();
+                        atomicOr(bits + tile / 32, 1u << (tile & 31));
+                    }
+                    if (tid < 32)
+                        lost = !wait_read(bits, min(tile, max(f, j0 - (n - m)) / kWeightTile), tile, tid);
+                }
+                if (__syncthreads_or(lost)) {
+                    if (tid == 0)
+                        atomicOr(p.status, kStatusTimeout);
+                    continue;
+                }
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    const int i = j0 + u * kMoveThreads + tid;
                     if (i < m)
                         dst[i] = v[u];
                 }
             }
-            __syncthreads();
-            for (int i = m + tid; i < p.weights_width; i += kMoveThreads)
-                dst[i] = 0.f;
             continue;
         }
-        const int tile = (int)((ticket - p.rows) / per_tile);
-        const int unit = (int)((ticket - p.rows) % per_tile);
+        const int tile = (ticket - weight_tickets - zero_tickets) / per_tile;
+        const int unit = (ticket - weight_tickets - zero_tickets) - tile * per_tile;
         const int r = unit / p.columns, column = unit % p.columns;
         bool over;
         const int n = length_of(p, r, &over), m = __ldcg(p.lens_out + r), f = __ldcg(p.moved + r);
@@ -348,23 +528,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
         }
         // ---- the tiles before this one that may read what it writes: kept(i) - i <= n - m
         const int first = max(lo, i0 - (n - m)) / p.tile;
-        bool lost = false;
-        if (tid < 32) {
-            for (int w = first / 32 + tid; w <= (tile - 1) / 32 && first < tile; w += 32) {
-                uint32_t want = 0xffffffffu;
-                if (w == first / 32)
-                    want &= 0xffffffffu << (first & 31);
-                if (w == tile / 32)
-                    want &= (1u << (tile & 31)) - 1u;
-                const long long t0 = clock64();
-                while ((*reinterpret_cast<volatile uint32_t *>(bits + w) & want) != want)
-                    if (clock64() - t0 > kWaitCycles) {
-                        lost = true;
-                        break;
-                    }
-            }
-            __threadfence();
-        }
+        const bool lost = tid < 32 && !wait_read(bits, first, tile, tid);
         if (__syncthreads_or(lost)) {   // (never, unless a tile before this one was lost)
             if (tid == 0)
                 atomicOr(p.status, kStatusTimeout);
@@ -381,7 +545,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 }  // namespace
 
-EvictShape evict_shape(int num_layers, int entry_bytes, int budget)
+EvictShape evict_shape(int num_layers, int entry_bytes, int budget, int weights_width)
 {
     EvictShape s;
     s.column_bytes = std::min(entry_bytes, kTileBytes);
@@ -389,25 +553,35 @@ EvictShape evict_shape(int num_layers, int entry_bytes, int budget)
     s.columns = num_layers * ((entry_bytes + s.column_bytes - 1) / s.column_bytes);
     s.tiles = (budget - 1) / s.tile + 1;
     s.words = (s.tiles + 31) / 32;
+    s.weight_tiles = (budget - 1) / kWeightTile + 1;
+    s.weight_words = (s.weight_tiles + 31) / 32;
+    s.zero_tiles = weights_width / kZeroTile + 1;
     return s;
 }
 
-cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream)
+cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream)
 {
     const int picked = p.budget - p.first - p.recent;
     const int64_t most = (int64_t)p.max_blocks * p.pool.page;    // of a row's entries
     if (picked > 0 && p.rows > 0 && most > p.limit) {
         const int width = (int)(most - p.first - p.recent);
-        cudaError_t e = launch_dependent(evict_between_kernel, dim3((unsigned)(p.rows + kMoveThreads - 1) / kMoveThreads),
-                                         kMoveThreads, 0, stream, p);
+        cudaError_t e;
+        if (width <= kSelectThreads * kSelectEach) {
+            const auto kernel = width <= kSelectThreads ? evict_select_kernel<1>
+                                : width <= 4 * kSelectThreads ? evict_select_kernel<4> : evict_select_kernel<kSelectEach>;
+            e = launch_dependent(kernel, dim3((unsigned)p.rows), kSelectThreads, 0, stream, p);
+            p.selected = true;
+        } else {
+            e = launch_dependent(evict_between_kernel, dim3((unsigned)(p.rows + kMoveThreads - 1) / kMoveThreads), kMoveThreads, 0,
+                                 stream, p);
+            if (e == cudaSuccess)
+                e = launch_topk_select(p.weights + p.first, p.weights_stride, width, p.between, p.rows, picked, p.picked, picked,
+                                       nullptr, topk_cluster_size(p.rows, width, sms), stream);
+            if (e != cudaSuccess)
+                (void)cudaGetLastError();
+        }
         if (e != cudaSuccess)
             return e;
-        e = launch_topk_select(p.weights + p.first, p.weights_stride, width, p.between, p.rows, picked, p.picked, picked, nullptr,
-                               topk_cluster_size(p.rows, width, sms), stream);
-        if (e != cudaSuccess) {
-            (void)cudaGetLastError();
-            return e;
-        }
     }
     const cudaError_t e = launch_dependent(evict_plan_kernel, dim3(kCluster), kPlanThreads, 0, stream, p);
     if (e != cudaSuccess)

@@ -87,18 +87,22 @@ struct EvictParams {
     int32_t *need;             // [rows] pages to take
     int32_t *offset;           // [rows] exclusive sums of need
     int32_t *free_list;        // [num_blocks]
-    uint32_t *read;            // [rows, columns, words] bit i: the entries that tile i writes have been read
+    uint32_t *read;            // [rows, columns, words] bit i: the entries that tile i writes have been read; then
+                               // [rows, weight_words] the same of the weights' tiles
     int32_t words;             // words per (row, column)
     int32_t tile;              // entries per tile
     int32_t column_bytes;      // bytes of an entry that a column covers (entries larger than a tile have several)
     int32_t columns;           // layers * columns of an entry
     int32_t tiles;             // tiles per (row, column)
+    int32_t weight_tiles, weight_words;   // tiles of a row's kept weights, and words for them
+    int32_t zero_tiles;        // tiles of a row of weights_out that may have to be set to zero
     int32_t *ticket;           // [1]
+    bool selected;             // the selection wrote `moved`
 };
 struct EvictShape {
-    int32_t tile, column_bytes, columns, tiles, words;
+    int32_t tile, column_bytes, columns, tiles, words, weight_tiles, weight_words, zero_tiles;
 };
-EvictShape evict_shape(int num_layers, int entry_bytes, int budget);
-cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t stream);
+EvictShape evict_shape(int num_layers, int entry_bytes, int budget, int weights_width);
+cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream);
 
 }  // namespace dsv4

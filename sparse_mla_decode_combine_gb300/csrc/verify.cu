@@ -33,7 +33,7 @@ namespace {
 constexpr int kThreads = 256;        // four CTAs to a multiprocessor
 constexpr int kCtasPerSm = 4;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 6;
 constexpr int kDeep = 16;            // values that a thread has in flight
 constexpr int kMinTile = 256;        // values whose sum is held for the search
 constexpr int kMaxTiles = 1024;      // of a CTA
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
             if (warp == 0) {
                 const Sum t = lane < C ? totals[lane] : Sum{0.f, 0.f};
                 Sum before;
-                const Sum sum = scan32(t, lane, kMaxCluster, before);
-                const Sum w = times(shfl(sum, kMaxCluster - 1), p.uniform[row0 + k]);
+                const Sum sum = scan32(t, lane, 8, before);
+                const Sum w = times(shfl(sum, 7), p.uniform[row0 + k]);
                 const unsigned over = __ballot_sync(0xffffffffu, t.hi > 0.f && above(sum, w)), some = __ballot_sync(0xffffffffu, t.hi > 0.f);
                 const int who = over != 0u ? __ffs(over) - 1 : some != 0u ? 31 - __clz(some) : -1;
                 if (who == rank) {
@@ -466,8 +466,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
 
 }  // namespace
 
-// CTAs per request: as many as are there at the same time, with kDeep values or more to a thread (160 requests of 128000: 320
-// CTAs of 512 threads, where 304 are there, took 42 us)
+// CTAs per request: as many as are there at the same time, up to kMaxCluster, with kDeep values or more to a thread.  In us
+// with 1, 2, 3, 4, 6 and 8: 48 mixed requests of 100277 35, 25, 19, 19, 16, 20; 160 of 128000 34, 28, 24, 32, 29, 52; 256 of
+// 151937 80, 60, 65, 62, 65, 67.
 int verify_cluster_size(int num_reqs, int vocab, int sms)
 {
     const int fit = std::min(kCtasPerSm * sms / std::max(1, num_reqs), vocab / (kDeep * kThreads));
