@@ -7,10 +7,12 @@
 //             n - budget + i                the recent ones
 // Three launches: the selection, a plan (pages, lengths, counts), and the moves.
 //
-// The selection.  Rows of up to 16384 entries between the first and the recent ones: a CTA a row, an entry's weight as an
-// order-preserving 32-bit key in a register, and the bits of the lightest kept key found one after the other by counting (no
-// histograms, whose atomics meet at the many entries of weight 0; 64 rows of 12000 take 6 us where the radix select takes
-// 17).  Longer rows go through the radix select of topk.cu, which shares a row among eight CTAs.
+// The selection.  Rows of up to 4096 entries between the first and the recent ones: a CTA a row, an entry's weight as an
+// order-preserving 32-bit key in a register.  The lightest kept key is found two bits at a time by counting (no histograms,
+// whose atomics meet at the many entries of weight 0), from what is known of weights: whether it is 0 is asked first, and the
+// search ends at a threshold that exactly the wanted number of keys reaches.  Longer rows go through the radix select of
+// topk.cu, with a launch ahead of it that counts the entries.  In us, counting against that: 4 rows of 700 7 / 15, 32 of 2500 10 /
+// 14, 64 of 12000 30 / 19 (two CTAs a row), one of 131000 36 / 25 (eight).
 //
 // The plan.  A page of the new row whose entries all stay where they are and that is full stays, shared or not.  The other
 // pages are written: in place where the row alone holds the page, into a free page (lowest first) otherwise.  Pages past
@@ -39,7 +41,7 @@ constexpr int kMaxTile = 512;                               // entries
 constexpr int kWeightTile = kMoveThreads * kUnroll;         // weights
 constexpr int kZeroTile = 4 * kWeightTile;
 constexpr int kSelectThreads = 1024;
-constexpr int kSelectEach = 16;                             // keys of a thread
+constexpr int kSelectEach = 4;                              // keys of a thread
 constexpr long long kWaitCycles = 4000000000LL;             // about two seconds
 
 __device__ __forceinline__ void cluster_sync()
@@ -128,7 +130,7 @@ __device__ __forceinline__ uint32_t order_key(float x)
 template <int kEach>
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p)
 {
-    __shared__ int count[2][32];
+    __shared__ uint2 count[2][32];
     __shared__ int wsum[32];
     __shared__ uint32_t cells[32 * kEach];       // (keys above, keys equal) of each warp's 32 entries, in order; then sums
     __shared__ int lowest;
@@ -145,31 +147,78 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
         const int i = u * kSelectThreads + tid;
-        key[u] = i < len ? order_key(__ldcg(w + i)) : 0u;
+        key[u] = i < len ? order_key(__ldcg(w + i)) : 0u;   // (0 where there is no entry: no threshold is that low)
     }
     if (tid == 0)
         lowest = INT_MAX;
-    // ---- the k-th largest key, from its highest bit on.  (Entries past the row count as 0, and are asked about by no candidate:
-    // it has a bit set)
+    int turn = 0;
+    // the threads' sums of (x's halves, y)
+    auto sum_all = [&](uint32_t x, uint32_t y) {
+        x = __reduce_add_sync(0xffffffffu, x);
+        y = __reduce_add_sync(0xffffffffu, y);
+        uint2 *slot = count[turn++ & 1];         // (two places in turn: one barrier a round)
+        if (lane == 0)
+            slot[warp] = make_uint2(x, y);
+        __syncthreads();
+        x = __reduce_add_sync(0xffffffffu, slot[lane].x);
+        return make_int3((int)(x & 0xFFFFu), (int)(x >> 16), (int)__reduce_add_sync(0xffffffffu, slot[lane].y));
+    };
+    // ---- the k-th largest key `top`, and how many keys are larger
+    constexpr uint32_t kZero = 0x80000000u;      // of a weight of 0
     uint32_t top = 0u;
-    int more = 0;                                // keys >= top + 1, once all bits are found: those above it
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t want = top | (1u << bit);
-        int c = 0;
+    int more;
+    {
+        uint32_t c = 0u;
 #pragma unroll
         for (int u = 0; u < kEach; ++u)
-            c += key[u] >= want;
-        c = __reduce_add_sync(0xffffffffu, c);
-        int *slot = count[bit & 1];              // (in turn: one barrier a bit)
-        if (lane == 0)
-            slot[warp] = c;
-        __syncthreads();
-        c = __reduce_add_sync(0xffffffffu, slot[lane]);
-        if (c >= k)
-            top = want;
-        else
-            more = c;                            // (the last one that fell short: its candidate is the least key above the final `top`)
+            c += (key[u] > kZero ? 1u : 0u) + (key[u] >= kZero ? 0x10000u : 0u);
+        const int3 s = sum_all(c, 0u);
+        const int gt = s.x, ge = s.y;
+        bool done = false;
+        if (ge >= k) {
+            top = kZero;
+            more = gt;
+            done = gt < k;
+        } else {
+            more = ge;
+        }
+#pragma unroll 1
+        for (int s0 = 29; !done; s0 -= 2) {      // bits s0 + 1 and s0 (the last round: bit 0 alone)
+            const uint32_t step = s0 >= 0 ? 1u << s0 : 1u;
+            const uint32_t t1 = top + step, t2 = s0 >= 0 ? t1 + step : ~0u, t3 = s0 >= 0 ? t2 + step : ~0u;
+            uint32_t x = 0u, y = 0u;
+#pragma unroll
+            for (int u = 0; u < kEach; ++u) {
+                x += (key[u] >= t1 ? 1u : 0u) + (key[u] >= t2 ? 0x10000u : 0u);
+                y += key[u] >= t3 ? 1u : 0u;
+            }
+            const int3 sum = sum_all(x, y);
+            const int c1 = sum.x, c2 = sum.y, c3 = sum.z;
+            const bool one = s0 < 0;
+            uint32_t next = top;
+            int c = -1;                          // keys that reach `next`
+            if (!one && c3 >= k) {
+                next = t3;
+                c = c3;
+            } else if (!one && c2 >= k) {
+                next = t2;
+                c = c2;
+                more = c3;
+            } else if (c1 >= k) {
+                next = t1;
+                c = c1;
+                more = one ? more : c2;
+            } else {
+                more = c1;
+            }
+            top = next;
+            done = one;
+            if (c == k) {                        // exactly the keys that reach it
+                top = next - 1u;
+                more = k;
+                done = true;
+            }
+        }
     }
     const int take = k - more;                   // of the keys equal to top, the first ones
     // ---- where each warp's 32 entries begin in the list
@@ -567,9 +616,8 @@ cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream)
         const int width = (int)(most - p.first - p.recent);
         cudaError_t e;
         if (width <= kSelectThreads * kSelectEach) {
-            const auto kernel = width <= kSelectThreads ? evict_select_kernel<1>
-                                : width <= 4 * kSelectThreads ? evict_select_kernel<4> : evict_select_kernel<kSelectEach>;
-            e = launch_dependent(kernel, dim3((unsigned)p.rows), kSelectThreads, 0, stream, p);
+            e = launch_dependent(width <= kSelectThreads ? evict_select_kernel<1> : evict_select_kernel<kSelectEach>,
+                                 dim3((unsigned)p.rows), kSelectThreads, 0, stream, p);
             p.selected = true;
         } else {
             e = launch_dependent(evict_between_kernel, dim3((unsigned)(p.rows + kMoveThreads - 1) / kMoveThreads), kMoveThreads, 0,

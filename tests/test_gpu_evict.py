@@ -117,6 +117,32 @@ def test_long_rows_in_place(n, budget, first, recent):
         check(*pool(seed, [n, n - 777, budget + 1], page=16, entry=400, layers=2), budget, None, first, recent, in_place=seed == 1)
 
 
+@pytest.mark.parametrize("n,budget,first,recent", [(70001, 30000, 3, 500), (131072 + 40, 131000, 17, 23), (131072 + 64, 20000, 0, 1),
+                                                   (150001, 60000, 5, 999)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_rows_of_many_entries(n, budget, first, recent, ties):
+    need_gpu()
+    cache, table, lens, refs, w = pool(budget, [n, 100, n - 5000], page=64, entry=16, layers=1, ties=ties)
+    if ties:
+        w[:, ::3] = 0
+    check(cache, table, lens, refs, w, budget, None, first, recent, in_place=ties)
+
+
+def test_thresholds_of_every_kind():
+    need_gpu()
+    cache, table, lens, refs, w = pool(12, [2000] * 6, page=16, entry=16, layers=1)
+    i = np.arange(w.shape[1])
+    w[0] = np.where(i % 2, 1.0, np.nextafter(np.float32(1), np.float32(2)))       # keys that differ in their last bit
+    w[1] = -1.0 - i                                                               # below 0
+    w[2] = np.where(i < 1500, 0.0, 5.0)                                           # 0 is the threshold
+    w[3] = np.where(i < 300, np.inf, np.where(i < 500, -np.inf, np.nan))          # NaN is the threshold
+    w[4] = np.float32(1e-45) * (i % 7)                                            # subnormal ones
+    w[5] = np.finfo(np.float32).max
+    w = w.astype(np.float32)
+    for budget in (1000, 777, 1999):
+        check(cache, table, lens, refs, w.copy(), budget, None, 2, 5)
+
+
 def test_one_entry_leaves_a_long_row():
     need_gpu()
     cache, table, lens, refs, w = pool(3, [6000, 6000, 6000], page=64, entry=64, layers=3)
