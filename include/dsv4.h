@@ -620,8 +620,8 @@ DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_st
  *   target_probs     fp32, or BF16 when probs_bf16 != 0, [num_rows, vocab], row stride target_stride (>= vocab).
  *   draft_probs      the same type, [num_drafts, vocab], row stride draft_stride; or NULL.
  *   vocab            1 .. 2^22.
- *   draft_tokens     int32 [num_drafts]; one outside [0, vocab) is turned down and sets DSV4_ERR_BAD_INDEX in the device
- *                    status word.
+ *   draft_tokens     int32 [num_drafts]; one outside [0, vocab) does not stand, and wherever it is among its request's
+ *                    drafts sets DSV4_ERR_BAD_INDEX in the device status word.
  *   query_start_loc  int32 [num_reqs + 1], increasing: every request has a row or more; num_reqs <= 2^24.
  *   uniform          fp32 [num_rows] in [0, 1).
  *   greedy           uint8 [num_reqs] or NULL (none is).

@@ -53,6 +53,7 @@ def verify(target, draft, tokens, start, uniform, greedy=None, seq=None, width=N
             may[b] = {-1}
             continue
         point = -1
+        bad += int(np.sum((np.asarray(tokens[d0:d0 + k]) < 0) | (np.asarray(tokens[d0:d0 + k]) >= V)))
         while a < k:
             d, p = int(tokens[d0 + a]), np.asarray(target[r0 + a], dtype=np.float64)
             if greedy is not None and greedy[b]:
@@ -61,7 +62,7 @@ def verify(target, draft, tokens, start, uniform, greedy=None, seq=None, width=N
                 qd = 1.0 if draft is None else float(draft[d0 + a][d])
                 ok = float(uniform[r0 + a]) * qd < p[d]
             else:
-                ok, bad = False, bad + 1
+                ok = False
             if not ok:
                 break
             out[b, a] = d

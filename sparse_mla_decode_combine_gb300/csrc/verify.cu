@@ -290,7 +290,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
         }
     } else {
         // ---- the drafts that stand, by every warp
-        bool bad = false;
         for (int j0 = 0; j0 < k; j0 += 32) {
             const int j = j0 + lane;
             bool good = false;
@@ -300,8 +299,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                     const float x = value(target[(int64_t)(row0 + j) * p.target_stride + d]);
                     const float y = draft != nullptr ? value(draft[(int64_t)(d0 + j) * p.draft_stride + d]) : 1.f;
                     good = product_below(p.uniform[row0 + j], y, x);
-                } else {
-                    bad = true;
                 }
             }
             const unsigned m = __ballot_sync(0xffffffffu, good);
@@ -309,8 +306,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
             if (m != 0xffffffffu)
                 break;
         }
-        if (bad)
-            atomicOr(p.status, kStatusBadIndex);
         Row<T> row;
         row.p = target + (int64_t)(row0 + a) * p.target_stride;
         row.q = a < k && draft != nullptr ? draft + (int64_t)(d0 + a) * p.draft_stride : nullptr;
@@ -453,9 +448,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
         }
     }
     if (rank == 0) {
-        for (int j = tid; j < p.out_width; j += kThreads)
+        for (int j = tid; j < p.out_width; j += kThreads) {
+            const int d = j < k ? p.tokens[d0 + j] : -1;
             if (j != a)
-                out[j] = j < a ? p.tokens[d0 + j] : -1;
+                out[j] = j < a ? d : -1;
+            if (j < k && (d < 0 || d >= V))
+                atomicOr(p.status, kStatusBadIndex);
+        }
         if (tid == 0) {
             p.accepted[b] = a;
             if (p.seq != nullptr)

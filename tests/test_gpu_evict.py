@@ -251,6 +251,48 @@ def test_graph_replays_evict_again():
     pkg.check(pkg.dsv4_get_device_status())
 
 
+def test_two_streams_and_other_work_at_once():
+    need_gpu()
+    # tiles wait for one another while other kernels take multiprocessors
+    pools = [pool(20 + i, [20000, 9000, 5000], page=64, entry=400, layers=2) for i in range(2)]
+    want = [serving.evict(*c, 3000, 3000, 4, 100) for c in pools]
+    state = [[dev(a) for a in c] for c in pools]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    a = torch.randn(2048, 2048, device="cuda").bfloat16()
+    torch.cuda.synchronize()
+    for turn in range(5):
+        got = []
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                c = state[i][0].clone()
+                got.append((c, pkg.cache_evict(c, *state[i][1:], 3000, None, 4, 100)))
+        with torch.cuda.stream(streams[2]):
+            for _ in range(20):
+                a @ a
+        torch.cuda.synchronize()
+        for (c, rest), ref in zip(got, want):
+            assert np.array_equal(c.cpu().numpy(), ref[0])
+            assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(rest, ref[1:]))
+    pkg.check(pkg.dsv4_get_device_status())
+
+
+def test_rows_and_pages_given_back_are_taken_by_a_later_call():
+    need_gpu()
+    cache, table, lens, refs, w = pool(13, [40, 40, 36, 40], shared=5, spare=14)
+    args = [cache, table, lens, refs, w]
+    d = [dev(a) for a in args]
+    for budget in (23, 17, 9, 3):
+        want = serving.evict(*args, budget, budget, 1, 2)
+        assert want[5] == 0
+        d[1:] = list(pkg.cache_evict(*d, budget, None, 1, 2))
+        torch.cuda.synchronize()
+        assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(d, want))
+        args = list(want[:5])
+        live = args[1][args[1] >= 0]
+        assert np.array_equal(np.bincount(live, minlength=len(refs)), args[3])
+    pkg.check(pkg.dsv4_get_device_status())
+
+
 def test_refusals():
     need_gpu()
     cache, table, lens, refs, w = (dev(a) for a in pool(11, [30, 20]))

@@ -118,6 +118,77 @@ def test_many_tokens_of_one_row():
     check(w)
 
 
+def test_hundreds_of_tokens_of_few_rows():
+    need_gpu()
+    w = synth.make_workload(name="w", seed=10, heads=16, req_seq_lens=[500, 260, 300], tokens_per_req=110, topk_width=12, window=9,
+                            sink=False)
+    order = np.random.default_rng(1).permutation(w.num_tokens)
+    check(dataclasses.replace(w, q=w.q[order], req_idx=w.req_idx[order], topk_idx=w.topk_idx[order], seq_lens=w.seq_lens[order]))
+
+
+def test_more_tokens_than_threads():
+    need_gpu()
+    w = synth.make_workload(name="w", seed=11, heads=16, req_seq_lens=np.random.default_rng(2).integers(0, 90, 1900), topk_width=6,
+                            window=3, sink=False, page=16)
+    check(w)
+    check(to_fp4(w))
+
+
+@pytest.mark.parametrize("entry", [400, 656])
+def test_a_cache_past_four_gigabytes(entry):
+    need_gpu()
+    # a few pages at both ends of a pool of 4.7 GB
+    w = synth.make_workload(name="w", seed=18, heads=16, req_seq_lens=[700, 300], topk_width=100, window=64, sink=False)
+    w = w if entry == 656 else to_fp4(w)
+    lse, table = lse_of(w), start_table(w)
+    n, B = len(w.kv_cache), 4_700_000_000 // (64 * entry)
+    to = np.where(np.arange(n) % 2, np.arange(n), B - 1 - np.arange(n)).astype(np.int32)
+    pool = torch.zeros(B, 64, entry, dtype=torch.uint8, device="cuda")
+    pool[torch.from_numpy(to.astype(np.int64)).cuda()] = torch.from_numpy(w.kv_cache).cuda()
+    t = np.where(w.block_table >= 0, to[w.block_table], -1).astype(np.int32)
+    far, status = run(dataclasses.replace(w, block_table=t), lse, table, kv_cache=pool)
+    assert status == pkg.DSV4_OK and np.array_equal(far, run(w, lse, table)[0])
+
+
+def test_beside_a_decode_and_matrix_products_on_other_streams():
+    need_gpu()
+    ws = both(synth.make_workload(name="w", seed=19, heads=128, req_seq_lens=[900, 300, 512, 77] * 20, topk_width=200, window=64,
+                                  sink=False))
+    ds = [synth.to_device(w, "cuda") for w in ws]
+    decode = [pkg.sparse_mla_decode, pkg.sparse_mla_decode_fp4]
+    lses = [f(**d)[1] for f, d in zip(decode, ds)]
+    a = torch.randn(1024, 1024, device="cuda").bfloat16()
+    spaces = [pkg.workspace_for_key_weights(w.num_tokens, 128, 200, 64) for w in ws]
+    tables = [torch.zeros(len(w.block_table), w.block_table.shape[1] * w.page, device="cuda") for w in ws]
+
+    def weights(i, t):
+        args = {n: v for n, v in ds[i].items() if n != "sink"}
+        pkg.check(pkg.dsv4_sparse_mla_key_weights(lse=lses[i], weights=t, workspace=spaces[i], **args))
+    want = []
+    for i in range(2):
+        t = tables[i].clone()
+        weights(i, t)
+        want.append(t)
+    outs, product = [f(**d)[0] for f, d in zip(decode, ds)], a @ a
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    got, other = [], []
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                t = torch.zeros_like(tables[i])
+                weights(i, t)
+                got.append((i, t))
+        with torch.cuda.stream(streams[2]):
+            other.append([f(**d)[0] for f, d in zip(decode, ds)])
+        with torch.cuda.stream(streams[3]):
+            other.append(a @ a)
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, want[i]) for i, t in got)
+    assert all(torch.equal(o, product) if torch.is_tensor(o) else all(map(torch.equal, o, outs)) for o in other)
+    pkg.check(pkg.dsv4_get_device_status())
+
+
 def test_bad_pages_rows_and_lengths():
     need_gpu()
     w = synth.make_workload(name="w", seed=5, heads=16, req_seq_lens=[900, 300, 512, 77], topk_width=100, window=64, sink=False)

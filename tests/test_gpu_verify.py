@@ -194,6 +194,71 @@ def test_bad_requests_and_tokens_are_flagged():
     check(dict(c, start=c["start"] + 1000))                                # only differences count
 
 
+def test_bad_tokens_after_the_last_accepted_one_are_flagged():
+    need_gpu()
+    for greedy in (None, np.ones(2, np.uint8)):
+        c = dict(batch(14, [3, 40], 300), greedy=greedy)
+        c["uniform"][:] = 0.999999                   # (drafts stand only where the target likes them more)
+        c["tokens"][-1] = 300
+        check(c)
+
+
+@pytest.mark.parametrize("u", [1.0, 1.5, -1.0, np.nan, np.inf])
+def test_numbers_outside_their_range_draw_some_token(u):
+    need_gpu()
+    for V, R in ((50, 3), (20000, 1)):
+        c = batch(15, [0] * R, V)
+        out, acc = torch.empty(R, 1, dtype=torch.int32, device="cuda"), torch.empty(R, dtype=torch.int32, device="cuda")
+        uniform = torch.full((R,), u, device="cuda")
+        pkg.check(pkg.dsv4_verify_drafts(dev(c["target"]), None, dev(c["tokens"]), dev(c["start"]), uniform, out, acc))
+        assert bool(((out >= 0) & (out < V)).all()) and acc.tolist() == [0] * R
+        if u >= 1.0:
+            assert bool((out == V - 1).all())        # the last one with weight
+
+
+@pytest.mark.parametrize("R", [1, 500])
+def test_the_widest_vocabulary(R):
+    need_gpu()
+    # one request of 2^22 values; with 500 requests (the others have no rows, and are flagged) one CTA sums them all
+    V = 1 << 22
+    rng = np.random.default_rng(R)
+    p = torch.from_numpy(rng.random((2, V)).astype(np.float32)).cuda()
+    q = torch.from_numpy(rng.random((1, V)).astype(np.float32)).cuda()
+    start = torch.full((R + 1,), 2, dtype=torch.int32, device="cuda")
+    start[0] = 0
+    for u in (0.0, 0.37, 0.999):
+        p[0, 17], q[0, 17] = 0.0, 0.5                # turned down
+        uniform = torch.tensor([0.5, u], device="cuda")
+        out, acc = torch.full((R, 2), 9, dtype=torch.int32, device="cuda"), torch.empty(R, dtype=torch.int32, device="cuda")
+        tok = torch.tensor([17], dtype=torch.int32, device="cuda")
+        pkg.check(pkg.dsv4_verify_drafts(p, q, tok, start, uniform, out, acc))
+        pkg.dsv4_get_device_status()
+        _, _, _, may, _ = serving.verify(p.cpu().numpy(), q.cpu().numpy(), [17], [0, 2], uniform.cpu().numpy(), width=2)
+        assert int(out[0, 0]) in may[0] and int(out[0, 1]) == -1 and bool((out[1:] == -1).all())
+        p[0, 17] = 1.0                               # accepted: 0.5 * 0.5 < 1
+        pkg.check(pkg.dsv4_verify_drafts(p, q, tok, start, uniform, out, acc))
+        pkg.dsv4_get_device_status()
+        _, _, _, may, _ = serving.verify(p.cpu().numpy(), q.cpu().numpy(), [17], [0, 2], uniform.cpu().numpy(), width=2)
+        assert int(out[0, 0]) == 17 and int(out[0, 1]) in may[0]
+
+
+def test_rows_past_two_gigabytes():
+    need_gpu()
+    V, N = 100000, 11000                             # 4.4 GB of float32
+    p = torch.zeros(N, V, device="cuda")
+    at = torch.randint(0, V, (N,), device="cuda")
+    p[torch.arange(N, device="cuda"), at] = 0.25
+    start = torch.tensor([0, N - 3, N - 2, N], dtype=torch.int32, device="cuda")
+    tok = torch.cat([at[:N - 4], at[N - 2:N - 1]]).int()
+    out, acc = torch.empty(3, N, dtype=torch.int32, device="cuda"), torch.empty(3, dtype=torch.int32, device="cuda")
+    pkg.check(pkg.dsv4_verify_drafts(p, None, tok, start, torch.full((N,), 0.2, device="cuda"), out, acc))
+    assert acc.tolist() == [N - 4, 0, 1]
+    want = torch.full((3, N), -1, dtype=torch.int32, device="cuda")
+    want[0, :N - 3], want[1, 0], want[2, :2] = at[:N - 3].int(), at[N - 3], at[N - 2:].int()
+    assert torch.equal(out, want)
+    pkg.check(pkg.dsv4_get_device_status())
+
+
 def test_empty_calls_and_single_tokens():
     need_gpu()
     e = torch.empty
