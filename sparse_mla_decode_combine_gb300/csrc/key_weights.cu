@@ -162,29 +162,29 @@ __device__ __forceinline__ float scale_of(uint32_t se)   // 2^(se - 127); 255: N
     return se == 255u ? __int_as_float(0x7FC00000) : se == 0u ? __int_as_float(0x00400000) : __int_as_float((int)(se << 23));
 }
 
-// 16 E4M3 codes times 2^(se - 127) -> 16 BF16 values as pairs.  A code s.eeee.mmm placed as the BF16 pattern
-// s.0000eeee.mmm0000 is its value times 2^-120; one multiply by 2^(se - 7) gives the value.  Pieces with the NaN code, or a scale
-// past 2^7, take the hardware's conversion.
-__device__ __forceinline__ void dequant16_e4m3(const uint4 &v, uint32_t se, uint32_t *o)
+// 64 E4M3 codes times 2^(se - 127) -> 64 BF16 values as pairs.  A code s.eeee.mmm placed as the BF16 pattern
+// s.0000eeee.mmm0000 is its value times 2^-120; one multiply by 2^(se - 7) gives the value.  The sign goes from bit 11 to bit 15
+// by adding 15 times it: multiplications, since the logic pipe (shifts and masks: five operations a pair) was what the
+// conversion waited for.  Chunks with the NaN code, or a scale past 2^7, take the hardware's conversion.
+__device__ __forceinline__ void dequant64_e4m3(const uint4 (&v)[4], uint32_t se, uint32_t (&o)[32])
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t odd = se > 134u ? 1u : 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        odd |= ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // a byte with magnitude 0x7F
-    if (odd != 0u) {
-        const float sc = scale_of(se);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o[i] = convert2_e4m3(w[i >> 1] >> (16 * (i & 1)), sc);
-        return;
-    }
-    uint32_t f = (se + 120u) << 7;
+    uint32_t f = (min(se, 134u) + 120u) << 7, odd = 0u;
     f |= f << 16;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t t = __byte_perm(w[i >> 1], 0u, i & 1 ? 0x3424 : 0x1404);   // [0, c, 0, c']
-        o[i] = mul_bf16x2((t & 0x80008000u) | ((t & 0x7F007F00u) >> 4), f);
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t w = (i & 6) == 0 ? v[i >> 3].x : (i & 6) == 2 ? v[i >> 3].y : (i & 6) == 4 ? v[i >> 3].z : v[i >> 3].w;
+        const uint32_t t = __byte_perm(w, 0u, i & 1 ? 0x4342 : 0x4140) * 16u;   // [c, 0, c', 0] << 4
+        const uint32_t x = (t & 0x08000800u) * 15u + t;
+        odd |= x + 0x00100010u;                                                 // (bit 11 of a half: its magnitude was 0x7F)
+        o[i] = mul_bf16x2(x, f);
+    }
+    if (se > 134u || (odd & 0x08000800u) != 0u) {
+        const float sc = scale_of(se);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t w = (i & 6) == 0 ? v[i >> 3].x : (i & 6) == 2 ? v[i >> 3].y : (i & 6) == 4 ? v[i >> 3].z : v[i >> 3].w;
+            o[i] = convert2_e4m3(w >> (16 * (i & 1)), sc);
+        }
     }
 }
 
@@ -475,35 +475,25 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                 prefetch_l2(q + 128 * i);
         };
         for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
+            if (n > 0)   // the products of the last segment are done with its Q
+                mbar_wait(bar_dfull + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
             {
                 const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)seg.t * p.q_token_stride);
-                constexpr int kQLoads = (kH * (kDim / 8) + 32 * kKeyWarps - 1) / (32 * kKeyWarps);
-                constexpr int kBatch = kQLoads < 9 ? kQLoads : 9;
-#pragma unroll 1
-                for (int j0 = 0; j0 < kQLoads; j0 += kBatch) {
-                    uint4 v[kBatch];
-#pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        const int i = 32 * kKeyWarps * (j0 + j) + 32 * kw + lane;
-                        if (i < kH * (kDim / 8))
-                            v[j] = __ldca(q + i);
-                    }
-                    if (n > 0 && j0 == 0)   // the products of the last segment are done with its Q
-                        mbar_wait(bar_dfull + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
-#pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        const int i = 32 * kKeyWarps * (j0 + j) + 32 * kw + lane;
-                        if (i >= kH * (kDim / 8))
-                            break;
-                        const int h = i / (kDim / 8), c = i % (kDim / 8);
-                        const uint32_t a = sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
-                        if (kFour && c < kLatent / 8)   // (the order of the latent dims that dequant32_e2m1 gives)
-                            st_shared_v4(a, __byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
-                                         __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
-                        else
-                            st_shared_v4(a, v[j].x, v[j].y, v[j].z, v[j].w);
-                    }
-                }
+                auto place = [&](int i) {   // of the i-th 16 bytes of Q
+                    const int h = i / (kDim / 8), c = i % (kDim / 8);
+                    return sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
+                };
+                for (int i = 32 * kw + lane; i < kH * (kDim / 8); i += 32 * kKeyWarps)
+                    copy16(place(i), q + i);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                if (kFour)   // (each thread its own pieces: the order of the latent dims that dequant32_e2m1 gives)
+                    for (int i = 32 * kw + lane; i < kH * (kDim / 8); i += 32 * kKeyWarps)
+                        if (i % (kDim / 8) < kLatent / 8) {
+                            const uint32_t a = place(i);
+                            const uint4 v = lds16(a);
+                            st_shared_v4(a, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                         __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+                        }
             }
             fence_async_smem();
             __syncwarp();
@@ -538,9 +528,11 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                     dequant32_e2m1(v1, s1, o + 16);
                 } else {
                     const uint32_t se = lds8(e + kScaleOffset + (c >> 1));
+                    uint4 v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        dequant16_e4m3(lds16(e + 64 * c + 16 * i), se, o + 8 * i);
+                        v[i] = lds16(e + 64 * c + 16 * i);
+                    dequant64_e4m3(v, se, o);
                 }
                 __syncwarp();
                 if (lane == 0) {
