@@ -20,6 +20,7 @@
 //
 // Tokens of one row are added in ascending order, one rounding each, so the result does not depend on timing: the first
 // token with keys that names a row is added by the epilogue, the others by a second kernel.
+#include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -624,7 +625,8 @@ cudaError_t launch(const KeyWeightsParams &p, int sms, cudaStream_t stream)
     const cudaError_t e = set_smem_once(reinterpret_cast<const void *>(kernel), Shape<kH, kFour>::kSmem, (AttrSlot)kSlot);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(kernel, dim3((unsigned)sms), kThreads, Shape<kH, kFour>::kSmem, stream, p);
+    const long long blocks = (long long)p.num_tokens * ((p.list_w + kBK - 1) / kBK);   // at most
+    return launch_dependent(kernel, dim3((unsigned)std::min<long long>(sms, blocks)), kThreads, Shape<kH, kFour>::kSmem, stream, p);
 }
 
 template <bool kFour>
