@@ -22,7 +22,8 @@ streams double-buffered against the calls (as a serving loop overlaps them), 64 
 Other ops, timed the same way on their own workloads: --op topk-select (top-k selection from
 indexer scores), --op combine-compressed (the compressed-region combine), --op
 qnorm-rope-insert (fused query norm/RoPE and FP8 KV insert), --op fp4-and-pages (the 4-bit cache's
-decode and insert and the page operators, every case of perf/operators.py and five more shapes of the decode).
+decode and insert and the page operators, every case of perf/operators.py and five more shapes of the decode), --op
+between-steps (draft verification, key weights and eviction: every case of perf/more_operators.py).
 N > 1: every rank decodes its own batch on its own GPU (no data-path
 collective; weak scaling).
 
@@ -70,7 +71,7 @@ def parse_args():
     ap.add_argument("--no-per-workload", action="store_true",
                     help="time only --workload (the default line also times all five decode workloads)")
     ap.add_argument("--op", choices=["decode", "combine-compressed", "topk-select", "qnorm-rope-insert", "mtp-union",
-                                     "fp4-and-pages"],
+                                     "fp4-and-pages", "between-steps"],
                     default="decode", help="decode (the headline), or one of the steps around it on its own")
     ap.add_argument("--topk-workload", choices=["long-batch", "long-decode"], default="long-batch",
                     help="top-k selection workload (synth.topk_config)")
@@ -758,23 +759,26 @@ def run_mtp_union(args):
     return 0
 
 
-def run_fp4_and_pages(args):
-    """The 4-bit cache's operators and the page operators: each case captured, twelve calls to a graph that is replayed ("graph_us"
-    a call), and called in a loop through the Python binding from an idle start ("loop_us"), over three prepared inputs in turn
-    (the small cases' inputs stay in L2).  240 calls a case, or fewer with --steps."""
-    import torch
-    import perf.operators as ops
-    from sparse_mla_decode_combine_gb300 import build as pkg_build
-    pkg_build.build()
-    torch.cuda.set_device(0)
-    props = torch.cuda.get_device_properties(0)
-    ops.own = True
+def fp4_and_pages_cases(ops):
     cases = ops.listed()
     heavy = next(c for c in cases if c["name"] == "decode-heavy")
     cases += [dict(heavy, name=f"decode-{h}-heads", heads=h) for h in (16, 32, 64)]
     cases += [dict(heavy, name="decode-one-token", tokens=1, heads=16),
               dict(heavy, name="decode-one-token-long", tokens=1, heads=16, topk=64, window=131008, seq_lo=200000, seq_hi=200000,
                    sink=False)]
+    return cases
+
+
+def run_cases(args, ops, cases):
+    """Operators as their cases give them: each captured, twelve calls to a graph that is replayed ("graph_us" a call), and called in
+    a loop through the Python binding from an idle start ("loop_us"), over three prepared inputs in turn (the small cases' inputs
+    stay in L2).  240 calls a case, or fewer with --steps."""
+    import torch
+    from sparse_mla_decode_combine_gb300 import build as pkg_build
+    pkg_build.build()
+    torch.cuda.set_device(0)
+    props = torch.cuda.get_device_properties(0)
+    ops.own = True
     sampler = ClockSampler(str(getattr(props, "uuid", "")))
     sampler.start()
     time.sleep(0.2)
@@ -812,7 +816,7 @@ def run_fp4_and_pages(args):
         torch.cuda.empty_cache()
     t1 = time.time()
     sampler.stop()
-    print(json.dumps({"op": "fp4-and-pages", "metric": "microseconds a call", "unit": "us", "higher_is_better": False, "n_gpus": 1,
+    print(json.dumps({"op": args.op, "metric": "microseconds a call", "unit": "us", "higher_is_better": False, "n_gpus": 1,
                       "data": "synthetic", "peak_source": peak_src, "cases": rows, "clocks": sampler.summary(t0, t1)}), flush=True)
     return 0
 
@@ -1094,10 +1098,14 @@ def main():
         if args.impl == "reference" or int(os.environ.get("RANK", "0")) != 0:
             return 0
         return run_combine_compressed(args)
-    if args.op == "fp4-and-pages":
+    if args.op in ("fp4-and-pages", "between-steps"):
         if args.impl == "reference" or int(os.environ.get("RANK", "0")) != 0:
             return 0
-        return run_fp4_and_pages(args)
+        if args.op == "fp4-and-pages":
+            import perf.operators as ops
+            return run_cases(args, ops, fp4_and_pages_cases(ops))
+        import perf.more_operators as more
+        return run_cases(args, more, more.listed())
     if args.op == "mtp-union":
         if args.impl == "reference" or int(os.environ.get("RANK", "0")) != 0:
             return 0
