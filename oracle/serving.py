@@ -57,7 +57,7 @@ def verify(target, draft, tokens, start, uniform, greedy=None, seq=None, width=N
         while a < k:
             d, p = int(tokens[d0 + a]), np.asarray(target[r0 + a], dtype=np.float64)
             if greedy is not None and greedy[b]:
-                ok = largest(p) == d
+                ok = 0 <= d == largest(p)
             elif 0 <= d < V:
                 qd = 1.0 if draft is None else float(draft[d0 + a][d])
                 ok = float(uniform[r0 + a]) * qd < p[d]

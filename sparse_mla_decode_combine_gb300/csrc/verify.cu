@@ -54,6 +54,10 @@ __device__ __forceinline__ void cluster_barrier()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The cluster's first barrier, in two halves: no CTA writes to another before that one has begun.
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_begun() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // v into the place of `local` in the shared memory of the cluster's CTA `rank`
 __device__ __forceinline__ void put_remote(void *local, uint32_t rank, unsigned long long v)
 {
@@ -206,6 +210,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const T *target = static_cast<const T *>(p.target), *draft = static_cast<const T *>(p.draft);
     const int V = p.vocab;
+    if (C > 1)
+        cluster_begun();
     griddep_wait();
     griddep_launch();
 
@@ -215,6 +221,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     const bool ok = rows >= 1 && rows <= p.num_rows && row0 >= 0 && row0 <= p.num_rows - rows && d0 >= 0 && d0 <= p.num_drafts - k &&
                     rows <= p.out_width;
     if (!ok) {   // (the same in every CTA of the cluster)
+        if (C > 1)
+            cluster_wait_begun();
         if (rank == 0) {
             for (int j = tid; j < p.out_width; j += kThreads)
                 out[j] = -1;
@@ -235,6 +243,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     int a = 0;
     if (greedy) {
         int token;
+        if (C > 1)
+            cluster_wait_begun();
         for (int j = 0;; ++j) {   // row j: its largest value, the lowest index of equal ones
             const T *row = target + (int64_t)(row0 + j) * p.target_stride;
             float best = -INFINITY;
@@ -279,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
             }
             token = key == 0ull ? -1 : (int)~(uint32_t)key;
             a = j;
-            if (j == k || token != p.tokens[d0 + j])
+            if (j == k || token < 0 || token != p.tokens[d0 + j])
                 break;
             __syncthreads();   // wbest is written again
         }
@@ -311,6 +321,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
         row.q = a < k && draft != nullptr ? draft + (int64_t)(d0 + a) * p.draft_stride : nullptr;
         row.point = a < k && draft == nullptr ? p.tokens[d0 + a] : -1;
         const int tiles = (hi - lo + p.tile - 1) / p.tile;
+        if (C > 1)
+            cluster_wait_begun();
         for (int turn = 0;; ++turn) {
             // ---- the sums of this CTA's tiles, a tile to a warp
             for (int t = warp; t < tiles; t += kWarps) {

@@ -194,6 +194,16 @@ def test_bad_requests_and_tokens_are_flagged():
     check(dict(c, start=c["start"] + 1000))                                # only differences count
 
 
+def test_a_draft_of_minus_one_never_stands():
+    need_gpu()
+    z = np.full((3, 5000), np.nan, np.float32)
+    z[1:, 7] = 1.0
+    for greedy in (None, np.ones(1, np.uint8)):
+        got = check(dict(target=z, draft=None, tokens=np.array([-1, 7], np.int32), start=np.array([0, 3], np.int32),
+                         uniform=np.zeros(3, np.float32), greedy=greedy, seq=np.array([9], np.int32)), exact=True)
+        assert got.tolist() == [[-1, -1, -1]]
+
+
 def test_bad_tokens_after_the_last_accepted_one_are_flagged():
     need_gpu()
     for greedy in (None, np.ones(2, np.uint8)):
