@@ -49,6 +49,7 @@ constexpr uint32_t kColKeys = 256;       // (two accumulators of up to 128 colum
 constexpr int kMaxDepth = 4;             // units of a quadrant's ring
 constexpr int kAddThreads = 256;
 constexpr int kAddSlices = 8;
+constexpr int kAddRows = 1 << 20;        // rows at a time
 
 // the small region after Q and the units
 constexpr int kOffLse = 0;               // float [128]: the token's lse in log2 units; before that int [23]: a sum over the warps
@@ -568,10 +569,9 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const KeyWeigh
     __shared__ int tokens[kAddThreads], wcount[kAddThreads / 32];
     griddep_wait();
     griddep_launch();
-    const int r = blockIdx.y, slice = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float *row = p.weights + (int64_t)r * p.weights_stride;
+    const int slice = blockIdx.x % kAddSlices, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kDeep = 4;
-    auto add = [&](int t, int i0, int step, bool deal) {
+    auto add = [&](float *row, int t, int i0, int step, bool deal) {
         const int len = __ldcg(p.lens + t);
         const int64_t at = (int64_t)t * p.list_w;
         for (; i0 < len; i0 += kDeep * step) {
@@ -590,30 +590,33 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const KeyWeigh
                     __stcg(row + pos[u], __ldcg(row + pos[u]) + got[u]);
         }
     };
-    for (int t0 = 0; t0 < p.num_tokens; t0 += kAddThreads) {
-        const int t = t0 + tid;
-        const bool mine = t < p.num_tokens && p.req_idx[t] == r && __ldcg(p.later + t) != 0;
-        const unsigned m = __ballot_sync(0xffffffffu, mine);
-        if (lane == 0)
-            wcount[warp] = __popc(m);
-        __syncthreads();
-        int before = 0, all = 0;
-        for (int w = 0; w < kAddThreads / 32; ++w) {
-            before += w < warp ? wcount[w] : 0;
-            all += wcount[w];
+    for (int64_t r = blockIdx.x / kAddSlices; r < p.num_reqs; r += gridDim.x / kAddSlices) {
+        float *row = p.weights + r * p.weights_stride;
+        for (int t0 = 0; t0 < p.num_tokens; t0 += kAddThreads) {
+            const int t = t0 + tid;
+            const bool mine = t < p.num_tokens && p.req_idx[t] == r && __ldcg(p.later + t) != 0;
+            const unsigned m = __ballot_sync(0xffffffffu, mine);
+            if (lane == 0)
+                wcount[warp] = __popc(m);
+            __syncthreads();
+            int before = 0, all = 0;
+            for (int w = 0; w < kAddThreads / 32; ++w) {
+                before += w < warp ? wcount[w] : 0;
+                all += wcount[w];
+            }
+            if (mine)
+                tokens[before + __popc(m & ((1u << lane) - 1u))] = t;
+            __syncthreads();
+            const bool deal = all > 1 || p.num_tokens > kAddThreads;   // (else it is the row's only one)
+            for (int k = 0; k < all; ++k) {
+                if (deal)
+                    add(row, tokens[k], tid, kAddThreads, true);
+                else
+                    add(row, tokens[k], slice * kAddThreads + tid, kAddSlices * kAddThreads, false);
+                __syncthreads();   // the next token's sums come on top
+            }
+            __syncthreads();
         }
-        if (mine)
-            tokens[before + __popc(m & ((1u << lane) - 1u))] = t;
-        __syncthreads();
-        const bool deal = all > 1 || p.num_tokens > kAddThreads;   // (else it is the row's only one)
-        for (int k = 0; k < all; ++k) {
-            if (deal)
-                add(tokens[k], tid, kAddThreads, true);
-            else
-                add(tokens[k], slice * kAddThreads + tid, kAddSlices * kAddThreads, false);
-            __syncthreads();   // the next token's sums come on top
-        }
-        __syncthreads();
     }
 }
 
@@ -650,7 +653,7 @@ cudaError_t launch_key_weights(const KeyWeightsParams &p, int sms, cudaStream_t 
     const cudaError_t e = p.entry_bytes == kEntry4Bytes ? launch_for<true>(p, sms, stream) : launch_for<false>(p, sms, stream);
     if (e != cudaSuccess || p.req_idx == nullptr)   // (without req_idx every token has a row of its own)
         return e;
-    return launch_dependent(add_weights_kernel, dim3(kAddSlices, (unsigned)p.num_reqs), kAddThreads, 0, stream, p);
+    return launch_dependent(add_weights_kernel, dim3(kAddSlices * (unsigned)std::min(p.num_reqs, kAddRows)), kAddThreads, 0, stream, p);
 }
 
 }  // namespace dsv4

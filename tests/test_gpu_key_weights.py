@@ -118,6 +118,17 @@ def test_many_tokens_of_one_row():
     check(w)
 
 
+@pytest.mark.parametrize("rows", [65536, 140000])
+def test_tables_of_many_rows(rows):
+    need_gpu()
+    w = synth.make_workload(name="w", seed=12, heads=16, req_seq_lens=[30, 17, 44], tokens_per_req=2, topk_width=6, window=9, sink=False,
+                            page=16)
+    table = np.full((rows, w.block_table.shape[1]), -1, np.int32)
+    at = np.array([rows - 1, 0, rows // 2])
+    table[at] = w.block_table
+    check(dataclasses.replace(w, block_table=table, req_idx=at[w.req_idx].astype(np.int32)))
+
+
 def test_hundreds_of_tokens_of_few_rows():
     need_gpu()
     w = synth.make_workload(name="w", seed=10, heads=16, req_seq_lens=[500, 260, 300], tokens_per_req=110, topk_width=12, window=9,
