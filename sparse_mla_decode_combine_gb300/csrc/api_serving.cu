@@ -45,7 +45,7 @@ bool weights_plan(int num_tokens, int num_heads, int topk_width, int window, Wei
         return false;
     pl->list_w = topk_width + window;
     const int tile = key_weights_block_keys();
-    if ((long long)num_tokens * std::max(1, (pl->list_w + tile - 1) / tile) > INT_MAX)
+    if ((long long)num_tokens * ((pl->list_w + tile - 1) / tile + 4) > INT_MAX)   // (and a few blocks' worth for a token's start)
         return false;
     const size_t lists = align_up(4 * (size_t)num_tokens * (size_t)pl->list_w, 256);
     pl->off_positions = lists;

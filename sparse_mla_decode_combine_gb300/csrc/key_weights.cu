@@ -40,25 +40,31 @@ constexpr int kCopyWarps = 2;            // warps 5 and 6, two quadrants each
 constexpr int kKeyWarp0 = kCopyWarp0 + kCopyWarps;
 constexpr int kKeyWarps = 16;            // warps 7-22, in four sets
 constexpr int kSets = kKeyWarps / 4;
-constexpr int kThreads = 32 * (kKeyWarp0 + kKeyWarps);
+constexpr int kQWarp = kKeyWarp0 + kKeyWarps;   // warp 23
+constexpr int kThreads = 32 * (kQWarp + 1);
 constexpr int kBK = 128;                 // keys per block = MMA M
 constexpr int kChunks = 9;               // 576 dims / 64
+constexpr int kQGroups = 3;              // of Q, three chunks each in the order of the products
 constexpr int kSlots = 8;                // chunks in tensor memory, 32 columns each
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColKeys = 256;       // (two accumulators of up to 128 columns before them)
 constexpr int kMaxDepth = 4;             // units of a quadrant's ring
+constexpr int kSwitch = 1;               // blocks' worth of time that a token's start takes
+constexpr int kLongRun = 4;              // blocks to a CTA from which on the starts count
 constexpr int kAddThreads = 256;
-constexpr int kAddSlices = 8;
+constexpr int kAddSlices = 4;
+constexpr int kFront = 8;                // entries of a token that a thread has in flight
 constexpr int kAddRows = 1 << 20;        // rows at a time
 
 // the small region after Q and the units
-constexpr int kOffLse = 0;               // float [128]: the token's lse in log2 units; before that int [23]: a sum over the warps
-constexpr int kOffBars = 512;            // u64: raw_full[16], raw_empty[16], full[8], empty[8], d_full[2], d_empty[2], q
-constexpr int kOffTmem = 944;            // u32
-constexpr int kOffAbort = 948;           // int
-constexpr int kOffStart = 952;           // int [2]: the token at the run's start, and its first block
+constexpr int kOffLse = 0;               // float [128]: the token's lse in log2 units; before that int2 [24]: a sum over the warps
+constexpr int kOffBars = 512;            // u64: raw_full[16], raw_empty[16], full[8], empty[8], d_full[2], d_empty[2],
+                                         // q[3], q_free[3], q_raw[3]
+constexpr int kOffTmem = 1008;           // u32
+constexpr int kOffAbort = 1012;          // int
+constexpr int kOffStart = 1016;          // int [2]: the token at the run's start, and its first block
 constexpr int kSmallBytes = 1024;
-static_assert(kOffBars + 8 * (8 * kMaxDepth + 2 * kSlots + 5) <= kOffTmem && 4 * (kThreads / 32) <= kOffBars, "small region");
+static_assert(kOffBars + 8 * (8 * kMaxDepth + 2 * kSlots + 4 + 3 * kQGroups) <= kOffTmem && 8 * (kThreads / 32) <= kOffBars, "small region");
 
 // N heads: Q takes 1152 N bytes; units of 16 entries fill what is left of 227 KB
 template <int kH, bool kFour>
@@ -151,6 +157,14 @@ __device__ __forceinline__ void dequant32_e2m1(const uint4 &v, uint32_t se, uint
     }
 }
 
+// bytes of w by the selector's nibbles, those of 8 and more the sign of byte - 8, eight times
+__device__ __forceinline__ uint32_t prmt(uint32_t w, uint32_t sel)
+{
+    uint32_t r;
+    asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(w), "r"(sel));
+    return r;
+}
+
 // two E4M3 codes times a scale -> a BF16 pair (exact for every code and scale; NaN codes stay NaN)
 __device__ __forceinline__ uint32_t convert2_e4m3(uint32_t two, float scale)
 {
@@ -165,22 +179,21 @@ __device__ __forceinline__ float scale_of(uint32_t se)   // 2^(se - 127); 255: N
 }
 
 // 64 E4M3 codes times 2^(se - 127) -> 64 BF16 values as pairs.  A code s.eeee.mmm placed as the BF16 pattern
-// s.0000eeee.mmm0000 is its value times 2^-120; one multiply by 2^(se - 7) gives the value.  The sign goes from bit 11 to bit 15
-// by adding 15 times it: multiplications, since the logic pipe (shifts and masks: five operations a pair) was what the
-// conversion waited for.  Chunks with the NaN code, or a scale past 2^7, take the hardware's conversion.
+// s.0000eeee.mmm0000 is its value times 2^-120; one multiply by 2^(se - 7) gives the value.  A byte and its sign eight
+// times over, shifted by four (a multiplication: the logic pipe is the fuller one), has every bit in its place.  Chunks with
+// the NaN code, or a scale past 2^7, take the hardware's conversion.
 __device__ __forceinline__ void dequant64_e4m3(const uint4 (&v)[4], uint32_t se, uint32_t (&o)[32])
 {
     uint32_t f = (min(se, 134u) + 120u) << 7, odd = 0u;
     f |= f << 16;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const uint32_t w = (i & 6) == 0 ? v[i >> 3].x : (i & 6) == 2 ? v[i >> 3].y : (i & 6) == 4 ? v[i >> 3].z : v[i >> 3].w;
-        const uint32_t t = __byte_perm(w, 0u, i & 1 ? 0x4342 : 0x4140) * 16u;   // [c, 0, c', 0] << 4
-        const uint32_t x = (t & 0x08000800u) * 15u + t;
-        odd |= x + 0x00100010u;                                                 // (bit 11 of a half: its magnitude was 0x7F)
-        o[i] = mul_bf16x2(x, f);
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t w = (i & 3) == 0 ? v[i >> 2].x : (i & 3) == 1 ? v[i >> 2].y : (i & 3) == 2 ? v[i >> 2].z : v[i >> 2].w;
+        o[2 * i] = mul_bf16x2((prmt(w, 0x9180) * 16u) & 0x87F087F0u, f);
+        o[2 * i + 1] = mul_bf16x2((prmt(w, 0xB3A2) * 16u) & 0x87F087F0u, f);
+        odd |= (w & 0x7F7F7F7Fu) + 0x01010101u;   // (bit 7 of a byte: its magnitude was 0x7F)
     }
-    if (se > 134u || (odd & 0x08000800u) != 0u) {
+    if (se > 134u || (odd & 0x80808080u) != 0u) {
         const float sc = scale_of(se);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -192,10 +205,11 @@ __device__ __forceinline__ void dequant64_e4m3(const uint4 (&v)[4], uint32_t se,
 
 __device__ __forceinline__ int blocks_of(int len) { return (len + kBK - 1) / kBK; }
 
-// The blocks of this CTA: [w, w1) of all tokens' blocks, in the order of the tokens.  Every role walks the same ones.
+// The work of this CTA: [w, w1) of all tokens' blocks, in the order of the tokens, each token with `extra` blocks' worth of time
+// before its first (its queries take the place of the last token's).  Every role walks the same blocks.
 struct Walk {
-    int w, w1;        // still to do
-    int t, start;     // token of block w, and that token's first block
+    int w, w1, extra;
+    int t, start;     // the next token, and where its work begins
 };
 
 struct Segment {
@@ -205,21 +219,17 @@ struct Segment {
 
 __device__ __forceinline__ bool next_segment(Walk &k, const KeyWeightsParams &p, Segment &s)
 {
-    if (k.w >= k.w1)
-        return false;
-    while (true) {    // (tokens without keys have no block)
+    while (k.start < k.w1) {    // (tokens without keys have no work)
         s.len = __ldcg(p.lens + k.t);
-        const int n = blocks_of(s.len);
-        if (k.start + n > k.w) {
-            s.t = k.t;
-            s.kb = k.w - k.start;
-            s.nb = min(n - s.kb, k.w1 - k.w);
-            k.w += s.nb;
+        s.t = k.t++;
+        const int n = blocks_of(s.len), at = k.start + k.extra;
+        s.kb = max(0, k.w - at);
+        s.nb = min(n, k.w1 - at) - s.kb;
+        k.start += n > 0 ? n + k.extra : 0;
+        if (s.nb > 0)
             return true;
-        }
-        k.start += n;
-        ++k.t;
     }
+    return false;
 }
 
 template <int kH, bool kFour>
@@ -241,16 +251,18 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
     const uint32_t bar_empty = bar_full + 8 * kSlots;          // [slot] read by its products
     const uint32_t bar_dfull = bar_empty + 8 * kSlots;         // [2] the block's products are complete
     const uint32_t bar_dempty = bar_dfull + 16;                // [2] read by the epilogue
-    const uint32_t bar_q = bar_dfull + 32;                     // Q of the segment written
+    const uint32_t bar_q = bar_dfull + 32;                     // [group] of the segment's Q is there
+    const uint32_t bar_qfree = bar_q + 8 * kQGroups;           // [group] the segment's last products with it are done
+    const uint32_t bar_qraw = bar_qfree + 8 * kQGroups;        // [group] (4-bit) copied, in the order of its dims
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(small + kOffAbort);
     int *first = reinterpret_cast<int *>(small + kOffStart);
-    int *scan = reinterpret_cast<int *>(small + kOffLse);
+    int2 *scan = reinterpret_cast<int2 *>(small + kOffLse);
 
     if (tid == 0) {
         for (int i = 0; i < 4 * kMaxDepth; ++i) {
             mbar_init(bar_raw_full + 8 * i, 32);
-            mbar_init(bar_raw_empty + 8 * i, kChunks);
+            mbar_init(bar_raw_empty + 8 * i, kSets);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(bar_full + 8 * i, 4);
@@ -260,13 +272,23 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             mbar_init(bar_dfull + 8 * i, 1);
             mbar_init(bar_dempty + 8 * i, kEpilogueWarps);
         }
-        mbar_init(bar_q, kKeyWarps);
+        for (int i = 0; i < kQGroups; ++i) {
+            mbar_init(bar_q + 8 * i, kFour ? kKeyWarps : 1);
+            mbar_init(bar_qfree + 8 * i, 1);
+            mbar_init(bar_qraw + 8 * i, 32);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort_flag = 0;
     }
     // (only the list kernel can still be running ahead of this one: it waited for what came before)
     if (warp == 0)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    {   // the queries of the token that the CTA begins with if all lists are equally long, while the lists are made
+        const int t = (int)((long long)p.num_tokens * blockIdx.x / gridDim.x);
+        const uint8_t *q = reinterpret_cast<const uint8_t *>(p.q + (int64_t)t * p.q_token_stride);
+        for (int i = tid; i < (kH * kDim * 2 + 127) / 128; i += kThreads)
+            prefetch_l2(q + 128 * i);
+    }
     griddep_wait();
 
     // ---- this CTA's blocks
@@ -274,29 +296,39 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
     {
         const int per = (p.num_tokens + kThreads - 1) / kThreads;
         const int t0 = min(p.num_tokens, tid * per), t1 = min(p.num_tokens, t0 + per);
-        int mine = 0;
-        for (int t = t0; t < t1; ++t)
-            mine += blocks_of(__ldcg(p.lens + t));
-        int incl = mine;
+        int mine = 0, mine_tokens = 0, n0 = 0;   // blocks, tokens with keys, blocks of the first
+        for (int t = t0; t < t1; ++t) {
+            const int n = blocks_of(__ldcg(p.lens + t));
+            n0 = t == t0 ? n : n0;
+            mine += n;
+            mine_tokens += n > 0;
+        }
+        int incl = mine, incl_tokens = mine_tokens;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d)
+            const int y = __shfl_up_sync(0xffffffffu, incl, d), z = __shfl_up_sync(0xffffffffu, incl_tokens, d);
+            if (lane >= d) {
                 incl += y;
+                incl_tokens += z;
+            }
         }
         if (lane == 31)
-            scan[warp] = incl;
+            scan[warp] = make_int2(incl, incl_tokens);
         __syncthreads();
-        int at = incl - mine, W = 0;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            at += i < warp ? scan[i] : 0;
-            W += scan[i];
-        }
-        walk.w = (int)((long long)W * blockIdx.x / gridDim.x);
-        walk.w1 = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
+        const int2 x = scan[min(lane, kThreads / 32 - 1)];
+        const bool sum = lane < kThreads / 32, below = lane < warp;
+        const int W = __reduce_add_sync(0xffffffffu, sum ? x.x : 0), tokens = __reduce_add_sync(0xffffffffu, sum ? x.y : 0);
+        int at = incl - mine + __reduce_add_sync(0xffffffffu, below ? x.x : 0);
+        const int at_tokens = incl_tokens - mine_tokens + __reduce_add_sync(0xffffffffu, below ? x.y : 0);
+        walk.extra = W >= kLongRun * (int)gridDim.x ? kSwitch : 0;
+        const unsigned all = W + tokens * walk.extra, each = all / gridDim.x, more = all % gridDim.x;
+        walk.w = (int)(each * blockIdx.x + min(blockIdx.x, more));
+        walk.w1 = walk.w + (int)(each + (blockIdx.x < more ? 1u : 0u));
+        at += at_tokens * walk.extra;
+        mine += mine_tokens * walk.extra;
         if (walk.w < walk.w1 && mine > 0 && at <= walk.w && walk.w < at + mine) {
-            int t = t0, n;
-            while (at + (n = blocks_of(__ldcg(p.lens + t))) <= walk.w) {
+            int t = t0;
+            for (int n = n0; at + (n > 0 ? n += walk.extra : 0) <= walk.w; n = blocks_of(__ldcg(p.lens + t))) {
                 at += n;
                 ++t;
             }
@@ -307,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
         __syncthreads();
         after_sync();
         walk.t = first[0];
-        walk.start = first[1];
+        walk.start = walk.w < walk.w1 ? first[1] : walk.w1;
     }
     const uint32_t tmem = *tmem_slot;
     griddep_launch();   // (the adding kernel waits for this grid itself)
@@ -320,7 +352,6 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
         const uint64_t db = sdesc(sQ, 16, 1024);
         uint32_t at = 0;   // chunks since the kernel began
         for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
-            mbar_wait(bar_q, n & 1u, abort_flag, p.status);
             for (int b = 0; b < seg.nb; ++b, ++g) {
                 const uint32_t x = g & 1u;
                 if (g >= 2) {
@@ -330,14 +361,18 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
 #pragma unroll 3
                 for (int c = 0; c < kChunks; ++c, ++at) {
                     const uint32_t slot = at % kSlots;
+                    if (b == 0 && c % 3 == 0)
+                        mbar_wait(bar_q + 8 * (c / 3), n & 1u, abort_flag, p.status);
                     mbar_wait(bar_full + 8 * slot, (at / kSlots) & 1u, abort_flag, p.status);
                     after_sync();
-                    const uint64_t bq = db + (uint64_t)((c * kQChunkBytes) >> 4);
+                    const uint64_t bq = db + (uint64_t)(((c + kChunks - 1) % kChunks * kQChunkBytes) >> 4);   // (the rope dims first)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         mma_bf16_ts(leader, tmem + kH * x, tmem + kColKeys + 32 * slot + 8 * k, bq + (uint64_t)(2 * k), kIdesc,
                                     (c != 0 || k != 0) ? 1u : 0u);
                     commit(leader, bar_empty + 8 * slot);
+                    if (b == seg.nb - 1 && c % 3 == 2)
+                        commit(leader, bar_qfree + 8 * (c / 3));
                 }
                 commit(leader, bar_dfull + 8 * x);
             }
@@ -361,14 +396,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             const int64_t list = (int64_t)t * p.list_w;
             auto load_place = [&](int b) {
                 const int i = (seg.kb + b) * kBK + row;
-                return b < seg.nb && i < seg.len && __ldcg(p.slots + list + i) >= 0 ? (first_of ? __ldcg(p.positions + list + i) : i) : -1;
+                return b < seg.nb && i < seg.len ? __ldcg(p.positions + list + i) : -1;
             };
-            float *out = first_of ? p.weights + (int64_t)max(r, 0) * p.weights_stride : p.got + list;
+            float *row_out = p.weights + (int64_t)max(r, 0) * p.weights_stride;
             int place_next = load_place(0);
             for (int b = 0; b < seg.nb; ++b, ++g) {
                 const uint32_t x = g & 1u;
                 const int place = place_next;
-                const float had = first_of && place >= 0 ? __ldcg(out + place) : 0.f;
+                const float had = first_of && place >= 0 ? __ldcg(row_out + place) : 0.f;
                 place_next = load_place(b + 1);
                 mbar_wait(bar_dfull + 8 * x, (g >> 1) & 1u, abort_flag, p.status);
                 after_sync();
@@ -391,8 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar_dempty + 8 * x);
-                if (place >= 0)
-                    __stcg(out + place, had + ((sum[0] + sum[1]) + (sum[2] + sum[3])));
+                const float weight = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                if (!first_of && (seg.kb + b) * kBK + row < seg.len)
+                    __stcg(p.got + list + (seg.kb + b) * kBK + row, weight);
+                else if (place >= 0)
+                    __stcg(row_out + place, had + weight);
             }
         }
     } else if (warp < kKeyWarp0) {
@@ -466,94 +504,136 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-        // ---- Q and the keys: lane l of quadrant q has key 32 q + l of the block, its set every kSets-th chunk
+    } else if (warp < kQWarp) {
+        // ---- the keys: lane l of quadrant q has key 32 q + l of the block.  A set has two latent chunks of it, the first set the
+        // rope dims as well, which need no conversion.  All are taken out of the ring at once, so that it fills again meanwhile
         const int kw = warp - kKeyWarp0, set = kw >> 2, quad = warp & 3;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + kColKeys;
-        uint32_t at = set;       // this set's next chunk, of block at / kChunks
-        auto prefetch_q = [&](int t) {
-            const uint8_t *q = reinterpret_cast<const uint8_t *>(p.q + (int64_t)t * p.q_token_stride);
-            for (int i = 32 * kw + lane; i < (kH * kDim * 2 + 127) / 128; i += 32 * kKeyWarps)
-                prefetch_l2(q + 128 * i);
-        };
-        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
-            if (n > 0)   // the products of the last segment are done with its Q
-                mbar_wait(bar_dfull + 8 * ((g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p.status);
-            {
-                const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)seg.t * p.q_token_stride);
-                auto place = [&](int i) {   // of the i-th 16 bytes of Q
-                    const int h = i / (kDim / 8), c = i % (kDim / 8);
-                    return sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
-                };
-                for (int i = 32 * kw + lane; i < kH * (kDim / 8); i += 32 * kKeyWarps)
-                    copy16(place(i), q + i);
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                if (kFour)   // (each thread its own pieces: the order of the latent dims that dequant32_e2m1 gives)
-                    for (int i = 32 * kw + lane; i < kH * (kDim / 8); i += 32 * kKeyWarps)
-                        if (i % (kDim / 8) < kLatent / 8) {
-                            const uint32_t a = place(i);
-                            const uint4 v = lds16(a);
-                            st_shared_v4(a, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                                         __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-                        }
+        const int c0 = (set + 3) & 3;   // its latent chunks: c0 and c0 + 4
+        constexpr int kRaw = kFour ? 2 : 4;
+        uint32_t blk = 0;        // blocks since the kernel began
+        // a chunk into the next slot (blk * kChunks + m is its number)
+        auto put = [&](const uint32_t (&o)[32], int m) {
+            const uint32_t at = blk * kChunks + m, slot = at % kSlots;
+            if (at >= kSlots) {
+                mbar_wait(bar_empty + 8 * slot, ((at / kSlots) & 1u) ^ 1u, abort_flag, p.status);
+                after_sync();
             }
-            fence_async_smem();
+            tmem_st32(lane_base + 32 * slot, o);
+            tmem_st_wait();
+            before_sync();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(bar_q);
-            if (walk.w < walk.w1)   // the next token's
-                prefetch_q(seg.t + 1);
-
+                mbar_arrive(bar_full + 8 * slot);
+        };
+        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
+            const uint32_t first_block = blk;
             g += (uint32_t)seg.nb;
-            for (; at < g * kChunks; at += kSets) {
-                const uint32_t blk = at / kChunks, c = at - blk * kChunks;
+            for (; blk < g; ++blk) {
                 // both units of the quadrant's half blocks, and this lane's entry in its own
                 const uint32_t u0 = 2 * blk, u1 = 2 * blk + 1;
                 const uint32_t unit0 = quad * kDepth + u0 % kDepth, unit1 = quad * kDepth + u1 % kDepth;
                 mbar_wait(bar_raw_full + 8 * unit0, (u0 / kDepth) & 1u, abort_flag, p.status);
                 mbar_wait(bar_raw_full + 8 * unit1, (u1 / kDepth) & 1u, abort_flag, p.status);
                 const uint32_t e = sRaw + (lane < 16 ? unit0 : unit1) * S::kUnitBytes + (lane & 15) * S::kEntry;
-                uint32_t o[32];
-                if (c == kChunks - 1) {
+                uint4 v[2][kRaw];
+                uint32_t se[2][2], o[32];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int c = c0 + 4 * j;
+#pragma unroll
+                    for (int i = 0; i < kRaw; ++i)
+                        v[j][i] = lds16(e + 16 * (kRaw * c + i));
+                    se[j][0] = lds8(e + (kFour ? kScale4Offset + 2 * c : kScaleOffset + (c >> 1)));
+                    se[j][1] = kFour ? lds8(e + kScale4Offset + 2 * c + 1) : 0u;
+                }
+                if (set == 0)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint4 v = lds16(e + (kFour ? kRope4Offset : kRopeOffset) + 16 * i);
-                        o[4 * i] = v.x;
-                        o[4 * i + 1] = v.y;
-                        o[4 * i + 2] = v.z;
-                        o[4 * i + 3] = v.w;
+                        const uint4 x = lds16(e + (kFour ? kRope4Offset : kRopeOffset) + 16 * i);
+                        o[4 * i] = x.x;
+                        o[4 * i + 1] = x.y;
+                        o[4 * i + 2] = x.z;
+                        o[4 * i + 3] = x.w;
                     }
-                } else if (kFour) {
-                    const uint4 v0 = lds16(e + 32 * c), v1 = lds16(e + 32 * c + 16);
-                    const uint32_t s0 = lds8(e + kScale4Offset + 2 * c), s1 = lds8(e + kScale4Offset + 2 * c + 1);
-                    dequant32_e2m1(v0, s0, o);
-                    dequant32_e2m1(v1, s1, o + 16);
-                } else {
-                    const uint32_t se = lds8(e + kScaleOffset + (c >> 1));
-                    uint4 v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = lds16(e + 64 * c + 16 * i);
-                    dequant64_e4m3(v, se, o);
-                }
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(bar_raw_empty + 8 * unit0);
                     mbar_arrive(bar_raw_empty + 8 * unit1);
                 }
-                const uint32_t slot = at % kSlots;
-                if (at >= kSlots) {
-                    mbar_wait(bar_empty + 8 * slot, ((at / kSlots) & 1u) ^ 1u, abort_flag, p.status);
-                    after_sync();
+                if (set == 0)
+                    put(o, 0);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (kFour) {
+                        dequant32_e2m1(v[j][0], se[j][0], o);
+                        dequant32_e2m1(v[j][1], se[j][1], o + 16);
+                    } else {
+                        dequant64_e4m3(v[j], se[j][0], o);
+                    }
+                    put(o, c0 + 1 + 4 * j);
+                    // the order of the latent dims that dequant32_e2m1 gives, for Q, after the chunks that go into tensor memory
+                    // without its products
+                    if (kFour && j == 0 && blk == first_block)
+                        for (int grp = 0; grp < kQGroups; ++grp) {
+                            mbar_wait(bar_qraw + 8 * grp, n & 1u, abort_flag, p.status);
+                            for (int i = (grp == 0 ? 8 * kH : 0) + 32 * kw + lane; i < 3 * 8 * kH; i += 32 * kKeyWarps) {
+                                const uint32_t a = sQ + (3 * grp - 1) * kQChunkBytes + 16 * i;
+                                const uint4 x = lds16(a);
+                                st_shared_v4(a, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                                             __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+                            }
+                            fence_async_smem();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(bar_q + 8 * grp);
+                        }
                 }
-                tmem_st32(lane_base + 32 * slot, o);
-                tmem_st_wait();
-                before_sync();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_full + 8 * slot);
             }
         }
+    } else {
+        // ---- Q, a group of chunks as soon as the products of the segment before are done with it
+        for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
+            const uint16_t *q = p.q + (int64_t)seg.t * p.q_token_stride + (lane >> 3) * kDim + 8 * (lane & 7);
+            auto done = [&](int grp) {   // this lane's copies of the group are complete
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_q + 8 * grp);
+            };
+#pragma unroll 1
+            for (int grp = 0; grp < kQGroups; ++grp) {
+                if (n > 0)
+                    mbar_wait(bar_qfree + 8 * grp, (n - 1) & 1u, abort_flag, p.status);
+#pragma unroll 1
+                for (int m = 3 * grp; m < 3 * grp + 3; ++m) {
+                    const int c = m == 0 ? kChunks - 1 : m - 1;
+                    const uint32_t dst = sQ + c * kQChunkBytes;
+#pragma unroll 8
+                    for (int h = 0; h < kH; h += 4)
+                        copy16(dst + sw128(h + (lane >> 3), lane & 7), q + h * kDim + 64 * c);
+                }
+                if (kFour) {
+                    arrive_copied(bar_qraw + 8 * grp);
+                } else {
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    if (grp > 0) {
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        done(grp - 1);
+                    }
+                }
+            }
+            if (!kFour) {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                done(kQGroups - 1);
+            }
+            if (walk.start < walk.w1) {   // the next token's
+                const uint8_t *next = reinterpret_cast<const uint8_t *>(p.q + (int64_t)(seg.t + 1) * p.q_token_stride);
+                for (int i = lane; i < (kH * kDim * 2 + 127) / 128; i += 32)
+                    prefetch_l2(next + 128 * i);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     before_sync();
     __syncthreads();
@@ -563,38 +643,26 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
 }
 
 // The tokens after a row's first one, in order.  One of them: the slices share its list.  Several: one after the other, positions
-// dealt out to the slices in runs of 256.
+// dealt out to the slices in runs of 256.  What the list kernel wrote was complete before the one with the products let this one
+// begin, so a thread has the positions of its first kFront entries before it waits for that one.
 __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const KeyWeightsParams p)
 {
     __shared__ int tokens[kAddThreads], wcount[kAddThreads / 32];
-    griddep_wait();
-    griddep_launch();
     const int slice = blockIdx.x % kAddSlices, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int kDeep = 4;
-    auto add = [&](float *row, int t, int i0, int step, bool deal) {
-        const int len = __ldcg(p.lens + t);
-        const int64_t at = (int64_t)t * p.list_w;
-        for (; i0 < len; i0 += kDeep * step) {
-            int pos[kDeep];
-            float got[kDeep];
-#pragma unroll
-            for (int u = 0; u < kDeep; ++u) {
-                const int i = i0 + u * step;
-                const bool in = i < len && __ldcg(p.slots + at + i) >= 0;
-                pos[u] = in ? __ldcg(p.positions + at + i) : -1;
-                got[u] = in ? __ldcg(p.got + at + i) : 0.f;
-            }
-#pragma unroll
-            for (int u = 0; u < kDeep; ++u)
-                if (pos[u] >= 0 && (!deal || (pos[u] >> 8) % kAddSlices == slice))
-                    __stcg(row + pos[u], __ldcg(row + pos[u]) + got[u]);
+    bool waited = false;
+    auto wait = [&]() {
+        if (!waited) {
+            griddep_wait();
+            griddep_launch();
         }
+        waited = true;
     };
     for (int64_t r = blockIdx.x / kAddSlices; r < p.num_reqs; r += gridDim.x / kAddSlices) {
         float *row = p.weights + r * p.weights_stride;
         for (int t0 = 0; t0 < p.num_tokens; t0 += kAddThreads) {
-            const int t = t0 + tid;
-            const bool mine = t < p.num_tokens && p.req_idx[t] == r && __ldcg(p.later + t) != 0;
+            const int t = min(t0 + tid, p.num_tokens - 1);
+            const int of = p.req_idx[t], after = __ldcg(p.later + t);
+            const bool mine = t == t0 + tid && of == r && after != 0;
             const unsigned m = __ballot_sync(0xffffffffu, mine);
             if (lane == 0)
                 wcount[warp] = __popc(m);
@@ -608,16 +676,41 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const KeyWeigh
                 tokens[before + __popc(m & ((1u << lane) - 1u))] = t;
             __syncthreads();
             const bool deal = all > 1 || p.num_tokens > kAddThreads;   // (else it is the row's only one)
+            const int begin = deal ? tid : slice * kAddThreads + tid, step = deal ? kAddThreads : kAddSlices * kAddThreads;
             for (int k = 0; k < all; ++k) {
-                if (deal)
-                    add(row, tokens[k], tid, kAddThreads, true);
-                else
-                    add(row, tokens[k], slice * kAddThreads + tid, kAddSlices * kAddThreads, false);
+                const int token = tokens[k], len = __ldcg(p.lens + token);
+                const int64_t at = (int64_t)token * p.list_w;
+                int64_t i0 = begin;
+                do {
+                    int pos[kFront];
+                    float got[kFront], had[kFront];
+#pragma unroll
+                    for (int u = 0; u < kFront; ++u) {
+                        const int64_t i = i0 + u * step;
+                        pos[u] = __ldcg(p.positions + at + min(i, (int64_t)p.list_w - 1));   // (beside the length)
+                        if (i >= len || (deal && (pos[u] >> 8) % kAddSlices != slice))
+                            pos[u] = -1;
+                        if (pos[u] >= 0)
+                            prefetch_l2(row + pos[u]);
+                    }
+                    wait();
+#pragma unroll
+                    for (int u = 0; u < kFront; ++u) {
+                        got[u] = pos[u] >= 0 ? __ldcg(p.got + at + i0 + u * step) : 0.f;
+                        had[u] = pos[u] >= 0 ? __ldcg(row + pos[u]) : 0.f;
+                    }
+#pragma unroll
+                    for (int u = 0; u < kFront; ++u)
+                        if (pos[u] >= 0)
+                            __stcg(row + pos[u], had[u] + got[u]);
+                    i0 += kFront * step;
+                } while (i0 < len);
                 __syncthreads();   // the next token's sums come on top
             }
             __syncthreads();
         }
     }
+    wait();
 }
 
 template <int kH, bool kFour>

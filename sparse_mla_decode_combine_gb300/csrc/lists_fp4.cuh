@@ -45,7 +45,7 @@ __device__ __forceinline__ unsigned insert(unsigned long long *tab, int bits, in
 // Token t's list, by kThreads threads (tid: this one's number; whole warps); returns its length.  tab: p.smem_bytes of
 // shared memory, wsum: kLoads * kThreads / 32 ints of it.  sync() is a barrier of these threads, sync.any(v) one that
 // tells them whether any has v.  range(length) says from which entry to which the window's part of the list is wanted.
-// kPositions: p.positions receives the entries' positions beside their slots.
+// kPositions: p.positions receives the entries' positions beside their slots (-1 as well for a page out of range).
 template <int kThreads, int kLoads, bool kPositions = false, typename Sync, typename Range>
 __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsigned long long *tab, int *wsum, const Sync &sync,
                                      const Range &range)
@@ -171,9 +171,10 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
             const int rank = total + before + __popc(bal[u] & ((1u << lane) - 1u));
             total += __reduce_add_sync(0xffffffffu, x);
             if ((bal[u] >> lane) & 1u) {
-                out[rank] = pg == 0 ? sv[u] : slot_of(vg[u]);
+                const int slot = pg == 0 ? sv[u] : slot_of(vg[u]);
+                out[rank] = slot;
                 if (kPositions)
-                    out_pos[rank] = vg[u];
+                    out_pos[rank] = slot >= 0 ? vg[u] : -1;
             }
         }
         sync();   // wsum is rewritten by the next group of passes
@@ -182,9 +183,11 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
     const int2 part = range(len);
     const int i1 = min(part.y, len);
     int i = max(part.x, total) + tid;
-    if (kPositions)
-        for (int k = i; k < i1; k += kThreads)
-            out_pos[k] = win_lo + (k - total);
+    auto write = [&](int i, int slot) {
+        out[i] = slot;
+        if (kPositions)
+            out_pos[i] = slot >= 0 ? win_lo + (i - total) : -1;
+    };
     for (; i + 3 * kThreads < i1; i += 4 * kThreads) {   // the window, four loads in flight
         int phys[4], at[4];
 #pragma unroll
@@ -195,11 +198,11 @@ __device__ __forceinline__ int build(const Lists4Params &p, int t, int tid, unsi
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            out[i + u * kThreads] = slot_in(phys[u], at[u]);
+            write(i + u * kThreads, slot_in(phys[u], at[u]));
     }
 #pragma unroll 1
     for (; i < i1; i += kThreads)
-        out[i] = slot_of(win_lo + (i - total));
+        write(i, slot_of(win_lo + (i - total)));
     return len;
 }
 
