@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
     const uint32_t bar_dempty = bar_dfull + 16;                // [2] read by the epilogue
     const uint32_t bar_q = bar_dfull + 32;                     // [group] of the segment's Q is there
     const uint32_t bar_qfree = bar_q + 8 * kQGroups;           // [group] the segment's last products with it are done
-    const uint32_t bar_qraw = bar_qfree + 8 * kQGroups;        // [group] (4-bit) copied, in the order of its dims
+    const uint32_t bar_qraw = bar_qfree + 8 * kQGroups;        // [group] copied (a later segment's)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(small + kOffTmem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(small + kOffAbort);
     int *first = reinterpret_cast<int *>(small + kOffStart);
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             mbar_init(bar_dempty + 8 * i, kEpilogueWarps);
         }
         for (int i = 0; i < kQGroups; ++i) {
-            mbar_init(bar_q + 8 * i, kFour ? kKeyWarps : 1);
+            mbar_init(bar_q + 8 * i, kKeyWarps);
             mbar_init(bar_qfree + 8 * i, 1);
             mbar_init(bar_qraw + 8 * i, 32);
         }
@@ -526,8 +526,32 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             if (lane == 0)
                 mbar_arrive(bar_full + 8 * slot);
         };
+        // 16 bytes of Q in the order of the latent dims that dequant32_e2m1 gives
+        auto order_q = [&](uint32_t a) {
+            const uint4 x = lds16(a);
+            st_shared_v4(a, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                         __byte_perm(x.y, x.w, 0x7632));
+        };
         for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
             const uint32_t first_block = blk;
+            if (n == 0) {   // the first Q by all of these warps: their entries are not there yet
+                const uint4 *q = reinterpret_cast<const uint4 *>(p.q + (int64_t)seg.t * p.q_token_stride);
+                auto place = [&](int i) {   // of the i-th 16 bytes of Q
+                    const int h = i / (kDim / 8), c = i % (kDim / 8);
+                    return sQ + (c >> 3) * kQChunkBytes + sw128(h, c & 7);
+                };
+                for (int i = 32 * kw + lane; i < kH * (kDim / 8); i += 32 * kKeyWarps)
+                    copy16(place(i), q + i);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                if (kFour)   // (each thread its own pieces)
+                    for (int i = 32 * kw + lane; i < kH * (kDim / 8); i += 32 * kKeyWarps)
+                        if (i % (kDim / 8) < kLatent / 8)
+                            order_q(place(i));
+                fence_async_smem();
+                __syncwarp();
+                if (lane < kQGroups)
+                    mbar_arrive(bar_q + 8 * lane);
+            }
             g += (uint32_t)seg.nb;
             for (; blk < g; ++blk) {
                 // both units of the quadrant's half blocks, and this lane's entry in its own
@@ -572,17 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                         dequant64_e4m3(v[j], se[j][0], o);
                     }
                     put(o, c0 + 1 + 4 * j);
-                    // the order of the latent dims that dequant32_e2m1 gives, for Q, after the chunks that go into tensor memory
-                    // without its products
-                    if (kFour && j == 0 && blk == first_block)
+                    // a later segment's Q, after the chunks that go into tensor memory without its products
+                    if (n > 0 && j == 0 && blk == first_block)
                         for (int grp = 0; grp < kQGroups; ++grp) {
-                            mbar_wait(bar_qraw + 8 * grp, n & 1u, abort_flag, p.status);
-                            for (int i = (grp == 0 ? 8 * kH : 0) + 32 * kw + lane; i < 3 * 8 * kH; i += 32 * kKeyWarps) {
-                                const uint32_t a = sQ + (3 * grp - 1) * kQChunkBytes + 16 * i;
-                                const uint4 x = lds16(a);
-                                st_shared_v4(a, __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                                             __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-                            }
+                            mbar_wait(bar_qraw + 8 * grp, (n - 1) & 1u, abort_flag, p.status);
+                            if (kFour)
+                                for (int i = (grp == 0 ? 8 * kH : 0) + 32 * kw + lane; i < 3 * 8 * kH; i += 32 * kKeyWarps)
+                                    order_q(sQ + (3 * grp - 1) * kQChunkBytes + 16 * i);
                             fence_async_smem();
                             __syncwarp();
                             if (lane == 0)
@@ -592,19 +612,12 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             }
         }
     } else {
-        // ---- Q, a group of chunks as soon as the products of the segment before are done with it
+        // ---- the Q of later segments, a group of chunks as soon as the products of the segment before are done with it
         for (uint32_t n = 0; next_segment(walk, p, seg); ++n) {
             const uint16_t *q = p.q + (int64_t)seg.t * p.q_token_stride + (lane >> 3) * kDim + 8 * (lane & 7);
-            auto done = [&](int grp) {   // this lane's copies of the group are complete
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_q + 8 * grp);
-            };
 #pragma unroll 1
-            for (int grp = 0; grp < kQGroups; ++grp) {
-                if (n > 0)
-                    mbar_wait(bar_qfree + 8 * grp, (n - 1) & 1u, abort_flag, p.status);
+            for (int grp = 0; grp < kQGroups && n > 0; ++grp) {
+                mbar_wait(bar_qfree + 8 * grp, (n - 1) & 1u, abort_flag, p.status);
 #pragma unroll 1
                 for (int m = 3 * grp; m < 3 * grp + 3; ++m) {
                     const int c = m == 0 ? kChunks - 1 : m - 1;
@@ -613,19 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                     for (int h = 0; h < kH; h += 4)
                         copy16(dst + sw128(h + (lane >> 3), lane & 7), q + h * kDim + 64 * c);
                 }
-                if (kFour) {
-                    arrive_copied(bar_qraw + 8 * grp);
-                } else {
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    if (grp > 0) {
-                        asm volatile("cp.async.wait_group 1;" ::: "memory");
-                        done(grp - 1);
-                    }
-                }
-            }
-            if (!kFour) {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-                done(kQGroups - 1);
+                arrive_copied(bar_qraw + 8 * grp);
             }
             if (walk.start < walk.w1) {   // the next token's
                 const uint8_t *next = reinterpret_cast<const uint8_t *>(p.q + (int64_t)(seg.t + 1) * p.q_token_stride);
