@@ -7,16 +7,24 @@
 //
 // Contraction.  S[128 keys x H heads] = K_tile[128 x 576] . Q^T, keys on the M side, so that a key's logits lie in one lane of
 // tensor memory and its sum over the heads is a thread's own loop.  Q of a token (H x 576 in BF16, up to 144 KB) stays in
-// shared memory.  The entries come whole, by asynchronous 16-byte copies whose neighbours are neighbours in memory (bulk copies
-// of an entry each take some 80 cycles), into a ring of 16-key units for each quadrant; a thread takes 64 dims of its key out of one, dequantises
-// them to BF16 (exactly) and writes them to tensor memory, from where the product reads them: written to shared memory
-// instead, the keys' stores and the products' reads of both operands (and loads to registers, whose pieces of 16 or 32
-// bytes a row take a pass of L1 each) kept L1 busy for 80 % of the time.
+// shared memory.  The entries come whole, by asynchronous 16-byte copies, into a ring of 16-key units for each quadrant; a thread
+// takes its 64-dim chunks out of one, dequantises them to BF16 (exactly) and writes them to tensor memory, from where the
+// product reads them: written to shared memory instead, the keys' stores and the products' reads of both operands (and loads to
+// registers, whose pieces of 16 or 32 bytes a row take a pass of L1 each) kept L1 busy for 80 % of the time.
 //
-// Roles (23 warps): warp 0 issues the products; warps 1-4 read a finished block out of one of two accumulators, a quadrant
-// each, while the next block is computed; warps 5 and 6 issue the copies; warps 7-22 bring Q and dequantise, in four sets that
-// take every fourth 64-dim chunk, a warp a quadrant.  A persistent CTA per multiprocessor takes an equal run of the blocks
-// of all tokens.
+// Roles (24 warps): warp 0 issues the products; warps 1-4 read a finished block out of one of two accumulators, a quadrant
+// each, while the next block is computed; warps 5 and 6 copy entries; warps 7-22 dequantise, in four sets, a warp a quadrant, and
+// bring the CTA's first Q; warp 23 brings the Q of later tokens, in three groups of chunks, each as soon as the last products
+// with what stood there are done.  A persistent CTA per multiprocessor takes an equal run of the blocks of all tokens.
+//
+// What bounds it (128 heads, 10 blocks a CTA): 54 us for 128 tokens of 8-bit entries and 35 for 6 histories of 20000 to 40000 4-bit ones, of
+// which this kernel takes 28 to 36 and 26.  A CTA's first products start 4 us after it (lengths, slots, entries, Q: 200 KB
+// through an L1 that takes 43 bytes a cycle); then a block takes 6.3 k cycles (8-bit) or 4.2 k, where its products are
+// 2.3 k.  Copying a block takes the two warps 3.6 k cycles, dequantising it the sixteen 3.3 k, and with two to three units to a
+// quadrant beside Q one waits for the other: the copies, whose rows of 400 or 656 bytes never fill L1's lines (64 bytes a row take 21
+// cycles for 512 bytes, 24 bytes a cycle at most; 12 cycles where a warp's lanes are neighbours).  Slower: a third copy warp (78 / 58 us),
+// 128 bytes a row (58 / 38), bulk copies for a quarter or an eighth of the rows (60 / 43; one takes its warp 60 cycles), units
+// finished by one lane after a wait for the group (59 / 38).
 //
 // Tokens of one row are added in ascending order, one rounding each, so the result does not depend on timing: the first
 // token with keys that names a row is added by the epilogue, the others by a second kernel.
@@ -49,8 +57,8 @@ constexpr int kSlots = 8;                // chunks in tensor memory, 32 columns 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColKeys = 256;       // (two accumulators of up to 128 columns before them)
 constexpr int kMaxDepth = 4;             // units of a quadrant's ring
-constexpr int kSwitch = 1;               // blocks' worth of time that a token's start takes
-constexpr int kLongRun = 4;              // blocks to a CTA from which on the starts count
+constexpr int kSwitch = 1;               // blocks' worth of time that a token's start takes (some 1 us; the dearest CTAs set the time)
+constexpr int kLongRun = 4;              // blocks to a CTA from which on the starts count (with fewer, some would get none)
 constexpr int kAddThreads = 256;
 constexpr int kAddSlices = 4;
 constexpr int kFront = 8;                // entries of a token that a thread has in flight
@@ -435,9 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
         }
     } else if (warp < kKeyWarp0) {
         // ---- the entries of two quadrants, four lanes to a row (rows without a key keep what was there: nobody reads their
-        // sums): a lane has the rows lane / 4, + 8, + 16 and + 24 of a quadrant, whose addresses are all that it computes (with
-        // consecutive lanes at consecutive pieces, a division and a shuffle each, the two warps were what the others waited
-        // for).  Every unit of a ring is filled by one warp, so it is never two phases behind its barrier
+        // sums): a lane has the rows lane / 4, + 8, + 16 and + 24 of a quadrant, whose addresses are all that it computes.  Every
+        // unit of a ring is filled by one warp, so it is never two phases behind its barrier
         constexpr int kPieces = S::kEntry / 16;
         const int quad0 = 2 * (warp - kCopyWarp0);
         const uint8_t *kv = p.kv + 16 * (lane & 3);
