@@ -129,6 +129,15 @@ def test_tables_of_many_rows(rows):
     check(dataclasses.replace(w, block_table=table, req_idx=at[w.req_idx].astype(np.int32)))
 
 
+@pytest.mark.parametrize("heads,kind", [(16, 0), (128, 0), (128, 1)])
+def test_long_runs_across_tokens(heads, kind):
+    need_gpu()
+    seqs = np.random.default_rng(heads).integers(700, 1500, 96)          # 9 blocks to a token, 5 to a multiprocessor
+    seqs[[3, 50, 51]] = 0, 1, 0
+    w = both(synth.make_workload(name="w", seed=13, heads=heads, req_seq_lens=seqs, topk_width=40, window=1300, sink=False))[kind]
+    check(w)
+
+
 def test_hundreds_of_tokens_of_few_rows():
     need_gpu()
     w = synth.make_workload(name="w", seed=10, heads=16, req_seq_lens=[500, 260, 300], tokens_per_req=110, topk_width=12, window=9,
