@@ -22,7 +22,7 @@
 // through an L1 that takes 43 bytes a cycle); then a block takes 6.3 k cycles (8-bit) or 4.2 k, where its products are
 // 2.3 k.  Copying a block takes the two warps 3.6 k cycles, dequantising it the sixteen 3.3 k, and with two to three units to a
 // quadrant beside Q one waits for the other: the copies, whose rows of 400 or 656 bytes never fill L1's lines (64 bytes a row take 21
-// cycles for 512 bytes, 24 bytes a cycle at most; 12 cycles where a warp's lanes are neighbours).  Slower: a third copy warp (78 / 58 us),
+// cycles for 512 bytes, 24 bytes a cycle at most; 12 cycles where a warp's lanes are neighbours).  Slower: a third copy warp (63 / 46 us),
 // 128 bytes a row (58 / 38), bulk copies for a quarter or an eighth of the rows (60 / 43; one takes its warp 60 cycles), units
 // finished by one lane after a wait for the group (59 / 38).
 //
@@ -498,16 +498,6 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                 }
                 // a block's units are free when all of its chunks are dequantised, so the next block's copies begin late: its
                 // entries wait in L2 (every 128-byte line of one: it starts and ends on 16-byte boundaries)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int from = next[i >> 2][i & 3];
-                    if (from >= 0) {
-                        const uint8_t *src = p.kv + (int64_t)from * S::kEntry + 128 * (lane & 3);
-                        prefetch_l2(src);
-                        if (512 + 128 * (lane & 3) < S::kEntry)
-                            prefetch_l2(src + 512);
-                    }
-                }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
