@@ -628,6 +628,8 @@ DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_st
  *   tokens           int32 [num_reqs, tokens_width], row stride tokens_stride; tokens_width >= k + 1.
  *   num_accepted     int32 [num_reqs].
  *   seq_lens, seq_lens_out  int32 [num_reqs], both or neither; may be one array.
+ * tokens, num_accepted and seq_lens_out must not overlap the inputs (seq_lens_out == seq_lens apart) or one another
+ * (DSV4_ERR_INVALID_ARG).
  * A request without a row, with rows or drafts outside the arrays, or with more of them than tokens_width gets -1 and
  * a = 0 (its length is kept); one without a positive value gets a token of -1.  Both set DSV4_ERR_BAD_INDEX in the device
  * status word.  Nothing is allocated.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.

@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "../../include/dsv4.h"
+#include "overlap.h"
 #include "serving.h"
 
 using namespace dsv4;
@@ -18,17 +19,10 @@ constexpr int kMaxWindow = 1 << 24;
 constexpr int kMaxVocab = 1 << 22;
 constexpr int kMaxPages = 1 << 30, kMaxRowPages = 1 << 20;
 
-// whether [a, a + na) and [b, b + nb) share a byte
-bool overlap(const void *a, size_t na, const void *b, size_t nb)
+// `rows` rows of `width` values of `unit` bytes
+Rows rows_of(const void *at, int rows, int64_t stride, int64_t width, int64_t unit = 4)
 {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-
-// bytes from the first to the last of `rows` rows of `width` 4-byte values
-size_t span4(int rows, int64_t stride, int64_t width)
-{
-    return rows > 0 && width > 0 ? 4 * ((size_t)(rows - 1) * (size_t)stride + (size_t)width) : 0;
+    return Rows{at, rows, stride * unit, width * unit};
 }
 
 // ---- the key weights' workspace: the tokens' slots, positions and lengths, and what each key received
@@ -111,8 +105,19 @@ extern "C" DSV4_API dsv4_status dsv4_verify_drafts(
         (num_drafts > 0 && (draft_tokens == nullptr || (draft_probs != nullptr && draft_stride < vocab))) ||
         (seq_lens == nullptr) != (seq_lens_out == nullptr))
         return DSV4_ERR_INVALID_ARG;
-    const size_t unit = probs_bf16 ? 2 : 4;
+    const int64_t unit = probs_bf16 ? 2 : 4;
     if (!aligned(target_probs, unit) || !aligned(draft_probs, unit))
+        return DSV4_ERR_INVALID_ARG;
+    // the CTAs of a request, and other requests, read their inputs at different times; lengths may be updated in place
+    const Rows target = rows_of(target_probs, num_rows, target_stride, vocab, unit),
+               draft = rows_of(draft_probs, num_drafts, draft_stride, vocab, unit), drafted = bytes(draft_tokens, 4ll * num_drafts),
+               starts = bytes(query_start_loc, 4 * (num_reqs + 1ll)), numbers = bytes(uniform, 4ll * num_rows),
+               modes = bytes(greedy, num_reqs), lens = bytes(seq_lens, 4ll * num_reqs),
+               out = rows_of(tokens, num_reqs, tokens_stride, tokens_width), accepted = bytes(num_accepted, 4ll * num_reqs),
+               new_lens = bytes(seq_lens_out, 4ll * num_reqs);
+    if (share(out, {target, draft, drafted, starts, numbers, modes, lens, accepted, new_lens}) ||
+        share(accepted, {target, draft, drafted, starts, numbers, modes, lens, new_lens}) ||
+        share(new_lens, {target, draft, drafted, starts, numbers, modes}) || (seq_lens_out != seq_lens && share(new_lens, lens)))
         return DSV4_ERR_INVALID_ARG;
     VerifyParams p{};
     int sms = 0;
@@ -280,11 +285,13 @@ extern "C" DSV4_API dsv4_status dsv4_cache_evict(
         return DSV4_ERR_INVALID_ARG;
     // the old rows are read while the new ones are written; counts and weights may be updated in place
     const bool same_weights = weights == weights_out && (num_rows <= 1 || weights_stride == weights_out_stride);
-    if (overlap(block_table, span4(num_rows, bt_stride, max_blocks), block_table_out, span4(num_rows, bt_out_stride, max_blocks)) ||
-        overlap(seq_lens, 4 * (size_t)num_rows, seq_lens_out, 4 * (size_t)num_rows) ||
-        (ref_counts != ref_counts_out && overlap(ref_counts, 4 * (size_t)num_blocks, ref_counts_out, 4 * (size_t)num_blocks)) ||
-        (!same_weights && overlap(weights, span4(num_rows, weights_stride, weights_width), weights_out,
-                                  span4(num_rows, weights_out_stride, weights_width))))
+    const Rows table = rows_of(block_table, num_rows, bt_stride, max_blocks), lens = bytes(seq_lens, 4ll * num_rows),
+               refs = bytes(ref_counts, 4ll * num_blocks), had = rows_of(weights, num_rows, weights_stride, weights_width),
+               new_table = rows_of(block_table_out, num_rows, bt_out_stride, max_blocks),
+               new_lens = bytes(seq_lens_out, 4ll * num_rows), new_refs = bytes(ref_counts_out, 4ll * num_blocks),
+               left = rows_of(weights_out, num_rows, weights_out_stride, weights_width);
+    if (share(table, new_table) || share(lens, new_lens) || (ref_counts != ref_counts_out && share(refs, new_refs)) ||
+        (!same_weights && share(had, left)))
         return DSV4_ERR_INVALID_ARG;
     EvictParams p{};
     int sms = 0;

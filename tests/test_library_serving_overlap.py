@@ -1,0 +1,63 @@
+"""CPU-only: calls whose outputs share bytes with what is still read are refused at the C ABI."""
+import ctypes
+
+import pytest
+import torch
+
+import sparse_mla_decode_combine_gb300 as pkg
+from sparse_mla_decode_combine_gb300 import build as b
+
+BAD = pkg.DSV4_ERR_INVALID_ARG
+made_up = pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up: only a machine without a GPU takes them so far")
+MB = 1 << 20
+R, V, N, W = 4, 100, 12, 6                   # requests, vocabulary, rows, width of the tokens
+VERIFY = dict(target=MB, draft=2 * MB, tokens=3 * MB, start=4 * MB, uniform=5 * MB, greedy=6 * MB, out=7 * MB, accepted=8 * MB,
+              seq=9 * MB, seq_out=9 * MB)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    b.build()
+    return pkg.load_library()
+
+
+def P(x):
+    return ctypes.c_void_p(x)
+
+
+def verify(lib, stride=W, **change):
+    """Byte addresses; nothing behind them is touched by a call that is refused."""
+    a = {**VERIFY, **change}
+    return lib.dsv4_verify_drafts(P(a["target"]), V, P(a["draft"]), V, 0, V, P(a["tokens"]), N - R, P(a["start"]), R, N,
+                                  P(a["uniform"]), P(a["greedy"]), P(a["out"]), stride, W, P(a["accepted"]), P(a["seq"]),
+                                  P(a["seq_out"]), None)
+
+
+# the inputs' sizes in bytes
+INPUTS = dict(target=4 * N * V, draft=4 * (N - R) * V, tokens=4 * (N - R), start=4 * (R + 1), uniform=4 * N, greedy=R, seq=4 * R)
+
+
+@pytest.mark.parametrize("name", INPUTS)
+def test_verify(lib, name):
+    at, n = VERIFY[name], INPUTS[name]
+    for out, size in (("out", 4 * R * W), ("accepted", 4 * R)):
+        for shift in (0, n // 4 * 4 - 4 if n > 4 else 0, 4 - size):
+            assert verify(lib, **{out: at + shift}) == BAD, (out, shift)
+    if name != "seq":
+        assert verify(lib, seq_out=at) == BAD
+    else:
+        assert verify(lib, seq_out=at + 4) == BAD and verify(lib, seq_out=at - 4) == BAD
+
+
+def test_verify_outputs_among_themselves(lib):
+    for a, b_ in (("out", "accepted"), ("out", "seq_out"), ("accepted", "seq_out"), ("accepted", "seq")):
+        assert verify(lib, **{a: VERIFY[b_]}) == BAD, (a, b_)
+    assert verify(lib, stride=10, accepted=VERIFY["out"] + 4 * (3 * 10 + W - 1)) == BAD
+
+
+@made_up
+def test_verify_arrays_that_do_not_meet_are_taken(lib):
+    gap = VERIFY["out"] + 4 * W             # between two rows of `out`, which are 10 values apart
+    for change in (dict(), dict(seq_out=10 * MB), dict(seq=None, seq_out=None), dict(stride=10, accepted=gap), dict(stride=10, seq_out=gap),
+                   dict(out=VERIFY["tokens"] - 4 * R * W), dict(out=VERIFY["tokens"] + 4 * (N - R)), dict(draft=None)):
+        assert verify(lib, **change) == pkg.DSV4_ERR_CUDA, change       # (there is no device; the arguments were taken)
