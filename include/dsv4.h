@@ -657,6 +657,7 @@ DSV4_API dsv4_status dsv4_verify_drafts(const void *target_probs, int64_t target
  *   weights         fp32 [num_reqs, weights_width], row stride weights_stride; weights_width >= max_blocks * page_block;
  *   workspace       at least dsv4_sparse_mla_key_weights_workspace_size(...) bytes, 256-byte aligned, not used by
  *                   anything else until the work enqueued by this call has finished.
+ * weights and the workspace must not overlap the inputs or each other (DSV4_ERR_INVALID_ARG).
  * Block-table entries and rows out of range are data errors, as in the decode; such keys are left out.
  * Returns DSV4_OK, DSV4_ERR_INVALID_ARG, DSV4_ERR_UNSUPPORTED (num_heads, topk_width, entry_bytes) or DSV4_ERR_CUDA.
  */

@@ -190,6 +190,17 @@ extern "C" DSV4_API dsv4_status dsv4_sparse_mla_key_weights(
     WeightsPlan pl;
     if (!weights_plan(num_tokens, num_heads, topk_width, window, &pl) || workspace_bytes < pl.total)
         return DSV4_ERR_INVALID_ARG;
+    // the table is written, and the workspace, while lists, rows and queries are read again
+    const Rows table = rows_of(weights, num_reqs, weights_stride, weights_width), ws_bytes = bytes(workspace, (int64_t)pl.total);
+    for (const Rows &in : {rows_of(q, num_tokens, q_token_stride, (int64_t)num_heads * kDim, 2),
+                           bytes(kv_cache, (int64_t)num_blocks * page_block * entry_bytes),
+                           rows_of(block_table, num_reqs, bt_stride, max_blocks), bytes(req_idx, 4ll * num_tokens),
+                           rows_of(topk_idx, num_tokens, topk_stride, topk_width), bytes(topk_lens, 4ll * num_tokens),
+                           bytes(seq_lens, 4ll * num_tokens), bytes(lse, 4ll * num_tokens * num_heads)})
+        if (share(table, in) || share(ws_bytes, in))
+            return DSV4_ERR_INVALID_ARG;
+    if (share(table, ws_bytes))
+        return DSV4_ERR_INVALID_ARG;
     if (pl.list_w == 0)
         return DSV4_OK;
     unsigned *status = nullptr;

@@ -61,3 +61,37 @@ def test_verify_arrays_that_do_not_meet_are_taken(lib):
     for change in (dict(), dict(seq_out=10 * MB), dict(seq=None, seq_out=None), dict(stride=10, accepted=gap), dict(stride=10, seq_out=gap),
                    dict(out=VERIFY["tokens"] - 4 * R * W), dict(out=VERIFY["tokens"] + 4 * (N - R)), dict(draft=None)):
         assert verify(lib, **change) == pkg.DSV4_ERR_CUDA, change       # (there is no device; the arguments were taken)
+
+
+WEIGHTS = dict(q=MB, kv=2 * MB, table=3 * MB, req=4 * MB, topk=5 * MB, lens=6 * MB, seq=7 * MB, lse=8 * MB, weights=9 * MB, ws=10 * MB)
+T, H = 5, 16                                 # rows of 2 pages of 64 entries; 3 rows
+WEIGHTS_INPUTS = dict(q=2 * T * H * 576, kv=7 * 64 * 400, table=4 * 3 * 2, req=4 * T, topk=4 * T * 8, lens=4 * T, seq=4 * T, lse=4 * T * H)
+
+
+def key_weights(lib, stride=128, **change):
+    a = {**WEIGHTS, **change}
+    n = lib.dsv4_sparse_mla_key_weights_workspace_size(T, H, 8, 4)
+    return lib.dsv4_sparse_mla_key_weights(P(a["q"]), 576 * H, P(a["kv"]), 7, 64, 400, P(a["table"]), 2, 2, 3, P(a["req"]), P(a["topk"]), 8,
+                                           8, P(a["lens"]), P(a["seq"]), T, H, 4, P(a["lse"]), 1.0, P(a["weights"]), stride, 128,
+                                           P(a["ws"]), n, None)
+
+
+@pytest.mark.parametrize("name", WEIGHTS_INPUTS)
+def test_key_weights(lib, name):
+    at, n = WEIGHTS[name], WEIGHTS_INPUTS[name]
+    for first in (at, at + n - 4, at + 4 - 4 * 3 * 128):
+        assert key_weights(lib, weights=first) == BAD, first
+    for first in (at, at + (n - 1) // 256 * 256):
+        assert key_weights(lib, ws=first) == BAD, first
+
+
+def test_key_weights_table_over_the_workspace(lib):
+    assert key_weights(lib, weights=WEIGHTS["ws"]) == BAD and key_weights(lib, weights=WEIGHTS["ws"] - 4 * 3 * 128 + 4) == BAD
+
+
+@made_up
+def test_key_weights_arrays_that_do_not_meet_are_taken(lib):
+    gap = WEIGHTS["weights"] + 4 * 128       # between two rows of a table whose rows are 256 values apart
+    for change in (dict(), dict(lens=None), dict(stride=256, lse=gap), dict(stride=256, seq=gap), dict(weights=WEIGHTS["seq"] + 4 * T),
+                   dict(weights=WEIGHTS["seq"] - 4 * 3 * 128)):
+        assert key_weights(lib, **change) == pkg.DSV4_ERR_CUDA, change
