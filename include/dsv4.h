@@ -702,6 +702,7 @@ DSV4_API size_t dsv4_sparse_mla_key_weights_workspace_size(int32_t num_tokens, i
  *                    may be weights (with the same stride).
  *   workspace        at least dsv4_cache_evict_workspace_size(...) bytes, 256-byte aligned, not used by anything else
  *                    until the call's work has finished.
+ * The outputs and the workspace must not overlap the inputs, those two pairs apart, or one another (DSV4_ERR_INVALID_ARG).
  * max_blocks <= 2^20, num_blocks <= 2^30.  A page number outside [0, num_blocks) in a row that is read becomes -1, entries
  * on such pages are not moved, a length past max_blocks * page_block is cut; both set DSV4_ERR_BAD_INDEX.  Nothing is
  * allocated; the call can be captured.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.

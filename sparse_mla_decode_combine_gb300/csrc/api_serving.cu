@@ -301,8 +301,11 @@ extern "C" DSV4_API dsv4_status dsv4_cache_evict(
                new_table = rows_of(block_table_out, num_rows, bt_out_stride, max_blocks),
                new_lens = bytes(seq_lens_out, 4ll * num_rows), new_refs = bytes(ref_counts_out, 4ll * num_blocks),
                left = rows_of(weights_out, num_rows, weights_out_stride, weights_width);
-    if (share(table, new_table) || share(lens, new_lens) || (ref_counts != ref_counts_out && share(refs, new_refs)) ||
-        (!same_weights && share(had, left)))
+    const Rows ws_bytes = bytes(workspace, (int64_t)pl.total);
+    if ((ref_counts != ref_counts_out && share(refs, new_refs)) || (!same_weights && share(had, left)) ||
+        share(new_table, {table, lens, refs, had, new_lens, new_refs, left, ws_bytes}) ||
+        share(new_lens, {table, lens, refs, had, new_refs, left, ws_bytes}) || share(new_refs, {table, lens, had, left, ws_bytes}) ||
+        share(left, {table, lens, refs, ws_bytes}) || share(ws_bytes, {table, lens, refs, had}))
         return DSV4_ERR_INVALID_ARG;
     EvictParams p{};
     int sms = 0;

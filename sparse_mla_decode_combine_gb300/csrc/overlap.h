@@ -15,11 +15,13 @@ struct Rows {
     int64_t rows, stride, width;
 };
 inline Rows bytes(const void *at, int64_t n) { return Rows{at, 1, n, n}; }
+inline Rows joined(const Rows &a) { return a.rows > 1 && a.stride == a.width ? bytes(a.at, a.rows * a.width) : a; }
 
 // Rows that lie between the other array's, as in a buffer that holds both side by side, do not share a byte with it; where the
-// strides differ that is not looked for, and what reaches into the other array's span counts as shared.
-inline bool share(const Rows &a, const Rows &b)
+// strides of both differ that is not looked for, and what reaches into the other array's span counts as shared.
+inline bool share(const Rows &x, const Rows &y)
 {
+    const Rows a = joined(x), b = joined(y);
     if (a.at == nullptr || b.at == nullptr || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0)
         return false;
     const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b.at) - reinterpret_cast<uintptr_t>(a.at));

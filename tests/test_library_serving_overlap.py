@@ -95,3 +95,41 @@ def test_key_weights_arrays_that_do_not_meet_are_taken(lib):
     for change in (dict(), dict(lens=None), dict(stride=256, lse=gap), dict(stride=256, seq=gap), dict(weights=WEIGHTS["seq"] + 4 * T),
                    dict(weights=WEIGHTS["seq"] - 4 * 3 * 128)):
         assert key_weights(lib, **change) == pkg.DSV4_ERR_CUDA, change
+
+
+EVICT = dict(table=MB, lens=2 * MB, weights=3 * MB, table_out=4 * MB, lens_out=5 * MB, refs=6 * MB, refs_out=7 * MB, left=8 * MB, ws=9 * MB)
+E_R, E_M, E_B = 3, 4, 9                      # rows of 4 pages of 4 entries; 9 pages
+EVICT_SIZES = dict(table=4 * E_R * E_M, lens=4 * E_R, refs=4 * E_B, weights=4 * E_R * 16, table_out=4 * E_R * E_M, lens_out=4 * E_R,
+                   refs_out=4 * E_B, left=4 * E_R * 16)
+
+
+def evict(lib, stride=16, **change):
+    a = {**EVICT, **change}
+    n = lib.dsv4_cache_evict_workspace_size(E_R, E_M, E_B, 2, 4, 16, 6)
+    return lib.dsv4_cache_evict(P(64 * MB), 2, 16 * 4 * E_B, E_B, 4, 16, P(a["table"]), E_M, P(a["lens"]), E_R, E_M, P(a["weights"]),
+                                stride, 16, 6, 7, 2, 2, P(a["table_out"]), E_M, P(a["lens_out"]), P(a["refs"]), P(a["refs_out"]),
+                                P(a["left"]), stride, P(a["ws"]), n, None)
+
+
+@pytest.mark.parametrize("out", ["table_out", "lens_out", "refs_out", "left"])
+def test_evict(lib, out):
+    pairs = {("refs_out", "refs"), ("left", "weights")}
+    for name, n in EVICT_SIZES.items():
+        if name != out:
+            for shift in (0, n - 4, 4 - EVICT_SIZES[out]):
+                if shift or (out, name) not in pairs:
+                    assert evict(lib, **{out: EVICT[name] + shift}) == BAD, (name, shift)
+    assert evict(lib, **{out: EVICT["ws"]}) == BAD
+
+
+def test_evict_workspace(lib):
+    for name in ("table", "lens", "refs", "weights"):
+        assert evict(lib, ws=EVICT[name]) == BAD, name
+
+
+@made_up
+def test_evict_arrays_that_do_not_meet_are_taken(lib):
+    gap = EVICT["left"] + 4 * 16             # between two rows of weights that are 64 values apart
+    for change in (dict(), dict(refs_out=EVICT["refs"]), dict(left=EVICT["weights"]), dict(stride=64, lens_out=gap),
+                   dict(stride=64, table_out=gap), dict(stride=64, left=EVICT["weights"] + 4 * 16), dict(lens_out=EVICT["lens"] + 4 * E_R)):
+        assert evict(lib, **change) == pkg.DSV4_ERR_CUDA, change
