@@ -287,10 +287,11 @@ __device__ __forceinline__ void make_plan(const EvictParams &p)
         } else if (cut) {   // the lowest i with kept(i) != i (kept(i) - i does not fall), 32 places at a time
             int a = 0, z = m;
             while (a < z) {
-                const int step = (z - a + 31) / 32, i = a + lane * step;
-                const unsigned still = __ballot_sync(0xffffffffu, i < z && kept(p, r, n, i) == i);
+                const int step = (z - a - 1) / 32 + 1;
+                const int64_t i = a + (int64_t)lane * step;   // (rows may have nearly 2^31 entries)
+                const unsigned still = __ballot_sync(0xffffffffu, i < z && kept(p, r, n, (int)i) == i);
                 const int c = __popc(still);          // (a run of the low lanes)
-                z = c == 0 ? a : min(z, a + c * step);
+                z = c == 0 ? a : (int)min((int64_t)z, a + (int64_t)c * step);
                 a = c == 0 ? a : a + (c - 1) * step + 1;
             }
             f = a;
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
             float *dst = p.weights_out + (int64_t)r * p.weights_out_stride;
             uint32_t *bits = p.read + (int64_t)p.rows * p.columns * p.words + (int64_t)r * p.weight_words;
             if (zeros) {   // [m, width), once every source has been read
-                const int i0 = tile * kZeroTile, i1 = min(p.weights_width, i0 + kZeroTile);
+                const int i0 = tile * kZeroTile, i1 = i0 + min(p.weights_width - i0, kZeroTile);
                 bool lost = false;
                 if (i1 <= m)
                     continue;
@@ -519,21 +520,23 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
                         atomicOr(p.status, kStatusTimeout);
                     continue;
                 }
-                for (int i = max(m, i0) + tid; i < i1; i += kMoveThreads)
-                    dst[i] = 0.f;
+                const int z0 = max(m, i0);
+                for (int u = tid; u < i1 - z0; u += kMoveThreads)
+                    dst[z0 + u] = 0.f;
                 continue;
             }
             const int i0 = tile * kWeightTile, f = m < n ? __ldcg(p.moved + r) : n;
             // (a row that is not cut may be longer than a tile for each of the budget's entries)
-            for (int j0 = i0; j0 < m; j0 += p.weight_tiles * kWeightTile) {
-                if (same_weights && j0 + kWeightTile <= f)
+            for (int64_t j = i0; j < m; j += (int64_t)p.weight_tiles * kWeightTile) {
+                const int j0 = (int)j, left = m - j0;   // (rows may have nearly 2^31 entries)
+                if (same_weights && f - j0 >= kWeightTile)
                     continue;   // (nothing moves)
                 float v[kUnroll];
                 float sum = 0.f;
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int i = j0 + u * kMoveThreads + tid;
-                    v[u] = i < m ? __ldcg(src + (i < f ? i : kept(p, r, n, i))) : 0.f;
+                    const int i = u * kMoveThreads + tid;
+                    v[u] = i < left ? __ldcg(src + (i < f - j0 ? j0 + i : kept(p, r, n, j0 + i))) : 0.f;
                     sum = fmaxf(sum, v[u]);
                 }
                 bool lost = false;
@@ -553,9 +556,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
                 }
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int i = j0 + u * kMoveThreads + tid;
-                    if (i < m)
-                        dst[i] = v[u];
+                    const int i = u * kMoveThreads + tid;
+                    if (i < left)
+                        dst[j0 + i] = v[u];
                 }
             }
             continue;
