@@ -614,7 +614,7 @@ DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_st
  *   num_accepted[b] = a
  *   seq_lens_out[b] = seq_lens[b] - (k - a)   (the cache's entries of the drafts that do not stand are dropped)
  * Products and comparisons are exact; sums are held to 2^-46 of themselves or better.  Probabilities are finite (they
- * need not sum to 1); negative values and NaN count as 0.
+ * need not sum to 1); negative values and NaN count as 0, in the comparisons as in the sums.
  *
  * Arguments:
  *   target_probs     fp32, or BF16 when probs_bf16 != 0, [num_rows, vocab], row stride target_stride (>= vocab).

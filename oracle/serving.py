@@ -59,8 +59,8 @@ def verify(target, draft, tokens, start, uniform, greedy=None, seq=None, width=N
             if greedy is not None and greedy[b]:
                 ok = 0 <= d == largest(p)
             elif 0 <= d < V:
-                qd = 1.0 if draft is None else float(draft[d0 + a][d])
-                ok = float(uniform[r0 + a]) * qd < p[d]
+                qd = 1.0 if draft is None else float(_clean(draft[d0 + a][d]))
+                ok = float(uniform[r0 + a]) * qd < _clean(p[d])
             else:
                 ok = False
             if not ok:

@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                 if (d >= 0 && d < V) {
                     const float x = value(target[(int64_t)(row0 + j) * p.target_stride + d]);
                     const float y = draft != nullptr ? value(draft[(int64_t)(d0 + j) * p.draft_stride + d]) : 1.f;
-                    good = product_below(p.uniform[row0 + j], y, x);
+                    good = product_below(p.uniform[row0 + j], fmaxf(y, 0.f), fmaxf(x, 0.f));   // (NaN counts as 0)
                 }
             }
             const unsigned m = __ballot_sync(0xffffffffu, good);
