@@ -613,7 +613,7 @@ DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_st
  *   tokens[b]       = d_0 .. d_{a-1}, token, then -1
  *   num_accepted[b] = a
  *   seq_lens_out[b] = seq_lens[b] - (k - a)   (the cache's entries of the drafts that do not stand are dropped)
- * Products and comparisons are exact; sums are held to 2^-46 of themselves or better.  Probabilities are finite (they
+ * Products and comparisons are exact; sums are held to 2^-40 of themselves or better.  Probabilities are finite (they
  * need not sum to 1); negative values and NaN count as 0, in the comparisons as in the sums.
  *
  * Arguments:

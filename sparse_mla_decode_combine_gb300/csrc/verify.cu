@@ -12,9 +12,12 @@
 // CTA of the request finds a (one load of p and q a draft), the request's cluster sums its row's weights tile by tile, the
 // CTA whose part holds the wanted sum finds the tile and then the token.
 //
-// What is decided next to a border has to be right, so sums are pairs of floats (high, low), good to about 2^-46 of
-// themselves: a weight is the exact difference of two floats, and Knuth's two-sum says what every addition loses.  In
-// fp64, whose rate is a sixty-fourth of fp32's here, the search alone took a CTA 20 us.
+// What is decided next to a border has to be right, so sums are pairs of floats (high, low), good to 2^-40 of themselves at the
+// worst: a weight is the exact difference of two floats, and Knuth's two-sum says what every addition loses.  In units of
+// 2^-48 of the sum: 26 for the roundings of the residuals in the groups of values, 3 for each of the additions of two pairs on
+// the way from a value to the sum: 4 to 32 groups of a lane, 5 for the lanes, up to 32 tiles of a run, 5 and 3 for the runs and the CTAs, 14 in
+// the search (wide tiles have few tiles to a run).  With the residuals of all of a lane's 64 to 256 values in one float, a likely token in front
+// of a flat tail took 2^-36.  In fp64, whose rate is a sixty-fourth of fp32's here, the search alone took a CTA 20 us.
 //
 // What bounds it.  Large batches: HBM, and the 20 additions a pair of values takes (half of the time at the measured rate of
 // both).  Loads of a thread's next 16 values are issued before any is used: with a load, its use and the next
@@ -80,17 +83,15 @@ __device__ __forceinline__ float add(Sum &s, float x)
     return r;
 }
 
-// max(p - q, 0), exactly, into the sum (q >= 0)
-__device__ __forceinline__ void add_difference(Sum &s, float p, float q)
+// max(p - q, 0), exactly (q >= 0; NaN has no weight)
+__device__ __forceinline__ Sum difference(float p, float q)
 {
     const float d = __fsub_rn(p, q), b = __fsub_rn(d, p);
     const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b));
-    // (the rounded difference has the exact one's sign; NaN has no weight)
-    const float r = add(s, fmaxf(d, 0.f));
-    s.lo = __fadd_rn(s.lo, __fadd_rn(r, d > 0.f ? e : 0.f));
+    return Sum{fmaxf(d, 0.f), d > 0.f ? e : 0.f};   // (the rounded difference has the exact one's sign)
 }
 
-__device__ __forceinline__ Sum plus(const Sum &a, const Sum &b)   // (of positive sums: within 2^-46)
+__device__ __forceinline__ Sum plus(const Sum &a, const Sum &b)   // (of positive sums: within 3 * 2^-48)
 {
     Sum s = {a.hi, 0.f};
     const float r = add(s, b.hi);
@@ -159,24 +160,34 @@ struct Row {
                     if (kQ)
                         y[u] = py[32 * u];
                 }
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u)
-                    one<kQ>(s, value(x[u]), kQ ? value(y[u]) : 0.f);
             } else {
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u)
-                    if (i0 + 32 * u + lane < t1) {
-                        x[u] = px[32 * u];
-                        if (kQ)
-                            y[u] = py[32 * u];
-                    }
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
                     const int i = i0 + 32 * u + lane;
-                    if (i < t1 && i != point)
-                        one<kQ>(s, value(x[u]), kQ ? value(y[u]) : 0.f);
+                    const bool counts = i < t1 && i != point;
+                    x[u] = counts ? px[32 * u] : T(0.f);
+                    if (kQ)
+                        y[u] = counts ? py[32 * u] : T(0.f);
                 }
             }
+            // a group's sum by halves, its additions' residuals beside it: they are small against the group, not against the lane's sum
+            float v[kLoads], lost = 0.f;
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const Sum w = kQ ? difference(value(x[u]), fmaxf(value(y[u]), 0.f)) : Sum{fmaxf(value(x[u]), 0.f), 0.f};
+                v[u] = w.hi;
+                if (kQ)
+                    lost = __fadd_rn(lost, w.lo);
+            }
+#pragma unroll
+            for (int d = 1; d < kLoads; d <<= 1)
+#pragma unroll
+                for (int u = 0; u < kLoads; u += 2 * d) {
+                    Sum pair = {v[u], 0.f};
+                    lost = __fadd_rn(lost, add(pair, v[u + d]));
+                    v[u] = pair.hi;
+                }
+            s = plus(s, Sum{v[0], lost});
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
@@ -184,14 +195,6 @@ struct Row {
             s = plus(s, Sum{hi, lo});
         }
         return s;
-    }
-    template <bool kQ>
-    static __device__ __forceinline__ void one(Sum &s, float x, float y)   // (values of NaN count as 0)
-    {
-        if (kQ)
-            add_difference(s, x, fmaxf(y, 0.f));
-        else
-            s.lo = __fadd_rn(s.lo, add(s, fmaxf(x, 0.f)));
     }
 };
 
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                 for (int u = 0; u < kEach; ++u) {
                     v[u] = Sum{0.f, 0.f};
                     if (i + u < t1 && i + u != row.point)
-                        add_difference(v[u], value(x[u]), row.q != nullptr ? fmaxf(value(y[u]), 0.f) : 0.f);
+                        v[u] = difference(value(x[u]), row.q != nullptr ? fmaxf(value(y[u]), 0.f) : 0.f);
                     sum = plus(sum, v[u]);
                 }
                 Sum before;
