@@ -614,7 +614,8 @@ DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_st
  *   num_accepted[b] = a
  *   seq_lens_out[b] = seq_lens[b] - (k - a)   (the cache's entries of the drafts that do not stand are dropped)
  * Products and comparisons are exact; sums are held to 2^-40 of themselves or better.  Probabilities are finite (they
- * need not sum to 1); negative values and NaN count as 0, in the comparisons as in the sums.
+ * need not sum to 1, but the positive ones of a row to less than 2^127); negative values and NaN count as 0, in the
+ * comparisons as in the sums.
  *
  * Arguments:
  *   target_probs     fp32, or BF16 when probs_bf16 != 0, [num_rows, vocab], row stride target_stride (>= vocab).
@@ -631,8 +632,8 @@ DSV4_API dsv4_status dsv4_cache_copy_pages(void *dst_cache, int64_t dst_layer_st
  * tokens, num_accepted and seq_lens_out must not overlap the inputs (seq_lens_out == seq_lens apart) or one another
  * (DSV4_ERR_INVALID_ARG).
  * A request without a row, with rows or drafts outside the arrays, or with more of them than tokens_width gets -1 and
- * a = 0 (its length is kept); one without a positive value gets a token of -1.  Both set DSV4_ERR_BAD_INDEX in the device
- * status word.  Nothing is allocated.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.
+ * a = 0 (its length is kept); one whose row a has no positive value, or sums to 2^127 or more, gets a token of -1.  Both set
+ * DSV4_ERR_BAD_INDEX in the device status word.  Nothing is allocated.  Returns DSV4_OK, DSV4_ERR_INVALID_ARG or DSV4_ERR_CUDA.
  */
 DSV4_API dsv4_status dsv4_verify_drafts(const void *target_probs, int64_t target_stride, const void *draft_probs,
                                         int64_t draft_stride, int32_t probs_bf16, int32_t vocab,

@@ -80,7 +80,7 @@ def verify(target, draft, tokens, start, uniform, greedy=None, seq=None, width=N
                 else:
                     left = _clean(p - _clean(draft[d0 + a]))
                 w = left if left.sum() > 0 else w
-            token, may[b] = drawn(w, float(uniform[r0 + k])) if w.sum() > 0 else (-1, {-1})
+            token, may[b] = drawn(w, float(uniform[r0 + k])) if 0 < w.sum() < 2.0 ** 127 else (-1, {-1})
         bad += token < 0
         out[b, a], acc[b] = token, a
         if seq is not None:

@@ -101,6 +101,8 @@ __device__ __forceinline__ Sum plus(const Sum &a, const Sum &b)   // (of positiv
 
 __device__ __forceinline__ bool above(const Sum &a, const Sum &b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
 
+__device__ __forceinline__ Sum scaled(const Sum &a, float power) { return Sum{__fmul_rn(a.hi, power), __fmul_rn(a.lo, power)}; }
+
 __device__ __forceinline__ Sum times(const Sum &a, float u)
 {
     const float p = __fmul_rn(a.hi, u);
@@ -207,6 +209,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
     __shared__ unsigned long long wbest[kWarps];
     __shared__ Sum wscan[kWarps];
     __shared__ Sum want, start;
+    __shared__ float lift;
     __shared__ int owner, chosen, found, last_positive;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = p.cluster, b = blockIdx.x / C;
@@ -358,9 +361,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                 const Sum t = lane < C ? totals[lane] : Sum{0.f, 0.f};
                 Sum before;
                 const Sum sum = scan32(t, lane, 8, before);
-                const Sum w = times(shfl(sum, 7), p.uniform[row0 + k]);
-                const unsigned over = __ballot_sync(0xffffffffu, t.hi > 0.f && above(sum, w)), some = __ballot_sync(0xffffffffu, t.hi > 0.f);
-                const int who = over != 0u ? __ffs(over) - 1 : some != 0u ? 31 - __clz(some) : -1;
+                const Sum all = shfl(sum, 7);
+                // small sums are compared at a scale at which the product has its low part
+                const float up = all.hi < 0x1p-64f ? 0x1p64f : 1.f;
+                const Sum w = times(scaled(all, up), p.uniform[row0 + k]);
+                const unsigned over = __ballot_sync(0xffffffffu, t.hi > 0.f && above(scaled(sum, up), w));
+                const unsigned some = __ballot_sync(0xffffffffu, t.hi > 0.f);
+                // (a sum past the range, which may have become infinite or NaN, draws nothing)
+                const int who = !(all.hi < 0x1p127f) ? -1 : over != 0u ? __ffs(over) - 1 : some != 0u ? 31 - __clz(some) : -1;
                 if (who == rank) {
                     // the lanes' runs, then the tiles of one run
                     Sum at = plus(shfl(before, who), before_run), last_at = at, first_at = at;
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                         if (v.hi > 0.f) {
                             last = i;
                             last_at = at;
-                            if (first < 0 && above(next, w)) {
+                            if (first < 0 && above(scaled(next, up), w)) {
                                 first = i;
                                 first_at = at;
                             }
@@ -385,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                         chosen = tile;
                         start = tile_at;
                         want = w;
+                        lift = up;
                         found = INT_MAX;
                         last_positive = -1;
                     }
@@ -412,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
             const int t0 = lo + chosen * p.tile, t1 = min(hi, t0 + p.tile);
             Sum run = start;
             const Sum w = want;
+            const float up = lift;
             for (int i0 = t0; i0 < t1; i0 += kEach * kThreads) {
                 const int i = i0 + kEach * tid;
                 T x[kEach], y[kEach];
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
                     at = plus(at, v[u]);
                     if (v[u].hi > 0.f) {
                         mine_last = i + u;
-                        if (mine_first == INT_MAX && above(at, w))
+                        if (mine_first == INT_MAX && above(scaled(at, up), w))
                             mine_first = i + u;
                     }
                 }

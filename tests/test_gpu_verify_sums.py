@@ -1,6 +1,7 @@
-"""The accuracy of draft verification's sums on the GPU, where it is hardest: rows of a likely token and a flat tail.
+"""The accuracy of draft verification's sums on the GPU, where it is hardest: rows of a likely token and a flat tail, sums of subnormal
+values, and sums past the range.
 
-Every value is a multiple of 2^-49 and the whole is below 1, so that sums are exact in 64 bits and the
+In the peaked rows every value is a multiple of 2^-49 and the whole is below 1, so that sums are exact in 64 bits and the
 wanted sum u T in 73: a row is set up to have a border 2^-39 (2^-40 in the smaller vocabularies) of the whole above or below its
 wanted sum.  The kernel's sums are within 2^-40 of themselves: with v = 2^-24, half a step of fp32, and an addition of two pairs
 good to 3 v^2 of their sum,
@@ -20,7 +21,7 @@ import torch
 
 import sparse_mla_decode_combine_gb300 as pkg
 from gpu_util import need_gpu
-from test_gpu_verify import dev
+from test_gpu_verify import check, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +91,59 @@ def test_peaked_differences(V, log_distance, R):
             q[0, 7] = 0.5                    # turned down: 0.75 0.5 is not below p(7)
             assert np.array_equal(np.maximum(p[0].astype(np.float64) - q[0], 0) * 2 ** 49, w)
             assert draw(p, q, [7], m, R) == token, (at, side)
+
+
+def rows(p, u, **over):
+    R = len(p)
+    return dict(target=p.astype(np.float32), draft=None, tokens=np.zeros(0, np.int32), start=np.arange(R + 1, dtype=np.int32),
+                uniform=np.asarray(u, np.float32), greedy=None, seq=np.arange(R, dtype=np.int32) + 5, **over)
+
+
+@pytest.mark.parametrize("V", [3, 700, 40000])
+@pytest.mark.parametrize("log", [-149, -130, -105, -70, -63])
+def test_small_sums(V, log):
+    need_gpu()
+    # whole numbers times a power of 2: sums are exact, and the product with u in 64 bits of fraction
+    R = 12
+    rng = np.random.default_rng(V - log)
+    p = np.ldexp(rng.integers(0, 4, (R, V)).astype(np.float64), log)
+    p[:, 0] = np.ldexp(1.0, log)
+    u = rng.random(R).astype(np.float32)
+    total = np.ldexp(p, -log).sum(1)
+    for r in range(R // 2):                  # on a border, or next to one
+        u[r] = np.float32(np.float32(rng.integers(0, total[r])) / np.float32(total[r]))
+    u[R - 1] = 0.0
+    check(rows(p, u), exact=True)
+
+
+def test_small_differences():
+    need_gpu()
+    V = 5000
+    rng = np.random.default_rng(5)
+    q = np.ldexp(rng.integers(0, 9, (1, V)).astype(np.float64), -149).astype(np.float32)
+    p = np.concatenate([q + np.ldexp(rng.integers(0, 3, (1, V)).astype(np.float64), -149), q]).astype(np.float32)
+    p[0, 9], q[0, 9] = 0.0, 1.0              # turned down
+    for u in (0.0, 0.25, 0.5, 0.75, 0.9999):
+        check(dict(target=p, draft=q, tokens=np.array([9], np.int32), start=np.array([0, 2], np.int32),
+                   uniform=np.array([0.5, u], np.float32), greedy=None, seq=np.array([7], np.int32)), exact=True)
+
+
+@pytest.mark.parametrize("V", [2, 3000, 50000])
+def test_sums_past_the_range_are_flagged(V):
+    need_gpu()
+    p = np.zeros((6, V), np.float32)
+    p[0, :2] = 3e38                          # past fp32's range
+    p[1, :2] = 2.0 ** 126                    # 2^127
+    p[2, 0], p[2, 1] = 2.0 ** 126, 2.0 ** 125
+    p[3, 1] = np.inf
+    p[4, 0], p[4, 1] = -3e38, 1e38
+    p[5] = 2e38
+    got = check(rows(p, [0.75, 0.5, 0.7, 0.5, 0.5, 0.1]), exact=True)
+    assert got[:5, 0].tolist() == [-1, -1, 1, -1, 1] and got[5, 0] == -1
+    q = np.zeros((1, V), np.float32)
+    q[0, 0] = 1e38
+    c = dict(target=np.stack([p[0], p[2]]), draft=q, tokens=np.array([0], np.int32), start=np.array([0, 2], np.int32),
+             uniform=np.array([np.nan, 0.5], np.float32), greedy=None, seq=np.array([7], np.int32))
+    assert check(c, exact=True)[0].tolist() == [-1, -1]
+    c["uniform"][0] = 0.5                    # accepted
+    assert check(c, exact=True)[0].tolist() == [0, 0]

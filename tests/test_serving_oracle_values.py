@@ -11,3 +11,9 @@ def test_negative_values_and_nan_count_as_nothing(pd, qd, stands):
     p, q = np.array([[0.0, pd, 0.5], [0.25, 0.0, 0.0]]), np.array([[0.0, qd, 0.0]])
     out, acc, _, _, bad = serving.verify(p, q, [1], [0, 2], [0.25, 0.5])
     assert acc.tolist() == [int(stands)] and out.tolist() == [[1, 0] if stands else [2, -1]] and bad == 0
+
+
+def test_sums_past_the_range():
+    p = np.array([[2.0 ** 126, 2.0 ** 126], [2.0 ** 126, 2.0 ** 125], [np.inf, 0.0]])
+    out, acc, _, _, bad = serving.verify(p, None, [], [0, 1, 2, 3], [0.5, 0.5, 0.5])
+    assert out.tolist() == [[-1], [0], [-1]] and acc.tolist() == [0, 0, 0] and bad == 2
