@@ -649,8 +649,8 @@ DSV4_API dsv4_status dsv4_verify_drafts(const void *target_probs, int64_t target
  *   weights[row][p] += sum over heads h of e^{s_p - lse[t][h]}
  * for each token t, with row, the positions p of its list K_t and the logits s_p as in dsv4_sparse_mla_decode (8-bit
  * entries) or dsv4_sparse_mla_decode_fp4 (4-bit ones), and the lse that it returned.  A head whose lse is -inf gives
- * nothing.  Tokens of one row are added in ascending order, one rounding to fp32 each.  Several layers may be added to
- * one table, a call each.
+ * nothing, whatever its query is; what a head gives below 2^-126 is 0.  Tokens of one row are added in ascending order,
+ * one rounding to fp32 each.  Several layers may be added to one table, a call each.
  *
  * Arguments: those of the decode, with
  *   entry_bytes     656 or 400 (others: DSV4_ERR_UNSUPPORTED): kv_cache uint8 [num_blocks, page_block, entry_bytes];

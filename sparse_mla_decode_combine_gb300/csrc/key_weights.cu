@@ -395,11 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
             const int r = p.req_idx != nullptr ? __ldcg(p.req_idx + t) : t;
             const bool first_of = __ldcg(p.later + t) == 0;
             named_bar(1, 32 * kEpilogueWarps);   // (slse has been read)
+            bool without = false;
             if (row < kH) {
                 const float l = __ldcg(p.lse + (int64_t)t * kH + row);
-                slse[row] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;   // (a head without weight)
+                without = l == -INFINITY;
+                const float m = l * -1.4426950408889634f;
+                slse[row] = without ? INFINITY : m == INFINITY ? 0x1.fffffep127f : m;
             }
-            named_bar(1, 32 * kEpilogueWarps);
+            const bool some_without = named_bar_or(1, 32 * kEpilogueWarps, without);   // (heads that give nothing, whatever their logits)
             // the place of a block's key (-1: none), read a block ahead
             const int64_t list = (int64_t)t * p.list_w;
             auto load_place = [&](int b) {
@@ -416,6 +419,19 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                 mbar_wait(bar_dfull + 8 * x, (g >> 1) & 1u, abort_flag, p.status);
                 after_sync();
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                if (some_without) {
+#pragma unroll 1
+                    for (int h = 0; h < kH; h += 16) {
+                        uint32_t s[16];
+                        tmem_ld16(lane_base + kH * x + h, s);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float l = slse[h + j];
+                            sum[j & 3] += l == INFINITY ? 0.f : exp2_approx(fmaf(__uint_as_float(s[j]), c2, l));
+                        }
+                    }
+                } else
 #pragma unroll
                 for (int h = 0; h < kH; h += 16) {
                     uint32_t s[16];
