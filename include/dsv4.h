@@ -651,6 +651,9 @@ DSV4_API dsv4_status dsv4_verify_drafts(const void *target_probs, int64_t target
  * entries) or dsv4_sparse_mla_decode_fp4 (4-bit ones), and the lse that it returned.  A head whose lse is -inf gives
  * nothing, whatever its query is; what a head gives below 2^-126 is 0.  Tokens of one row are added in ascending order,
  * one rounding to fp32 each.  Several layers may be added to one table, a call each.
+ * Where some of the tokens are drafts, the call belongs after dsv4_verify_drafts, with a length of 0 for tokens
+ * num_accepted + 1 and on of each request: before it, the attention of the drafts that fall is added for good, and their
+ * own positions keep a weight that the tokens after them inherit (until an eviction, which clears what lies past a row's end).
  *
  * Arguments: those of the decode, with
  *   entry_bytes     656 or 400 (others: DSV4_ERR_UNSUPPORTED): kv_cache uint8 [num_blocks, page_block, entry_bytes];
