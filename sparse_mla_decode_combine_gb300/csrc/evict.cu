@@ -6,7 +6,7 @@
 //             first + picked[i - first]     the picked ones
 //             n - budget + i                the recent ones
 // Three launches: the selection, a plan (pages, lengths, counts), and the moves; two for a few short rows, whose selection and plan
-// are one cluster's (4 rows of 700: 15.7 us with three, 14.7 with two).
+// are one cluster's (4 rows of 300 to 700: 15.7 us with three, 13.8 with two).
 //
 // The selection.  Rows of up to 4096 entries between the first and the recent ones: a CTA a row, an entry's weight as an
 // order-preserving 32-bit key in a register.  The lightest kept key is found two bits at a time by counting (no histograms,
@@ -22,8 +22,11 @@
 // The moves go through every layer, in place and in one pass over the bytes.  A row's new entries are cut into tiles; a
 // CTA reads the sources of a tile into registers, says so in a bitmap, waits until the tiles before it whose sources its own
 // writes would overwrite have been read (sources lie at or past their targets, so only earlier tiles can be in the way),
-// and writes.  Tiles are handed out by a ticket in that order, so those that a tile waits for were begun before it and
-// never wait for it; every wait is bounded.  The weights go the same way, in tiles of their own.
+// and writes.  Tiles are handed out by a ticket in that order, and a CTA draws its next one while it has one in hand, so a tile may wait
+// for one that nobody has begun.  All the same every wait ends: a CTA says that its tile has been read before it waits,
+// so the lowest ticket that has not been read is either being read, or it is the next one of a CTA whose tile in hand, a lower
+// ticket, waits for still lower ones, which have all been read.  Each wait is bounded besides.  The weights go the same way, in
+// tiles of their own.
 #include <algorithm>
 #include <climits>
 
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
         if (ticket >= tickets)
             return;
         __syncthreads();   // (`next` has been read; src_at and dst_at are free)
-        if (tid == 0)      // (the next one is on its way meanwhile)
+        if (tid == 0)      // (the next one is on its way meanwhile; one and no more, or waits might not end)
             next = atomicAdd(p.ticket, 1);
         if (ticket < weight_tickets + zero_tickets) {
             const bool zeros = ticket >= weight_tickets;

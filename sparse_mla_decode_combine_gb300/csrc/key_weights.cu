@@ -512,8 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const KeyWeigh
                         ++round;
                     }
                 }
-                // a block's units are free when all of its chunks are dequantised, so the next block's copies begin late: its
-                // entries wait in L2 (every 128-byte line of one: it starts and ends on 16-byte boundaries)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
