@@ -19,8 +19,7 @@
 // the search (wide tiles have few tiles to a run).  With the residuals of all of a lane's 64 to 256 values in one float, a likely token in front
 // of a flat tail took 2^-36.  In fp64, whose rate is a sixty-fourth of fp32's here, the search alone took a CTA 20 us.
 //
-// What bounds it.  Large batches: HBM, and the 20 additions a pair of values takes (half of the time at the measured rate of
-// both).  Loads of a thread's next 16 values are issued before any is used: with a load, its use and the next
+// What bounds it.  Large batches: HBM, and the 15 additions and four comparisons that a pair of values takes.  Loads of a thread's next 16 values are issued before any is used: with a load, its use and the next
 // load one behind the other, 256 requests of 151937 took 217 us.  One request: the chain of dependent loads (row numbers,
 // tokens, probabilities, the row, the tile again) and the cluster's barrier.
 #include <algorithm>
@@ -91,12 +90,17 @@ __device__ __forceinline__ Sum difference(float p, float q)
     return Sum{fmaxf(d, 0.f), d > 0.f ? e : 0.f};   // (the rounded difference has the exact one's sign)
 }
 
+__device__ __forceinline__ Sum normal(float x, float y)   // x + y, exactly (|y| <= |x|)
+{
+    const float hi = __fadd_rn(x, y);
+    return Sum{hi, __fsub_rn(y, __fsub_rn(hi, x))};
+}
+
 __device__ __forceinline__ Sum plus(const Sum &a, const Sum &b)   // (of positive sums: within 3 * 2^-48)
 {
     Sum s = {a.hi, 0.f};
     const float r = add(s, b.hi);
-    const float l = __fadd_rn(__fadd_rn(a.lo, b.lo), r), hi = __fadd_rn(s.hi, l);
-    return Sum{hi, __fsub_rn(l, __fsub_rn(hi, s.hi))};
+    return normal(s.hi, __fadd_rn(__fadd_rn(a.lo, b.lo), r));
 }
 
 __device__ __forceinline__ bool above(const Sum &a, const Sum &b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
@@ -106,8 +110,7 @@ __device__ __forceinline__ Sum scaled(const Sum &a, float power) { return Sum{__
 __device__ __forceinline__ Sum times(const Sum &a, float u)
 {
     const float p = __fmul_rn(a.hi, u);
-    const float l = __fadd_rn(__fmaf_rn(a.hi, u, -p), __fmul_rn(a.lo, u)), hi = __fadd_rn(p, l);
-    return Sum{hi, __fsub_rn(l, __fsub_rn(hi, p))};
+    return normal(p, __fadd_rn(__fmaf_rn(a.hi, u, -p), __fmul_rn(a.lo, u)));
 }
 
 __device__ __forceinline__ Sum shfl(const Sum &s, int lane)
@@ -189,7 +192,7 @@ struct Row {
                     lost = __fadd_rn(lost, add(pair, v[u + d]));
                     v[u] = pair.hi;
                 }
-            s = plus(s, Sum{v[0], lost});
+            s = plus(s, normal(v[0], lost));
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
