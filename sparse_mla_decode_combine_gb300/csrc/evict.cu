@@ -46,6 +46,7 @@ constexpr int kWeightTile = kMoveThreads * kUnroll;         // weights
 constexpr int kZeroTile = 4 * kWeightTile;
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectEach = 4;                              // keys of a thread
+constexpr int kWide = 1 << 30;                              // positions and tiles' ends of rows up to this fit 32 bits with room
 constexpr long long kWaitCycles = 4000000000LL;             // about two seconds
 
 __device__ __forceinline__ void cluster_sync()
@@ -290,12 +291,11 @@ __device__ __forceinline__ void make_plan(const EvictParams &p)
         } else if (cut) {   // the lowest i with kept(i) != i (kept(i) - i does not fall), 32 places at a time
             int a = 0, z = m;
             while (a < z) {
-                const int step = (z - a - 1) / 32 + 1;
-                const int64_t i = a + (int64_t)lane * step;   // (rows may have nearly 2^31 entries)
-                const unsigned still = __ballot_sync(0xffffffffu, i < z && kept(p, r, n, (int)i) == i);
+                const unsigned step = ((unsigned)(z - a) + 31u) / 32u, i = a + lane * step;   // (rows may have nearly 2^31 entries)
+                const unsigned still = __ballot_sync(0xffffffffu, i < (unsigned)z && kept(p, r, n, (int)i) == (int)i);
                 const int c = __popc(still);          // (a run of the low lanes)
-                z = c == 0 ? a : (int)min((int64_t)z, a + (int64_t)c * step);
-                a = c == 0 ? a : a + (c - 1) * step + 1;
+                z = c == 0 ? a : (int)min((unsigned)z, a + c * step);
+                a = c == 0 ? a : (int)(a + (c - 1) * step + 1u);
             }
             f = a;
         }
@@ -481,6 +481,8 @@ __device__ __forceinline__ bool wait_read(const uint32_t *bits, int first, int t
 
 // In the order of the tickets: the rows' weights in tiles (of all rows the first, then the second, ..), what has to be zero after
 // them, then the entries' tiles (of all rows and columns the first, then the second, ..).
+// Index: int, or int64_t where rows or weights past kWide would wrap around (with it for all, a row of 131000 took 1 % longer).
+template <typename Index>
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictParams p)
 {
     __shared__ int64_t src_at[kMaxTile], dst_at[kMaxTile];   // byte offsets in the layer; -1: not written
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
             float *dst = p.weights_out + (int64_t)r * p.weights_out_stride;
             uint32_t *bits = p.read + (int64_t)p.rows * p.columns * p.words + (int64_t)r * p.weight_words;
             if (zeros) {   // [m, width), once every source has been read
-                const int i0 = tile * kZeroTile, i1 = i0 + min(p.weights_width - i0, kZeroTile);
+                const Index i0 = tile * kZeroTile, i1 = min((Index)p.weights_width, i0 + kZeroTile);
                 bool lost = false;
                 if (i1 <= m)
                     continue;
@@ -523,23 +525,21 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
                         atomicOr(p.status, kStatusTimeout);
                     continue;
                 }
-                const int z0 = max(m, i0);
-                for (int u = tid; u < i1 - z0; u += kMoveThreads)
-                    dst[z0 + u] = 0.f;
+                for (Index i = max((Index)m, i0) + tid; i < i1; i += kMoveThreads)
+                    dst[i] = 0.f;
                 continue;
             }
             const int i0 = tile * kWeightTile, f = m < n ? __ldcg(p.moved + r) : n;
             // (a row that is not cut may be longer than a tile for each of the budget's entries)
-            for (int64_t j = i0; j < m; j += (int64_t)p.weight_tiles * kWeightTile) {
-                const int j0 = (int)j, left = m - j0;   // (rows may have nearly 2^31 entries)
-                if (same_weights && f - j0 >= kWeightTile)
+            for (Index j0 = i0; j0 < m; j0 += (Index)p.weight_tiles * kWeightTile) {
+                if (same_weights && j0 + kWeightTile <= f)
                     continue;   // (nothing moves)
                 float v[kUnroll];
                 float sum = 0.f;
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int i = u * kMoveThreads + tid;
-                    v[u] = i < left ? __ldcg(src + (i < f - j0 ? j0 + i : kept(p, r, n, j0 + i))) : 0.f;
+                    const Index i = j0 + u * kMoveThreads + tid;
+                    v[u] = i < m ? __ldcg(src + (i < f ? i : (Index)kept(p, r, n, (int)i))) : 0.f;
                     sum = fmaxf(sum, v[u]);
                 }
                 bool lost = false;
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
                         atomicOr(bits + tile / 32, 1u << (tile & 31));
                     }
                     if (tid < 32)
-                        lost = !wait_read(bits, min(tile, max(f, j0 - (n - m)) / kWeightTile), tile, tid);
+                        lost = !wait_read(bits, min(tile, max(f, (int)j0 - (n - m)) / kWeightTile), tile, tid);
                 }
                 if (__syncthreads_or(lost)) {
                     if (tid == 0)
@@ -559,9 +559,9 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
                 }
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) {
-                    const int i = u * kMoveThreads + tid;
-                    if (i < left)
-                        dst[j0 + i] = v[u];
+                    const Index i = j0 + u * kMoveThreads + tid;
+                    if (i < m)
+                        dst[i] = v[u];
                 }
             }
             continue;
@@ -652,6 +652,7 @@ cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream)
     const int64_t most = (int64_t)p.max_blocks * p.pool.page;    // of a row's entries
     // four moving CTAs to a multiprocessor, or as many as there are tiles
     const int64_t tickets = (int64_t)p.rows * (p.weight_tiles + p.zero_tiles + (int64_t)p.columns * p.tiles);
+    const auto move = std::max<int64_t>(most, p.weights_width) > kWide ? evict_move_kernel<int64_t> : evict_move_kernel<int>;
     const dim3 movers((unsigned)std::max<int64_t>(1, std::min<int64_t>(4ll * sms, tickets)));
     if (picked > 0 && p.rows > 0 && most > p.limit) {
         const int width = (int)(most - p.first - p.recent);
@@ -677,7 +678,7 @@ cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream)
                     (void)cudaGetLastError();
                     return e;
                 }
-                return launch_dependent(evict_move_kernel, movers, kMoveThreads, 0, stream, p);
+                return launch_dependent(move, movers, kMoveThreads, 0, stream, p);
             }
             e = launch_dependent(width <= kSelectThreads ? evict_select_kernel<1> : evict_select_kernel<kSelectEach>,
                                  dim3((unsigned)p.rows), kSelectThreads, 0, stream, p);
@@ -696,7 +697,7 @@ cudaError_t launch_evict(EvictParams p, int sms, cudaStream_t stream)
     const cudaError_t e = launch_dependent(evict_plan_kernel, dim3(kCluster), kPlanThreads, 0, stream, p);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(evict_move_kernel, movers, kMoveThreads, 0, stream, p);
+    return launch_dependent(move, movers, kMoveThreads, 0, stream, p);
 }
 
 }  // namespace dsv4
