@@ -494,8 +494,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_kernel(const Veri
 }  // namespace
 
 // CTAs per request: as many as are there at the same time, up to kMaxCluster, with kDeep values or more to a thread.  In us
-// with 1, 2, 3, 4, 6 and 8: 48 mixed requests of 100277 35, 25, 19, 19, 16, 20; 160 of 128000 34, 28, 24, 32, 29, 52; 256 of
-// 151937 80, 60, 65, 62, 65, 67.
+// with 1, 2, 3, 4, 6 and 8: 48 mixed requests of 100277 39, 25, 19, 18, 16, 17; 160 of 128000 33, 27, 23, 31, 28, 46; 256 of
+// 151937 77, 58, 63, 59, 63, 65.  One request of 32000 14, 13, 10, 11, 10, 11.  Few requests with wide vocabularies would take more:
+// one of 151937 28, 21, 15, 14, 14, 11, sixteen 40, 25, 19, 18, 15, 14.
 int verify_cluster_size(int num_reqs, int vocab, int sms)
 {
     const int fit = std::min(kCtasPerSm * sms / std::max(1, num_reqs), vocab / (kDeep * kThreads));
