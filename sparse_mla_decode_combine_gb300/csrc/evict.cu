@@ -22,11 +22,11 @@
 // The moves go through every layer, in place and in one pass over the bytes.  A row's new entries are cut into tiles; a
 // CTA reads the sources of a tile into registers, says so in a bitmap, waits until the tiles before it whose sources its own
 // writes would overwrite have been read (sources lie at or past their targets, so only earlier tiles can be in the way),
-// and writes.  Tiles are handed out by a ticket in that order, and a CTA draws its next one while it has one in hand, so a tile may wait
-// for one that nobody has begun.  All the same every wait ends: a CTA says that its tile has been read before it waits,
-// so the lowest ticket that has not been read is either being read, or it is the next one of a CTA whose tile in hand, a lower
-// ticket, waits for still lower ones, which have all been read.  Each wait is bounded besides.  The weights go the same way, in
-// tiles of their own.
+// and writes.  Tiles are handed out by a ticket in that order, and a CTA draws its next one while it has one in hand, so a
+// tile may wait for one that nobody has begun.  All the same every wait ends: a CTA says that its tile has been read before it
+// waits, so the lowest ticket that has not been read is either being read, or it is the next one of a CTA whose tile in hand,
+// a lower ticket, waits for still lower ones, which have all been read.  Each wait is bounded besides.  The weights go the
+// same way, in tiles of their own.
 #include <algorithm>
 #include <climits>
 

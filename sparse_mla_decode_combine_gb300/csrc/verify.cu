@@ -12,16 +12,18 @@
 // CTA of the request finds a (one load of p and q a draft), the request's cluster sums its row's weights tile by tile, the
 // CTA whose part holds the wanted sum finds the tile and then the token.
 //
-// What is decided next to a border has to be right, so sums are pairs of floats (high, low), good to 2^-40 of themselves at the
-// worst: a weight is the exact difference of two floats, and Knuth's two-sum says what every addition loses.  In units of
-// 2^-48 of the sum: 26 for the roundings of the residuals in the groups of values, 3 for each of the additions of two pairs on
-// the way from a value to the sum: 4 to 32 groups of a lane, 5 for the lanes, up to 32 tiles of a run, 5 and 3 for the runs and the CTAs, 14 in
-// the search (wide tiles have few tiles to a run).  With the residuals of all of a lane's 64 to 256 values in one float, a likely token in front
-// of a flat tail took 2^-36.  In fp64, whose rate is a sixty-fourth of fp32's here, the search alone took a CTA 20 us.
+// What is decided next to a border has to be right, so sums are pairs of floats (high, low), good to 2^-40 of themselves at
+// the worst: a weight is the exact difference of two floats, and Knuth's two-sum says what every addition loses.  In units of
+// 2^-48 of the sum: 26 for the roundings of the residuals in the groups of values, and 3 for each of the additions of two
+// pairs on the way from a value to the sum: 4 to 32 groups of a lane, 5 for the lanes, up to 32 tiles of a run, 5 and 3 for
+// the runs and the CTAs, 14 in the search (wide tiles have few tiles to a run).  With the residuals of all of a lane's 64 to
+// 256 values in one float, a likely token in front of a flat tail took 2^-36.  In fp64, whose rate is a sixty-fourth of
+// fp32's here, the search alone took a CTA 20 us.
 //
-// What bounds it.  Large batches: HBM, and the 15 additions and four comparisons that a pair of values takes.  Loads of a thread's next 16 values are issued before any is used: with a load, its use and the next
-// load one behind the other, 256 requests of 151937 took 217 us.  One request: the chain of dependent loads (row numbers,
-// tokens, probabilities, the row, the tile again) and the cluster's barrier.
+// What bounds it.  Large batches: HBM, and the 15 additions and four comparisons that a pair of values takes.  Loads of a
+// thread's next 16 values are issued before any is used: with a load, its use and the next load one behind the other, 256
+// requests of 151937 took 217 us.  One request: the chain of dependent loads (row numbers, tokens, probabilities, the row,
+// the tile again) and the cluster's barrier.
 #include <algorithm>
 #include <cuda_bf16.h>
 #include <limits.h>
@@ -175,7 +177,7 @@ struct Row {
                         y[u] = counts ? py[32 * u] : T(0.f);
                 }
             }
-            // a group's sum by halves, its additions' residuals beside it: they are small against the group, not against the lane's sum
+            // a group's sum by halves, its additions' residuals beside it: small against the group, not against the lane's sum
             float v[kLoads], lost = 0.f;
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
